@@ -234,13 +234,16 @@ def _code_only(text):
 
 def kernel_source_hash(workload):
     """Hash of the code a workload's kernels and launch choices come from:
-    the quantiser's own files for quantize_act, every other file for the
-    GEMM workloads (the host code, which plans and launches both, in each);
-    comments and blank space do not count."""
+    the quantiser's own files for quantize_act, the FP8 GEMMs' for the GEMM
+    workloads (the host code, which plans and launches both, in each; the
+    files of the operators around them in none); comments and blank space do
+    not count."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "moe_grouped_gemm_bf16_gb300", "csrc")
     quant = workload == "quantize_act"
     for f in sorted(os.listdir(csrc)):
+        if f.startswith(("dg_norm", "dg_swiglu", "dg_bf16", "dg_ops")):
+            continue
         if f != "dg_host.cu" and f.startswith("dg_quant") != quant:
             continue
         with open(os.path.join(csrc, f), encoding="utf-8") as fh:

@@ -79,7 +79,8 @@ typedef enum dg_status {
   DG_ERR_TIMEOUT = 7,           /* device: an internal wait gave up */
   DG_ERR_MASK_RANGE = 8,        /* device: masked_m[g] outside [0, max_m] (clamped) */
   DG_ERR_EXPERT_RANGE = 9,      /* device: m_indices outside [-1, G) or a 128-row block mixes experts */
-  DG_ERR_KS_RANGE = 10,         /* device: ks[g] negative, not a multiple of 128, or past K_total */
+  DG_ERR_KS_RANGE = 10,         /* device: ks[g] negative, not a multiple of 128, or past K_total
+                                   (ragged products: a size negative or past the rows) */
   DG_ERR_DEBUG_BOUNDS = 11,     /* device, checked build only: an access outside a tensor (skipped) */
   DG_ERR_DEBUG_PHASE = 12       /* device, checked build only: a ring slot held another fill */
 } dg_status;
@@ -255,6 +256,118 @@ dg_status dg_quantize_fp8_1x128(const void* X, void* Q, float* sa, int num_group
  * of ld_sa). */
 dg_status dg_quantize_fp8_1x128_ue8m0(const void* X, void* Q, int32_t* sfa, int num_groups,
                                       int M, int K, int ld_sfa, void* stream);
+
+/* Root-mean-square norm of X + R, its output quantised 1x128 as by
+ * dg_quantize_fp8_1x128: the step in front of a layer's first FP8 GEMM.  Per
+ * row m, in fp32:
+ *   h = X[m,k] + R[m,k];  rstd[m] = 1 / sqrt(mean_k(h^2) + eps);
+ *   y = h * rstd[m] * W[k];  H = bf16(h);  Y = bf16(y);
+ *   Q, sa = the 1x128 quantisation of y (of the fp32 value, not of Y)
+ *   X   bf16 [M][K]; R bf16 [M][K] or null (h = X); W bf16 [K]; finite values
+ *   H   bf16 [M][K] or null (not written; needs R): may be X or R itself
+ *   Y   bf16 [M][K] or null; Q e4m3 [M][K] or null: one of them at least
+ *   sa  fp32 [K/128][ld_sa] with Q: columns m < M are written
+ *   rstd fp32 [M] or null: kept for dg_rms_norm_backward
+ * K a multiple of 128 up to 16384 (else DG_ERR_UNSUPPORTED_SHAPE); eps >= 0;
+ * with Q, ld_sa >= M (else DG_ERR_INVALID_ARG) and a multiple of 4; tensors
+ * 16-byte, rstd 4-byte aligned (else DG_ERR_MISALIGNED).  M == 0 is a no-op. */
+dg_status dg_rms_norm_quantize_fp8_1x128(const void* X, const void* R, const void* W, void* H,
+                                         void* Y, void* Q, float* sa, float* rstd, int M, int K,
+                                         int ld_sa, float eps, void* stream);
+/* The same with packed UE8M0 scales (sfa int32 [ceil(K/512)][ld_sfa], as
+ * dg_quantize_fp8_1x128_ue8m0 writes them). */
+dg_status dg_rms_norm_quantize_fp8_1x128_ue8m0(const void* X, const void* R, const void* W, void* H,
+                                               void* Y, void* Q, int32_t* sfa, float* rstd, int M,
+                                               int K, int ld_sfa, float eps, void* stream);
+
+/* Gradient of the norm.  With dY the gradient of y, xh = H[m,k] * rstd[m] and
+ * g = dY[m,k] * W[k], in fp32:
+ *   dX[m,k] = bf16( rstd[m] * (g - xh * mean_k(g * xh)) + dR[m,k] )
+ *   dW[k]   = sum_m dY[m,k] * xh
+ * (dX is the gradient of X and of R alike; the rounding to 8 bits passes its
+ * gradient through.)
+ *   dY, H  bf16 [M][K] (H: what the forward call wrote, or its X without a
+ *          residual); rstd fp32 [M]; W bf16 [K]
+ *   dR     bf16 [M][K] or null: the gradient that reaches H along the residual
+ *          stream; dX bf16 [M][K], may be dR itself
+ *   dW     fp32 [K], written (not accumulated)
+ *   workspace  at least dg_rms_norm_backward_workspace_bytes(M, K) bytes of
+ *          device memory, 16-byte aligned; its contents need not be kept
+ * The sums run in a fixed order: the same inputs give the same bits on the
+ * same number of SMs.  K as in the forward call.  M == 0 writes dW = 0. */
+dg_status dg_rms_norm_backward(const void* dY, const void* H, const float* rstd, const void* W,
+                               const void* dR, void* dX, float* dW, void* workspace,
+                               long long workspace_bytes, int M, int K, void* stream);
+/* Bytes of workspace dg_rms_norm_backward needs (-1 for negative sizes). */
+long long dg_rms_norm_backward_workspace_bytes(int M, int K);
+
+/* Gated activation between the two products of an expert, y = silu(g) * u, its
+ * output quantised 1x128, and an 8-bit checkpoint of its input.  A row of GU
+ * holds the I gate columns, then the I up columns.  In fp32:
+ *   s = 1 / (1 + exp(-g));  y = g * s * u;  Y = bf16(y);
+ *   Q, sa = the 1x128 quantisation of y;  CQ, csa = that of GU (exactly what
+ *   dg_quantize_fp8_1x128 writes for GU as a matrix of K = 2 I columns)
+ *   GU  bf16 [num_groups][M][2 I], finite values
+ *   Y   bf16 [num_groups][M][I] or null; Q e4m3 [num_groups][M][I] or null, with
+ *   sa  fp32 [num_groups][I/128][ld_sa]
+ *   CQ  e4m3 [num_groups][M][2 I] or null, with csa fp32 [num_groups][2 I/128][ld_sa]
+ *       (one of Y, Q and CQ at least)
+ *   masked_m  int32 [num_groups] on the device, or null (all M rows): only the
+ *       rows m < masked_m[z] are read and written (the masked GEMMs' layout; a
+ *       value outside [0, M] is clamped and reported as DG_ERR_MASK_RANGE)
+ * I a multiple of 128, I/128 <= 32767, num_groups <= 65535 (else
+ * DG_ERR_UNSUPPORTED_SHAPE); ld_sa >= M and a multiple of 4 where scales are
+ * written; tensors 16-byte, masked_m 4-byte aligned.  M == 0 is a no-op. */
+dg_status dg_swiglu_quantize_fp8_1x128(const void* GU, void* Y, void* Q, float* sa, void* CQ,
+                                       float* csa, const int32_t* masked_m, int num_groups, int M,
+                                       int I, int ld_sa, void* stream);
+/* The same with packed UE8M0 scales of Q (sfa int32 [num_groups][ceil(I/512)]
+ * [ld_sfa]); the checkpoint keeps fp32 scales. */
+dg_status dg_swiglu_quantize_fp8_1x128_ue8m0(const void* GU, void* Y, void* Q, int32_t* sfa,
+                                             void* CQ, float* csa, const int32_t* masked_m,
+                                             int num_groups, int M, int I, int ld_sfa,
+                                             void* stream);
+
+/* Gradient of the gated activation from its checkpoint: g and u are
+ * code * scale, and with dY the gradient of y, in fp32:
+ *   dGU = bf16( dY * u * s * (1 + g * (1 - s)) ), bf16( dY * g * s )
+ *   Y   = bf16( g * s * u ) again, or null: the right operand of the second
+ *         product's weight gradient, which so needs no checkpoint of its own
+ * Layouts, masked_m and requirements as in the forward call. */
+dg_status dg_swiglu_backward_fp8_1x128(const void* CQ, const float* csa, const void* dY, void* dGU,
+                                       void* Y, const int32_t* masked_m, int num_groups, int M,
+                                       int I, int ld_csa, void* stream);
+
+/* bf16 products grouped by expert with ragged sizes: the experts kept in bf16,
+ * and the backward pass of those that run in FP8.  Group g owns the rows
+ * [r_g, r_g + ms[g]) of A, r_g = ms[0] + ... + ms[g-1]; sizes are any numbers
+ * >= 0 (no alignment), read on the device only.
+ *   nt  D[t][n] = bf16( sum_k A[t][k] B[g][n][k] )   (t in group g; forward)
+ *   nn  D[t][n] = bf16( sum_k A[t][k] B[g][k][n] )   (gradient of the activations)
+ *   A  bf16 [M_total][K]; B bf16 [num_groups][N][K] (nn: [num_groups][K][N]);
+ *   D  bf16 [M_total][N]; ms int32 [num_groups] on the device
+ * Rows of D past the groups' total are not written.  A negative size counts as
+ * zero and the total is clamped to M_total; both are reported as
+ * DG_ERR_KS_RANGE by dg_get_device_status.  Sums in fp32, one rounding.
+ * N and K positive multiples of 8 (else DG_ERR_UNSUPPORTED_SHAPE); 1 <=
+ * num_groups <= 1024; tensors 16-byte, sizes 4-byte aligned.  M_total == 0 is
+ * a no-op. */
+dg_status dg_m_grouped_gemm_bf16_nt_ragged(const void* A, const void* B, void* D, const int32_t* ms,
+                                           int M_total, int N, int K, int num_groups,
+                                           void* stream);
+dg_status dg_m_grouped_gemm_bf16_nn_ragged(const void* A, const void* B, void* D, const int32_t* ms,
+                                           int M_total, int N, int K, int num_groups,
+                                           void* stream);
+/*   tn  D[g][m][n] = bf16( C[g][m][n] + sum over the rows t of group g of
+ *                          A[t][m] B[t][n] )        (gradient of the weights)
+ *   A  bf16 [K_total][M], B bf16 [K_total][N], ks int32 [num_groups] on the
+ *   device (as ms above), C bf16 [num_groups][M][N] or null (may be D itself),
+ *   D  bf16 [num_groups][M][N]: all of it is written, a group without rows as C
+ *   or +0.  M and N multiples of 8.  M == 0 is a no-op; with K_total == 0, A and
+ *   B may be null. */
+dg_status dg_k_grouped_gemm_bf16_tn_ragged(const void* A, const void* B, const void* C, void* D,
+                                           const int32_t* ks, int num_groups, int M, int N,
+                                           int K_total, void* stream);
 
 /* Maximum number of SMs the kernels may use (DeepGEMM set_num_sms / get_num_sms,
  * es.news.hada.io/topic?id=19459, "Utilidades y variables de entorno").

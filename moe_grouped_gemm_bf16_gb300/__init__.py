@@ -24,7 +24,11 @@ __all__ = [
     "get_tma_aligned_size", "get_mk_alignment_for_contiguous_layout", "get_device_status",
     "plan_config", "num_output_tiles", "set_wait_timeout_ns", "debug_set_skip_producer",
     "debug_force_config", "debug_force_pair", "debug_force_block_scaled", "STATUS_NAMES",
-    "EXPORTED_SYMBOLS",
+    "EXPORTED_SYMBOLS", "rms_norm_quantize_fp8_1x128", "rms_norm_quantize_fp8_1x128_ue8m0",
+    "rms_norm_backward", "rms_norm_backward_workspace_bytes", "swiglu_quantize_fp8_1x128",
+    "swiglu_quantize_fp8_1x128_ue8m0", "swiglu_backward_fp8_1x128",
+    "m_grouped_gemm_bf16_nt_ragged", "m_grouped_gemm_bf16_nn_ragged",
+    "k_grouped_gemm_bf16_tn_ragged",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -57,6 +61,11 @@ EXPORTED_SYMBOLS = [
     "dg_num_output_tiles",
     "dg_set_wait_timeout_ns", "dg_debug_set_skip_producer", "dg_debug_force_config",
     "dg_debug_force_pair", "dg_debug_force_block_scaled",
+    "dg_rms_norm_quantize_fp8_1x128", "dg_rms_norm_quantize_fp8_1x128_ue8m0",
+    "dg_rms_norm_backward", "dg_rms_norm_backward_workspace_bytes",
+    "dg_swiglu_quantize_fp8_1x128", "dg_swiglu_quantize_fp8_1x128_ue8m0",
+    "dg_swiglu_backward_fp8_1x128", "dg_m_grouped_gemm_bf16_nt_ragged",
+    "dg_m_grouped_gemm_bf16_nn_ragged", "dg_k_grouped_gemm_bf16_tn_ragged",
 ]
 
 
@@ -127,8 +136,25 @@ def lib():
         L.dg_debug_force_config.argtypes = [_i, _i]
         L.dg_debug_force_pair.argtypes = [_i]
         L.dg_debug_force_block_scaled.argtypes = [_i]
+        for suffix in ("", "_ue8m0"):
+            getattr(L, "dg_rms_norm_quantize_fp8_1x128" + suffix).argtypes = [
+                _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, ctypes.c_float, _vp]
+            getattr(L, "dg_swiglu_quantize_fp8_1x128" + suffix).argtypes = [
+                _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp]
+        L.dg_rms_norm_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                           ctypes.c_longlong, _i, _i, _vp]
+        L.dg_rms_norm_backward_workspace_bytes.argtypes = [_i, _i]
+        L.dg_rms_norm_backward_workspace_bytes.restype = ctypes.c_longlong
+        L.dg_swiglu_backward_fp8_1x128.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
+                                                   _vp]
+        for name in ("nt", "nn"):
+            getattr(L, f"dg_m_grouped_gemm_bf16_{name}_ragged").argtypes = [
+                _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp]
+        L.dg_k_grouped_gemm_bf16_tn_ragged.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
+                                                       _vp]
         for f in EXPORTED_SYMBOLS:
-            if f not in ("dg_last_error_string", "dg_num_output_tiles"):
+            if f not in ("dg_last_error_string", "dg_num_output_tiles",
+                         "dg_rms_norm_backward_workspace_bytes"):
                 getattr(L, f).restype = _i
         _LIB = L
     return _LIB
@@ -270,6 +296,85 @@ def quantize_fp8_1x128(X, Q, sa, num_groups, M, K, ld_sa, stream=None):
     sa [G,K/128,ld_sa]; see dg_quantize_fp8_1x128."""
     _check(lib().dg_quantize_fp8_1x128(_ptr(X), _ptr(Q), _ptr(sa), num_groups, M, K, ld_sa,
                                        _stream(stream)))
+
+
+def rms_norm_quantize_fp8_1x128(X, R, W, H, Y, Q, sa, rstd, M, K, ld_sa, eps, stream=None):
+    """RMS norm of bf16 X + R [M,K] with weight W: H = X + R (bf16), Y (bf16) and
+    Q, sa (e4m3, fp32 [K/128, ld_sa]) its output, rstd fp32 [M]; R, H, rstd and
+    one of Y and Q may be None."""
+    _check(lib().dg_rms_norm_quantize_fp8_1x128(
+        _ptr(X), _ptr(R), _ptr(W), _ptr(H), _ptr(Y), _ptr(Q), _ptr(sa), _ptr(rstd), M, K, ld_sa,
+        eps, _stream(stream)))
+
+
+def rms_norm_quantize_fp8_1x128_ue8m0(X, R, W, H, Y, Q, sfa, rstd, M, K, ld_sfa, eps, stream=None):
+    """The RMS norm with packed UE8M0 scales sfa int32 [ceil(K/512), ld_sfa]."""
+    _check(lib().dg_rms_norm_quantize_fp8_1x128_ue8m0(
+        _ptr(X), _ptr(R), _ptr(W), _ptr(H), _ptr(Y), _ptr(Q), _ptr(sfa), _ptr(rstd), M, K, ld_sfa,
+        eps, _stream(stream)))
+
+
+def rms_norm_backward_workspace_bytes(M, K):
+    """Bytes of device workspace rms_norm_backward needs."""
+    return int(lib().dg_rms_norm_backward_workspace_bytes(int(M), int(K)))
+
+
+def rms_norm_backward(dY, H, rstd, W, dR, dX, dW, workspace, workspace_bytes, M, K, stream=None):
+    """Gradient of the RMS norm: dX bf16 [M,K] (plus dR, the residual stream's
+    gradient, or None; dX may be dR) and dW fp32 [K]."""
+    _check(lib().dg_rms_norm_backward(
+        _ptr(dY), _ptr(H), _ptr(rstd), _ptr(W), _ptr(dR), _ptr(dX), _ptr(dW), _ptr(workspace),
+        workspace_bytes, M, K, _stream(stream)))
+
+
+def swiglu_quantize_fp8_1x128(GU, Y, Q, sa, CQ, csa, num_groups, M, I, ld_sa, masked_m=None,
+                              stream=None):
+    """y = silu(gate) * up of bf16 GU [G,M,2I] (gate columns, then up columns): Y
+    (bf16), Q, sa (e4m3, fp32 [G,I/128,ld_sa]) and the 8-bit checkpoint CQ, csa of
+    GU ([G,M,2I], fp32 [G,2I/128,ld_sa]), each or None; masked_m int32 [G] on the
+    device limits the rows."""
+    _check(lib().dg_swiglu_quantize_fp8_1x128(
+        _ptr(GU), _ptr(Y), _ptr(Q), _ptr(sa), _ptr(CQ), _ptr(csa), _ptr(masked_m), num_groups, M,
+        I, ld_sa, _stream(stream)))
+
+
+def swiglu_quantize_fp8_1x128_ue8m0(GU, Y, Q, sfa, CQ, csa, num_groups, M, I, ld_sfa,
+                                    masked_m=None, stream=None):
+    """The gated activation with packed UE8M0 scales sfa int32 [G,ceil(I/512),ld_sfa]
+    of Q (the checkpoint's scales stay fp32)."""
+    _check(lib().dg_swiglu_quantize_fp8_1x128_ue8m0(
+        _ptr(GU), _ptr(Y), _ptr(Q), _ptr(sfa), _ptr(CQ), _ptr(csa), _ptr(masked_m), num_groups, M,
+        I, ld_sfa, _stream(stream)))
+
+
+def swiglu_backward_fp8_1x128(CQ, csa, dY, dGU, Y, num_groups, M, I, ld_csa, masked_m=None,
+                              stream=None):
+    """Gradient dGU bf16 [G,M,2I] of the gated activation from its checkpoint, and
+    the activation Y bf16 [G,M,I] again (or None)."""
+    _check(lib().dg_swiglu_backward_fp8_1x128(
+        _ptr(CQ), _ptr(csa), _ptr(dY), _ptr(dGU), _ptr(Y), _ptr(masked_m), num_groups, M, I,
+        ld_csa, _stream(stream)))
+
+
+def m_grouped_gemm_bf16_nt_ragged(A, B, D, ms, M_total, N, K, num_groups, stream=None):
+    """D[t] = A[t] B[g]^T for the rows t of group g: bf16 A [M_total,K], B [G,N,K],
+    D [M_total,N]; ms int32 [G] on the device, any sizes."""
+    _check(lib().dg_m_grouped_gemm_bf16_nt_ragged(_ptr(A), _ptr(B), _ptr(D), _ptr(ms), M_total, N,
+                                                  K, num_groups, _stream(stream)))
+
+
+def m_grouped_gemm_bf16_nn_ragged(A, B, D, ms, M_total, N, K, num_groups, stream=None):
+    """D[t] = A[t] B[g] for the rows t of group g: bf16 A [M_total,K], B [G,K,N],
+    D [M_total,N]; ms int32 [G] on the device, any sizes."""
+    _check(lib().dg_m_grouped_gemm_bf16_nn_ragged(_ptr(A), _ptr(B), _ptr(D), _ptr(ms), M_total, N,
+                                                  K, num_groups, _stream(stream)))
+
+
+def k_grouped_gemm_bf16_tn_ragged(A, B, D, ks, num_groups, M, N, K_total, C=None, stream=None):
+    """D[g] = C[g] + A_g^T B_g over each group's rows: bf16 A [K_total,M], B
+    [K_total,N], D (and C) [G,M,N]; ks int32 [G] on the device, any sizes."""
+    _check(lib().dg_k_grouped_gemm_bf16_tn_ragged(_ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(ks),
+                                                  num_groups, M, N, K_total, _stream(stream)))
 
 
 def get_num_sms():

@@ -19,6 +19,7 @@
 #include <vector>
 
 #include "dg.h"
+#include "dg_host.h"
 #include "dg_instances.cuh"
 #include "dg_quant.h"
 
@@ -633,6 +634,36 @@ dg_status run(int kind, const void* A, const float* sa, int ld_sa, const void* B
 
 }  // namespace
 
+// What the other operators' entry points share with these (dg_host.h).
+namespace dgk {
+
+dg_status host_fail(dg_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(s, "%s", buf);
+}
+
+dg_status host_ok() { return ok(); }
+
+dg_status host_state(HostState* out) {
+  DeviceState* st = nullptr;
+  int dev = 0;
+  const dg_status s = device_state(&st, &dev);
+  if (s != DG_OK) return s;
+  out->device = dev;
+  out->sms = sms_in_use(*st);
+  out->status = st->status;
+  out->timeout_ns = g_timeout_ns.load();
+  out->debug_flags = g_skip_producer.load() ? DBG_SKIP_PRODUCER : 0u;
+  out->encode = g_encode;
+  return DG_OK;
+}
+
+}  // namespace dgk
+
 // ====================================================================== ABI ==
 extern "C" {
 
@@ -851,7 +882,9 @@ dg_status dg_get_device_status(void* stream) {
     case dgk::ST_EXPERT_RANGE:
       return fail(DG_ERR_EXPERT_RANGE, "m_indices out of range or a block mixes experts");
     case dgk::ST_KS_RANGE:
-      return fail(DG_ERR_KS_RANGE, "ks: a negative or partial K group, or past K_total");
+      return fail(DG_ERR_KS_RANGE,
+                  "ks: a negative or partial K group, or past K_total (ragged sizes: negative, or "
+                  "past the rows)");
     case dgk::ST_DEBUG_BOUNDS:
       return fail(DG_ERR_DEBUG_BOUNDS, "checked build: an access outside a tensor was skipped");
     case dgk::ST_DEBUG_PHASE:

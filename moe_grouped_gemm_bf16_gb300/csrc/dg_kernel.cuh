@@ -43,6 +43,7 @@
 #include <cstdint>
 
 #include "dg_params.h"
+#include "dg_wait.cuh"
 #include "ptx.cuh"
 
 namespace dgk {
@@ -123,18 +124,6 @@ __device__ __forceinline__ float ue8m0_to_float(uint32_t e) {
 // Byte g % 4 of a packed UE8M0 word, as a scale.
 __device__ __forceinline__ float ue8m0_scale(uint32_t word, int g) {
   return ue8m0_to_float((word >> (8 * (g & 3))) & 0xFFu);
-}
-
-__device__ __forceinline__ void raise_status(const Params& p, unsigned int code) {
-  atomicCAS(p.status, 0u, code);
-}
-
-// Checked build: record a failed check and abort the CTA (every later wait
-// returns at once and no further TMA or MMA is issued).
-__device__ __forceinline__ void dbg_fail(const Params& p, unsigned int code,
-                                         volatile uint32_t* abort_flag) {
-  raise_status(p, code);
-  *abort_flag = 1;
 }
 
 // Tile t of the persistent schedule.  Tiles are numbered in raster bands of
@@ -244,44 +233,6 @@ __device__ __forceinline__ bool dbg_tile_ok(const Params& p, const Tile& T, int 
 
 __device__ __forceinline__ int num_tiles_dense(const Params& p) {
   return p.num_m_blocks * p.num_n_blocks;
-}
-
-// Bounded mbarrier wait.  Returns false (without waiting) once the CTA has
-// aborted, or after `timeout_ns`, in which case it records the timeout and
-// aborts the CTA.
-template <bool ACQ_CLUSTER = false>
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                         const Params& p) {
-  auto try_once = [&]() {
-    return ACQ_CLUSTER ? mbar_try_wait_acq_cluster(bar, parity) : mbar_try_wait(bar, parity);
-  };
-  if (try_once()) return true;
-  if (*abort_flag) return false;
-  const uint64_t t0 = globaltimer_ns();
-  uint32_t it = 0;
-  while (!try_once()) {
-    if ((++it & 15u) == 0) {
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > p.timeout_ns) {
-        raise_status(p, ST_TIMEOUT);
-        *abort_flag = 1;
-        return false;
-      }
-    }
-  }
-  return true;
-}
-
-// Wait used while draining at the end: ignores the abort flag, gives up only
-// on the time limit.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const Params& p) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > p.timeout_ns) {
-      raise_status(p, ST_TIMEOUT);
-      return;
-    }
-  }
 }
 
 }  // namespace dgk

@@ -1,0 +1,25 @@
+// Launch helper of the one-dimensional and three-dimensional grids below.
+#pragma once
+#include <cuda_runtime.h>
+
+namespace dgk {
+
+// Launches with programmatic dependent launch: the blocks may be scheduled
+// while the previous kernel in the stream finishes (they wait for it with
+// griddepcontrol before they read anything).
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream,
+                             A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+}  // namespace dgk

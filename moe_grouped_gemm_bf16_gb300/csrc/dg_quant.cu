@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "dg_fp8.cuh"
 #include "dg_quant.h"
 
 namespace dgk {
@@ -31,25 +32,6 @@ namespace {
 
 constexpr int QT_THREADS = 256;  // 8 warps x 4 rows = 32 rows per pass
 constexpr int QT_ROWS = 2;       // passes (rows per thread)
-
-// two fp32 -> two e4m3 codes (round to nearest even, saturating to +-448),
-// `lo` in the low byte
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ uint4 ld_stream_v4(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 template <bool UE8M0>
 __global__ void __launch_bounds__(QT_THREADS)
@@ -81,12 +63,7 @@ quantize_1x128_kernel(const uint4* __restrict__ X, uint4* __restrict__ Q, float*
     const int m = row0 + j * 32;
     float x[16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      x[8 * h + 0] = bf16_lo(v[j][h].x); x[8 * h + 1] = bf16_hi(v[j][h].x);
-      x[8 * h + 2] = bf16_lo(v[j][h].y); x[8 * h + 3] = bf16_hi(v[j][h].y);
-      x[8 * h + 4] = bf16_lo(v[j][h].z); x[8 * h + 5] = bf16_hi(v[j][h].z);
-      x[8 * h + 6] = bf16_lo(v[j][h].w); x[8 * h + 7] = bf16_hi(v[j][h].w);
-    }
+    for (int h = 0; h < 2; ++h) bf16x8_to_float(v[j][h], x + 8 * h);
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
@@ -94,38 +71,18 @@ quantize_1x128_kernel(const uint4* __restrict__ X, uint4* __restrict__ Q, float*
     // within the unit's 8 lanes
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float a = fmaxf(amax, 1e-4f);
+    const float a = fmaxf(amax, kScaleFloor);
     float factor;
-    uint32_t e8 = 0;   // UE8M0: the scale's exponent code
-    if constexpr (UE8M0) {
-      // t = a / 448 is a normal fp32 number here (a >= 1e-4, a <= bf16's largest);
-      // its power-of-two ceiling is 2^(E - 127) when the mantissa is zero, else
-      // 2^(E - 126), E the biased exponent; the factor 1 / s is exact
-      const uint32_t tb = __float_as_uint(__fdiv_rn(a, 448.0f));
-      e8 = ((tb >> 23) & 0xFFu) + ((tb & 0x7FFFFFu) != 0u ? 1u : 0u);
-      factor = __uint_as_float((254u - e8) << 23);
-    } else {
-      factor = __fdiv_rn(448.0f, a);
-    }
+    uint32_t e8;
+    group_factor<UE8M0>(a, factor, e8);
     uint4 w;
-    w.x = cvt_e4m3x2(x[0] * factor, x[1] * factor) | (cvt_e4m3x2(x[2] * factor, x[3] * factor) << 16);
-    w.y = cvt_e4m3x2(x[4] * factor, x[5] * factor) | (cvt_e4m3x2(x[6] * factor, x[7] * factor) << 16);
-    w.z = cvt_e4m3x2(x[8] * factor, x[9] * factor) |
-          (cvt_e4m3x2(x[10] * factor, x[11] * factor) << 16);
-    w.w = cvt_e4m3x2(x[12] * factor, x[13] * factor) |
-          (cvt_e4m3x2(x[14] * factor, x[15] * factor) << 16);
+    w.x = cvt_e4m3x4(x[0] * factor, x[1] * factor, x[2] * factor, x[3] * factor);
+    w.y = cvt_e4m3x4(x[4] * factor, x[5] * factor, x[6] * factor, x[7] * factor);
+    w.z = cvt_e4m3x4(x[8] * factor, x[9] * factor, x[10] * factor, x[11] * factor);
+    w.w = cvt_e4m3x4(x[12] * factor, x[13] * factor, x[14] * factor, x[15] * factor);
     if (m < M) {
       Q[off[j]] = w;
-      if (sub == 0) {
-        if constexpr (UE8M0) {
-          // byte g % 4 of the packed word [z][g / 4][m] (little-endian)
-          const int kbp = (kb + 3) >> 2;
-          reinterpret_cast<uint8_t*>(sa)[((static_cast<size_t>(z) * kbp + (g >> 2)) * ld_sa + m) * 4 +
-                                         (g & 3)] = static_cast<uint8_t>(e8);
-        } else {
-          sa[(static_cast<size_t>(z) * kb + g) * ld_sa + m] = __fdiv_rn(a, 448.0f);
-        }
-      }
+      if (sub == 0) store_scale<UE8M0>(sa, z, kb, ld_sa, g, m, a, e8);
     }
   }
 }
