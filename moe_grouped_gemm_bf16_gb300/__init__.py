@@ -11,6 +11,7 @@ There is no fallback: if the library has not been built, `lib()` raises.
 """
 import ctypes
 import os
+import sys
 
 __all__ = [
     "DGError", "lib", "gemm_fp8_fp8_bf16_nt", "gemm_fp8_fp8_bf16_nt_add_c",
@@ -170,12 +171,10 @@ def _ptr(x):
 
 def _stream(s):
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available() and torch.cuda.is_initialized():
-                return int(torch.cuda.current_stream().cuda_stream)
-        except Exception:  # pragma: no cover
-            pass
+        torch = sys.modules.get("torch")   # (a process that never imported it has no torch stream)
+        if torch is not None and torch.cuda.is_initialized():
+            # the raw handle of torch's current stream (0.2 us; a Stream object costs 3 us)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return None
     if isinstance(s, int):
         return s

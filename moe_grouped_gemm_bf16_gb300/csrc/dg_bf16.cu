@@ -6,20 +6,28 @@
 //   nn  D[t][n]    = sum_k A[t][k] B[e][k][n]     gradient of the activations
 //   tn  D[e][m][n] = C[e][m][n] + sum_{t in e} A[t][m] B[t][n]   gradient of the weights
 //
-// Every form is one computation: a tile of D with BL = 128 consecutive columns
-// of a row of D on the tensor memory's lanes (B is the MMA's first operand)
-// and up to BC rows of D on its columns (A is the second operand).  The ragged
-// dimension of nt and nn is then the MMA's N, which the instruction takes in
-// steps of 16: a group of 20 rows costs 32 columns, not 128 lanes, and a
-// weight tile is always full.
+// Every form is one computation: a tile of D with `lanes` consecutive columns
+// of D on the tensor memory's lanes (B is the MMA's first operand) and up to
+// BC rows of D on its columns (A is the second operand).  The ragged dimension
+// of nt and nn is then the MMA's N, which the instruction takes in steps of
+// 16 or 32: a group of 20 rows costs 32 columns, not 128 lanes, and a weight
+// tile is always full.
 //
-// One persistent CTA per SM; warp 0 loads by TMA into a ring of STAGES slots
-// (64 deep in the reduction), warp 1 issues tcgen05.mma kind::f16 into one of
-// two fp32 accumulators in tensor memory, warps 4-7 round the other one to
-// bf16 and store it.  tn's reduction ends at a group's last row, which need
-// not end a 64-row slot: the rows behind it, up to the next multiple of the
-// MMA's 16, are zeroed in shared memory (in both operands: the next group's
-// rows may hold anything).
+// Two kernels:
+//  * PAIR: a persistent CTA pair per 256 x 256 tile (cta_group::2: each CTA
+//    holds 128 lanes of B and half of A's rows), for groups of many rows;
+//  * single: one persistent CTA per tile of up to 256 lanes x BC rows, for
+//    groups of few rows, where the time is that of reading the weights: the
+//    host picks the lanes so that the tiles fill the SMs once (all of them
+//    stream at HBM's rate and end together).
+//
+// Warps 0 and 2 load by TMA (B's tile and A's) into a ring of slots 64 deep in
+// the reduction, warp 1 (of the pair's leader) issues tcgen05.mma kind::f16
+// into one of two fp32 accumulators in tensor memory, warps 4-7 round the
+// other one to bf16 and store it.  tn's reduction ends at a group's last row,
+// which need not end a slot: warp 3 zeroes the rows behind it, up to the next
+// multiple of the MMA's 16, in both operands (the next group's rows may hold
+// anything).
 //
 // Every wait is bounded, as in the FP8 kernels.
 #include <algorithm>
@@ -32,20 +40,24 @@
 namespace dgk {
 namespace {
 
-constexpr int BL = 128;      // lanes: columns of D per tile
-constexpr int BK = 64;       // reduction depth per slot (128 bytes)
+constexpr int BK = 64;          // reduction depth per slot (128 bytes)
 constexpr int BF_THREADS = 256;
-constexpr int BF_BAND = 8;   // column blocks (rows of D) per raster band
+constexpr int BF_BAND = 8;      // column blocks (rows of D) per raster band
+constexpr int BF_MAX_STAGES = 12;
+constexpr int kBfMaxSmem = 232448;
 
 struct BfParams {
-  int form;
   int G;
   int rows;        // rows of A over all groups
   int M;           // tn: rows of each D[e]
   int N;           // columns of D
   int nk;          // nt, nn: 64-deep slots of the reduction
-  int nl;          // lane blocks: ceil(N / BL)
+  int lanes;       // columns of D per tile (pair: 256)
+  int nl;          // lane blocks: ceil(N / lanes)
   int nc;          // tn: column blocks of each group: ceil(M / BC)
+  int stages;
+  int p_bytes;     // bytes of a slot's lane operand (per CTA)
+  int q_bytes;     // bytes of a slot's column operand (per CTA)
   int p_split;     // lane operand loaded in 64-wide boxes (N not a multiple of 64)
   int q_split;     // column operand (tn) loaded in 64-wide boxes (M not a multiple of 64)
   const int32_t* sizes;
@@ -56,26 +68,20 @@ struct BfParams {
   unsigned int debug_flags;
 };
 
-template <int BC, int STAGES>
+// Shared memory behind the ring: barriers, TMEM base and abort flag, then the
+// groups' first rows and first column blocks.
 struct BfSmem {
-  static constexpr int P_BYTES = BL * BK * 2;
-  static constexpr int Q_BYTES = BC * BK * 2;
-  static constexpr int P_OFF = 0;
-  static constexpr int Q_OFF = STAGES * P_BYTES;
-  static constexpr int BAR_OFF = Q_OFF + STAGES * Q_BYTES;
-  static constexpr int FULL = 0, EMPTY = STAGES, T_FULL = 2 * STAGES, T_EMPTY = T_FULL + 2,
-                       MMA_DONE = T_EMPTY + 2, NUM_BARS = MMA_DONE + 1;
-  static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;   // TMEM base, abort flag
-  static constexpr int TAB_OFF = (MISC_OFF + 8 + 15) / 16 * 16;
-  // first row of each group, then first column block of each group
-  static constexpr int bytes(int G) { return 1024 + TAB_OFF + 2 * (G + 1) * 4; }
-  static constexpr int TMEM_COLS = 2 * BC < 32 ? 32 : 2 * BC;
+  static constexpr int FULL = 0, EMPTY = BF_MAX_STAGES, TAIL = 2 * BF_MAX_STAGES,
+                       T_FULL = 3 * BF_MAX_STAGES, T_EMPTY = T_FULL + 2, MMA_DONE = T_EMPTY + 2,
+                       NUM_BARS = MMA_DONE + 1;
+  static constexpr int MISC = NUM_BARS * 8;
+  static constexpr int TAB = (MISC + 8 + 15) / 16 * 16;
+  __host__ __device__ static constexpr int fixed(int G) { return 1024 + TAB + 2 * (G + 1) * 4; }
 };
 
 struct BfTile {
   int g;       // group
   int l0;      // first column of D
-  int c0;      // first row of D within the group (nt, nn: row of the group; tn: m)
   int cols;    // rows of D in this tile
   int q0;      // first row of the column operand (nt, nn: row of A; tn: m)
   int k0;      // tn: first row of the group
@@ -83,12 +89,12 @@ struct BfTile {
   int nk;      // slots
 };
 
-template <int BC>
+template <int BC, int FORM>
 __device__ __forceinline__ BfTile bf_tile(int t, const BfParams& p, const int* first,
                                           const int* blk) {
   BfTile T;
   int nc;
-  if (p.form == kBfTN) {
+  if (FORM == kBfTN) {
     const int per = p.nc * p.nl;
     T.g = t / per;
     t -= T.g * per;
@@ -110,18 +116,18 @@ __device__ __forceinline__ BfTile bf_tile(int t, const BfParams& p, const int* f
   const int band = t / (BF_BAND * p.nl);
   const int r = t - band * BF_BAND * p.nl;
   const int h = min(BF_BAND, nc - band * BF_BAND);
-  T.l0 = (r / h) * BL;
-  T.c0 = (band * BF_BAND + r % h) * BC;
+  T.l0 = (r / h) * p.lanes;
+  const int c0 = (band * BF_BAND + r % h) * BC;
   const int n = first[T.g + 1] - first[T.g];
-  if (p.form == kBfTN) {
-    T.cols = min(BC, p.M - T.c0);
-    T.q0 = T.c0;
+  if (FORM == kBfTN) {
+    T.cols = min(BC, p.M - c0);
+    T.q0 = c0;
     T.k0 = first[T.g];
     T.kn = n;
     T.nk = (n + BK - 1) / BK;
   } else {
-    T.cols = min(BC, n - T.c0);
-    T.q0 = first[T.g] + T.c0;
+    T.cols = min(BC, n - c0);
+    T.q0 = first[T.g] + c0;
     T.k0 = 0;
     T.kn = p.nk * BK;
     T.nk = p.nk;
@@ -129,29 +135,39 @@ __device__ __forceinline__ BfTile bf_tile(int t, const BfParams& p, const int* f
   return T;
 }
 
-template <int BC, int STAGES>
+template <bool PAIR, int BC, int FORM>
 __global__ void __launch_bounds__(BF_THREADS, 1)
 bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                     const BfParams p) {
-  using L = BfSmem<BC, STAGES>;
+  using L = BfSmem;
+  // columns of one accumulator: two M = 128 halves side by side, or the pair's
+  constexpr int ACC = PAIR ? BC : 2 * BC;
+  static_assert(2 * ACC <= 512, "two accumulators");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
+  const uint32_t q_off = p.stages * p.p_bytes;
+  const int ring = p.stages * (p.p_bytes + p.q_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto bar = [&](int i) -> uint32_t { return sbase + L::BAR_OFF + 8 * i; };
-  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
+  auto bar = [&](int i) -> uint32_t { return sbase + ring + 8 * i; };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + ring + L::MISC);
   volatile uint32_t* abort_flag = misc + 1;
-  int* first = reinterpret_cast<int*>(smem + L::TAB_OFF);
+  int* first = reinterpret_cast<int*>(smem + ring + L::TAB);
   int* blk = first + p.G + 1;
+  const uint32_t crank = PAIR ? cluster_ctarank() : 0;
+  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
+  constexpr bool TN = FORM == kBfTN, P_MN = FORM != kBfNT;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(bar(L::FULL + s), 1);
+    for (int s = 0; s < p.stages; ++s) {
+      // the two producers (pair: the leader's, for both CTAs' bytes)
+      mbar_init(bar(L::FULL + s), 2);
       mbar_init(bar(L::EMPTY + s), 1);
+      mbar_init(bar(L::TAIL + s), 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(L::T_FULL + b), 1);
-      mbar_init(bar(L::T_EMPTY + b), 4);
+      mbar_init(bar(L::T_EMPTY + b), PAIR ? 8 : 4);
     }
     mbar_init(bar(L::MMA_DONE), 1);
     misc[1] = 0;
@@ -160,8 +176,13 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     prefetch_tmap(&tmQ);
   }
   if (warp == 1) {
-    tmem_alloc(sbase + L::MISC_OFF, L::TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(sbase + ring + L::MISC, 2 * ACC);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(sbase + ring + L::MISC, 2 * ACC);
+      tmem_relinquish();
+    }
   }
   grid_dep_wait();
   grid_dep_launch_dependents();
@@ -205,169 +226,259 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // the peer signals this CTA's barriers from here on (their initialisation was
+  // made visible to the cluster by thread 0's fence)
+  if constexpr (PAIR) {
+    cluster_arrive_relaxed();
+    cluster_wait();
+  }
   const uint32_t tmem = misc[0];
-  const bool tn = p.form == kBfTN;
-  const int tiles = tn ? p.G * p.nc * p.nl : blk[p.G] * p.nl;
+  const int tiles = TN ? p.G * p.nc * p.nl : blk[p.G] * p.nl;
+  // the MMA's N: whole instruction steps; a pair's CTA holds half of the
+  // columns each (tn: in whole 64-wide boxes)
+  auto mma_n = [&](int cols) {
+    return PAIR ? (TN ? (cols + 127) & ~127 : (cols + 31) & ~31) : (cols + 15) & ~15;
+  };
+  // a tile's last slot needs zeroed rows (tn)
+  auto ragged = [&](const BfTile& T) { return TN && (T.kn & 15) != 0; };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------- TMA producers --
+    // warp 0: the lane operand (B), warp 2: the column operand (A); one load
+    // each per slot (a thread that issues one stalls for ~250 cycles)
     if (lane == 0 && !(p.debug_flags & DBG_SKIP_PRODUCER)) {
+      const bool lanes_op = warp == 0;
+      const CUtensorMap* tm = lanes_op ? &tmP : &tmQ;
+      const bool mn = lanes_op ? P_MN : TN;
+      const bool split = lanes_op ? p.p_split : p.q_split;
+      const uint32_t bytes = lanes_op ? p.p_bytes : p.q_bytes;
+      const uint32_t base = sbase + (lanes_op ? 0 : q_off);
       int s = 0;
-      uint32_t ph = 0, issued = 0, issued_par = 0;
-      for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const BfTile T = bf_tile<BC>(t, p, first, blk);
+      uint32_t ph = 0, issued = 0, issued_par = 0, tails = 0, tail_par = 0;
+      for (int t = unit; t < tiles; t += units) {
+        const BfTile T = bf_tile<BC, FORM>(t, p, first, blk);
+        const int at = lanes_op ? T.l0 + static_cast<int>(crank) * 128
+                                : T.q0 + static_cast<int>(crank) * (mma_n(T.cols) / 2);
+        const int g = (lanes_op && !TN) ? T.g : 0;
+        const bool rag = ragged(T);
         for (int i = 0; i < T.nk; ++i) {
           bool go = wait_bar(bar(L::EMPTY + s), ph ^ 1, abort_flag, p);
+          const int k = T.k0 + i * BK;
           if constexpr (kDebug) {
-            const int qmax = tn ? p.M : p.rows;
-            if (go && (T.l0 >= p.N || T.g >= p.G || T.q0 < 0 || T.q0 >= qmax || T.k0 < 0 ||
-                       (tn && T.k0 + i * BK >= p.rows))) {
+            const int rows = lanes_op ? p.N : (TN ? p.M : p.rows);
+            // (a pair's second CTA may start past the tensor: zero-filled)
+            if (go && (T.g >= p.G || at < 0 || at >= rows + (PAIR ? 128 : 0) || k < 0 ||
+                       (TN && k >= p.rows))) {
               dbg_fail(p, ST_DEBUG_BOUNDS, abort_flag);
               go = false;
             }
           }
           if (go) {
-            const uint32_t full = bar(L::FULL + s);
-            const uint32_t pd = sbase + L::P_OFF + s * L::P_BYTES;
-            const uint32_t qd = sbase + L::Q_OFF + s * L::Q_BYTES;
-            mbar_arrive_expect_tx(full, L::P_BYTES + L::Q_BYTES);
-            if (p.form == kBfNT) {
-              tma_load_4d(pd, &tmP, full, i * BK, T.l0, 0, T.g);
+            const uint32_t dst = base + s * bytes;
+            // a slot whose rows warp 3 completes arrives on its own CTA's TAIL
+            const bool to_tail = rag && i == T.nk - 1;
+            const uint32_t b = to_tail ? bar(L::TAIL + s)
+                               : PAIR  ? map_cluster(bar(L::FULL + s), 0)
+                                       : bar(L::FULL + s);
+            // the leader expects both CTAs' bytes (a remote arrival of the peer
+            // at cluster scope would cost it a microsecond per slot)
+            if (to_tail || crank == 0)
+              mbar_arrive_expect_tx(to_tail ? b : bar(L::FULL + s), PAIR && !to_tail ? 2 * bytes : bytes);
+            auto load = [&](uint32_t d, int x, int y, int z) {
+              if (PAIR && !to_tail) tma_load_4d_pair(map_cluster(d, crank), tm, b, x, y, z, g);
+              else tma_load_4d(d, tm, b, x, y, z, g);
+            };
+            if (!mn) {
+              load(dst, k, at, 0);
+            } else if (!split) {
+              load(dst, 0, k, at >> 6);
             } else {
-              const int k = T.k0 + i * BK, g = tn ? 0 : T.g;
-              if (p.p_split) {
-                for (int j = 0; j < BL / 64; ++j)
-                  tma_load_4d(pd + j * 64 * 128, &tmP, full, T.l0 + 64 * j, k, 0, g);
-              } else {
-                tma_load_4d(pd, &tmP, full, 0, k, T.l0 / 64, g);
-              }
+              for (uint32_t j = 0; j < bytes / 8192; ++j) load(dst + j * 8192, at + 64 * j, k, 0);
             }
-            if (!tn) {
-              tma_load_4d(qd, &tmQ, full, i * BK, T.q0, 0, 0);
+            // (the slot's latest load, for the drain below: on one barrier or
+            // the other)
+            if (to_tail) {
+              tails |= 1u << s;
+              tail_par ^= 1u << s;
+              issued &= ~(1u << s);
             } else {
-              const int k = T.k0 + i * BK;
-              if (p.q_split) {
-                for (int j = 0; j < BC / 64; ++j)
-                  tma_load_4d(qd + j * 64 * 128, &tmQ, full, T.q0 + 64 * j, k, 0, 0);
-              } else {
-                tma_load_4d(qd, &tmQ, full, 0, k, T.q0 / 64, 0);
-              }
+              issued |= 1u << s;
+              issued_par = (issued_par & ~(1u << s)) | (ph << s);
             }
-            issued |= 1u << s;
-            issued_par = (issued_par & ~(1u << s)) | (ph << s);
           }
-          if (++s == STAGES) { s = 0; ph ^= 1; }
+          if (++s == p.stages) { s = 0; ph ^= 1; }
         }
       }
       // after an abort the latest load into a slot may still be in flight
-      for (int q = 0; q < STAGES; ++q)
-        if ((issued >> q) & 1u) drain_wait(bar(L::FULL + q), (issued_par >> q) & 1u, p);
+      // (pair: both CTAs' loads count on the leader's barriers; the CTAs leave
+      // together)
+      for (int q = 0; q < p.stages; ++q) {
+        if (((issued >> q) & 1u) && (!PAIR || crank == 0))
+          drain_wait(bar(L::FULL + q), (issued_par >> q) & 1u, p);
+        if ((tails >> q) & 1u) drain_wait(bar(L::TAIL + q), ((tail_par >> q) & 1u) ^ 1u, p);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
-    const bool p_mn = p.form != kBfNT, q_mn = tn;
-    // a K step of 16: 32 bytes inside a K-major row, two 8-row atoms (2 KB) of
-    // an MN-major slot, whose 64-wide atoms lie 64 rows x 128 bytes apart
-    const uint64_t p_step = (p_mn ? 2048 : 32) >> 4, q_step = (q_mn ? 2048 : 32) >> 4;
-    int s = 0, b = 0;
-    uint32_t ph = 0, bph = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const BfTile T = bf_tile<BC>(t, p, first, blk);
-      if (T.nk == 0) continue;
-      const uint32_t idesc = idesc_bf16_f32(BL, (T.cols + 15) & ~15, p_mn, q_mn);
-      const uint32_t d = tmem + static_cast<uint32_t>(b * BC);
-      bool ok = wait_bar(bar(L::T_EMPTY + b), bph ^ 1, abort_flag, p);
-      tc_fence_after();
-      for (int i = 0; i < T.nk; ++i) {
-        ok = wait_bar(bar(L::FULL + s), ph, abort_flag, p) && ok;
+    // ---------------------------------------------------------- MMA issuer --
+    if (lane == 0 && crank == 0) {
+      // a K step of 16: 32 bytes inside a K-major row, two 8-row atoms (2 KB) of
+      // an MN-major slot, whose 64-wide atoms lie 64 rows x 128 bytes apart
+      constexpr uint64_t P_STEP = (P_MN ? 2048 : 32) >> 4, Q_STEP = (TN ? 2048 : 32) >> 4;
+      const bool two = !PAIR && p.lanes > 128;
+      int s = 0, b = 0;
+      uint32_t ph = 0, bph = 0;
+      for (int t = unit; t < tiles; t += units) {
+        const BfTile T = bf_tile<BC, FORM>(t, p, first, blk);
+        if (T.nk == 0) continue;
+        const uint32_t idesc = idesc_bf16_f32(PAIR ? 256 : 128, mma_n(T.cols), P_MN, TN);
+        const uint32_t d = tmem + static_cast<uint32_t>(b * ACC);
+        bool ok = wait_bar(bar(L::T_EMPTY + b), bph ^ 1, abort_flag, p);
         tc_fence_after();
-        const uint32_t ps = sbase + L::P_OFF + s * L::P_BYTES;
-        const uint32_t qs = sbase + L::Q_OFF + s * L::Q_BYTES;
-        const int left = min(BK, T.kn - i * BK), steps = (left + 15) >> 4;
-        if (tn && (left & 15)) {
-          // zero rows left .. 16 steps - 1 of both operands (a row is one
-          // 128-byte line of each 64-wide atom)
-          const int r = 16 * steps - left;
-          for (int u = lane; u < r * 8 * (BL + BC) / 64; u += 32) {
-            const int atom = u / (r * 8), w = u - atom * (r * 8);
-            const uint32_t base = atom < BL / 64 ? ps + atom * 8192 : qs + (atom - BL / 64) * 8192;
-            st_shared_v4(base + (left + (w >> 3)) * 128 + (w & 7) * 16, 0, 0, 0, 0);
+        for (int i = 0; i < T.nk; ++i) {
+          // (the peer's warp 3 wrote a ragged slot's zeros itself)
+          const bool zeroed = PAIR && i == T.nk - 1 && ragged(T);
+          ok = (zeroed ? wait_bar<true>(bar(L::FULL + s), ph, abort_flag, p)
+                       : wait_bar(bar(L::FULL + s), ph, abort_flag, p)) && ok;
+          tc_fence_after();
+          if (ok) {
+            const uint32_t ps = sbase + s * p.p_bytes, qs = sbase + q_off + s * p.q_bytes;
+            const uint64_t pd = P_MN ? smem_desc_sw128_mnmajor(ps, 8192) : smem_desc_sw128_kmajor(ps);
+            const uint64_t qd = TN ? smem_desc_sw128_mnmajor(qs, 8192) : smem_desc_sw128_kmajor(qs);
+            auto step = [&](int kk, uint32_t acc) {
+              if constexpr (PAIR) {
+                mma_bf16_pair(d, pd + P_STEP * kk, qd + Q_STEP * kk, idesc, acc);
+              } else {
+                mma_bf16(d, pd + P_STEP * kk, qd + Q_STEP * kk, idesc, acc);
+                // the second 128 lanes (the rows past `lanes` are not stored)
+                if (two) mma_bf16(d + BC, pd + (16384 >> 4) + P_STEP * kk, qd + Q_STEP * kk, idesc, acc);
+              }
+            };
+            const int left = T.kn - i * BK;
+            if (!TN || left >= BK) {
+              step(0, i > 0);
+#pragma unroll
+              for (int kk = 1; kk < BK / 16; ++kk) step(kk, 1);
+            } else {
+              for (int kk = 0; 16 * kk < left; ++kk) step(kk, i > 0 || kk > 0);
+            }
+            if constexpr (PAIR) mma_commit_pair_multicast(bar(L::EMPTY + s), 0x3);
+            else mma_commit(bar(L::EMPTY + s));
+            if (i == T.nk - 1) {
+              if constexpr (PAIR) mma_commit_pair_multicast(bar(L::T_FULL + b), 0x3);
+              else mma_commit(bar(L::T_FULL + b));
+            }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
+          if (++s == p.stages) { s = 0; ph ^= 1; }
         }
-        if (lane == 0 && ok) {
-          const uint64_t pd = p_mn ? smem_desc_sw128_mnmajor(ps, 8192) : smem_desc_sw128_kmajor(ps);
-          const uint64_t qd = q_mn ? smem_desc_sw128_mnmajor(qs, 8192) : smem_desc_sw128_kmajor(qs);
-          for (int kk = 0; kk < steps; ++kk)
-            mma_bf16(d, pd + p_step * kk, qd + q_step * kk, idesc, (i | kk) ? 1u : 0u);
-          mma_commit(bar(L::EMPTY + s));
-          if (i == T.nk - 1) mma_commit(bar(L::T_FULL + b));
-        }
-        __syncwarp();
-        if (++s == STAGES) { s = 0; ph ^= 1; }
+        b ^= 1;
+        if (b == 0) bph ^= 1;
       }
-      b ^= 1;
-      if (b == 0) bph ^= 1;
-    }
-    if (lane == 0) {
-      mma_commit(bar(L::MMA_DONE));
+      if constexpr (PAIR) mma_commit_pair_multicast(bar(L::MMA_DONE), 0x1);
+      else mma_commit(bar(L::MMA_DONE));
       drain_wait(bar(L::MMA_DONE), 0, p);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    // ------------------------------------------------------ tn's last rows --
+    if (TN) {
+      int s = 0;
+      uint32_t par = 0;
+      for (int t = unit; t < tiles; t += units) {
+        const BfTile T = bf_tile<BC, FORM>(t, p, first, blk);
+        if (T.nk == 0) continue;
+        s = (s + T.nk - 1) % p.stages;
+        if (ragged(T)) {
+          // all 32 lanes: wait for this CTA's two loads, then zero the rows
+          // behind the group's last one, up to the next multiple of 16 (a row
+          // is one 128-byte line of each 64-wide atom)
+          const bool ok = wait_bar(bar(L::TAIL + s), (par >> s) & 1u, abort_flag, p);
+          par ^= 1u << s;
+          if (ok) {
+            const int left = T.kn - (T.nk - 1) * BK, r = ((left + 15) & ~15) - left;
+            const int pa = p.p_bytes / 8192, n = r * 8 * (pa + p.q_bytes / 8192);
+            const uint32_t ps = sbase + s * p.p_bytes, qs = sbase + q_off + s * p.q_bytes;
+            for (int u = lane; u < n; u += 32) {
+              const int atom = u / (r * 8), w = u - atom * (r * 8);
+              const uint32_t base = atom < pa ? ps + atom * 8192 : qs + (atom - pa) * 8192;
+              st_shared_v4(base + (left + (w >> 3)) * 128 + (w & 7) * 16, 0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          // in place of the two producers' arrivals: one per CTA of a pair, or two
+          if constexpr (PAIR) {
+            if (lane == 0) mbar_arrive_remote_release(bar(L::FULL + s), 0);
+          } else {
+            if (lane < 2) mbar_arrive(bar(L::FULL + s));
+          }
+        }
+        s = (s + 1) % p.stages;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue --
     const int q = warp & 3;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const int halves = PAIR ? 1 : (p.lanes + 127) / 128;
     int b = 0;
     uint32_t bph = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const BfTile T = bf_tile<BC>(t, p, first, blk);
+    for (int t = unit; t < tiles; t += units) {
+      const BfTile T = bf_tile<BC, FORM>(t, p, first, blk);
       const bool have = T.nk > 0;
       const bool ok = !have || wait_bar(bar(L::T_FULL + b), bph, abort_flag, p);
       tc_fence_after();
-      // this thread's pair of columns of D (lanes l and l ^ 1 share them)
-      const int l = T.l0 + q * 32 + (lane & ~1);
-      const size_t row0 = tn ? static_cast<size_t>(T.g) * p.M + T.c0 : static_cast<size_t>(T.q0);
-      for (int c = 0; c < T.cols; c += 32) {
-        uint32_t v[32];
-        if (have) {
-          tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * BC + c), v);
-          tmem_wait_ld(v);
-        } else {
+      const size_t row0 = TN ? static_cast<size_t>(T.g) * p.M + T.q0 : static_cast<size_t>(T.q0);
+      const int l_end = min(p.N, T.l0 + p.lanes);
+      for (int a = 0; a < halves; ++a) {
+        // this thread's pair of columns of D (lanes l and l ^ 1 share them)
+        const int l = T.l0 + (PAIR ? static_cast<int>(crank) : a) * 128 + q * 32 + (lane & ~1);
+        for (int c = 0; c < T.cols; c += 32) {
+          uint32_t v[32];
+          if (have) {
+            tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
+            tmem_wait_ld(v);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0u;
-        }
-        // a lane holds 32 rows of one column of D: exchange with the
-        // neighbouring lane, so that the even lane stores two columns of row j
-        // and the odd one those of row j + 1
+            for (int j = 0; j < 32; ++j) v[j] = 0u;
+          }
+          // a lane holds 32 rows of one column of D: exchange with the
+          // neighbouring lane, so that the even lane stores two columns of row
+          // j and the odd one those of row j + 1
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const uint32_t give = (lane & 1) ? v[j] : v[j + 1];
-          const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
-          float lo = __uint_as_float((lane & 1) ? got : v[j]);
-          float hi = __uint_as_float((lane & 1) ? v[j + 1] : got);
-          const int r = c + j + (lane & 1);
-          if (ok && r < T.cols && l < p.N) {
-            const size_t at = (row0 + r) * p.N + l;
-            if constexpr (kDebug) {
-              if (row0 + r >= static_cast<size_t>(tn ? p.G * static_cast<long long>(p.M) : p.rows)) {
-                raise_status(p, ST_DEBUG_BOUNDS);
-                continue;
+          for (int j = 0; j < 32; j += 2) {
+            const uint32_t give = (lane & 1) ? v[j] : v[j + 1];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+            float lo = __uint_as_float((lane & 1) ? got : v[j]);
+            float hi = __uint_as_float((lane & 1) ? v[j + 1] : got);
+            const int r = c + j + (lane & 1);
+            if (ok && r < T.cols && l < l_end) {
+              const size_t at = (row0 + r) * p.N + l;
+              if constexpr (kDebug) {
+                if (row0 + r >= static_cast<size_t>(TN ? p.G * static_cast<long long>(p.M) : p.rows)) {
+                  raise_status(p, ST_DEBUG_BOUNDS);
+                  continue;
+                }
               }
+              if (p.C) {
+                // the addend in fp32, then one rounding
+                const uint32_t cw = *reinterpret_cast<const uint32_t*>(p.C + at);
+                lo += __uint_as_float(cw << 16);
+                hi += __uint_as_float(cw & 0xFFFF0000u);
+              }
+              *reinterpret_cast<uint32_t*>(p.D + at) = pack_bf16x2(lo, hi);
             }
-            if (p.C) {
-              // the addend in fp32, then one rounding
-              const uint32_t cw = *reinterpret_cast<const uint32_t*>(p.C + at);
-              lo += __uint_as_float(cw << 16);
-              hi += __uint_as_float(cw & 0xFFFF0000u);
-            }
-            *reinterpret_cast<uint32_t*>(p.D + at) = pack_bf16x2(lo, hi);
           }
         }
       }
       if (have) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::T_EMPTY + b));
+        if (lane == 0) {
+          if (PAIR && crank != 0) mbar_arrive_remote_relaxed(bar(L::T_EMPTY + b), 0);
+          else mbar_arrive(bar(L::T_EMPTY + b));
+        }
         b ^= 1;
         if (b == 0) bph ^= 1;
       }
@@ -378,27 +489,30 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, L::TMEM_COLS);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, 2 * ACC);
+    else tmem_dealloc(tmem, 2 * ACC);
   }
+  // no CTA leaves while its peer may still signal it or read its operands
+  if constexpr (PAIR) cluster_sync_relaxed();
 }
 
-constexpr int STAGES_WIDE = 4, STAGES_NARROW = 8;
-constexpr int BC_WIDE = 256, BC_NARROW = 64;
-constexpr int kBfMaxSmem = 232448;
-
-template <int BC, int STAGES>
-cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode, int num_sms, cudaStream_t stream) {
-  using L = BfSmem<BC, STAGES>;
-  const bool tn = c.form == kBfTN;
+template <bool PAIR, int BC, int FORM>
+cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode, int lanes,
+                         int num_sms, cudaStream_t stream) {
+  constexpr bool tn = FORM == kBfTN;
   BfParams p{};
-  p.form = c.form;
   p.G = c.G;
   p.rows = c.rows;
   p.M = c.M;
   p.N = c.N;
   p.nk = tn ? 0 : (c.K + BK - 1) / BK;
-  p.nl = (c.N + BL - 1) / BL;
+  p.lanes = lanes;
+  p.nl = (c.N + lanes - 1) / lanes;
   p.nc = tn ? (c.M + BC - 1) / BC : 0;
+  const int p_rows = PAIR ? 128 : lanes, q_rows = PAIR ? BC / 2 : BC;
+  p.p_bytes = (p_rows * 128 + 1023) / 1024 * 1024;
+  p.q_bytes = q_rows * 128;
+  p.stages = std::min(BF_MAX_STAGES, (kBfMaxSmem - BfSmem::fixed(c.G)) / (p.p_bytes + p.q_bytes));
   p.p_split = c.N % 64 != 0;
   p.q_split = c.M % 64 != 0;
   p.sizes = c.sizes;
@@ -434,45 +548,86 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
   // (a reduction without rows loads nothing; its maps still need an extent)
   const uint64_t G = c.G, N = c.N, K = c.K, R = std::max(c.rows, 1);
   const bool good =
-      (c.form == kBfNT   ? k_major(&mp, c.B, G, N, K, BL)
-       : c.form == kBfNN ? mn_major(&mp, c.B, G, K, N, BL)
-                         : mn_major(&mp, c.B, 1, R, N, BL)) &&
-      (tn ? mn_major(&mq, c.A, 1, R, c.M, BC) : k_major(&mq, c.A, 1, R, K, BC));
+      (FORM == kBfNT   ? k_major(&mp, c.B, G, N, K, p_rows)
+       : FORM == kBfNN ? mn_major(&mp, c.B, G, K, N, p_rows)
+                         : mn_major(&mp, c.B, 1, R, N, p_rows)) &&
+      (tn ? mn_major(&mq, c.A, 1, R, c.M, q_rows) : k_major(&mq, c.A, 1, R, K, q_rows));
   if (!good) return cudaErrorInvalidValue;
 
-  // as many CTAs as there can be tiles, at most one per SM
+  // as many CTAs (pairs) as there can be tiles, at most one per SM
   const long long most = tn ? static_cast<long long>(c.G) * p.nc * p.nl
                             : (std::min<long long>(c.G, c.rows) + c.rows / BC) * p.nl;
+  const long long fit = PAIR ? num_sms / 2 : num_sms;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, std::min<long long>(most, num_sms))), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, std::min(most, fit)) * (PAIR ? 2 : 1)), 1, 1);
   cfg.blockDim = dim3(BF_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = L::bytes(c.G);
+  cfg.dynamicSmemBytes = p.stages * (p.p_bytes + p.q_bytes) + BfSmem::fixed(c.G);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, bf16_grouped_kernel<BC, STAGES>, mp, mq, p);
+  if (PAIR) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  cfg.attrs = attr;
+  return cudaLaunchKernelEx(&cfg, bf16_grouped_kernel<PAIR, BC, FORM>, mp, mq, p);
+}
+
+template <int FORM>
+cudaError_t set_up_form() {
+  const void* kernels[] = {reinterpret_cast<const void*>(bf16_grouped_kernel<true, 256, FORM>),
+                           reinterpret_cast<const void*>(bf16_grouped_kernel<false, 128, FORM>),
+                           reinterpret_cast<const void*>(bf16_grouped_kernel<false, 64, FORM>)};
+  for (const void* k : kernels) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBfMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <int FORM>
+cudaError_t launch_form(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode, int num_sms,
+                        cudaStream_t stream) {
+  constexpr bool tn = FORM == kBfTN;
+  // rows of D that a group has: the average (nt, nn), M (tn)
+  const long long per = tn ? c.M : (c.rows + c.G - 1) / c.G;
+  const long long groups = tn ? c.G : std::min(c.G, c.rows);
+  // (a limit on the SMs may leave a single one: no pair fits)
+  if (per > 128 && num_sms >= 2)
+    return launch_tiles<true, 256, FORM>(c, encode, 256, num_sms, stream);
+  // lanes such that the tiles fill the SMs once, in whole MMA boxes: 64 where
+  // the lane operand is MN-major, else 16
+  const int bc = per > 64 ? 128 : 64, step = FORM == kBfNT ? 16 : 64;
+  const long long cols = groups * ((per + bc - 1) / bc);
+  const long long blocks = std::max(1ll, num_sms / cols);   // lane blocks per column block
+  const long long want = ((c.N + blocks - 1) / blocks + step - 1) / step * step;
+  const int lanes = static_cast<int>(std::min(256ll, std::max(64ll, want)));
+  return bc == 128 ? launch_tiles<false, 128, FORM>(c, encode, lanes, num_sms, stream)
+                   : launch_tiles<false, 64, FORM>(c, encode, lanes, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t bf16_set_up() {
-  static_assert(BfSmem<BC_WIDE, STAGES_WIDE>::bytes(kBfMaxGroups) <= kBfMaxSmem, "shared memory");
-  static_assert(BfSmem<BC_NARROW, STAGES_NARROW>::bytes(kBfMaxGroups) <= kBfMaxSmem, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(bf16_grouped_kernel<BC_WIDE, STAGES_WIDE>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kBfMaxSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(bf16_grouped_kernel<BC_NARROW, STAGES_NARROW>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, kBfMaxSmem);
+  cudaError_t e = set_up_form<kBfNT>();
+  if (e == cudaSuccess) e = set_up_form<kBfNN>();
+  if (e == cudaSuccess) e = set_up_form<kBfTN>();
+  return e;
 }
 
-cudaError_t launch_bf16_grouped(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode, int num_sms, cudaStream_t stream) {
-  // rows of D that a tile holds: the average group's (nt, nn), M (tn)
-  const long long per = c.form == kBfTN ? c.M : (c.rows + c.G - 1) / c.G;
-  return per <= BC_NARROW ? launch_tiles<BC_NARROW, STAGES_NARROW>(c, encode, num_sms, stream)
-                          : launch_tiles<BC_WIDE, STAGES_WIDE>(c, encode, num_sms, stream);
+cudaError_t launch_bf16_grouped(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode,
+                                int num_sms, cudaStream_t stream) {
+  switch (c.form) {
+    case kBfNT: return launch_form<kBfNT>(c, encode, num_sms, stream);
+    case kBfNN: return launch_form<kBfNN>(c, encode, num_sms, stream);
+    default: return launch_form<kBfTN>(c, encode, num_sms, stream);
+  }
 }
 
 }  // namespace dgk
