@@ -321,7 +321,13 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer --
-    if (lane == 0 && crank == 0) {
+    // The whole warp walks the loop, converged, and one elected thread issues:
+    // with a single thread in the loop the descriptors of every instruction
+    // cost the issue more than the instruction takes to run (nt, 32647 rows, N =
+    // 4096, K = 7168, the loads switched off: 1092 us; so 830 us, the tensor
+    // cores' rate).
+    if (crank == 0) {
+      const bool issuer = elect_one();
       // a K step of 16: 32 bytes inside a K-major row, two 8-row atoms (2 KB) of
       // an MN-major slot, whose 64-wide atoms lie 64 rows x 128 bytes apart
       constexpr uint64_t P_STEP = (P_MN ? 2048 : 32) >> 4, Q_STEP = (TN ? 2048 : 32) >> 4;
@@ -341,7 +347,7 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
           ok = (zeroed ? wait_bar<true>(bar(L::FULL + s), ph, abort_flag, p)
                        : wait_bar(bar(L::FULL + s), ph, abort_flag, p)) && ok;
           tc_fence_after();
-          if (ok) {
+          if (issuer && ok) {
             const uint32_t ps = sbase + s * p.p_bytes, qs = sbase + q_off + s * p.q_bytes;
             const uint64_t pd = P_MN ? smem_desc_sw128_mnmajor(ps, 8192) : smem_desc_sw128_kmajor(ps);
             const uint64_t qd = TN ? smem_desc_sw128_mnmajor(qs, 8192) : smem_desc_sw128_kmajor(qs);
@@ -369,14 +375,17 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
               else mma_commit(bar(L::T_FULL + b));
             }
           }
+          __syncwarp();
           if (++s == p.stages) { s = 0; ph ^= 1; }
         }
         b ^= 1;
         if (b == 0) bph ^= 1;
       }
-      if constexpr (PAIR) mma_commit_pair_multicast(bar(L::MMA_DONE), 0x1);
-      else mma_commit(bar(L::MMA_DONE));
-      drain_wait(bar(L::MMA_DONE), 0, p);
+      if (issuer) {
+        if constexpr (PAIR) mma_commit_pair_multicast(bar(L::MMA_DONE), 0x1);
+        else mma_commit(bar(L::MMA_DONE));
+        drain_wait(bar(L::MMA_DONE), 0, p);
+      }
     }
     __syncwarp();
   } else if (warp == 3) {
