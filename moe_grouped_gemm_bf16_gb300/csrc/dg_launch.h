@@ -1,4 +1,4 @@
-// Launch helper of the one-dimensional and three-dimensional grids below.
+// Launch helper of the kernels that need no cluster.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -9,10 +9,11 @@ namespace dgk {
 // griddepcontrol before they read anything).
 template <class... P, class... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream,
-                             A... args) {
+                             int smem, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

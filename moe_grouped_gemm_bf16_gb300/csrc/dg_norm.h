@@ -5,7 +5,7 @@
 namespace dgk {
 
 constexpr int kNormMaxK = 16384;      // longest row the norm kernels hold in registers
-constexpr int kNormBwdBlocks = 304;   // most rows of partial weight gradients
+constexpr int kNormBwdBlocks = 608;   // most rows of partial weight gradients
 
 // Device pointers of one call; the optional ones may be null.
 struct NormFwd {
@@ -19,6 +19,8 @@ struct NormFwd {
   float* rstd;       // fp32 [M] or null
   int M, K, ld_sa;
   float eps;
+  unsigned int* status;           // device status word and the waits' limit
+  unsigned long long timeout_ns;
 };
 
 struct NormBwd {
@@ -31,10 +33,13 @@ struct NormBwd {
   float* dW;         // fp32 [K]
   float* part;       // fp32 [blocks][K], blocks <= min(M, kNormBwdBlocks)
   int M, K;
+  unsigned int* status;
+  unsigned long long timeout_ns;
 };
 
 // The caller has validated the arguments (K % 128 == 0, K <= kNormMaxK,
 // 16-byte aligned tensors).
+cudaError_t norm_set_up();  // opts the kernels into their shared memory (once per device)
 cudaError_t launch_rms_norm(const NormFwd& a, bool ue8m0, int num_sms, cudaStream_t stream);
 cudaError_t launch_rms_norm_backward(const NormBwd& a, int num_sms, cudaStream_t stream);
 

@@ -26,7 +26,19 @@ dg_status cuda_fail(cudaError_t e, const char* what) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-dg_status rms_norm(const dgk::NormFwd& a, void* stream, bool ue8m0) {
+// Opts an operator's kernels into their shared memory, once per device.
+template <cudaError_t (*SET_UP)()>
+dg_status set_up_once(int device) {
+  static std::atomic<bool> done[dgk::kHostMaxDevices];
+  if (done[device].load(std::memory_order_acquire)) return DG_OK;
+  const cudaError_t e = SET_UP();
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
+  done[device].store(true, std::memory_order_release);
+  return DG_OK;
+}
+
+dg_status rms_norm(const dgk::NormFwd& a0, void* stream, bool ue8m0) {
+  dgk::NormFwd a = a0;
   const char* name = "dg_rms_norm_quantize_fp8_1x128";
   if (!a.X || !a.W || (!a.Y && !a.Q) || (a.Q && !a.sa))
     return host_fail(DG_ERR_INVALID_ARG, "%s: null pointer (X, W, one of Y and Q, sa with Q)", name);
@@ -43,8 +55,11 @@ dg_status rms_norm(const dgk::NormFwd& a, void* stream, bool ue8m0) {
                 "%s: ld_sa a multiple of 4; rstd 4-byte, the other tensors 16-byte aligned", name);
   if (a.M == 0) return host_ok();
   dgk::HostState st;
-  const dg_status s = dgk::host_state(&st);
+  dg_status s = dgk::host_state(&st);
+  if (s == DG_OK) s = set_up_once<dgk::norm_set_up>(st.device);
   if (s != DG_OK) return s;
+  a.status = st.status;
+  a.timeout_ns = st.timeout_ns;
   const cudaError_t e =
       dgk::launch_rms_norm(a, ue8m0, st.sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "norm launch") : host_ok();
@@ -77,15 +92,6 @@ dg_status swiglu(const dgk::SwigluFwd& a0, void* stream, bool ue8m0) {
   return e != cudaSuccess ? cuda_fail(e, "swiglu launch") : host_ok();
 }
 
-// Opts the ragged products' kernels into their shared memory, once per device.
-cudaError_t bf16_ready(int device) {
-  static std::atomic<bool> done[dgk::kHostMaxDevices];
-  if (done[device].load(std::memory_order_acquire)) return cudaSuccess;
-  const cudaError_t e = dgk::bf16_set_up();
-  if (e == cudaSuccess) done[device].store(true, std::memory_order_release);
-  return e;
-}
-
 // Shared path of the ragged bf16 products.  rows: rows of A over all groups
 // (M_total; tn: K_total).  M: tn only.
 dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void* C, void* D,
@@ -111,10 +117,9 @@ dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void
   if (!aligned16(A) || !aligned16(B) || !aligned16(C) || !aligned16(D) || !aligned(sizes, 4))
     return host_fail(DG_ERR_MISALIGNED, "A, B, C and D need 16-byte alignment, the sizes 4");
   dgk::HostState st;
-  const dg_status s = dgk::host_state(&st);
+  dg_status s = dgk::host_state(&st);
+  if (s == DG_OK) s = set_up_once<dgk::bf16_set_up>(st.device);
   if (s != DG_OK) return s;
-  cudaError_t e = bf16_ready(st.device);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
   dgk::BfCall c{};
   c.form = form;
   c.A = A ? A : D;
@@ -130,7 +135,8 @@ dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void
   c.status = st.status;
   c.timeout_ns = st.timeout_ns;
   c.debug_flags = st.debug_flags;
-  e = dgk::launch_bf16_grouped(c, st.encode, st.sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t e =
+      dgk::launch_bf16_grouped(c, st.encode, st.sms, static_cast<cudaStream_t>(stream));
   if (e == cudaErrorInvalidValue) {
     cudaGetLastError();
     return host_fail(DG_ERR_CUDA, "ragged bf16 product: tensor map or launch rejected");
@@ -144,13 +150,15 @@ extern "C" {
 dg_status dg_rms_norm_quantize_fp8_1x128(const void* X, const void* R, const void* W, void* H,
                                          void* Y, void* Q, float* sa, float* rstd, int M, int K,
                                          int ld_sa, float eps, void* stream) {
-  return rms_norm(dgk::NormFwd{X, R, W, H, Y, Q, sa, rstd, M, K, ld_sa, eps}, stream, false);
+  return rms_norm(dgk::NormFwd{X, R, W, H, Y, Q, sa, rstd, M, K, ld_sa, eps, nullptr, 0}, stream,
+                  false);
 }
 
 dg_status dg_rms_norm_quantize_fp8_1x128_ue8m0(const void* X, const void* R, const void* W, void* H,
                                                void* Y, void* Q, int32_t* sfa, float* rstd, int M,
                                                int K, int ld_sfa, float eps, void* stream) {
-  return rms_norm(dgk::NormFwd{X, R, W, H, Y, Q, sfa, rstd, M, K, ld_sfa, eps}, stream, true);
+  return rms_norm(dgk::NormFwd{X, R, W, H, Y, Q, sfa, rstd, M, K, ld_sfa, eps, nullptr, 0}, stream,
+                  true);
 }
 
 long long dg_rms_norm_backward_workspace_bytes(int M, int K) {
@@ -175,10 +183,12 @@ dg_status dg_rms_norm_backward(const void* dY, const void* H, const float* rstd,
       !aligned16(dW) || !aligned16(workspace) || !aligned(rstd, 4))
     return host_fail(DG_ERR_MISALIGNED, "%s: rstd 4-byte, the other tensors 16-byte aligned", name);
   dgk::HostState st;
-  const dg_status s = dgk::host_state(&st);
+  dg_status s = dgk::host_state(&st);
+  if (s == DG_OK) s = set_up_once<dgk::norm_set_up>(st.device);
   if (s != DG_OK) return s;
   const cudaError_t e = dgk::launch_rms_norm_backward(
-      dgk::NormBwd{dY, H, rstd, W, dR, dX, dW, static_cast<float*>(workspace), M, K},
+      dgk::NormBwd{dY, H, rstd, W, dR, dX, dW, static_cast<float*>(workspace), M, K, st.status,
+                   st.timeout_ns},
       st.sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "norm gradient launch") : host_ok();
 }

@@ -189,11 +189,11 @@ dim3 grid_of(int G, int M, int I) {
 
 cudaError_t launch_swiglu(const SwigluFwd& a, bool ue8m0, cudaStream_t stream) {
   return launch_dependent(ue8m0 ? swiglu_kernel<true> : swiglu_kernel<false>,
-                          grid_of(a.G, a.M, a.I), SG_THREADS, stream, a);
+                          grid_of(a.G, a.M, a.I), SG_THREADS, stream, 0, a);
 }
 
 cudaError_t launch_swiglu_backward(const SwigluBwd& a, cudaStream_t stream) {
-  return launch_dependent(swiglu_backward_kernel, grid_of(a.G, a.M, a.I), SG_THREADS, stream, a);
+  return launch_dependent(swiglu_backward_kernel, grid_of(a.G, a.M, a.I), SG_THREADS, stream, 0, a);
 }
 
 }  // namespace dgk
