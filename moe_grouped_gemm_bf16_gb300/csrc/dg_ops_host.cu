@@ -85,10 +85,12 @@ dg_status swiglu(const dgk::SwigluFwd& a0, void* stream, bool ue8m0) {
                 name);
   if (a.M == 0) return host_ok();
   dgk::HostState st;
-  const dg_status s = dgk::host_state(&st);
+  dg_status s = dgk::host_state(&st);
+  if (s == DG_OK) s = set_up_once<dgk::swiglu_set_up>(st.device);
   if (s != DG_OK) return s;
   a.status = st.status;
-  const cudaError_t e = dgk::launch_swiglu(a, ue8m0, static_cast<cudaStream_t>(stream));
+  a.timeout_ns = st.timeout_ns;
+  const cudaError_t e = dgk::launch_swiglu(a, ue8m0, st.sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "swiglu launch") : host_ok();
 }
 
@@ -196,7 +198,7 @@ dg_status dg_rms_norm_backward(const void* dY, const void* H, const float* rstd,
 dg_status dg_swiglu_quantize_fp8_1x128(const void* GU, void* Y, void* Q, float* sa, void* CQ,
                                        float* csa, const int32_t* masked_m, int num_groups, int M,
                                        int I, int ld_sa, void* stream) {
-  return swiglu(dgk::SwigluFwd{GU, Y, Q, sa, CQ, csa, masked_m, num_groups, M, I, ld_sa, nullptr},
+  return swiglu(dgk::SwigluFwd{GU, Y, Q, sa, CQ, csa, masked_m, num_groups, M, I, ld_sa, nullptr, 0},
                 stream, false);
 }
 
@@ -204,7 +206,7 @@ dg_status dg_swiglu_quantize_fp8_1x128_ue8m0(const void* GU, void* Y, void* Q, i
                                              void* CQ, float* csa, const int32_t* masked_m,
                                              int num_groups, int M, int I, int ld_sfa,
                                              void* stream) {
-  return swiglu(dgk::SwigluFwd{GU, Y, Q, sfa, CQ, csa, masked_m, num_groups, M, I, ld_sfa, nullptr},
+  return swiglu(dgk::SwigluFwd{GU, Y, Q, sfa, CQ, csa, masked_m, num_groups, M, I, ld_sfa, nullptr, 0},
                 stream, true);
 }
 
@@ -226,11 +228,13 @@ dg_status dg_swiglu_backward_fp8_1x128(const void* CQ, const float* csa, const v
                 name);
   if (M == 0) return host_ok();
   dgk::HostState st;
-  const dg_status s = dgk::host_state(&st);
+  dg_status s = dgk::host_state(&st);
+  if (s == DG_OK) s = set_up_once<dgk::swiglu_set_up>(st.device);
   if (s != DG_OK) return s;
   const cudaError_t e = dgk::launch_swiglu_backward(
-      dgk::SwigluBwd{CQ, csa, dY, dGU, Y, masked_m, num_groups, M, I, ld_csa, st.status},
-      static_cast<cudaStream_t>(stream));
+      dgk::SwigluBwd{CQ, csa, dY, dGU, Y, masked_m, num_groups, M, I, ld_csa, st.status,
+                     st.timeout_ns},
+      st.sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "swiglu gradient launch") : host_ok();
 }
 

@@ -16,7 +16,8 @@ struct SwigluFwd {
   float* csa;               // fp32 [G][2 I / 128][ld]
   const int32_t* masked_m;  // int32 [G] or null
   int G, M, I, ld;
-  unsigned int* status;
+  unsigned int* status;           // device status word and the waits' limit
+  unsigned long long timeout_ns;
 };
 
 struct SwigluBwd {
@@ -27,12 +28,14 @@ struct SwigluBwd {
   void* Y;                  // bf16 [G][M][I] or null: the activation again
   const int32_t* masked_m;
   int G, M, I, ld;
-  unsigned int* status;
+  unsigned int* status;           // device status word and the waits' limit
+  unsigned long long timeout_ns;
 };
 
 // The caller has validated the arguments (I % 128 == 0, I / 128 and G <=
 // 65535, 16-byte aligned tensors, ld >= M).
-cudaError_t launch_swiglu(const SwigluFwd& a, bool ue8m0, cudaStream_t stream);
-cudaError_t launch_swiglu_backward(const SwigluBwd& a, cudaStream_t stream);
+cudaError_t swiglu_set_up();  // opts the kernels into their shared memory (once per device)
+cudaError_t launch_swiglu(const SwigluFwd& a, bool ue8m0, int num_sms, cudaStream_t stream);
+cudaError_t launch_swiglu_backward(const SwigluBwd& a, int num_sms, cudaStream_t stream);
 
 }  // namespace dgk
