@@ -1,6 +1,7 @@
 // Conversions and the 1x128 scale arithmetic shared by the kernels that write
 // or read e4m3 activations (the quantiser, the norm, the gated activation).
 #pragma once
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -59,6 +60,89 @@ __device__ __forceinline__ uint4 float_to_bf16x8(const float* x) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.z) : "f"(x[5]), "f"(x[4]));
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.w) : "f"(x[7]), "f"(x[6]));
   return v;
+}
+
+// Two fp32 products or sums in one instruction (round to nearest, the same
+// results as one by one).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// a b + c
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// Eight values as four pairs.
+struct Pairs {
+  float2 v[4];
+};
+__device__ __forceinline__ Pairs bf16x8_to_pairs(const uint4& w) {
+  return Pairs{{make_float2(bf16_lo(w.x), bf16_hi(w.x)), make_float2(bf16_lo(w.y), bf16_hi(w.y)),
+                make_float2(bf16_lo(w.z), bf16_hi(w.z)), make_float2(bf16_lo(w.w), bf16_hi(w.w))}};
+}
+__device__ __forceinline__ uint4 pairs_to_bf16x8(const Pairs& p) {
+  uint4 w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(p.v[0].y), "f"(p.v[0].x));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(p.v[1].y), "f"(p.v[1].x));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.z) : "f"(p.v[2].y), "f"(p.v[2].x));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.w) : "f"(p.v[3].y), "f"(p.v[3].x));
+  return w;
+}
+// e4m3 codes of the values times f
+__device__ __forceinline__ uint2 pairs_to_e4m3x8(const Pairs& p, float f) {
+  const float2 f2 = make_float2(f, f);
+  const float2 a = mul2(p.v[0], f2), b = mul2(p.v[1], f2), c = mul2(p.v[2], f2), d = mul2(p.v[3], f2);
+  return make_uint2(cvt_e4m3x4(a.x, a.y, b.x, b.y), cvt_e4m3x4(c.x, c.y, d.x, d.y));
+}
+// the values of eight codes times s
+__device__ __forceinline__ Pairs e4m3x8_to_pairs(const uint2& w, float s) {
+  const float2 s2 = make_float2(s, s);
+  return Pairs{{mul2(e4m3x2_to_float2(w.x & 0xFFFFu), s2), mul2(e4m3x2_to_float2(w.x >> 16), s2),
+                mul2(e4m3x2_to_float2(w.y & 0xFFFFu), s2), mul2(e4m3x2_to_float2(w.y >> 16), s2)}};
+}
+__device__ __forceinline__ float pairs_amax(const Pairs& p) {
+  return fmaxf(fmaxf(fmaxf(fabsf(p.v[0].x), fabsf(p.v[0].y)), fmaxf(fabsf(p.v[1].x), fabsf(p.v[1].y))),
+               fmaxf(fmaxf(fabsf(p.v[2].x), fabsf(p.v[2].y)), fmaxf(fabsf(p.v[3].x), fabsf(p.v[3].y))));
+}
+// largest magnitude of eight bf16 values, exactly
+__device__ __forceinline__ float bf16x8_amax(const uint4& w) {
+  auto mag = [](uint32_t x) {
+    __nv_bfloat162_raw r;
+    r.x = static_cast<uint16_t>(x);
+    r.y = static_cast<uint16_t>(x >> 16);
+    return __habs2(__nv_bfloat162(r));
+  };
+  const float2 m = __bfloat1622float2(
+      __hmax2(__hmax2(mag(w.x), mag(w.y)), __hmax2(mag(w.z), mag(w.w))));
+  return fmaxf(m.x, m.y);
 }
 
 // The factor a group's values are multiplied by before the conversion to

@@ -14,12 +14,14 @@
 // Both are memory-bound: a row is read once and stays on the chip between the
 // statistics and the output.  A thread takes VPT vectors of 8 columns.  Two
 // forms of each:
-//  * one block per row, loads straight to registers: the shortest latency, for
-//    few rows;
+//  * one block per row, loads straight to registers (the gradient of few rows:
+//    further blocks of the same launch sum the weight's gradient by columns);
 //  * persistent blocks fed by bulk copies, several rows ahead, into a ring in
-//    shared memory: a block that waits for its row's loads, reduces, and only
-//    then stores keeps too few bytes in flight (4096 x 7168: 56 us at two
-//    blocks per SM).
+//    shared memory (the gradient: each keeps its share of the weight's in
+//    registers, and a second kernel adds the shares).
+// Measured: 4096 x 7168 forward 45 us (5.9 TB/s; one block per row 47 us),
+// 8192 x 7168 backward 79 us (5.9 TB/s; the one-launch form 171 us).
+
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -53,37 +55,43 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // Output of a normalised row: the thread's VPT vectors h (w: the weight's,
 // packed), those below nv stored.
 template <int VPT, bool UE8M0>
-__device__ __forceinline__ void norm_output(const NormFwd& a, int m, int nv, float (&h)[VPT][8],
-                                            float rs, const uint4 (&w)[VPT]) {
+__device__ __forceinline__ void norm_output(const NormFwd& a, int m, int nv, Pairs (&h)[VPT], float rs,
+                                            const uint4 (&w)[VPT]) {
   const int T = blockDim.x, kb = a.K >> 7;
   const size_t base = static_cast<size_t>(m) * (a.K >> 3);
+  const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = i * T + threadIdx.x;
-    float wf[8];
-    bf16x8_to_float(w[i], wf);
-    float amax = 0.f;
+    const Pairs wp = bf16x8_to_pairs(w[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h[i][j] = h[i][j] * rs * wf[j];
-      amax = fmaxf(amax, fabsf(h[i][j]));
-    }
-    if (a.Y && v < nv) static_cast<uint4*>(a.Y)[base + v] = float_to_bf16x8(h[i]);
+    for (int j = 0; j < 4; ++j) h[i].v[j] = mul2(mul2(h[i].v[j], rs2), wp.v[j]);
+    if (a.Y && v < nv) static_cast<uint4*>(a.Y)[base + v] = pairs_to_bf16x8(h[i]);
     if (!a.Q) continue;
-    // a 128-column group is 16 consecutive lanes (T is a multiple of 32)
+    // a 128-column group is 16 consecutive lanes (T is a multiple of 32); its
+    // even lanes compute 448 / a, which all take, its odd ones the scale a / 448
+    float amax = pairs_amax(h[i]);
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     amax = fmaxf(amax, kScaleFloor);
-    float f;
-    uint32_t e8;
-    group_factor<UE8M0>(amax, f, e8);
-    if (v < nv) {
-      uint2 q;
-      q.x = cvt_e4m3x4(h[i][0] * f, h[i][1] * f, h[i][2] * f, h[i][3] * f);
-      q.y = cvt_e4m3x4(h[i][4] * f, h[i][5] * f, h[i][6] * f, h[i][7] * f);
-      static_cast<uint2*>(a.Q)[base + v] = q;
-      if ((v & 15) == 0)
-        store_scale<UE8M0>(static_cast<float*>(a.sa), 0, kb, a.ld_sa, v >> 4, m, amax, e8);
+    if constexpr (UE8M0) {
+      float f;
+      uint32_t e8;
+      group_factor<true>(amax, f, e8);
+      if (v < nv) {
+        static_cast<uint2*>(a.Q)[base + v] = pairs_to_e4m3x8(h[i], f);
+        if ((v & 15) == 1)
+          store_scale<true>(static_cast<float*>(a.sa), 0, kb, a.ld_sa, v >> 4, m, amax, e8);
+      }
+    } else {
+      const bool odd = v & 1;
+      const float quot = __fdiv_rn(odd ? amax : 448.0f, odd ? 448.0f : amax);
+      const float f = __shfl_sync(0xffffffffu, quot, threadIdx.x & 30);
+      if (v < nv) {
+        static_cast<uint2*>(a.Q)[base + v] = pairs_to_e4m3x8(h[i], f);
+        if ((v & 15) == 1)
+          static_cast<float*>(a.sa)[static_cast<size_t>(v >> 4) * a.ld_sa + m] = quot;
+      }
     }
   }
 }
@@ -99,19 +107,18 @@ __device__ __forceinline__ void load_weight(const void* W, int nv, uint4 (&w)[VP
 
 // h = x (+ r), its sum of squares, and the residual stream's output.
 __device__ __forceinline__ float add_residual(const NormFwd& a, size_t at, const uint4& x,
-                                              const uint4& r, float (&h)[8]) {
-  bf16x8_to_float(x, h);
+                                              const uint4& r, Pairs& h) {
+  h = bf16x8_to_pairs(x);
   if (a.R) {
-    float rf[8];
-    bf16x8_to_float(r, rf);
+    const Pairs rp = bf16x8_to_pairs(r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] += rf[j];
-    if (a.H) static_cast<uint4*>(a.H)[at] = float_to_bf16x8(h);
+    for (int j = 0; j < 4; ++j) h.v[j] = add2(h.v[j], rp.v[j]);
+    if (a.H) static_cast<uint4*>(a.H)[at] = pairs_to_bf16x8(h);
   }
-  float ss = 0.f;
+  float2 ss = mul2(h.v[0], h.v[0]);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) ss = fmaf(h[j], h[j], ss);
-  return ss;
+  for (int j = 1; j < 4; ++j) ss = fma2(h.v[j], h.v[j], ss);
+  return ss.x + ss.y;
 }
 
 template <int VPT, bool UE8M0>
@@ -134,16 +141,12 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormFwd a) {
     }
   }
   load_weight<VPT>(a.W, nv, w);
-  float h[VPT][8], ss = 0.f;
+  Pairs h[VPT] = {};
+  float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = i * T + threadIdx.x;
-    if (v < nv) {
-      ss += add_residual(a, base + v, x[i], r[i], h[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
-    }
+    if (v < nv) ss += add_residual(a, base + v, x[i], r[i], h[i]);
   }
   ss = block_sum(ss, red);
   const float rs = __frsqrt_rn(ss / static_cast<float>(a.K) + a.eps);
@@ -179,12 +182,11 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
     const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a);
     const size_t base = static_cast<size_t>(m) * nv;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
-    float h[VPT][8], ss = 0.f;
+    Pairs h[VPT] = {};
+    float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * T + threadIdx.x;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
       if (v < nv && ok) ss += add_residual(a, base + v, x[v], a.R ? x[nv + v] : x[v], h[i]);
     }
     ss = block_sum(ss, red[par]);
@@ -201,30 +203,31 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
   if (threadIdx.x == 0 && *abort_flag) ring.drain(a);
 }
 
-// Gradient, a row: the products' sum for dX, and the block's share of dW.
+// Gradient, a vector of a row: its share of sum(g xh), the block's of dW.
 __device__ __forceinline__ float grad_sums(const uint4& dy, const uint4& hv, const uint4& wv, float rs,
-                                           float (&g)[8], float (&xh)[8], float (&dw)[8]) {
-  float w[8], dot = 0.f;
-  bf16x8_to_float(dy, g);
-  bf16x8_to_float(hv, xh);
-  bf16x8_to_float(wv, w);
+                                           Pairs& g, Pairs& xh, Pairs& dw) {
+  const Pairs w = bf16x8_to_pairs(wv);
+  const float2 rs2 = make_float2(rs, rs);
+  g = bf16x8_to_pairs(dy);
+  xh = bf16x8_to_pairs(hv);
+  float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    xh[j] *= rs;
-    dw[j] = fmaf(g[j], xh[j], dw[j]);
-    g[j] *= w[j];
-    dot = fmaf(g[j], xh[j], dot);
+  for (int j = 0; j < 4; ++j) {
+    xh.v[j] = mul2(xh.v[j], rs2);
+    dw.v[j] = fma2(g.v[j], xh.v[j], dw.v[j]);
+    g.v[j] = mul2(g.v[j], w.v[j]);
+    dot = fma2(g.v[j], xh.v[j], dot);
   }
-  return dot;
+  return dot.x + dot.y;
 }
 
-__device__ __forceinline__ uint4 grad_row(const float (&g)[8], const float (&xh)[8], float rs,
-                                          float mean, const uint4& dr) {
-  float r[8];
-  bf16x8_to_float(dr, r);
+__device__ __forceinline__ uint4 grad_row(const Pairs& g, const Pairs& xh, float rs, float mean,
+                                          const uint4& dr) {
+  const float2 rs2 = make_float2(rs, rs), minus = make_float2(-mean, -mean);
+  Pairs r = bf16x8_to_pairs(dr);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = fmaf(rs, g[j] - xh[j] * mean, r[j]);
-  return float_to_bf16x8(r);
+  for (int j = 0; j < 4; ++j) r.v[j] = fma2(rs2, fma2(xh.v[j], minus, g.v[j]), r.v[j]);
+  return pairs_to_bf16x8(r);
 }
 
 // Few rows: blocks [0, M) take a row each, the blocks behind them 64 columns of
@@ -255,7 +258,8 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_kernel(const NormBwd a
       }
     }
     load_weight<VPT>(a.W, nv, w);
-    float g[VPT][8], xh[VPT][8], dw[8] = {}, dot = 0.f;
+    Pairs g[VPT], xh[VPT], dw = {};
+    float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) dot += grad_sums(dy[i], hv[i], w[i], rs, g[i], xh[i], dw);
     const float mean = block_sum(dot, red) / static_cast<float>(a.K);
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
   load_weight<VPT>(a.W, nv, w);
   __syncthreads();
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  float dw[VPT][8] = {};
+  Pairs dw[VPT] = {};
   int s = 0, par = 0;
   uint32_t ph = 0;
   for (long long m = blockIdx.x; m < a.M; m += step, par ^= 1) {
@@ -322,7 +326,8 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
     const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a);
     const size_t base = static_cast<size_t>(m) * nv;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
-    float g[VPT][8], xh[VPT][8], dot = 0.f;
+    Pairs g[VPT], xh[VPT];
+    float dot = 0.f;
     uint4 r[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -348,8 +353,8 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
     const int v = i * T + threadIdx.x;
     if (v >= nv) continue;
     float4* out = reinterpret_cast<float4*>(a.part + static_cast<size_t>(blockIdx.x) * a.K) + 2 * v;
-    out[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-    out[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    out[0] = make_float4(dw[i].v[0].x, dw[i].v[0].y, dw[i].v[1].x, dw[i].v[1].y);
+    out[1] = make_float4(dw[i].v[2].x, dw[i].v[2].y, dw[i].v[3].x, dw[i].v[3].y);
   }
   if (threadIdx.x == 0 && *abort_flag) ring.drain(a);
 }
@@ -400,7 +405,11 @@ cudaError_t launch_ring(void (*kernel)(P...), const RingShape& r, cudaStream_t s
 template <bool UE8M0>
 cudaError_t launch_fwd(const NormFwd& a, int num_sms, cudaStream_t stream) {
   const int vpt = a.K <= 8192 ? 1 : 2;
-  if (a.M > 2 * num_sms) {
+  // Long rows leave room for one or two blocks per SM, which wait for their
+  // loads in turn: the ring is ahead from some 12 rows per SM (2432 x 7168: 27.7
+  // against 29.7 us).  Shorter rows, with more blocks per SM, need none (4864 x
+  // 4096: 32.2 with it, 29.6 without; 2432 x 1024: 4.8, 3.9).
+  if (a.K > 6144 && a.M >= 12 * num_sms) {
     const RingShape r = ring_shape(a.M, a.K, a.R ? 2 : 1, vpt, num_sms, a.M);
     return vpt == 1 ? launch_ring(rms_norm_ring_kernel<1, UE8M0>, r, stream, a)
                     : launch_ring(rms_norm_ring_kernel<2, UE8M0>, r, stream, a);
@@ -433,8 +442,13 @@ cudaError_t launch_rms_norm(const NormFwd& a, bool ue8m0, int num_sms, cudaStrea
 
 cudaError_t launch_rms_norm_backward(const NormBwd& a, int num_sms, cudaStream_t stream) {
   const int vpt = a.K <= 8192 ? 1 : 2;
-  if (a.M <= 4 * num_sms) {
-    const int threads = row_threads(a.K, vpt);
+  // The one-launch form reads its rows a second time, in chains that grow with
+  // M; the ring pays a second kernel (about 1.5 us).  Measured with both, 456
+  // rows of 512, 2048, 7168 columns: 5.0, 5.5, 9.3 us in one launch, 5.0, 6.7,
+  // 8.8 us with the ring; 608 rows: 6.0, 7.2, 11.9 and 5.4, 7.1, 10.1 us.
+  if (a.M <= 3 * num_sms) {
+    // (at least 32 chains of rows in a block of dW's columns)
+    const int threads = std::max(256, row_threads(a.K, vpt));
     const dim3 grid(a.M + a.K / 64);
     const int smem = threads / 8 * 64 * 4;
     return vpt == 1 ? launch_dependent(rms_norm_backward_kernel<1>, grid, threads, stream, smem, a)

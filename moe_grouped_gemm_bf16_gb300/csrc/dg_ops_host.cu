@@ -228,13 +228,11 @@ dg_status dg_swiglu_backward_fp8_1x128(const void* CQ, const float* csa, const v
                 name);
   if (M == 0) return host_ok();
   dgk::HostState st;
-  dg_status s = dgk::host_state(&st);
-  if (s == DG_OK) s = set_up_once<dgk::swiglu_set_up>(st.device);
+  const dg_status s = dgk::host_state(&st);
   if (s != DG_OK) return s;
   const cudaError_t e = dgk::launch_swiglu_backward(
-      dgk::SwigluBwd{CQ, csa, dY, dGU, Y, masked_m, num_groups, M, I, ld_csa, st.status,
-                     st.timeout_ns},
-      st.sms, static_cast<cudaStream_t>(stream));
+      dgk::SwigluBwd{CQ, csa, dY, dGU, Y, masked_m, num_groups, M, I, ld_csa, st.status},
+      static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "swiglu gradient launch") : host_ok();
 }
 

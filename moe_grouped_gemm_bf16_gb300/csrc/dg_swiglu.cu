@@ -34,7 +34,19 @@ namespace {
 
 constexpr int SG_THREADS = 256;   // direct form: 32 rows of one 128-column group
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + exp(-g)) with the hardware's exponential and reciprocal; a gate whose
+// exponential is not finite gives 0 (below -88) or 1.
+__device__ __forceinline__ float2 sigmoid2(float2 g) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float2 t = mul2(g, make_float2(-kLog2e, -kLog2e));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = add2(e, make_float2(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return r;
+}
 
 // Rows of batch z that hold a token, the count clamped to [0, M] (reported).
 __device__ __forceinline__ int valid_rows(const int32_t* masked_m, int z, int M,
@@ -51,30 +63,6 @@ __device__ __forceinline__ float lanes_max(float a) {
 #pragma unroll
   for (int o = 4; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   return fmaxf(a, kScaleFloor);
-}
-
-__device__ __forceinline__ float group_max(const float* x) {
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x[i]));
-  return lanes_max(a);
-}
-
-__device__ __forceinline__ uint2 quantise8(const float* x, float f) {
-  return make_uint2(cvt_e4m3x4(x[0] * f, x[1] * f, x[2] * f, x[3] * f),
-                    cvt_e4m3x4(x[4] * f, x[5] * f, x[6] * f, x[7] * f));
-}
-
-__device__ __forceinline__ void dequantise8(const uint2& w, float s, float* x) {
-  const uint32_t c[2] = {w.x, w.y};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 lo = e4m3x2_to_float2(c[i] & 0xFFFFu), hi = e4m3x2_to_float2(c[i] >> 16);
-    x[4 * i] = lo.x * s;
-    x[4 * i + 1] = lo.y * s;
-    x[4 * i + 2] = hi.x * s;
-    x[4 * i + 3] = hi.y * s;
-  }
 }
 
 // Where lane j of the group `grp` of row m of batch z finds its two vectors of
@@ -94,49 +82,66 @@ struct Place {
 
 // One lane's share of a group, forward: v = {gate, gate + 8, up, up + 8}.
 // Every lane of the warp takes part; `on`: this one's row is stored.
+//
+// The time goes to instructions as much as to memory (38.8 per element in a
+// plain version, 28.8 so), so values are taken in pairs and the group's six
+// quotients are shared out over its lanes: 448 / a for y, gate and up in lanes
+// 0 to 2 (the others fetch them), a / 448 in lanes 3 to 5, which store them.
 template <bool UE8M0>
 __device__ __forceinline__ void forward_group(const SwigluFwd& a, const Place& p, const uint4 (&v)[4],
                                               bool on) {
   const int kb = a.I >> 7;
-  float g[16], u[16], y[16];
-  bf16x8_to_float(v[0], g);
-  bf16x8_to_float(v[1], g + 8);
-  bf16x8_to_float(v[2], u);
-  bf16x8_to_float(v[3], u + 8);
+  Pairs g[2] = {bf16x8_to_pairs(v[0]), bf16x8_to_pairs(v[1])};
+  Pairs u[2] = {bf16x8_to_pairs(v[2]), bf16x8_to_pairs(v[3])};
+  Pairs y[2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) y[i] = g[i] * sigmoid(g[i]) * u[i];
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      y[h].v[i] = mul2(mul2(g[h].v[i], sigmoid2(g[h].v[i])), u[h].v[i]);
   if (a.Y && on) {
     uint4* Y = static_cast<uint4*>(a.Y) + p.at;
-    Y[0] = float_to_bf16x8(y);
-    Y[8] = float_to_bf16x8(y + 8);
+    Y[0] = pairs_to_bf16x8(y[0]);
+    Y[8] = pairs_to_bf16x8(y[1]);
   }
-  float f;
-  uint32_t e8;
+  float ay = kScaleFloor, ag = kScaleFloor, au = kScaleFloor;
+  if (a.Q) ay = lanes_max(fmaxf(pairs_amax(y[0]), pairs_amax(y[1])));
+  if (a.CQ) {
+    ag = lanes_max(fmaxf(bf16x8_amax(v[0]), bf16x8_amax(v[1])));
+    au = lanes_max(fmaxf(bf16x8_amax(v[2]), bf16x8_amax(v[3])));
+  }
+  const int j = p.lane8;
+  const float mine = (j == 0 || j == 3) ? ay : (j == 1 || j == 4) ? ag : au;
+  const float quot = j < 3 ? __fdiv_rn(448.0f, mine) : __fdiv_rn(mine, 448.0f);
+  const int first = (threadIdx.x & 31) - j;
   if (a.Q) {
-    const float amax = group_max(y);
-    group_factor<UE8M0>(amax, f, e8);
+    float f;
+    uint32_t e8;
+    if constexpr (UE8M0) group_factor<true>(ay, f, e8);
+    else f = __shfl_sync(0xffffffffu, quot, first);
     if (on) {
       uint2* Q = static_cast<uint2*>(a.Q) + p.at;
-      Q[0] = quantise8(y, f);
-      Q[8] = quantise8(y + 8, f);
-      if (p.lane8 == 0)
-        store_scale<UE8M0>(static_cast<float*>(a.sa), p.z, kb, a.ld, p.grp, p.m, amax, e8);
+      Q[0] = pairs_to_e4m3x8(y[0], f);
+      Q[8] = pairs_to_e4m3x8(y[1], f);
+      if constexpr (UE8M0) {
+        if (j == 3) store_scale<true>(static_cast<float*>(a.sa), p.z, kb, a.ld, p.grp, p.m, ay, e8);
+      } else {
+        if (j == 3)
+          static_cast<float*>(a.sa)[(static_cast<size_t>(p.z) * kb + p.grp) * a.ld + p.m] = quot;
+      }
     }
   }
   if (a.CQ) {
-    const float ag = group_max(g), au = group_max(u);
-    uint2* CQ = static_cast<uint2*>(a.CQ);
+    const float fg = __shfl_sync(0xffffffffu, quot, first + 1);
+    const float fu = __shfl_sync(0xffffffffu, quot, first + 2);
     if (on) {
-      group_factor<false>(ag, f, e8);
-      CQ[p.gate] = quantise8(g, f);
-      CQ[p.gate + 8] = quantise8(g + 8, f);
-      group_factor<false>(au, f, e8);
-      CQ[p.up] = quantise8(u, f);
-      CQ[p.up + 8] = quantise8(u + 8, f);
-      if (p.lane8 == 0) {
-        store_scale<false>(a.csa, p.z, 2 * kb, a.ld, p.grp, p.m, ag, 0);
-        store_scale<false>(a.csa, p.z, 2 * kb, a.ld, kb + p.grp, p.m, au, 0);
-      }
+      uint2* CQ = static_cast<uint2*>(a.CQ);
+      CQ[p.gate] = pairs_to_e4m3x8(g[0], fg);
+      CQ[p.gate + 8] = pairs_to_e4m3x8(g[1], fg);
+      CQ[p.up] = pairs_to_e4m3x8(u[0], fu);
+      CQ[p.up + 8] = pairs_to_e4m3x8(u[1], fu);
+      if (j == 4 || j == 5)
+        a.csa[(static_cast<size_t>(p.z) * (2 * kb) + (j - 4) * kb + p.grp) * a.ld + p.m] = quot;
     }
   }
 }
@@ -149,26 +154,25 @@ __device__ __forceinline__ void backward_group(const SwigluBwd& a, const Place& 
   uint4* dGU = static_cast<uint4*>(a.dGU);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float g[8], u[8], d[8], y[8];
-    dequantise8(c[h], sg, g);
-    dequantise8(c[2 + h], su, u);
-    bf16x8_to_float(dv[h], d);
+    Pairs g = e4m3x8_to_pairs(c[h], sg), u = e4m3x8_to_pairs(c[2 + h], su), y;
+    const Pairs d = bf16x8_to_pairs(dv[h]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float s = sigmoid(g[i]), gs = g[i] * s;
-      y[i] = gs * u[i];
+    for (int i = 0; i < 4; ++i) {
+      const float2 s = sigmoid2(g.v[i]), gs = mul2(g.v[i], s);
+      y.v[i] = mul2(gs, u.v[i]);
       // s (1 + g (1 - s)) = s + g s (1 - s)
-      g[i] = d[i] * u[i] * fmaf(gs, 1.0f - s, s);
-      u[i] = d[i] * gs;
+      const float2 slope = fma2(gs, fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f)), s);
+      g.v[i] = mul2(mul2(d.v[i], u.v[i]), slope);
+      u.v[i] = mul2(d.v[i], gs);
     }
-    dGU[p.gate + 8 * h] = float_to_bf16x8(g);
-    dGU[p.up + 8 * h] = float_to_bf16x8(u);
-    if (a.Y) static_cast<uint4*>(a.Y)[p.at + 8 * h] = float_to_bf16x8(y);
+    dGU[p.gate + 8 * h] = pairs_to_bf16x8(g);
+    dGU[p.up + 8 * h] = pairs_to_bf16x8(u);
+    if (a.Y) static_cast<uint4*>(a.Y)[p.at + 8 * h] = pairs_to_bf16x8(y);
   }
 }
 
 template <bool UE8M0>
-__global__ void __launch_bounds__(SG_THREADS) swiglu_kernel(const SwigluFwd a) {
+__global__ void __launch_bounds__(SG_THREADS, 4) swiglu_kernel(const SwigluFwd a) {
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int m = blockIdx.x * 32 + (threadIdx.x >> 3), z = blockIdx.z;
@@ -227,18 +231,26 @@ __global__ void __launch_bounds__(SG_THREADS) swiglu_ring_kernel(const SwigluFwd
     for (int s = 0; s < stages && blockIdx.x + s * gridDim.x < chunks; ++s)
       fill(blockIdx.x + s * gridDim.x, s);
   __syncthreads();
+  // this thread's first unit of a chunk (row, lane of the row), and the next
+  const int r0 = threadIdx.x / lanes, q0 = threadIdx.x - r0 * lanes;
+  const int dr = SG_THREADS / lanes, dq = SG_THREADS - dr * lanes;
+  auto advance = [&](int& r, int& q) {
+    r += dr;
+    q += dq;
+    if (q >= lanes) { q -= lanes; ++r; }
+  };
   int s = 0;
   uint32_t ph = 0;
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a);
     const int n = ok ? min(rows, total - c * rows) * lanes : 0;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
-    for (int u0 = threadIdx.x & ~31; u0 < n; u0 += SG_THREADS) {
-      const int u = u0 + (threadIdx.x & 31), r = u / lanes, q = u - r * lanes;
-      const int row = c * rows + r, z = row / a.M;
+    int r = r0, q = q0;
+    for (int u0 = threadIdx.x & ~31; u0 < n; u0 += SG_THREADS, advance(r, q)) {
+      const int row = c * rows + r, z = a.G > 1 ? row / a.M : 0;
       const Place p(z, row - z * a.M, q >> 3, q & 7, a.M, a.I);
       const uint4* g = x + r * (a.I >> 2) + p.grp * 16 + p.lane8;
-      const bool on = u < n;
+      const bool on = u0 + static_cast<int>(threadIdx.x & 31) < n;
       uint4 v[4] = {};
       if (on) {
         v[0] = g[0];
@@ -256,110 +268,46 @@ __global__ void __launch_bounds__(SG_THREADS) swiglu_ring_kernel(const SwigluFwd
   if (threadIdx.x == 0 && *abort_flag) ring.drain(a);
 }
 
-// (the codes are a row of 2 I bytes, and so is the gradient's row: two operands
-// of equal chunks)
-__global__ void __launch_bounds__(SG_THREADS) swiglu_backward_ring_kernel(const SwigluBwd a, int rows,
-                                                                          int stages) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full[kMaxRing];
-  __shared__ uint32_t aborted;
-  volatile uint32_t* abort_flag = &aborted;
-  const int lanes = a.I >> 4, total = a.G * a.M, kb = a.I >> 7;
-  ChunkRing ring{{a.CQ, a.dY, nullptr}, smem, full, stages, 2, rows * a.I * 2, 0, 0};
-  auto fill = [&](int c, int s) { ring.fill(c, s, min(rows, total - c * rows) * a.I * 2); };
-  const int chunks = (total + rows - 1) / rows;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) mbar_init(smem_u32(full + s), 1);
-    aborted = 0;
-    fence_mbarrier_init();
-  }
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  if (threadIdx.x == 0)
-    for (int s = 0; s < stages && blockIdx.x + s * gridDim.x < chunks; ++s)
-      fill(blockIdx.x + s * gridDim.x, s);
-  __syncthreads();
-  int s = 0;
-  uint32_t ph = 0;
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a);
-    const int n = ok ? min(rows, total - c * rows) * lanes : 0;
-    const uint2* x = reinterpret_cast<const uint2*>(ring.slot(s));
-    const uint4* y = reinterpret_cast<const uint4*>(ring.slot(s) + ring.bytes);
-    for (int u = threadIdx.x; u < n; u += SG_THREADS) {
-      const int r = u / lanes, q = u - r * lanes;
-      const int row = c * rows + r, z = row / a.M;
-      const Place p(z, row - z * a.M, q >> 3, q & 7, a.M, a.I);
-      const float* cs = a.csa + static_cast<size_t>(z) * (2 * kb) * a.ld + p.m;
-      const float sg = __ldg(cs + static_cast<size_t>(p.grp) * a.ld);
-      const float su = __ldg(cs + static_cast<size_t>(kb + p.grp) * a.ld);
-      const uint2* g = x + r * (a.I >> 2) + p.grp * 16 + p.lane8;
-      const uint4* dy = y + r * (a.I >> 3) + p.grp * 16 + p.lane8;
-      const uint2 cd[4] = {g[0], g[8], g[a.I >> 3], g[(a.I >> 3) + 8]};
-      const uint4 d[2] = {dy[0], dy[8]};
-      backward_group(a, p, cd, sg, su, d);
-    }
-    __syncthreads();   // the slot has been read
-    const long long next = c + static_cast<long long>(stages) * gridDim.x;
-    if (threadIdx.x == 0 && next < chunks && *abort_flag == 0) fill(static_cast<int>(next), s);
-    if (++s == stages) { s = 0; ph ^= 1; }
-  }
-  if (threadIdx.x == 0 && *abort_flag) ring.drain(a);
-}
-
 dim3 grid_of(int G, int M, int I) { return dim3((M + 31) / 32, I / 128, G); }
 
-struct RingShape {
-  int rows, stages, smem, blocks;
-};
-
-// Chunks of about CHUNK bytes in rows of `row` bytes, PER_SM blocks per SM.
-// Returns stages = 0 where a row is too long for a ring of two.
-template <int PER_SM, int CHUNK>
-RingShape ring_shape(long long total, int row, int num_sms) {
-  RingShape r;
-  r.rows = std::max(1, CHUNK / row);
-  r.stages = std::min(kMaxRing, ring_bytes(PER_SM) / (r.rows * row));
-  if (r.stages < 2) r.stages = 0;
-  r.smem = r.stages * r.rows * row;
-  r.blocks = static_cast<int>(std::min<long long>((total + r.rows - 1) / r.rows,
-                                                  static_cast<long long>(PER_SM) * num_sms));
-  return r;
-}
-
-constexpr int kFwdPerSm = 3, kBwdPerSm = 4, kChunk = 16384;
+// Ring: two blocks per SM (112 registers a thread; a third block, or a ring in
+// smaller chunks, was slower), chunks of about 48 KB, which are three units of
+// work per thread between two barriers.  32647 rows, I = 2048: 76 us, with
+// chunks of 16 KB 83 us, three blocks of 85 registers each 91 us; loads straight
+// to registers 90-101 us.  (The gradient, with two thirds of the instructions
+// per byte, runs at 96% of the copy rate without a ring.)
+constexpr int kRingPerSm = 2, kChunk = 49152;
 
 }  // namespace
 
 cudaError_t swiglu_set_up() {
-  cudaError_t e = cudaFuncSetAttribute(swiglu_ring_kernel<false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       ring_bytes(kFwdPerSm));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(swiglu_ring_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             ring_bytes(kFwdPerSm));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(swiglu_backward_ring_kernel,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(kBwdPerSm));
-  return e;
+  const cudaError_t e = cudaFuncSetAttribute(swiglu_ring_kernel<false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             ring_bytes(kRingPerSm));
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(swiglu_ring_kernel<true>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 ring_bytes(kRingPerSm));
 }
 
 cudaError_t launch_swiglu(const SwigluFwd& a, bool ue8m0, int num_sms, cudaStream_t stream) {
   const long long total = static_cast<long long>(a.G) * a.M;
-  const RingShape r = ring_shape<kFwdPerSm, kChunk>(total, 4 * a.I, num_sms);
-  if (!a.masked_m && r.stages && total < (1ll << 31) && r.blocks == kFwdPerSm * num_sms)
+  const int row = 4 * a.I, rows = std::max(1, kChunk / row);
+  const int stages = std::min(kMaxRing, ring_bytes(kRingPerSm) / (rows * row));
+  const int blocks = kRingPerSm * num_sms;
+  // whole rows only (no masked layout), and enough chunks for every block to
+  // make up for the ring's 2 us of start (measured both ways, I = 256 to 4096:
+  // with a checkpoint the ring is ahead from about 6 chunks per block, 46 to 41
+  // us at 16384 x 2048, without one from 14, 61 to 58 us at 32647 x 2048)
+  if (!a.masked_m && stages >= 2 && total < (1ll << 31) &&
+      total >= (a.CQ ? 6ll : 14ll) * blocks * rows)
     return launch_dependent(ue8m0 ? swiglu_ring_kernel<true> : swiglu_ring_kernel<false>,
-                            dim3(r.blocks), SG_THREADS, stream, r.smem, a, r.rows, r.stages);
+                            dim3(blocks), SG_THREADS, stream, stages * rows * row, a, rows, stages);
   return launch_dependent(ue8m0 ? swiglu_kernel<true> : swiglu_kernel<false>,
                           grid_of(a.G, a.M, a.I), SG_THREADS, stream, 0, a);
 }
 
-cudaError_t launch_swiglu_backward(const SwigluBwd& a, int num_sms, cudaStream_t stream) {
-  const long long total = static_cast<long long>(a.G) * a.M;
-  const RingShape r = ring_shape<kBwdPerSm, kChunk>(total, 4 * a.I, num_sms);
-  if (!a.masked_m && r.stages && total < (1ll << 31) && r.blocks == kBwdPerSm * num_sms)
-    return launch_dependent(swiglu_backward_ring_kernel, dim3(r.blocks), SG_THREADS, stream, r.smem,
-                            a, r.rows, r.stages);
+cudaError_t launch_swiglu_backward(const SwigluBwd& a, cudaStream_t stream) {
   return launch_dependent(swiglu_backward_kernel, grid_of(a.G, a.M, a.I), SG_THREADS, stream, 0, a);
 }
 

@@ -28,14 +28,13 @@ struct SwigluBwd {
   void* Y;                  // bf16 [G][M][I] or null: the activation again
   const int32_t* masked_m;
   int G, M, I, ld;
-  unsigned int* status;           // device status word and the waits' limit
-  unsigned long long timeout_ns;
+  unsigned int* status;
 };
 
 // The caller has validated the arguments (I % 128 == 0, I / 128 and G <=
 // 65535, 16-byte aligned tensors, ld >= M).
 cudaError_t swiglu_set_up();  // opts the kernels into their shared memory (once per device)
 cudaError_t launch_swiglu(const SwigluFwd& a, bool ue8m0, int num_sms, cudaStream_t stream);
-cudaError_t launch_swiglu_backward(const SwigluBwd& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_swiglu_backward(const SwigluBwd& a, cudaStream_t stream);
 
 }  // namespace dgk

@@ -68,7 +68,8 @@ def check(X, Rs, W, got, M, K, ue8m0, outs, what):
 
 
 SHAPES = [(1, 128, 4), (1, 7168, 4), (3, 256, 8), (7, 1536, 8), (33, 640, 36), (130, 2048, 132),
-          (5, 8192, 8), (4, 8320, 4), (3, 16384, 4), (700, 384, 700), (1500, 512, 1500)]
+          (5, 8192, 8), (4, 8320, 4), (3, 16384, 4), (700, 384, 700), (1500, 512, 1500),
+          (1900, 7168, 1900), (1830, 16384, 1832), (4100, 6272, 4100)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
@@ -177,7 +178,8 @@ def check_backward(dY, H, rstd, W, dR, dX, dW, what):
 
 
 @pytest.mark.parametrize("shape", [(1, 128), (1, 7168), (2, 256), (33, 640), (150, 2048), (305, 1024),
-                                   (611, 384), (9, 8320), (4, 16384), (2500, 512)],
+                                   (611, 384), (9, 8320), (4, 16384), (2500, 512),
+                                   (460, 7168), (500, 16384), (1300, 2048)],
                          ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("residual", [False, True])
 def test_norm_gradient(shape, residual):
