@@ -8,7 +8,7 @@
 //
 // Every form is one computation: a tile of D with `lanes` consecutive columns
 // of D on the tensor memory's lanes (B is the MMA's first operand) and up to
-// BC rows of D on its columns (A is the second operand).  The ragged dimension
+// `bc` rows of D on its columns (A is the second operand).  The ragged dimension
 // of nt and nn is then the MMA's N, which the instruction takes in steps of
 // 16 or 32: a group of 20 rows costs 32 columns, not 128 lanes, and a weight
 // tile is always full.
@@ -16,14 +16,20 @@
 // Two kernels:
 //  * PAIR: a persistent CTA pair per 256 x 256 tile (cta_group::2: each CTA
 //    holds 128 lanes of B and half of A's rows), for groups of many rows;
-//  * single: one persistent CTA per tile of up to 256 lanes x BC rows, for
+//  * single: one persistent CTA per tile of up to 256 lanes x 128 rows, for
 //    groups of few rows, where the time is that of reading the weights: the
 //    host picks the lanes so that the tiles fill the SMs once (all of them
 //    stream at HBM's rate and end together).
+// Where there are too few tiles for the SMs, either splits the reduction over
+// the CTAs (pairs) of a cluster, one tile per cluster: each leaves its fp32
+// partial in shared memory, and each then adds up a share of the rows in the
+// order of the ranks.
 //
-// Warps 0 and 2 load by TMA (B's tile and A's) into a ring of slots 64 deep in
-// the reduction, warp 1 (of the pair's leader) issues tcgen05.mma kind::f16
-// into one of two fp32 accumulators in tensor memory, warps 4-7 round the
+// Warps 0 and 2 load by TMA (B's tile and A's) into a ring of slots, BK deep in
+// the reduction: 64 for the pair (six slots of 32 KB a CTA, whose latency-bound
+// cases want many in flight), 128 for the single form (half the loads to
+// issue).  Warp 1 (of the pair's leader) issues tcgen05.mma kind::f16
+// into one of two fp32 accumulators in tensor memory, warps 4-11 round the
 // other one to bf16 and store it.  tn's reduction ends at a group's last row,
 // which need not end a slot: warp 3 zeroes the rows behind it, up to the next
 // multiple of the MMA's 16, in both operands (the next group's rows may hold
@@ -40,26 +46,29 @@
 namespace dgk {
 namespace {
 
-constexpr int BK = 64;          // reduction depth per slot (128 bytes)
-constexpr int BF_THREADS = 256;
+constexpr int BF_EPI = 8;       // epilogue warps
+constexpr int BF_THREADS = 128 + 32 * BF_EPI;
 constexpr int BF_BAND = 8;      // column blocks (rows of D) per raster band
-constexpr int BF_MAX_STAGES = 12;
+constexpr int BF_MAX_STAGES = 10;
 constexpr int kBfMaxSmem = 232448;
+constexpr int kBfMaxCluster = 8;
 
 struct BfParams {
   int G;
   int rows;        // rows of A over all groups
   int M;           // tn: rows of each D[e]
   int N;           // columns of D
-  int nk;          // nt, nn: 64-deep slots of the reduction
+  int K;           // nt, nn: the reduction
   int lanes;       // columns of D per tile (pair: 256)
   int nl;          // lane blocks: ceil(N / lanes)
-  int nc;          // tn: column blocks of each group: ceil(M / BC)
+  int bc;          // rows of D per tile (pair: 256)
+  int nc;          // tn: column blocks of each group: ceil(M / bc)
+  int split;       // CTAs (pairs) of a cluster that share a tile's reduction
   int stages;
   int p_bytes;     // bytes of a slot's lane operand (per CTA)
   int q_bytes;     // bytes of a slot's column operand (per CTA)
-  int p_split;     // lane operand loaded in 64-wide boxes (N not a multiple of 64)
-  int q_split;     // column operand (tn) loaded in 64-wide boxes (M not a multiple of 64)
+  int p_pieces;    // loads of a slot's lane operand; 0: a single load takes all its pieces
+  int q_pieces;    // (see `operand` below)
   const int32_t* sizes;
   uint16_t* D;
   const uint16_t* C;
@@ -79,19 +88,23 @@ struct BfSmem {
   __host__ __device__ static constexpr int fixed(int G) { return 1024 + TAB + 2 * (G + 1) * 4; }
 };
 
+// Reduction depth of a slot.
+__host__ __device__ constexpr int bf_bk(bool pair) { return pair ? 64 : 128; }
+
 struct BfTile {
-  int g;       // group
-  int l0;      // first column of D
-  int cols;    // rows of D in this tile
-  int q0;      // first row of the column operand (nt, nn: row of A; tn: m)
-  int k0;      // tn: first row of the group
-  int kn;      // reduction length (nt, nn: all of K, in whole slots)
-  int nk;      // slots
+  int g;          // group
+  int l0;         // first column of D
+  int cols;       // rows of D in this tile
+  int q0;         // first row of the column operand (nt, nn: row of A; tn: m)
+  int k0;         // tn: first row of the group
+  int kn;         // reduction length
+  int nk;         // slots of it
+  int kbeg, kend; // this CTA's (pair's) slots
 };
 
-template <int BC, int FORM>
+template <int BK, int FORM>
 __device__ __forceinline__ BfTile bf_tile(int t, const BfParams& p, const int* first,
-                                          const int* blk) {
+                                          const int* blk, int krank) {
   BfTile T;
   int nc;
   if (FORM == kBfTN) {
@@ -117,29 +130,45 @@ __device__ __forceinline__ BfTile bf_tile(int t, const BfParams& p, const int* f
   const int r = t - band * BF_BAND * p.nl;
   const int h = min(BF_BAND, nc - band * BF_BAND);
   T.l0 = (r / h) * p.lanes;
-  const int c0 = (band * BF_BAND + r % h) * BC;
+  const int c0 = (band * BF_BAND + r % h) * p.bc;
   const int n = first[T.g + 1] - first[T.g];
   if (FORM == kBfTN) {
-    T.cols = min(BC, p.M - c0);
+    T.cols = min(p.bc, p.M - c0);
     T.q0 = c0;
     T.k0 = first[T.g];
     T.kn = n;
-    T.nk = (n + BK - 1) / BK;
   } else {
-    T.cols = min(BC, n - c0);
+    T.cols = min(p.bc, n - c0);
     T.q0 = first[T.g] + c0;
     T.k0 = 0;
-    T.kn = p.nk * BK;
-    T.nk = p.nk;
+    T.kn = p.K;
   }
+  T.nk = (T.kn + BK - 1) / BK;
+  T.kbeg = static_cast<int>(static_cast<long long>(T.nk) * krank / p.split);
+  T.kend = static_cast<int>(static_cast<long long>(T.nk) * (krank + 1) / p.split);
   return T;
 }
 
+// Four columns of a row of D: the addend in fp32, then one rounding.
+__device__ __forceinline__ void store_four(const BfParams& p, size_t at, float4 v) {
+  if (p.C) {
+    const uint2 c = *reinterpret_cast<const uint2*>(p.C + at);
+    v.x += __uint_as_float(c.x << 16);
+    v.y += __uint_as_float(c.x & 0xFFFF0000u);
+    v.z += __uint_as_float(c.y << 16);
+    v.w += __uint_as_float(c.y & 0xFFFF0000u);
+  }
+  *reinterpret_cast<uint2*>(p.D + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+// BC: capacity of an accumulator in rows of D (`bc` at most).
 template <bool PAIR, int BC, int FORM>
 __global__ void __launch_bounds__(BF_THREADS, 1)
 bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                     const BfParams p) {
   using L = BfSmem;
+  constexpr int BK = bf_bk(PAIR);
+  constexpr bool TN = FORM == kBfTN, P_MN = FORM != kBfNT;
   // columns of one accumulator: two M = 128 halves side by side, or the pair's
   constexpr int ACC = PAIR ? BC : 2 * BC;
   static_assert(2 * ACC <= 512, "two accumulators");
@@ -154,9 +183,12 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
   volatile uint32_t* abort_flag = misc + 1;
   int* first = reinterpret_cast<int*>(smem + ring + L::TAB);
   int* blk = first + p.G + 1;
-  const uint32_t crank = PAIR ? cluster_ctarank() : 0;
-  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
-  constexpr bool TN = FORM == kBfTN, P_MN = FORM != kBfNT;
+  const int cluster = (PAIR ? 2 : 1) * p.split;
+  const uint32_t crank = cluster > 1 ? cluster_ctarank() : 0;
+  const uint32_t side = PAIR ? crank & 1 : 0;    // CTA of the pair
+  const uint32_t leader = crank - side;          // its leader's rank
+  const int krank = static_cast<int>(PAIR ? crank >> 1 : crank);   // share of the reduction
+  const int unit = blockIdx.x / cluster, units = gridDim.x / cluster;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -167,7 +199,7 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(L::T_FULL + b), 1);
-      mbar_init(bar(L::T_EMPTY + b), PAIR ? 8 : 4);
+      mbar_init(bar(L::T_EMPTY + b), (PAIR ? 2 : 1) * BF_EPI);
     }
     mbar_init(bar(L::MMA_DONE), 1);
     misc[1] = 0;
@@ -207,7 +239,7 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
       const int end = static_cast<int>(min(row + x, static_cast<long long>(p.rows)));
       const int prev = __shfl_up_sync(0xffffffffu, end, 1);
       const int mine = end - (lane == 0 ? row : prev);
-      int c = (mine + BC - 1) / BC;
+      int c = (mine + p.bc - 1) / p.bc;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, c, o);
@@ -226,9 +258,9 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // the peer signals this CTA's barriers from here on (their initialisation was
-  // made visible to the cluster by thread 0's fence)
-  if constexpr (PAIR) {
+  // the peers signal this CTA's barriers from here on (their initialisation
+  // was made visible to the cluster by thread 0's fence)
+  if (cluster > 1) {
     cluster_arrive_relaxed();
     cluster_wait();
   }
@@ -239,8 +271,10 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
   auto mma_n = [&](int cols) {
     return PAIR ? (TN ? (cols + 127) & ~127 : (cols + 31) & ~31) : (cols + 15) & ~15;
   };
-  // a tile's last slot needs zeroed rows (tn)
-  auto ragged = [&](const BfTile& T) { return TN && (T.kn & 15) != 0; };
+  // the tile's last slot needs zeroed rows, and is this CTA's
+  auto ragged = [&](const BfTile& T) {
+    return TN && (T.kn & 15) != 0 && T.kend == T.nk && T.kbeg < T.kend;
+  };
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------- TMA producers --
@@ -250,25 +284,27 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
       const bool lanes_op = warp == 0;
       const CUtensorMap* tm = lanes_op ? &tmP : &tmQ;
       const bool mn = lanes_op ? P_MN : TN;
-      const bool split = lanes_op ? p.p_split : p.q_split;
+      const int pieces = lanes_op ? p.p_pieces : p.q_pieces;
       const uint32_t bytes = lanes_op ? p.p_bytes : p.q_bytes;
       const uint32_t base = sbase + (lanes_op ? 0 : q_off);
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0, tails = 0, tail_par = 0;
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BC, FORM>(t, p, first, blk);
-        const int at = lanes_op ? T.l0 + static_cast<int>(crank) * 128
-                                : T.q0 + static_cast<int>(crank) * (mma_n(T.cols) / 2);
+        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank);
+        const int at = lanes_op ? T.l0 + static_cast<int>(side) * 128
+                                : T.q0 + static_cast<int>(side) * (mma_n(T.cols) / 2);
         const int g = (lanes_op && !TN) ? T.g : 0;
         const bool rag = ragged(T);
-        for (int i = 0; i < T.nk; ++i) {
+        for (int n = T.kend - T.kbeg, j = 0; j < n; ++j) {
+          // a ragged last slot is loaded first
+          const int i = !rag ? T.kbeg + j : j == 0 ? T.kend - 1 : T.kbeg + j - 1;
           bool go = wait_bar(bar(L::EMPTY + s), ph ^ 1, abort_flag, p);
           const int k = T.k0 + i * BK;
           if constexpr (kDebug) {
             const int rows = lanes_op ? p.N : (TN ? p.M : p.rows);
             // (a pair's second CTA may start past the tensor: zero-filled)
             if (go && (T.g >= p.G || at < 0 || at >= rows + (PAIR ? 128 : 0) || k < 0 ||
-                       (TN && k >= p.rows))) {
+                       k >= (TN ? p.rows : p.K))) {
               dbg_fail(p, ST_DEBUG_BOUNDS, abort_flag);
               go = false;
             }
@@ -276,24 +312,28 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
           if (go) {
             const uint32_t dst = base + s * bytes;
             // a slot whose rows warp 3 completes arrives on its own CTA's TAIL
-            const bool to_tail = rag && i == T.nk - 1;
+            const bool to_tail = rag && j == 0;
             const uint32_t b = to_tail ? bar(L::TAIL + s)
-                               : PAIR  ? map_cluster(bar(L::FULL + s), 0)
+                               : PAIR  ? map_cluster(bar(L::FULL + s), leader)
                                        : bar(L::FULL + s);
             // the leader expects both CTAs' bytes (a remote arrival of the peer
             // at cluster scope would cost it a microsecond per slot)
-            if (to_tail || crank == 0)
+            if (to_tail || side == 0)
               mbar_arrive_expect_tx(to_tail ? b : bar(L::FULL + s), PAIR && !to_tail ? 2 * bytes : bytes);
             auto load = [&](uint32_t d, int x, int y, int z) {
               if (PAIR && !to_tail) tma_load_4d_pair(map_cluster(d, crank), tm, b, x, y, z, g);
               else tma_load_4d(d, tm, b, x, y, z, g);
             };
-            if (!mn) {
-              load(dst, k, at, 0);
-            } else if (!split) {
-              load(dst, 0, k, at >> 6);
+            // one load where the boxes lie side by side (64-wide pieces of K,
+            // or of the width), else one per piece
+            if (pieces == 0) {
+              if (mn) load(dst, 0, k, at >> 6);
+              else load(dst, 0, at, k >> 6);
             } else {
-              for (uint32_t j = 0; j < bytes / 8192; ++j) load(dst + j * 8192, at + 64 * j, k, 0);
+              for (int j = 0; j < pieces; ++j) {
+                if (mn) load(dst + j * (bytes / pieces), at + 64 * j, k, 0);
+                else load(dst + j * (bytes / pieces), k + 64 * j, at, 0);
+              }
             }
             // (the slot's latest load, for the drain below: on one barrier or
             // the other)
@@ -313,7 +353,7 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
       // (pair: both CTAs' loads count on the leader's barriers; the CTAs leave
       // together)
       for (int q = 0; q < p.stages; ++q) {
-        if (((issued >> q) & 1u) && (!PAIR || crank == 0))
+        if (((issued >> q) & 1u) && side == 0)
           drain_wait(bar(L::FULL + q), (issued_par >> q) & 1u, p);
         if ((tails >> q) & 1u) drain_wait(bar(L::TAIL + q), ((tail_par >> q) & 1u) ^ 1u, p);
       }
@@ -326,52 +366,67 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     // cost the issue more than the instruction takes to run (nt, 32647 rows, N =
     // 4096, K = 7168, the loads switched off: 1092 us; so 830 us, the tensor
     // cores' rate).
-    if (crank == 0) {
+    if (side == 0) {
       const bool issuer = elect_one();
-      // a K step of 16: 32 bytes inside a K-major row, two 8-row atoms (2 KB) of
-      // an MN-major slot, whose 64-wide atoms lie 64 rows x 128 bytes apart
-      constexpr uint64_t P_STEP = (P_MN ? 2048 : 32) >> 4, Q_STEP = (TN ? 2048 : 32) >> 4;
+      // a K step of 16: 32 bytes inside a K-major row, whose 64-wide pieces lie
+      // `half` bytes apart; two 8-row atoms (2 KB) of an MN-major slot, whose
+      // 64-wide atoms of 128 rows lie 16 KB apart
+      constexpr uint32_t ATOM = BK * 128;
+      const uint32_t p_half = P_MN ? 0 : p.p_bytes / 2, q_half = TN ? 0 : p.q_bytes / 2;
       const bool two = !PAIR && p.lanes > 128;
+      // (desc units of 16 bytes) the second 128 lanes
+      constexpr uint32_t P_SECOND = (P_MN ? 2 * ATOM : 16384) >> 4;
+      const uint16_t mask = static_cast<uint16_t>(PAIR ? 0x3u << leader : 0x1u);
       int s = 0, b = 0;
       uint32_t ph = 0, bph = 0;
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BC, FORM>(t, p, first, blk);
-        if (T.nk == 0) continue;
+        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank);
+        if (T.kbeg == T.kend) continue;
         const uint32_t idesc = idesc_bf16_f32(PAIR ? 256 : 128, mma_n(T.cols), P_MN, TN);
         const uint32_t d = tmem + static_cast<uint32_t>(b * ACC);
         bool ok = wait_bar(bar(L::T_EMPTY + b), bph ^ 1, abort_flag, p);
         tc_fence_after();
-        for (int i = 0; i < T.nk; ++i) {
-          // (the peer's warp 3 wrote a ragged slot's zeros itself)
-          const bool zeroed = PAIR && i == T.nk - 1 && ragged(T);
-          ok = (zeroed ? wait_bar<true>(bar(L::FULL + s), ph, abort_flag, p)
-                       : wait_bar(bar(L::FULL + s), ph, abort_flag, p)) && ok;
+        const bool rag = ragged(T);
+        const int n = T.kend - T.kbeg;
+        for (int j = 0; j < n; ++j) {
+          // a ragged last slot comes first, when warp 3 has had the time of the
+          // previous tile for it (8192 rows in 16 groups, 2048 x 7168: 189 us with
+          // it last, 179 so, 166 without any zeroing)
+          const bool tail = rag && j == 0;
+          const int i = !rag ? T.kbeg + j : tail ? T.kend - 1 : T.kbeg + j - 1;
+          // (the peer's warp 3 wrote the zeros of its own half)
+          ok = (PAIR && tail ? wait_bar<true>(bar(L::FULL + s), ph, abort_flag, p)
+                             : wait_bar(bar(L::FULL + s), ph, abort_flag, p)) && ok;
           tc_fence_after();
           if (issuer && ok) {
             const uint32_t ps = sbase + s * p.p_bytes, qs = sbase + q_off + s * p.q_bytes;
-            const uint64_t pd = P_MN ? smem_desc_sw128_mnmajor(ps, 8192) : smem_desc_sw128_kmajor(ps);
-            const uint64_t qd = TN ? smem_desc_sw128_mnmajor(qs, 8192) : smem_desc_sw128_kmajor(qs);
+            const uint64_t pd = P_MN ? smem_desc_sw128_mnmajor(ps, ATOM) : smem_desc_sw128_kmajor(ps);
+            const uint64_t qd = TN ? smem_desc_sw128_mnmajor(qs, ATOM) : smem_desc_sw128_kmajor(qs);
             auto step = [&](int kk, uint32_t acc) {
+              const uint64_t pk = pd + (P_MN ? kk * (2048 >> 4)
+                                             : (kk >> 2) * (p_half >> 4) + (kk & 3) * (32 >> 4));
+              const uint64_t qk = qd + (TN ? kk * (2048 >> 4)
+                                           : (kk >> 2) * (q_half >> 4) + (kk & 3) * (32 >> 4));
               if constexpr (PAIR) {
-                mma_bf16_pair(d, pd + P_STEP * kk, qd + Q_STEP * kk, idesc, acc);
+                mma_bf16_pair(d, pk, qk, idesc, acc);
               } else {
-                mma_bf16(d, pd + P_STEP * kk, qd + Q_STEP * kk, idesc, acc);
-                // the second 128 lanes (the rows past `lanes` are not stored)
-                if (two) mma_bf16(d + BC, pd + (16384 >> 4) + P_STEP * kk, qd + Q_STEP * kk, idesc, acc);
+                mma_bf16(d, pk, qk, idesc, acc);
+                // (the rows past `lanes` are not stored)
+                if (two) mma_bf16(d + BC, pk + P_SECOND, qk, idesc, acc);
               }
             };
             const int left = T.kn - i * BK;
-            if (!TN || left >= BK) {
-              step(0, i > 0);
+            if (left >= BK) {
+              step(0, j > 0);
 #pragma unroll
               for (int kk = 1; kk < BK / 16; ++kk) step(kk, 1);
             } else {
-              for (int kk = 0; 16 * kk < left; ++kk) step(kk, i > 0 || kk > 0);
+              for (int kk = 0; 16 * kk < left; ++kk) step(kk, j > 0 || kk > 0);
             }
-            if constexpr (PAIR) mma_commit_pair_multicast(bar(L::EMPTY + s), 0x3);
+            if constexpr (PAIR) mma_commit_pair_multicast(bar(L::EMPTY + s), mask);
             else mma_commit(bar(L::EMPTY + s));
-            if (i == T.nk - 1) {
-              if constexpr (PAIR) mma_commit_pair_multicast(bar(L::T_FULL + b), 0x3);
+            if (j == n - 1) {
+              if constexpr (PAIR) mma_commit_pair_multicast(bar(L::T_FULL + b), mask);
               else mma_commit(bar(L::T_FULL + b));
             }
           }
@@ -382,7 +437,7 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         if (b == 0) bph ^= 1;
       }
       if (issuer) {
-        if constexpr (PAIR) mma_commit_pair_multicast(bar(L::MMA_DONE), 0x1);
+        if constexpr (PAIR) mma_commit_pair_multicast(bar(L::MMA_DONE), static_cast<uint16_t>(1u << leader));
         else mma_commit(bar(L::MMA_DONE));
         drain_wait(bar(L::MMA_DONE), 0, p);
       }
@@ -394,9 +449,7 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
       int s = 0;
       uint32_t par = 0;
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BC, FORM>(t, p, first, blk);
-        if (T.nk == 0) continue;
-        s = (s + T.nk - 1) % p.stages;
+        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank);
         if (ragged(T)) {
           // all 32 lanes: wait for this CTA's two loads, then zero the rows
           // behind the group's last one, up to the next multiple of 16 (a row
@@ -404,94 +457,189 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
           const bool ok = wait_bar(bar(L::TAIL + s), (par >> s) & 1u, abort_flag, p);
           par ^= 1u << s;
           if (ok) {
-            const int left = T.kn - (T.nk - 1) * BK, r = ((left + 15) & ~15) - left;
-            const int pa = p.p_bytes / 8192, n = r * 8 * (pa + p.q_bytes / 8192);
-            const uint32_t ps = sbase + s * p.p_bytes, qs = sbase + q_off + s * p.q_bytes;
-            for (int u = lane; u < n; u += 32) {
-              const int atom = u / (r * 8), w = u - atom * (r * 8);
-              const uint32_t base = atom < pa ? ps + atom * 8192 : qs + (atom - pa) * 8192;
-              st_shared_v4(base + (left + (w >> 3)) * 128 + (w & 7) * 16, 0, 0, 0, 0);
-            }
+            const int left = T.kn - (T.nk - 1) * BK, end = (left + 15) & ~15;
+            constexpr int ATOM = BK * 128;
+            // a lane takes 16 bytes of every fourth row, in each atom
+            const uint32_t off = (left + (lane >> 3)) * 128 + (lane & 7) * 16;
+            auto zero = [&](uint32_t base, int atoms) {
+              for (int i = 0; i < atoms; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                  if (left + (lane >> 3) + r < end)
+                    st_shared_v4(base + i * ATOM + off + r * 128, 0, 0, 0, 0);
+            };
+            zero(sbase + s * p.p_bytes, p.p_bytes / ATOM);
+            zero(sbase + q_off + s * p.q_bytes, p.q_bytes / ATOM);
           }
           fence_proxy_async_smem();
           __syncwarp();
           // in place of the two producers' arrivals: one per CTA of a pair, or two
           if constexpr (PAIR) {
-            if (lane == 0) mbar_arrive_remote_release(bar(L::FULL + s), 0);
+            if (lane == 0) mbar_arrive_remote_release(bar(L::FULL + s), leader);
           } else {
             if (lane < 2) mbar_arrive(bar(L::FULL + s));
           }
         }
-        s = (s + 1) % p.stages;
+        s = (s + T.kend - T.kbeg) % p.stages;
       }
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ epilogue --
-    const int q = warp & 3;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const int halves = PAIR ? 1 : (p.lanes + 127) / 128;
-    int b = 0;
-    uint32_t bph = 0;
-    for (int t = unit; t < tiles; t += units) {
-      const BfTile T = bf_tile<BC, FORM>(t, p, first, blk);
-      const bool have = T.nk > 0;
-      const bool ok = !have || wait_bar(bar(L::T_FULL + b), bph, abort_flag, p);
-      tc_fence_after();
-      const size_t row0 = TN ? static_cast<size_t>(T.g) * p.M + T.q0 : static_cast<size_t>(T.q0);
-      const int l_end = min(p.N, T.l0 + p.lanes);
-      for (int a = 0; a < halves; ++a) {
-        // this thread's pair of columns of D (lanes l and l ^ 1 share them)
-        const int l = T.l0 + (PAIR ? static_cast<int>(crank) : a) * 128 + q * 32 + (lane & ~1);
-        for (int c = 0; c < T.cols; c += 32) {
-          uint32_t v[32];
-          if (have) {
-            tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
-            tmem_wait_ld(v);
-          } else {
+  }
+
+  // -------------------------------------------------------------- epilogue --
+  const int q = warp & 3, eh = (warp >> 2) - 1;   // lane quarter; which of the warps on it
+  const int halves = PAIR ? 1 : (p.lanes + 127) / 128;
+  // Rows c .. c + 31 of the tile from a lane's 32 values of one column of D:
+  // rounded in pairs of rows, then exchanged with the neighbouring lane, so that
+  // the even lane stores two columns of the even row and the odd one those of
+  // the odd row.  With an addend the exchange is of fp32 values: one rounding,
+  // after the sum.
+  auto store_rows = [&](const BfTile& T, int l, int c, const uint32_t (&v)[32]) {
+    const int odd = lane & 1;
+    const size_t row = (TN ? static_cast<size_t>(T.g) * p.M : 0) + T.q0 + c + odd;
+    // rows this lane may store: those of its parity below the tile's end
+    int n = l < min(p.N, T.l0 + p.lanes) ? min(16, (T.cols - c - odd + 1) >> 1) : 0;
+    if constexpr (kDebug) {
+      const size_t end = TN ? static_cast<size_t>(p.G) * p.M : static_cast<size_t>(p.rows);
+      if (n > 0 && row + 2 * (n - 1) >= end) {
+        raise_status(p, ST_DEBUG_BOUNDS);
+        n = 0;
+      }
+    }
+    const size_t step = 2 * static_cast<size_t>(p.N);
+    uint16_t* d = p.D + row * p.N + l;
+    if (p.C == nullptr) {
+      const uint32_t sel = odd ? 0x3276u : 0x5410u;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0u;
-          }
-          // a lane holds 32 rows of one column of D: exchange with the
-          // neighbouring lane, so that the even lane stores two columns of row
-          // j and the odd one those of row j + 1
+      for (int j = 0; j < 16; ++j, d += step) {
+        const uint32_t w = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        const uint32_t o = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), sel);
+        if (j < n) *reinterpret_cast<uint32_t*>(d) = o;
+      }
+    } else {
+      const uint16_t* cp = p.C + row * p.N + l;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const uint32_t give = (lane & 1) ? v[j] : v[j + 1];
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
-            float lo = __uint_as_float((lane & 1) ? got : v[j]);
-            float hi = __uint_as_float((lane & 1) ? v[j + 1] : got);
-            const int r = c + j + (lane & 1);
-            if (ok && r < T.cols && l < l_end) {
-              const size_t at = (row0 + r) * p.N + l;
-              if constexpr (kDebug) {
-                if (row0 + r >= static_cast<size_t>(TN ? p.G * static_cast<long long>(p.M) : p.rows)) {
-                  raise_status(p, ST_DEBUG_BOUNDS);
-                  continue;
-                }
-              }
-              if (p.C) {
-                // the addend in fp32, then one rounding
-                const uint32_t cw = *reinterpret_cast<const uint32_t*>(p.C + at);
-                lo += __uint_as_float(cw << 16);
-                hi += __uint_as_float(cw & 0xFFFF0000u);
-              }
-              *reinterpret_cast<uint32_t*>(p.D + at) = pack_bf16x2(lo, hi);
+      for (int j = 0; j < 16; ++j, d += step, cp += step) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * j] : v[2 * j + 1], 1);
+        if (j < n) {
+          const uint32_t cw = *reinterpret_cast<const uint32_t*>(cp);
+          const float lo = __uint_as_float(odd ? got : v[2 * j]) + __uint_as_float(cw << 16);
+          const float hi =
+              __uint_as_float(odd ? v[2 * j + 1] : got) + __uint_as_float(cw & 0xFFFF0000u);
+          *reinterpret_cast<uint32_t*>(d) = pack_bf16x2(lo, hi);
+        }
+      }
+    }
+  };
+  // first column of the thread's pair of columns of D, in half `a` of the lanes
+  auto column = [&](const BfTile& T, int a) {
+    return T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + q * 32 + (lane & ~1);
+  };
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16);
+  if (p.split == 1) {
+    if (warp >= 4) {
+      int b = 0;
+      uint32_t bph = 0;
+      for (int t = unit; t < tiles; t += units) {
+        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, 0);
+        const bool have = T.nk > 0;
+        // (the warp's lanes agree, for the exchange)
+        const bool ok = __all_sync(0xffffffffu,
+                                   !have || wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
+        tc_fence_after();
+        for (int a = 0; a < halves; ++a) {
+          const int l = column(T, a);
+          // two chunks of 32 rows at a time, for one wait on tensor memory
+          for (int c = 32 * eh; c < T.cols; c += 128) {
+            uint32_t v[32], w[32];
+            const bool more = c + 64 < T.cols;
+            if (have) {
+              const uint32_t at = t_lane + static_cast<uint32_t>(b * ACC + a * BC + c);
+              tmem_ld_32x32b_x32(at, v);
+              if (more) tmem_ld_32x32b_x32(at + 64, w);
+              tmem_wait_ld(v);
+              if (more) tmem_wait_ld(w);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = w[j] = 0u;
+            }
+            if (ok) {
+              store_rows(T, l, c, v);
+              if (more) store_rows(T, l, c + 64, w);
             }
           }
         }
-      }
-      if (have) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR && crank != 0) mbar_arrive_remote_relaxed(bar(L::T_EMPTY + b), 0);
-          else mbar_arrive(bar(L::T_EMPTY + b));
+        if (have) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR && side != 0) mbar_arrive_remote_relaxed(bar(L::T_EMPTY + b), leader);
+            else mbar_arrive(bar(L::T_EMPTY + b));
+          }
+          b ^= 1;
+          if (b == 0) bph ^= 1;
         }
-        b ^= 1;
-        if (b == 0) bph ^= 1;
       }
     }
+  } else {
+    // One tile per cluster.  Its MMAs and loads are done once the accumulator
+    // is complete: the ring now holds the partial [half][row][128] in fp32.
+    const bool mine = unit < tiles;
+    BfTile T{};
+    if (mine) T = bf_tile<BK, FORM>(unit, p, first, blk, krank);
+    float* part = reinterpret_cast<float*>(smem);
+    bool ok = true;
+    if (warp >= 4 && mine && T.kbeg < T.kend) {
+      ok = wait_bar(bar(L::T_FULL), 0, abort_flag, p);
+      tc_fence_after();
+      for (int a = 0; a < halves; ++a)
+        for (int c = 32 * eh; c < T.cols; c += 64) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(a * BC + c), v);
+          tmem_wait_ld(v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            part[(a * BC + c + j) * 128 + q * 32 + lane] = __uint_as_float(v[j]);
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 4 && mine && __all_sync(0xffffffffu, ok && *abort_flag == 0)) {
+      // ranks that had slots of the reduction
+      uint32_t has = 0;
+      for (int r = 0; r < p.split; ++r) {
+        const long long nk = T.nk;
+        if (nk * r / p.split < nk * (r + 1) / p.split) has |= 1u << r;
+      }
+      // a warp adds up four rows at a time, a lane four columns of each
+      constexpr int U = 4;
+      for (int a = 0; a < halves; ++a) {
+        const int l = T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + 4 * lane;
+        const int l_end = min(p.N, T.l0 + p.lanes);
+        for (int c = U * (BF_EPI * krank + warp - 4); c < T.cols; c += U * BF_EPI * p.split) {
+          float4 sum[U] = {};
+          const uint32_t at = sbase + ((a * BC + c) * 128 + 4 * lane) * 4;
+          for (int r = 0; r < p.split; ++r) {
+            if (!((has >> r) & 1u)) continue;
+            const uint32_t from = map_cluster(at, PAIR ? 2 * r + side : r);
+            float4 x[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) x[j] = ld_cluster_v4(from + j * 512);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+              sum[j].x += x[j].x; sum[j].y += x[j].y; sum[j].z += x[j].z; sum[j].w += x[j].w;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < U; ++j) {
+            if (c + j >= T.cols || l >= l_end) continue;   // (l_end is a multiple of 8)
+            store_four(p, ((TN ? static_cast<size_t>(T.g) * p.M : 0) + T.q0 + c + j) * p.N + l,
+                       sum[j]);
+          }
+        }
+      }
+    }
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -501,29 +649,68 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     if constexpr (PAIR) tmem_dealloc_pair(tmem, 2 * ACC);
     else tmem_dealloc(tmem, 2 * ACC);
   }
-  // no CTA leaves while its peer may still signal it or read its operands
-  if constexpr (PAIR) cluster_sync_relaxed();
+  // no CTA leaves while a peer may still signal it or read its shared memory
+  if (cluster > 1) {
+    __syncwarp();
+    cluster_sync_relaxed();
+  }
+}
+
+// How a call is tiled.
+struct BfPlan {
+  bool pair;
+  int lanes, bc, split;
+};
+
+BfPlan bf_plan(const BfCall& c, int num_sms) {
+  const bool tn = c.form == kBfTN;
+  // rows of D that a group has: the average (nt, nn), M (tn)
+  const long long per = tn ? c.M : (c.rows + c.G - 1) / c.G;
+  const long long groups = tn ? c.G : std::min(c.G, c.rows);
+  const long long depth = tn ? c.rows / c.G : c.K;
+  // CTAs (pairs) per tile: as many as leave every cluster an SM set, each with
+  // four slots at least
+  auto split_of = [&](long long tiles, int width) {
+    const long long room = num_sms / (width * std::max(1ll, tiles));
+    return static_cast<int>(std::max(
+        1ll, std::min({room, depth / 512, static_cast<long long>(kBfMaxCluster / width)})));
+  };
+  // (a limit on the SMs may leave a single one: no pair fits)
+  if (per > 128 && num_sms >= 2) {
+    const long long tiles = groups * ((per + 255) / 256) * ((c.N + 255) / 256);
+    return {true, 256, 256, split_of(tiles, 2)};
+  }
+  // lanes such that the tiles fill the SMs once, in whole MMA boxes: 64 where
+  // the lane operand is MN-major, else 16
+  const int bc = per > 64 ? 128 : 64, step = c.form == kBfNT ? 16 : 64;
+  const long long cols = groups * ((per + bc - 1) / bc);
+  const long long blocks = std::max(1ll, num_sms / cols);   // lane blocks per column block
+  const long long want = ((c.N + blocks - 1) / blocks + step - 1) / step * step;
+  const int lanes = static_cast<int>(std::min(256ll, std::max(64ll, want)));
+  return {false, lanes, bc, split_of(cols * ((c.N + lanes - 1) / lanes), 1)};
 }
 
 template <bool PAIR, int BC, int FORM>
-cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode, int lanes,
-                         int num_sms, cudaStream_t stream) {
+cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode,
+                         const BfPlan& plan, int num_sms, cudaStream_t stream) {
   constexpr bool tn = FORM == kBfTN;
+  const int lanes = plan.lanes, bc = plan.bc, split = plan.split;
+  constexpr int BK = bf_bk(PAIR);
   BfParams p{};
   p.G = c.G;
   p.rows = c.rows;
   p.M = c.M;
   p.N = c.N;
-  p.nk = tn ? 0 : (c.K + BK - 1) / BK;
+  p.K = c.K;
   p.lanes = lanes;
   p.nl = (c.N + lanes - 1) / lanes;
-  p.nc = tn ? (c.M + BC - 1) / BC : 0;
-  const int p_rows = PAIR ? 128 : lanes, q_rows = PAIR ? BC / 2 : BC;
-  p.p_bytes = (p_rows * 128 + 1023) / 1024 * 1024;
-  p.q_bytes = q_rows * 128;
+  p.bc = bc;
+  p.nc = tn ? (c.M + bc - 1) / bc : 0;
+  p.split = split;
+  const int p_rows = PAIR ? 128 : lanes, q_rows = PAIR ? bc / 2 : bc;
+  p.p_bytes = p_rows * BK * 2;
+  p.q_bytes = q_rows * BK * 2;
   p.stages = std::min(BF_MAX_STAGES, (kBfMaxSmem - BfSmem::fixed(c.G)) / (p.p_bytes + p.q_bytes));
-  p.p_split = c.N % 64 != 0;
-  p.q_split = c.M % 64 != 0;
   p.sizes = c.sizes;
   p.D = static_cast<uint16_t*>(c.D);
   p.C = static_cast<const uint16_t*>(c.C);
@@ -540,35 +727,37 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  // A K-major operand [z][rows][K] is read in boxes of 64 (K) x rows; an
-  // MN-major one [z][K][width] in boxes of 64 (width) x 64 rows of K, several
-  // side by side in one load where the width is a multiple of 64.
-  auto k_major = [&](CUtensorMap* m, const void* x, uint64_t z, uint64_t rows, uint64_t k,
-                     uint32_t box) {
-    return map(m, x, {k, rows, 1, z}, {2 * k, 2 * k * rows, 2 * k * rows}, {BK, box, 1, 1});
-  };
-  auto mn_major = [&](CUtensorMap* m, const void* x, uint64_t z, uint64_t k, uint64_t width,
-                      uint32_t box) {
-    const uint64_t all = 2 * width * k;
-    if (width % 64 != 0) return map(m, x, {width, k, 1, z}, {2 * width, all, all}, {64, BK, 1, 1});
-    return map(m, x, {64, k, width / 64, z}, {2 * width, 128, all}, {64, BK, box / 64, 1});
+  // A slot of a K-major operand [z][rows][K] is two pieces of 64 (K) x box rows,
+  // one of an MN-major operand [z][K][width] is box / 64 pieces of 64 (width) x
+  // 128 rows of K; a single load takes them all where K (the width) is a multiple
+  // of 64, as the third dimension of the map.
+  auto operand = [&](CUtensorMap* m, int* loads, const void* x, bool mn, uint64_t z, uint64_t rows,
+                     uint64_t k, uint32_t box) {
+    const uint64_t wide = mn ? rows : k, deep = mn ? k : rows, all = 2 * wide * deep;
+    const uint32_t pieces = mn ? box / 64 : BK / 64, height = mn ? BK : box;
+    *loads = wide % 64 == 0 ? 0 : static_cast<int>(pieces);
+    if (*loads == 0)
+      return map(m, x, {64, deep, wide / 64, z}, {2 * wide, 128, all}, {64, height, pieces, 1});
+    return map(m, x, {wide, deep, 1, z}, {2 * wide, all, all}, {64, height, 1, 1});
   };
   CUtensorMap mp, mq;
   // (a reduction without rows loads nothing; its maps still need an extent)
-  const uint64_t G = c.G, N = c.N, K = c.K, R = std::max(c.rows, 1);
+  const uint64_t rows = std::max(c.rows, 1);
   const bool good =
-      (FORM == kBfNT   ? k_major(&mp, c.B, G, N, K, p_rows)
-       : FORM == kBfNN ? mn_major(&mp, c.B, G, K, N, p_rows)
-                         : mn_major(&mp, c.B, 1, R, N, p_rows)) &&
-      (tn ? mn_major(&mq, c.A, 1, R, c.M, q_rows) : k_major(&mq, c.A, 1, R, K, q_rows));
+      (tn ? operand(&mp, &p.p_pieces, c.B, true, 1, c.N, rows, p_rows)
+          : operand(&mp, &p.p_pieces, c.B, FORM == kBfNN, c.G, c.N, c.K, p_rows)) &&
+      (tn ? operand(&mq, &p.q_pieces, c.A, true, 1, c.M, rows, q_rows)
+          : operand(&mq, &p.q_pieces, c.A, false, 1, rows, c.K, q_rows));
   if (!good) return cudaErrorInvalidValue;
 
-  // as many CTAs (pairs) as there can be tiles, at most one per SM
+  // as many CTAs (pairs) as there can be tiles, at most one per SM; with a
+  // split reduction a cluster for each of them
   const long long most = tn ? static_cast<long long>(c.G) * p.nc * p.nl
-                            : (std::min<long long>(c.G, c.rows) + c.rows / BC) * p.nl;
-  const long long fit = PAIR ? num_sms / 2 : num_sms;
+                            : (std::min<long long>(c.G, c.rows) + c.rows / bc) * p.nl;
+  const int cluster = (PAIR ? 2 : 1) * split;
+  const long long units = split > 1 ? most : std::min<long long>(most, num_sms / cluster);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, std::min(most, fit)) * (PAIR ? 2 : 1)), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, units) * cluster), 1, 1);
   cfg.blockDim = dim3(BF_THREADS, 1, 1);
   cfg.dynamicSmemBytes = p.stages * (p.p_bytes + p.q_bytes) + BfSmem::fixed(c.G);
   cfg.stream = stream;
@@ -576,9 +765,9 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 1;
-  if (PAIR) {
+  if (cluster > 1) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
@@ -603,22 +792,10 @@ cudaError_t set_up_form() {
 template <int FORM>
 cudaError_t launch_form(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode, int num_sms,
                         cudaStream_t stream) {
-  constexpr bool tn = FORM == kBfTN;
-  // rows of D that a group has: the average (nt, nn), M (tn)
-  const long long per = tn ? c.M : (c.rows + c.G - 1) / c.G;
-  const long long groups = tn ? c.G : std::min(c.G, c.rows);
-  // (a limit on the SMs may leave a single one: no pair fits)
-  if (per > 128 && num_sms >= 2)
-    return launch_tiles<true, 256, FORM>(c, encode, 256, num_sms, stream);
-  // lanes such that the tiles fill the SMs once, in whole MMA boxes: 64 where
-  // the lane operand is MN-major, else 16
-  const int bc = per > 64 ? 128 : 64, step = FORM == kBfNT ? 16 : 64;
-  const long long cols = groups * ((per + bc - 1) / bc);
-  const long long blocks = std::max(1ll, num_sms / cols);   // lane blocks per column block
-  const long long want = ((c.N + blocks - 1) / blocks + step - 1) / step * step;
-  const int lanes = static_cast<int>(std::min(256ll, std::max(64ll, want)));
-  return bc == 128 ? launch_tiles<false, 128, FORM>(c, encode, lanes, num_sms, stream)
-                   : launch_tiles<false, 64, FORM>(c, encode, lanes, num_sms, stream);
+  const BfPlan f = bf_plan(c, num_sms);
+  return f.pair       ? launch_tiles<true, 256, FORM>(c, encode, f, num_sms, stream)
+         : f.bc <= 64 ? launch_tiles<false, 64, FORM>(c, encode, f, num_sms, stream)
+                      : launch_tiles<false, 128, FORM>(c, encode, f, num_sms, stream);
 }
 
 }  // namespace

@@ -86,7 +86,11 @@ def test_product(form, dims, sizes):
     ("tn", [700, 1, 1300, 0, 520], 1024, 1536), ("tn", [900, 0, 77], 776, 1032),
     ("nt", [6] * 8, 4096, 2048), ("nt", [61], 2112, 7168), ("nn", [3, 0, 1, 9], 2048, 1024),
     ("nt", [1], 7168, 2048), ("nn", [1, 0], 7168, 2048), ("tn", [4097], 264, 520),
-    ("tn", [20000], 128, 256)])
+    ("tn", [20000], 128, 256),
+    # few tiles: the reduction split over a cluster, with uneven and empty shares
+    ("nt", [1], 64, 8192), ("nt", [5, 0], 72, 4168), ("nn", [33], 128, 6000), ("nn", [2], 64, 1160),
+    ("nt", [300], 256, 8192), ("nn", [170, 180], 264, 5000), ("tn", [3000, 0, 20], 64, 128),
+    ("tn", [5001, 7], 256, 264), ("tn", [8000], 520, 40), ("nt", [100], 200, 7176)])
 def test_larger_products(form, sizes, N, K):
     A, B = inputs(form, sizes, N, K, seed=7)
     check(form, A, B, sizes, run(form, A, B, sizes, N), f"{form} {sizes}")
