@@ -67,14 +67,20 @@ struct BfParams {
   int stages;
   int p_bytes;     // bytes of a slot's lane operand (per CTA)
   int q_bytes;     // bytes of a slot's column operand (per CTA)
-  int p_pieces;    // loads of a slot's lane operand; 0: a single load takes all its pieces
-  int q_pieces;    // (see `operand` below)
+  int p_whole;     // extent of the operands' whole 64-wide pieces (see `operand` below)
+  int q_whole;
   const int32_t* sizes;
   uint16_t* D;
   const uint16_t* C;
   unsigned int* status;
   unsigned long long timeout_ns;
   unsigned int debug_flags;
+};
+
+// Tensor maps of the lane and the column operand: [0] takes a slot's 64-wide
+// pieces in one load, [1] one piece.
+struct BfMaps {
+  CUtensorMap p[2], q[2];
 };
 
 // Shared memory behind the ring: barriers, TMEM base and abort flag, then the
@@ -164,8 +170,7 @@ __device__ __forceinline__ void store_four(const BfParams& p, size_t at, float4 
 // BC: capacity of an accumulator in rows of D (`bc` at most).
 template <bool PAIR, int BC, int FORM>
 __global__ void __launch_bounds__(BF_THREADS, 1)
-bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                    const BfParams p) {
+bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
   using L = BfSmem;
   constexpr int BK = bf_bk(PAIR);
   constexpr bool TN = FORM == kBfTN, P_MN = FORM != kBfNT;
@@ -204,8 +209,8 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     mbar_init(bar(L::MMA_DONE), 1);
     misc[1] = 0;
     fence_mbarrier_init();
-    prefetch_tmap(&tmP);
-    prefetch_tmap(&tmQ);
+    prefetch_tmap(&maps.p[0]);
+    prefetch_tmap(&maps.q[0]);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -282,9 +287,10 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     // each per slot (a thread that issues one stalls for ~250 cycles)
     if (lane == 0 && !(p.debug_flags & DBG_SKIP_PRODUCER)) {
       const bool lanes_op = warp == 0;
-      const CUtensorMap* tm = lanes_op ? &tmP : &tmQ;
+      const CUtensorMap* wide = lanes_op ? &maps.p[0] : &maps.q[0];
+      const CUtensorMap* piece = lanes_op ? &maps.p[1] : &maps.q[1];
       const bool mn = lanes_op ? P_MN : TN;
-      const int pieces = lanes_op ? p.p_pieces : p.q_pieces;
+      const int whole = lanes_op ? p.p_whole : p.q_whole;
       const uint32_t bytes = lanes_op ? p.p_bytes : p.q_bytes;
       const uint32_t base = sbase + (lanes_op ? 0 : q_off);
       int s = 0;
@@ -320,19 +326,22 @@ bf16_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             // at cluster scope would cost it a microsecond per slot)
             if (to_tail || side == 0)
               mbar_arrive_expect_tx(to_tail ? b : bar(L::FULL + s), PAIR && !to_tail ? 2 * bytes : bytes);
-            auto load = [&](uint32_t d, int x, int y, int z) {
-              if (PAIR && !to_tail) tma_load_4d_pair(map_cluster(d, crank), tm, b, x, y, z, g);
-              else tma_load_4d(d, tm, b, x, y, z, g);
+            auto load = [&](const CUtensorMap* m, uint32_t d, int x, int y, int z) {
+              if (PAIR && !to_tail) tma_load_4d_pair(map_cluster(d, crank), m, b, x, y, z, g);
+              else tma_load_4d(d, m, b, x, y, z, g);
             };
-            // one load where the boxes lie side by side (64-wide pieces of K,
-            // or of the width), else one per piece
-            if (pieces == 0) {
-              if (mn) load(dst, 0, k, at >> 6);
-              else load(dst, 0, at, k >> 6);
+            // one load where all the slot's 64-wide pieces are whole, else one
+            // per piece (what lies past the tensor's edge is filled with zeros)
+            const int first_x = mn ? at : k;
+            const int pieces = mn ? static_cast<int>(bytes / (BK * 128)) : BK / 64;
+            if (first_x + 64 * pieces <= whole) {
+              if (mn) load(wide, dst, 0, k, at >> 6);
+              else load(wide, dst, 0, at, k >> 6);
             } else {
               for (int j = 0; j < pieces; ++j) {
-                if (mn) load(dst + j * (bytes / pieces), at + 64 * j, k, 0);
-                else load(dst + j * (bytes / pieces), k + 64 * j, at, 0);
+                const uint32_t d = dst + j * (bytes / pieces);
+                if (mn) load(piece, d, at + 64 * j, k, 0);
+                else load(piece, d, k + 64 * j, at, 0);
               }
             }
             // (the slot's latest load, for the drain below: on one barrier or
@@ -727,27 +736,31 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  // A slot of a K-major operand [z][rows][K] is two pieces of 64 (K) x box rows,
-  // one of an MN-major operand [z][K][width] is box / 64 pieces of 64 (width) x
-  // 128 rows of K; a single load takes them all where K (the width) is a multiple
-  // of 64, as the third dimension of the map.
-  auto operand = [&](CUtensorMap* m, int* loads, const void* x, bool mn, uint64_t z, uint64_t rows,
+  // A slot of a K-major operand [z][rows][K] is BK / 64 pieces of 64 (K) x box
+  // rows, one of an MN-major operand [z][K][width] is box / 64 pieces of 64
+  // (width) x BK rows of K.  One load takes them all, with the pieces as the third
+  // dimension of a map of the whole pieces; where the extent is no multiple of
+  // 64, its edge needs the other map, a load per piece.
+  auto operand = [&](CUtensorMap* m, int* whole, const void* x, bool mn, uint64_t z, uint64_t rows,
                      uint64_t k, uint32_t box) {
     const uint64_t wide = mn ? rows : k, deep = mn ? k : rows, all = 2 * wide * deep;
     const uint32_t pieces = mn ? box / 64 : BK / 64, height = mn ? BK : box;
-    *loads = wide % 64 == 0 ? 0 : static_cast<int>(pieces);
-    if (*loads == 0)
-      return map(m, x, {64, deep, wide / 64, z}, {2 * wide, 128, all}, {64, height, pieces, 1});
-    return map(m, x, {wide, deep, 1, z}, {2 * wide, all, all}, {64, height, 1, 1});
+    *whole = static_cast<int>(wide / 64 * 64);
+    if (!map(m + 1, x, {wide, deep, 1, z}, {2 * wide, all, all}, {64, height, 1, 1})) return false;
+    if (*whole == 0) {
+      m[0] = m[1];   // (never used)
+      return true;
+    }
+    return map(m, x, {64, deep, wide / 64, z}, {2 * wide, 128, all}, {64, height, pieces, 1});
   };
-  CUtensorMap mp, mq;
+  BfMaps maps;
   // (a reduction without rows loads nothing; its maps still need an extent)
   const uint64_t rows = std::max(c.rows, 1);
   const bool good =
-      (tn ? operand(&mp, &p.p_pieces, c.B, true, 1, c.N, rows, p_rows)
-          : operand(&mp, &p.p_pieces, c.B, FORM == kBfNN, c.G, c.N, c.K, p_rows)) &&
-      (tn ? operand(&mq, &p.q_pieces, c.A, true, 1, c.M, rows, q_rows)
-          : operand(&mq, &p.q_pieces, c.A, false, 1, rows, c.K, q_rows));
+      (tn ? operand(maps.p, &p.p_whole, c.B, true, 1, c.N, rows, p_rows)
+          : operand(maps.p, &p.p_whole, c.B, FORM == kBfNN, c.G, c.N, c.K, p_rows)) &&
+      (tn ? operand(maps.q, &p.q_whole, c.A, true, 1, c.M, rows, q_rows)
+          : operand(maps.q, &p.q_whole, c.A, false, 1, rows, c.K, q_rows));
   if (!good) return cudaErrorInvalidValue;
 
   // as many CTAs (pairs) as there can be tiles, at most one per SM; with a
@@ -773,7 +786,7 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
     cfg.numAttrs = 2;
   }
   cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, bf16_grouped_kernel<PAIR, BC, FORM>, mp, mq, p);
+  return cudaLaunchKernelEx(&cfg, bf16_grouped_kernel<PAIR, BC, FORM>, maps, p);
 }
 
 template <int FORM>
