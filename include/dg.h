@@ -470,6 +470,14 @@ dg_status dg_debug_force_pair(int mode);
  * variable DG_FORCE_BLOCK_SCALED=0|1 sets the same before the first call. */
 dg_status dg_debug_force_block_scaled(int mode);
 
+/* Test and benchmark hook: force the tiles of the following ragged bf16
+ * products: CTA pairs (pair != 0: lanes = rows = 256, split 1, 2 or 4) or single
+ * CTAs (lanes: columns of D per tile, 64..256; rows: rows of D per tile, 16..128;
+ * both multiples of 16, of 64 where the form's operand is read in 64-wide boxes,
+ * else the calls return DG_ERR_UNSUPPORTED_SHAPE; split: CTAs sharing a tile's
+ * reduction, 1..8).  lanes = 0 leaves the choice to the library. */
+dg_status dg_debug_force_ragged_plan(int pair, int lanes, int rows, int split);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,7 +29,7 @@ __all__ = [
     "rms_norm_backward", "rms_norm_backward_workspace_bytes", "swiglu_quantize_fp8_1x128",
     "swiglu_quantize_fp8_1x128_ue8m0", "swiglu_backward_fp8_1x128",
     "m_grouped_gemm_bf16_nt_ragged", "m_grouped_gemm_bf16_nn_ragged",
-    "k_grouped_gemm_bf16_tn_ragged",
+    "k_grouped_gemm_bf16_tn_ragged", "debug_force_ragged_plan",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -67,6 +67,7 @@ EXPORTED_SYMBOLS = [
     "dg_swiglu_quantize_fp8_1x128", "dg_swiglu_quantize_fp8_1x128_ue8m0",
     "dg_swiglu_backward_fp8_1x128", "dg_m_grouped_gemm_bf16_nt_ragged",
     "dg_m_grouped_gemm_bf16_nn_ragged", "dg_k_grouped_gemm_bf16_tn_ragged",
+    "dg_debug_force_ragged_plan",
 ]
 
 
@@ -153,6 +154,7 @@ def lib():
                 _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp]
         L.dg_k_grouped_gemm_bf16_tn_ragged.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
                                                        _vp]
+        L.dg_debug_force_ragged_plan.argtypes = [_i, _i, _i, _i]
         for f in EXPORTED_SYMBOLS:
             if f not in ("dg_last_error_string", "dg_num_output_tiles",
                          "dg_rms_norm_backward_workspace_bytes"):
@@ -427,3 +429,8 @@ def debug_force_pair(mode=-1):
 def debug_force_block_scaled(mode=-1):
     """-1 heuristic, 0 never, 1 only the block-scaled kernels (packed UE8M0 forms)."""
     _check(lib().dg_debug_force_block_scaled(int(mode)))
+
+
+def debug_force_ragged_plan(pair=False, lanes=0, rows=0, split=1):
+    """Force the tiles of the ragged bf16 products (lanes=0: the library's choice)."""
+    _check(lib().dg_debug_force_ragged_plan(1 if pair else 0, int(lanes), int(rows), int(split)))

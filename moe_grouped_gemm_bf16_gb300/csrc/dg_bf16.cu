@@ -37,6 +37,7 @@
 //
 // Every wait is bounded, as in the FP8 kernels.
 #include <algorithm>
+#include <cmath>
 
 #include "dg_bf16.h"
 #include "dg_params.h"
@@ -292,13 +293,22 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       const bool mn = lanes_op ? P_MN : TN;
       const int whole = lanes_op ? p.p_whole : p.q_whole;
       const uint32_t bytes = lanes_op ? p.p_bytes : p.q_bytes;
+      // 64-wide pieces of a slot, and the bytes of those that an MN-major operand
+      // has at column x (what lies wholly past its edge is neither loaded nor
+      // stored)
+      const int pieces = mn ? static_cast<int>(bytes / (BK * 128)) : BK / 64;
+      const int extent = lanes_op ? p.N : p.M;
+      auto there = [&](int x) { return mn ? min(pieces, max(0, (extent - x + 63) >> 6)) : pieces; };
       const uint32_t base = sbase + (lanes_op ? 0 : q_off);
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0, tails = 0, tail_par = 0;
       for (int t = unit; t < tiles; t += units) {
         const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank);
-        const int at = lanes_op ? T.l0 + static_cast<int>(side) * 128
-                                : T.q0 + static_cast<int>(side) * (mma_n(T.cols) / 2);
+        const int half = lanes_op ? 128 : mma_n(T.cols) / 2;   // from one CTA of a pair to the other
+        const int at = (lanes_op ? T.l0 : T.q0) + static_cast<int>(side) * half;
+        const uint32_t piece_bytes = bytes / pieces;
+        const uint32_t mine = there(at) * piece_bytes;
+        const uint32_t both = mine + (PAIR ? there(at + half) * piece_bytes : 0);   // (the leader's)
         const int g = (lanes_op && !TN) ? T.g : 0;
         const bool rag = ragged(T);
         for (int n = T.kend - T.kbeg, j = 0; j < n; ++j) {
@@ -325,21 +335,19 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
             // the leader expects both CTAs' bytes (a remote arrival of the peer
             // at cluster scope would cost it a microsecond per slot)
             if (to_tail || side == 0)
-              mbar_arrive_expect_tx(to_tail ? b : bar(L::FULL + s), PAIR && !to_tail ? 2 * bytes : bytes);
+              mbar_arrive_expect_tx(to_tail ? b : bar(L::FULL + s), to_tail ? mine : both);
             auto load = [&](const CUtensorMap* m, uint32_t d, int x, int y, int z) {
               if (PAIR && !to_tail) tma_load_4d_pair(map_cluster(d, crank), m, b, x, y, z, g);
               else tma_load_4d(d, m, b, x, y, z, g);
             };
             // one load where all the slot's 64-wide pieces are whole, else one
-            // per piece (what lies past the tensor's edge is filled with zeros)
-            const int first_x = mn ? at : k;
-            const int pieces = mn ? static_cast<int>(bytes / (BK * 128)) : BK / 64;
-            if (first_x + 64 * pieces <= whole) {
+            // per piece (a piece's part past the tensor's edge is filled with zeros)
+            if ((mn ? at : k) + 64 * pieces <= whole) {
               if (mn) load(wide, dst, 0, k, at >> 6);
               else load(wide, dst, 0, at, k >> 6);
             } else {
-              for (int j = 0; j < pieces; ++j) {
-                const uint32_t d = dst + j * (bytes / pieces);
+              for (int j = 0; j < there(at); ++j) {
+                const uint32_t d = dst + j * piece_bytes;
                 if (mn) load(piece, d, at + 64 * j, k, 0);
                 else load(piece, d, k + 64 * j, at, 0);
               }
@@ -665,38 +673,67 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
   }
 }
 
-// How a call is tiled.
-struct BfPlan {
-  bool pair;
-  int lanes, bc, split;
-};
+// Estimated time of a plan beyond the launch (us), for the choice between
+// plans only.  The groups' sizes are on the device: one group stands for all, at
+// 1.4 times the average rows (some get none).  Constants fitted to timings of
+// every plan below on 800 shapes drawn over 1 to 64 groups, 1 to 32647 rows and
+// widths of 256 to 8192, all forms: the choice is 3.1% slower than the best plan
+// on average (fixed rules on the group's rows and the tile count: 11%).
+//  * a slot costs a pair 0.33 us (64 deep), the single form (128 deep) 2.7 ns per
+//    lane and 2.3 ns per row of A: what they take to load;
+//  * a tile's epilogue 3.7 ns per row of D and 128 lanes, hidden behind the next
+//    tile but for the last one;
+//  * a split adds 1.9 us (two cluster barriers) and 0.37 ns per partial sum a
+//    thread's CTA reads from the others, and large clusters leave SMs empty;
+//  * memory 8.3 TB/s over what is read and written once (weights in L2 count in).
+double bf_cost(const BfCall& c, const BfPlan& f, int num_sms) {
+  const bool tn = c.form == kBfTN;
+  const double groups = tn ? c.G : std::min(c.G, c.rows), fill = groups > 1 ? 1.4 : 1.0;
+  const double per = tn ? c.M : fill * c.rows / groups;       // rows of D in a group
+  const double depth = tn ? fill * c.rows / c.G : c.K;
+  const int cluster = (f.pair ? 2 : 1) * f.split;
+  const double room = std::max(
+      1.0, std::floor(num_sms * (cluster >= 8 ? 0.4 : cluster >= 4 ? 0.86 : 1.0) / cluster));
+  const double tiles = groups * std::ceil(per / f.bc) * ((c.N + f.lanes - 1) / f.lanes);
+  const double waves = std::max(1.0, std::ceil(tiles / room));
+  const int halves = f.pair ? 1 : (f.lanes + 127) / 128;
+  const double cols = std::min<double>(f.bc, per);
+  const double slots = std::max(1.0, std::ceil(depth / bf_bk(f.pair) / f.split));
+  const double main = slots * (f.pair ? 0.33 : 0.0027 * f.lanes + 0.0023 * f.bc);
+  const double epilogue = 0.0037 * cols * halves;
+  const double run = main + epilogue + (waves - 1) * std::max(main, epilogue);
+  const double N = c.N, K = c.K, M = c.M, T = c.rows;
+  const double memory =
+      2 * (tn ? c.G * M * N + T * (M + N) : groups * N * K + T * (N + K)) / 8.3e6;
+  return std::max(run, memory) + 0.19 * std::min(run, memory) +
+         (f.split > 1 ? 1.9 + 3.7e-4 * 128 * halves * cols * (f.split - 1) / f.split : 0.0);
+}
 
 BfPlan bf_plan(const BfCall& c, int num_sms) {
   const bool tn = c.form == kBfTN;
-  // rows of D that a group has: the average (nt, nn), M (tn)
-  const long long per = tn ? c.M : (c.rows + c.G - 1) / c.G;
-  const long long groups = tn ? c.G : std::min(c.G, c.rows);
-  const long long depth = tn ? c.rows / c.G : c.K;
-  // CTAs (pairs) per tile: as many as leave every cluster an SM set, each with
-  // four slots at least
-  auto split_of = [&](long long tiles, int width) {
-    const long long room = num_sms / (width * std::max(1ll, tiles));
-    return static_cast<int>(std::max(
-        1ll, std::min({room, depth / 512, static_cast<long long>(kBfMaxCluster / width)})));
+  const int per = tn ? c.M : (c.rows + std::min(c.G, c.rows) - 1) / std::max(1, std::min(c.G, c.rows));
+  const int depth = tn ? c.rows / c.G : c.K;
+  BfPlan best{false, 128, 64, 1};
+  double least = 1e300;
+  auto consider = [&](bool pair, int lanes, int bc) {
+    const int width = pair ? 2 : 1;
+    for (int split = 1; split * width <= kBfMaxCluster && (split == 1 || depth >= 128 * split); split *= 2) {
+      if (split * width > num_sms) break;   // (a limit on the SMs may leave fewer)
+      const BfPlan f{pair, lanes, bc, split};
+      const double t = bf_cost(c, f, num_sms);
+      if (t < least) {
+        least = t;
+        best = f;
+      }
+    }
   };
-  // (a limit on the SMs may leave a single one: no pair fits)
-  if (per > 128 && num_sms >= 2) {
-    const long long tiles = groups * ((per + 255) / 256) * ((c.N + 255) / 256);
-    return {true, 256, 256, split_of(tiles, 2)};
+  if (per > 32) consider(true, 256, 256);
+  // rows of D per tile near the average group's (tn: whole 64-wide boxes)
+  for (int bc = tn ? 64 : 16; bc <= 128; bc *= 2) {
+    if (!tn && (per > 4 * bc || (bc > 16 && per < bc / 4))) continue;
+    for (int lanes = 128; lanes <= 256 && lanes - 64 < c.N; lanes += 64) consider(false, lanes, bc);
   }
-  // lanes such that the tiles fill the SMs once, in whole MMA boxes: 64 where
-  // the lane operand is MN-major, else 16
-  const int bc = per > 64 ? 128 : 64, step = c.form == kBfNT ? 16 : 64;
-  const long long cols = groups * ((per + bc - 1) / bc);
-  const long long blocks = std::max(1ll, num_sms / cols);   // lane blocks per column block
-  const long long want = ((c.N + blocks - 1) / blocks + step - 1) / step * step;
-  const int lanes = static_cast<int>(std::min(256ll, std::max(64ll, want)));
-  return {false, lanes, bc, split_of(cols * ((c.N + lanes - 1) / lanes), 1)};
+  return best;
 }
 
 template <bool PAIR, int BC, int FORM>
@@ -805,7 +842,7 @@ cudaError_t set_up_form() {
 template <int FORM>
 cudaError_t launch_form(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode, int num_sms,
                         cudaStream_t stream) {
-  const BfPlan f = bf_plan(c, num_sms);
+  const BfPlan f = c.forced.lanes > 0 ? c.forced : bf_plan(c, num_sms);
   return f.pair       ? launch_tiles<true, 256, FORM>(c, encode, f, num_sms, stream)
          : f.bc <= 64 ? launch_tiles<false, 64, FORM>(c, encode, f, num_sms, stream)
                       : launch_tiles<false, 128, FORM>(c, encode, f, num_sms, stream);

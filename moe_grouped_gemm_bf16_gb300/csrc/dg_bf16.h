@@ -14,6 +14,13 @@ enum BfForm : int { kBfNT = 0, kBfNN = 1, kBfTN = 2 };
 
 constexpr int kBfMaxGroups = 1024;
 
+// How a call is tiled: CTA pairs or single CTAs, columns and rows of D per tile,
+// CTAs (pairs) that share a tile's reduction.
+struct BfPlan {
+  bool pair;
+  int lanes, bc, split;
+};
+
 struct BfCall {
   BfForm form;
   const void* A;
@@ -28,6 +35,7 @@ struct BfCall {
   unsigned int* status;
   unsigned long long timeout_ns;
   unsigned int debug_flags;
+  BfPlan forced;         // lanes > 0: this plan (tests)
 };
 
 // Opts the kernels into their shared memory (once per device).

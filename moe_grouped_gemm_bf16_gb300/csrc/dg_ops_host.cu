@@ -26,6 +26,9 @@ dg_status cuda_fail(cudaError_t e, const char* what) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// dg_debug_force_ragged_plan: pair, lanes, rows, split packed; 0: the heuristic.
+std::atomic<unsigned long long> g_ragged_plan{0};
+
 // Opts an operator's kernels into their shared memory, once per device.
 template <cudaError_t (*SET_UP)()>
 dg_status set_up_once(int device) {
@@ -137,6 +140,14 @@ dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void
   c.status = st.status;
   c.timeout_ns = st.timeout_ns;
   c.debug_flags = st.debug_flags;
+  if (const unsigned long long f = g_ragged_plan.load()) {
+    c.forced = {(f >> 48) != 0, static_cast<int>(f >> 32 & 0xFFFF), static_cast<int>(f >> 16 & 0xFFFF),
+                static_cast<int>(f & 0xFFFF)};
+    // boxes of an MN-major operand are 64 wide (nn, tn: B's; tn: A's)
+    if ((!c.forced.pair && ((form != dgk::kBfNT && c.forced.lanes % 64) || (tn && c.forced.bc % 64))) ||
+        c.forced.split * (c.forced.pair ? 2 : 1) > st.sms)
+      return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "no kernel for the forced plan");
+  }
   const cudaError_t e =
       dgk::launch_bf16_grouped(c, st.encode, st.sms, static_cast<cudaStream_t>(stream));
   if (e == cudaErrorInvalidValue) {
@@ -252,6 +263,23 @@ dg_status dg_k_grouped_gemm_bf16_tn_ragged(const void* A, const void* B, const v
                                            const int32_t* ks, int num_groups, int M, int N,
                                            int K_total, void* stream) {
   return bf16_ragged(dgk::kBfTN, A, B, C, D, ks, K_total, M, N, 0, num_groups, stream);
+}
+
+dg_status dg_debug_force_ragged_plan(int pair, int lanes, int rows, int split) {
+  if (lanes == 0) {
+    g_ragged_plan.store(0);
+    return host_ok();
+  }
+  const bool ok = pair ? lanes == 256 && rows == 256 && (split == 1 || split == 2 || split == 4)
+                       : lanes >= 64 && lanes <= 256 && lanes % 16 == 0 && rows >= 16 && rows <= 128 &&
+                             rows % 16 == 0 && split >= 1 && split <= 8;
+  if (!ok)
+    return host_fail(DG_ERR_INVALID_ARG, "ragged plan pair=%d lanes=%d rows=%d split=%d", pair, lanes,
+                     rows, split);
+  g_ragged_plan.store(static_cast<unsigned long long>(pair ? 1 : 0) << 48 |
+                      static_cast<unsigned long long>(lanes) << 32 |
+                      static_cast<unsigned long long>(rows) << 16 | static_cast<unsigned>(split));
+  return host_ok();
 }
 
 }  // extern "C"

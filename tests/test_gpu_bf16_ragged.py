@@ -20,6 +20,7 @@ def built():
     dg.debug_set_skip_producer(False)
     dg.set_wait_timeout_ns(0)
     dg.set_num_sms(0)
+    dg.debug_force_ragged_plan()
 
 
 def normal(*shape, seed, scale=1.0):
@@ -94,6 +95,34 @@ def test_product(form, dims, sizes):
 def test_larger_products(form, sizes, N, K):
     A, B = inputs(form, sizes, N, K, seed=7)
     check(form, A, B, sizes, run(form, A, B, sizes, N), f"{form} {sizes}")
+
+
+PLANS = [(True, 256, 256, s) for s in (1, 2, 4)] + [
+    (False, l, r, s) for l, r, s in ((64, 16, 1), (64, 64, 8), (112, 48, 1), (128, 64, 3), (128, 128, 1),
+                                     (192, 16, 5), (192, 128, 1), (256, 64, 2), (256, 128, 8))]
+
+
+@pytest.mark.parametrize("plan", PLANS, ids=lambda p: "-".join(map(str, p)))
+@pytest.mark.parametrize("form", ["nt", "nn", "tn"])
+def test_every_tiling(form, plan):
+    """Every kernel form on the same ragged shapes: edges of lanes, rows and
+    reduction, shares of the reduction without a slot, groups without rows."""
+    dg.debug_force_ragged_plan(*plan)
+    try:
+        for sizes, N, K in (([5, 0, 300, 33], 264, 392), ([130, 257, 0], 520, 1032), ([70], 200, 64),
+                            ([17, 16, 1], 328, 2056)):
+            A, B = inputs(form, sizes, N, K, seed=sum(sizes))
+            check(form, A, B, sizes, run(form, A, B, sizes, N), f"{form} {plan} {sizes}")
+        if form == "tn":
+            C = normal(4, 392, 264, seed=51)
+            A, B = inputs(form, [5, 0, 300, 33], 264, 392, seed=52)
+            check(form, A, B, [5, 0, 300, 33], run(form, A, B, [5, 0, 300, 33], 264, C=C),
+                  f"addend {plan}", C=C)
+    except dg.DGError as e:
+        # (a 64-wide box where the forced tile is narrower: refused, not wrong)
+        assert e.status == 2 and not plan[0] and (plan[1] % 64 or (form == "tn" and plan[2] % 64))
+    finally:
+        dg.debug_force_ragged_plan()
 
 
 @pytest.mark.parametrize("form", ["nt", "nn", "tn"])
@@ -228,12 +257,15 @@ def test_two_streams_at_once():
         check("nt", A, B, sizes, D, "two streams")
 
 
+@pytest.mark.parametrize("plan", [(False, 0, 0, 1), (True, 256, 256, 1), (True, 256, 256, 4),
+                                  (False, 128, 64, 4)], ids=lambda p: "-".join(map(str, p)))
 @pytest.mark.parametrize("form", ["nt", "tn"])
-def test_waits_that_run_out_are_reported(form):
+def test_waits_that_run_out_are_reported(form, plan):
     """With the TMA producer switched off and a short limit every wait gives up,
     the call reports it, and the next call is right again."""
     sizes = [40, 24]
     A, B = inputs(form, sizes, 256, 128, seed=43)
+    dg.debug_force_ragged_plan(*plan)
     dg.set_wait_timeout_ns(20_000_000)
     dg.debug_set_skip_producer(True)
     try:
@@ -242,7 +274,10 @@ def test_waits_that_run_out_are_reported(form):
     finally:
         dg.debug_set_skip_producer(False)
         dg.set_wait_timeout_ns(0)
-    check(form, A, B, sizes, run(form, A, B, sizes, 256), f"{form} after a timeout")
+    try:
+        check(form, A, B, sizes, run(form, A, B, sizes, 256), f"{form} after a timeout")
+    finally:
+        dg.debug_force_ragged_plan()
 
 
 def test_offsets_past_32_bits():
@@ -283,7 +318,11 @@ def test_matches_the_checked_build(tmp_path):
         "for form in ('nt', 'nn', 'tn'):\n"
         "    for sizes, N, K in (([5, 0, 3], 136, 72), ([300, 17, 256], 392, 520), ([31] * 40, 128, 64)):\n"
         "        A, B = T.inputs(form, sizes, N, K)\n"
-        "        T.check(form, A, B, sizes, T.run(form, A, B, sizes, N), form)\n"
+        "        for plan in [()] + T.PLANS:\n"
+        "            dg.debug_force_ragged_plan(*plan)\n"
+        "            try: D = T.run(form, A, B, sizes, N)\n"
+        "            except dg.DGError as e: assert e.status == 2, e; continue\n"
+        "            T.check(form, A, B, sizes, D, form)\n"
         "assert dg.lib()._name.endswith('libdg_debug.so')\nprint('checked ok')\n")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     out = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, DG_DEBUG="1"),

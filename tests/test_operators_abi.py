@@ -131,3 +131,14 @@ GRAD = dict(A=P, B=P, C=P, D=P, ks=P, num_groups=4, M=64, N=128, K_total=256)
     (dict(M=0), OK)])
 def test_ragged_gradient_refusals(kw, code):
     assert status(dg.k_grouped_gemm_bf16_tn_ragged, {**GRAD, **kw}) == code
+
+
+@pytest.mark.parametrize("plan,code", [
+    ((True, 256, 256, 1), OK), ((True, 128, 256, 1), INVALID), ((True, 256, 256, 8), INVALID),
+    ((False, 32, 64, 1), INVALID), ((False, 264, 64, 1), INVALID), ((False, 128, 136, 1), INVALID),
+    ((False, 128, 64, 9), INVALID), ((False, 128, 64, 0), INVALID), ((False, 0, 0, 0), OK)])
+def test_forced_plan_refusals(plan, code):
+    try:
+        assert status(lambda: dg.debug_force_ragged_plan(*plan), {}) == code
+    finally:
+        dg.debug_force_ragged_plan()
