@@ -171,6 +171,11 @@ def _ptr(x):
     return int(x.data_ptr())
 
 
+def _ptrs(*xs):
+    """_ptr of each argument, without a call for each."""
+    return [x if x is None or x.__class__ is int else x.data_ptr() for x in xs]
+
+
 def _stream(s):
     if s is None:
         torch = sys.modules.get("torch")   # (a process that never imported it has no torch stream)
@@ -304,14 +309,14 @@ def rms_norm_quantize_fp8_1x128(X, R, W, H, Y, Q, sa, rstd, M, K, ld_sa, eps, st
     Q, sa (e4m3, fp32 [K/128, ld_sa]) its output, rstd fp32 [M]; R, H, rstd and
     one of Y and Q may be None."""
     _check(lib().dg_rms_norm_quantize_fp8_1x128(
-        _ptr(X), _ptr(R), _ptr(W), _ptr(H), _ptr(Y), _ptr(Q), _ptr(sa), _ptr(rstd), M, K, ld_sa,
+        *_ptrs(X, R, W, H, Y, Q, sa, rstd), M, K, ld_sa,
         eps, _stream(stream)))
 
 
 def rms_norm_quantize_fp8_1x128_ue8m0(X, R, W, H, Y, Q, sfa, rstd, M, K, ld_sfa, eps, stream=None):
     """The RMS norm with packed UE8M0 scales sfa int32 [ceil(K/512), ld_sfa]."""
     _check(lib().dg_rms_norm_quantize_fp8_1x128_ue8m0(
-        _ptr(X), _ptr(R), _ptr(W), _ptr(H), _ptr(Y), _ptr(Q), _ptr(sfa), _ptr(rstd), M, K, ld_sfa,
+        *_ptrs(X, R, W, H, Y, Q, sfa, rstd), M, K, ld_sfa,
         eps, _stream(stream)))
 
 
@@ -324,7 +329,7 @@ def rms_norm_backward(dY, H, rstd, W, dR, dX, dW, workspace, workspace_bytes, M,
     """Gradient of the RMS norm: dX bf16 [M,K] (plus dR, the residual stream's
     gradient, or None; dX may be dR) and dW fp32 [K]."""
     _check(lib().dg_rms_norm_backward(
-        _ptr(dY), _ptr(H), _ptr(rstd), _ptr(W), _ptr(dR), _ptr(dX), _ptr(dW), _ptr(workspace),
+        *_ptrs(dY, H, rstd, W, dR, dX, dW, workspace),
         workspace_bytes, M, K, _stream(stream)))
 
 
@@ -335,7 +340,7 @@ def swiglu_quantize_fp8_1x128(GU, Y, Q, sa, CQ, csa, num_groups, M, I, ld_sa, ma
     GU ([G,M,2I], fp32 [G,2I/128,ld_sa]), each or None; masked_m int32 [G] on the
     device limits the rows."""
     _check(lib().dg_swiglu_quantize_fp8_1x128(
-        _ptr(GU), _ptr(Y), _ptr(Q), _ptr(sa), _ptr(CQ), _ptr(csa), _ptr(masked_m), num_groups, M,
+        *_ptrs(GU, Y, Q, sa, CQ, csa, masked_m), num_groups, M,
         I, ld_sa, _stream(stream)))
 
 
@@ -344,7 +349,7 @@ def swiglu_quantize_fp8_1x128_ue8m0(GU, Y, Q, sfa, CQ, csa, num_groups, M, I, ld
     """The gated activation with packed UE8M0 scales sfa int32 [G,ceil(I/512),ld_sfa]
     of Q (the checkpoint's scales stay fp32)."""
     _check(lib().dg_swiglu_quantize_fp8_1x128_ue8m0(
-        _ptr(GU), _ptr(Y), _ptr(Q), _ptr(sfa), _ptr(CQ), _ptr(csa), _ptr(masked_m), num_groups, M,
+        *_ptrs(GU, Y, Q, sfa, CQ, csa, masked_m), num_groups, M,
         I, ld_sfa, _stream(stream)))
 
 
@@ -353,28 +358,28 @@ def swiglu_backward_fp8_1x128(CQ, csa, dY, dGU, Y, num_groups, M, I, ld_csa, mas
     """Gradient dGU bf16 [G,M,2I] of the gated activation from its checkpoint, and
     the activation Y bf16 [G,M,I] again (or None)."""
     _check(lib().dg_swiglu_backward_fp8_1x128(
-        _ptr(CQ), _ptr(csa), _ptr(dY), _ptr(dGU), _ptr(Y), _ptr(masked_m), num_groups, M, I,
+        *_ptrs(CQ, csa, dY, dGU, Y, masked_m), num_groups, M, I,
         ld_csa, _stream(stream)))
 
 
 def m_grouped_gemm_bf16_nt_ragged(A, B, D, ms, M_total, N, K, num_groups, stream=None):
     """D[t] = A[t] B[g]^T for the rows t of group g: bf16 A [M_total,K], B [G,N,K],
     D [M_total,N]; ms int32 [G] on the device, any sizes."""
-    _check(lib().dg_m_grouped_gemm_bf16_nt_ragged(_ptr(A), _ptr(B), _ptr(D), _ptr(ms), M_total, N,
+    _check(lib().dg_m_grouped_gemm_bf16_nt_ragged(*_ptrs(A, B, D, ms), M_total, N,
                                                   K, num_groups, _stream(stream)))
 
 
 def m_grouped_gemm_bf16_nn_ragged(A, B, D, ms, M_total, N, K, num_groups, stream=None):
     """D[t] = A[t] B[g] for the rows t of group g: bf16 A [M_total,K], B [G,K,N],
     D [M_total,N]; ms int32 [G] on the device, any sizes."""
-    _check(lib().dg_m_grouped_gemm_bf16_nn_ragged(_ptr(A), _ptr(B), _ptr(D), _ptr(ms), M_total, N,
+    _check(lib().dg_m_grouped_gemm_bf16_nn_ragged(*_ptrs(A, B, D, ms), M_total, N,
                                                   K, num_groups, _stream(stream)))
 
 
 def k_grouped_gemm_bf16_tn_ragged(A, B, D, ks, num_groups, M, N, K_total, C=None, stream=None):
     """D[g] = C[g] + A_g^T B_g over each group's rows: bf16 A [K_total,M], B
     [K_total,N], D (and C) [G,M,N]; ks int32 [G] on the device, any sizes."""
-    _check(lib().dg_k_grouped_gemm_bf16_tn_ragged(_ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(ks),
+    _check(lib().dg_k_grouped_gemm_bf16_tn_ragged(*_ptrs(A, B, C, D, ks),
                                                   num_groups, M, N, K_total, _stream(stream)))
 
 
