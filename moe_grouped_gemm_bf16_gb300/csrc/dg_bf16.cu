@@ -17,23 +17,28 @@
 //  * PAIR: a persistent CTA pair per 256 x 256 tile (cta_group::2: each CTA
 //    holds 128 lanes of B and half of A's rows), for groups of many rows;
 //  * single: one persistent CTA per tile of up to 256 lanes x 128 rows, for
-//    groups of few rows, where the time is that of reading the weights: the
-//    host picks the lanes so that the tiles fill the SMs once (all of them
-//    stream at HBM's rate and end together).
+//    groups of few rows, where the time is that of reading the weights.
 // Where there are too few tiles for the SMs, either splits the reduction over
 // the CTAs (pairs) of a cluster, one tile per cluster: each leaves its fp32
 // partial in shared memory, and each then adds up a share of the rows in the
-// order of the ranks.
+// order of the ranks.  The host estimates each tiling's time and takes the
+// least (bf_cost).
 //
 // Warps 0 and 2 load by TMA (B's tile and A's) into a ring of slots, BK deep in
-// the reduction: 64 for the pair (six slots of 32 KB a CTA, whose latency-bound
-// cases want many in flight), 128 for the single form (half the loads to
-// issue).  Warp 1 (of the pair's leader) issues tcgen05.mma kind::f16
-// into one of two fp32 accumulators in tensor memory, warps 4-11 round the
-// other one to bf16 and store it.  tn's reduction ends at a group's last row,
-// which need not end a slot: warp 3 zeroes the rows behind it, up to the next
-// multiple of the MMA's 16, in both operands (the next group's rows may hold
-// anything).
+// the reduction: 64 for the pair (six or seven slots of 32 KB a CTA: with three
+// of 64 KB the memory-bound nn case took 168 us, so 156), 128 for the single form
+// (half the loads to issue).  Warp 1 (of the pair's leader) issues tcgen05.mma
+// kind::f16 into one of two fp32 accumulators in tensor memory, warps 4-11
+// round the other one to bf16 and store it.  tn's reduction ends at a group's
+// last row, which need not end a slot: warp 3 zeroes the rows behind it, up to
+// the next multiple of the MMA's 16, in both operands (the next group's rows
+// may hold anything).
+//
+// Measured: nt 32647 rows in 4 groups, 4096 x 7168: 1135-1170 us (1640-1690
+// TFLOP/s under the power cap, 1.43 GHz; the tensor pipe 94% active), tn 16391
+// rows 2048 x 7168: 257 us alone, 294 us in a loop; nn 5003 rows in 29 of 32
+// groups: 156 us (6.0 TB/s); nt 61 rows on 6 of 8 groups, 4096 x 7168: 58 us (6.1
+// TB/s).
 //
 // Every wait is bounded, as in the FP8 kernels.
 #include <algorithm>
@@ -621,16 +626,20 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     }
     __syncwarp();
     cluster_sync();
-    if (warp >= 4 && mine && __all_sync(0xffffffffu, ok && *abort_flag == 0)) {
-      // ranks that had slots of the reduction
+    if (warp >= 4 && mine) {
+      // ranks that had slots of the reduction; nothing is stored where one of
+      // them gave up a wait
       uint32_t has = 0;
       for (int r = 0; r < p.split; ++r) {
         const long long nk = T.nk;
         if (nk * r / p.split < nk * (r + 1) / p.split) has |= 1u << r;
+        const uint32_t flag = map_cluster(smem_u32(misc + 1), PAIR ? 2 * r + side : r);
+        ok = ok && ld_cluster_u32(flag) == 0;
       }
+      ok = __all_sync(0xffffffffu, ok);
       // a warp adds up four rows at a time, a lane four columns of each
       constexpr int U = 4;
-      for (int a = 0; a < halves; ++a) {
+      for (int a = 0; ok && a < halves; ++a) {
         const int l = T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + 4 * lane;
         const int l_end = min(p.N, T.l0 + p.lanes);
         for (int c = U * (BF_EPI * krank + warp - 4); c < T.cols; c += U * BF_EPI * p.split) {
