@@ -176,13 +176,21 @@ def _ptrs(*xs):
     return [x if x is None or x.__class__ is int else x.data_ptr() for x in xs]
 
 
+#: (current device, current raw stream of a device) once torch has started CUDA
+_torch_stream = None
+
+
 def _stream(s):
+    global _torch_stream
     if s is None:
-        torch = sys.modules.get("torch")   # (a process that never imported it has no torch stream)
-        if torch is not None and torch.cuda.is_initialized():
-            # the raw handle of torch's current stream (0.2 us; a Stream object costs 3 us)
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        return None
+        if _torch_stream is None:
+            torch = sys.modules.get("torch")   # (a process that never imported it has no torch stream)
+            if torch is None or not torch.cuda.is_initialized():
+                return None
+            # (raw handles take 0.2 us; a Stream object costs 3 us)
+            _torch_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        device, stream = _torch_stream
+        return stream(device())
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)
