@@ -70,6 +70,7 @@ struct BfParams {
   int bc;          // rows of D per tile (pair: 256)
   int nc;          // tn: column blocks of each group: ceil(M / bc)
   int split;       // CTAs (pairs) of a cluster that share a tile's reduction
+  unsigned long long inv_nl, inv_band, inv_per;   // Divisor of nl, BF_BAND nl, nc nl (tn)
   int stages;
   int p_bytes;     // bytes of a slot's lane operand (per CTA)
   int q_bytes;     // bytes of a slot's column operand (per CTA)
@@ -114,35 +115,46 @@ struct BfTile {
   int kbeg, kend; // this CTA's (pair's) slots
 };
 
+// x / d for any 32-bit x with inv = floor(2^64 / d) + 1 (d > 1), 0 for d = 1
+// (Lemire, Kaser and Kurz, "Faster remainder by direct computation", 2019).  The
+// roles decode a tile each, on their critical path: with five integer divisions
+// and a binary search that took 1000 to 1450 cycles a tile.
+__host__ __device__ constexpr unsigned long long bf_inverse(unsigned d) {
+  return d <= 1 ? 0 : ~0ull / d + 1;
+}
+__device__ __forceinline__ int bf_div(int x, unsigned long long inv) {
+  return inv == 0 ? x : static_cast<int>(__umul64hi(static_cast<unsigned>(x), inv));
+}
+
+// Tile t; `from`: a group at or before the tile's (a role's tiles come in
+// rising order), replaced by the tile's.  (350 to 500 cycles so.)
 template <int BK, int FORM>
 __device__ __forceinline__ BfTile bf_tile(int t, const BfParams& p, const int* first,
-                                          const int* blk, int krank) {
+                                          const int* blk, int krank, int& from) {
   BfTile T;
   int nc;
   if (FORM == kBfTN) {
-    const int per = p.nc * p.nl;
-    T.g = t / per;
-    t -= T.g * per;
+    T.g = bf_div(t, p.inv_per);
+    t -= T.g * (p.nc * p.nl);
     nc = p.nc;
   } else {
-    // largest g with blk[g] * nl <= t
-    int lo = 0, hi = p.G - 1;
-    const int b = t / p.nl;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (blk[mid] <= b) lo = mid; else hi = mid - 1;
-    }
-    T.g = lo;
-    t -= blk[lo] * p.nl;
-    nc = blk[lo + 1] - blk[lo];
+    // largest g with blk[g] <= b
+    const int b = bf_div(t, p.inv_nl);
+    while (blk[from + 1] <= b) ++from;
+    T.g = from;
+    t -= blk[from] * p.nl;
+    nc = blk[from + 1] - blk[from];
   }
   // bands of BF_BAND column blocks; within a band first along the column
   // blocks, then along the lanes, so that concurrent tiles share operands in L2
-  const int band = t / (BF_BAND * p.nl);
-  const int r = t - band * BF_BAND * p.nl;
+  const int band = bf_div(t, p.inv_band);
+  const int r = t - band * (BF_BAND * p.nl);
   const int h = min(BF_BAND, nc - band * BF_BAND);
-  T.l0 = (r / h) * p.lanes;
-  const int c0 = (band * BF_BAND + r % h) * p.bc;
+  // r / h with h <= 8: exact below 2^20 (r + 0.5 is half a unit or more from any
+  // multiple of h, the product off by less than 2^-22 of itself)
+  const int q = static_cast<int>((static_cast<float>(r) + 0.5f) * __frcp_rn(static_cast<float>(h)));
+  T.l0 = q * p.lanes;
+  const int c0 = (band * BF_BAND + r - q * h) * p.bc;
   const int n = first[T.g + 1] - first[T.g];
   if (FORM == kBfTN) {
     T.cols = min(p.bc, p.M - c0);
@@ -156,8 +168,12 @@ __device__ __forceinline__ BfTile bf_tile(int t, const BfParams& p, const int* f
     T.kn = p.K;
   }
   T.nk = (T.kn + BK - 1) / BK;
-  T.kbeg = static_cast<int>(static_cast<long long>(T.nk) * krank / p.split);
-  T.kend = static_cast<int>(static_cast<long long>(T.nk) * (krank + 1) / p.split);
+  T.kbeg = 0;
+  T.kend = T.nk;
+  if (p.split > 1) {
+    T.kbeg = static_cast<int>(static_cast<long long>(T.nk) * krank / p.split);
+    T.kend = static_cast<int>(static_cast<long long>(T.nk) * (krank + 1) / p.split);
+  }
   return T;
 }
 
@@ -282,6 +298,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
   auto mma_n = [&](int cols) {
     return PAIR ? (TN ? (cols + 127) & ~127 : (cols + 31) & ~31) : (cols + 15) & ~15;
   };
+  int group = 0;   // this thread's place in the groups (bf_tile)
   // the tile's last slot needs zeroed rows, and is this CTA's
   auto ragged = [&](const BfTile& T) {
     return TN && (T.kn & 15) != 0 && T.kend == T.nk && T.kbeg < T.kend;
@@ -308,7 +325,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0, tails = 0, tail_par = 0;
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank);
+        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank, group);
         const int half = lanes_op ? 128 : mma_n(T.cols) / 2;   // from one CTA of a pair to the other
         const int at = (lanes_op ? T.l0 : T.q0) + static_cast<int>(side) * half;
         const uint32_t piece_bytes = bytes / pieces;
@@ -402,7 +419,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       int s = 0, b = 0;
       uint32_t ph = 0, bph = 0;
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank);
+        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank, group);
         if (T.kbeg == T.kend) continue;
         const uint32_t idesc = idesc_bf16_f32(PAIR ? 256 : 128, mma_n(T.cols), P_MN, TN);
         const uint32_t d = tmem + static_cast<uint32_t>(b * ACC);
@@ -471,7 +488,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       int s = 0;
       uint32_t par = 0;
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank);
+        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank, group);
         if (ragged(T)) {
           // all 32 lanes: wait for this CTA's two loads, then zero the rows
           // behind the group's last one, up to the next multiple of 16 (a row
@@ -531,12 +548,21 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     const size_t step = 2 * static_cast<size_t>(p.N);
     uint16_t* d = p.D + row * p.N + l;
     if (p.C == nullptr) {
+      // all exchanges first: between predicated stores they would run one by one
       const uint32_t sel = odd ? 0x3276u : 0x5410u;
+      uint32_t o[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j, d += step) {
-        const uint32_t w = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-        const uint32_t o = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), sel);
-        if (j < n) *reinterpret_cast<uint32_t*>(d) = o;
+      for (int j = 0; j < 16; ++j)
+        o[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] = __byte_perm(o[j], __shfl_xor_sync(0xffffffffu, o[j], 1), sel);
+      if (n == 16) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j, d += step) *reinterpret_cast<uint32_t*>(d) = o[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j, d += step)
+          if (j < n) *reinterpret_cast<uint32_t*>(d) = o[j];
       }
     } else {
       const uint16_t* cp = p.C + row * p.N + l;
@@ -563,11 +589,24 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       int b = 0;
       uint32_t bph = 0;
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, 0);
-        const bool have = T.nk > 0;
+        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, 0, group);
+        const int l_end = min(p.N, T.l0 + p.lanes);
+        if (T.nk == 0) {
+          // tn, a group without rows: its block of D is C, or zero
+          const int l0 = T.l0 + static_cast<int>(side) * 128;
+          const int per = PAIR ? 16 : p.lanes >> 3;   // 8 columns each
+          for (int u = static_cast<int>(threadIdx.x) - 128; u < per * T.cols; u += 32 * BF_EPI) {
+            const int r = u / per, l = l0 + 8 * (u - r * per);
+            if (l >= l_end) continue;
+            const size_t at = (static_cast<size_t>(T.g) * p.M + T.q0 + r) * p.N + l;
+            *reinterpret_cast<uint4*>(p.D + at) =
+                p.C ? *reinterpret_cast<const uint4*>(p.C + at) : make_uint4(0, 0, 0, 0);
+          }
+          continue;
+        }
         // (the warp's lanes agree, for the exchange)
-        const bool ok = __all_sync(0xffffffffu,
-                                   !have || wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
+        const bool ok =
+            __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
         tc_fence_after();
         for (int a = 0; a < halves; ++a) {
           const int l = column(T, a);
@@ -575,32 +614,25 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
           for (int c = 32 * eh; c < T.cols; c += 128) {
             uint32_t v[32], w[32];
             const bool more = c + 64 < T.cols;
-            if (have) {
-              const uint32_t at = t_lane + static_cast<uint32_t>(b * ACC + a * BC + c);
-              tmem_ld_32x32b_x32(at, v);
-              if (more) tmem_ld_32x32b_x32(at + 64, w);
-              tmem_wait_ld(v);
-              if (more) tmem_wait_ld(w);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = w[j] = 0u;
-            }
+            const uint32_t at = t_lane + static_cast<uint32_t>(b * ACC + a * BC + c);
+            tmem_ld_32x32b_x32(at, v);
+            if (more) tmem_ld_32x32b_x32(at + 64, w);
+            tmem_wait_ld(v);
+            if (more) tmem_wait_ld(w);
             if (ok) {
               store_rows(T, l, c, v);
               if (more) store_rows(T, l, c + 64, w);
             }
           }
         }
-        if (have) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (PAIR && side != 0) mbar_arrive_remote_relaxed(bar(L::T_EMPTY + b), leader);
-            else mbar_arrive(bar(L::T_EMPTY + b));
-          }
-          b ^= 1;
-          if (b == 0) bph ^= 1;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR && side != 0) mbar_arrive_remote_relaxed(bar(L::T_EMPTY + b), leader);
+          else mbar_arrive(bar(L::T_EMPTY + b));
         }
+        b ^= 1;
+        if (b == 0) bph ^= 1;
       }
     }
   } else {
@@ -608,7 +640,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     // is complete: the ring now holds the partial [half][row][128] in fp32.
     const bool mine = unit < tiles;
     BfTile T{};
-    if (mine) T = bf_tile<BK, FORM>(unit, p, first, blk, krank);
+    if (mine) T = bf_tile<BK, FORM>(unit, p, first, blk, krank, group);
     float* part = reinterpret_cast<float*>(smem);
     bool ok = true;
     if (warp >= 4 && mine && T.kbeg < T.kend) {
@@ -762,6 +794,9 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
   p.bc = bc;
   p.nc = tn ? (c.M + bc - 1) / bc : 0;
   p.split = split;
+  p.inv_nl = bf_inverse(p.nl);
+  p.inv_band = bf_inverse(BF_BAND * p.nl);
+  p.inv_per = tn ? bf_inverse(p.nc * p.nl) : 0;
   const int p_rows = PAIR ? 128 : lanes, q_rows = PAIR ? bc / 2 : bc;
   p.p_bytes = p_rows * BK * 2;
   p.q_bytes = q_rows * BK * 2;

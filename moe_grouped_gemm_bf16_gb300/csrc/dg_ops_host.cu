@@ -110,7 +110,7 @@ dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void
   if (N < 8 || N % 8 != 0 || (!tn && (K < 8 || K % 8 != 0)) || (tn && M % 8 != 0))
     return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "N=%d, %s=%d: need positive multiples of 8", N,
                 tn ? "M" : "K", tn ? M : K);
-  if ((long long)N * K >= (1ll << 34) || (long long)N * M >= (1ll << 34) ||
+  if (N >= (1 << 23) || (long long)N * K >= (1ll << 34) || (long long)N * M >= (1ll << 34) ||
       ((long long)rows / 16 + G) * (N / 64 + 1) >= (1ll << 31) ||
       (long long)G * (M / 16 + 1) * (N / 64 + 1) >= (1ll << 31) ||
       (long long)rows * std::max(std::max(N, K), M) >= (1ll << 38))
