@@ -1,7 +1,7 @@
 // Entry points of the operators around the FP8 GEMMs (include/dg.h): the
 // root-mean-square norm, the gated activation with its 8-bit checkpoint and the
 // ragged bf16 products.  Validation on the host, then one launch (the norm's
-// gradient: two); errors as in dg_host.cu.
+// gradient of many rows: two); errors as in dg_host.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
