@@ -37,6 +37,8 @@ LIB_PATH = os.path.join(HERE, "libdg.so")
 #: the checked build (bounds and ring-fill checks in every kernel), loaded in
 #: place of libdg.so when the environment sets DG_DEBUG=1
 LIB_DEBUG_PATH = os.path.join(HERE, "libdg_debug.so")
+#: CPython module through which the operators around the GEMMs are called
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 
 STATUS_NAMES = {
     0: "DG_OK", 1: "DG_ERR_INVALID_ARG", 2: "DG_ERR_UNSUPPORTED_SHAPE", 3: "DG_ERR_MISALIGNED",
@@ -85,18 +87,20 @@ class DGConfig(ctypes.Structure):
 
 
 _LIB = None
+_calls = None   # the CPython module _binding, opened with the library (csrc/dg_ops_binding.cpp)
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 
 
 def lib():
     """The loaded library.  Raises if it has not been built (no fallback)."""
-    global _LIB
+    global _LIB, _calls
     if _LIB is None:
         path = LIB_DEBUG_PATH if os.environ.get("DG_DEBUG", "0") not in ("", "0") else LIB_PATH
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with "
-                               "`python -m moe_grouped_gemm_bf16_gb300._build`")
+        for built in (path, BINDING_PATH):
+            if not os.path.exists(built):
+                raise RuntimeError(f"{built} is missing: build it with "
+                                   "`python -m moe_grouped_gemm_bf16_gb300._build`")
         L = ctypes.CDLL(path)
         L.dg_gemm_fp8_fp8_bf16_nt.argtypes = [_vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp]
         L.dg_gemm_fp8_fp8_bf16_nt_add_c.argtypes = [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i,
@@ -159,8 +163,18 @@ def lib():
             if f not in ("dg_last_error_string", "dg_num_output_tiles",
                          "dg_rms_norm_backward_workspace_bytes"):
                 getattr(L, f).restype = _i
-        _LIB = L
+        from . import _binding
+        _binding.open(path)
+        _LIB, _calls = L, _binding
     return _LIB
+
+
+def _ops():
+    """The entry points of the operators around the GEMMs, with _ptr done on
+    their arguments."""
+    if _calls is None:
+        lib()
+    return _calls
 
 
 def _ptr(x):
@@ -169,11 +183,6 @@ def _ptr(x):
     if isinstance(x, int):
         return x
     return int(x.data_ptr())
-
-
-def _ptrs(*xs):
-    """_ptr of each argument, without a call for each."""
-    return [x if x is None or x.__class__ is int else x.data_ptr() for x in xs]
 
 
 #: (current device, current raw stream of a device) once torch has started CUDA
@@ -316,16 +325,14 @@ def rms_norm_quantize_fp8_1x128(X, R, W, H, Y, Q, sa, rstd, M, K, ld_sa, eps, st
     """RMS norm of bf16 X + R [M,K] with weight W: H = X + R (bf16), Y (bf16) and
     Q, sa (e4m3, fp32 [K/128, ld_sa]) its output, rstd fp32 [M]; R, H, rstd and
     one of Y and Q may be None."""
-    _check(lib().dg_rms_norm_quantize_fp8_1x128(
-        *_ptrs(X, R, W, H, Y, Q, sa, rstd), M, K, ld_sa,
-        eps, _stream(stream)))
+    _check(_ops().rms_norm_quantize_fp8_1x128(
+        X, R, W, H, Y, Q, sa, rstd, M, K, ld_sa, eps, _stream(stream)))
 
 
 def rms_norm_quantize_fp8_1x128_ue8m0(X, R, W, H, Y, Q, sfa, rstd, M, K, ld_sfa, eps, stream=None):
     """The RMS norm with packed UE8M0 scales sfa int32 [ceil(K/512), ld_sfa]."""
-    _check(lib().dg_rms_norm_quantize_fp8_1x128_ue8m0(
-        *_ptrs(X, R, W, H, Y, Q, sfa, rstd), M, K, ld_sfa,
-        eps, _stream(stream)))
+    _check(_ops().rms_norm_quantize_fp8_1x128_ue8m0(
+        X, R, W, H, Y, Q, sfa, rstd, M, K, ld_sfa, eps, _stream(stream)))
 
 
 def rms_norm_backward_workspace_bytes(M, K):
@@ -336,9 +343,8 @@ def rms_norm_backward_workspace_bytes(M, K):
 def rms_norm_backward(dY, H, rstd, W, dR, dX, dW, workspace, workspace_bytes, M, K, stream=None):
     """Gradient of the RMS norm: dX bf16 [M,K] (plus dR, the residual stream's
     gradient, or None; dX may be dR) and dW fp32 [K]."""
-    _check(lib().dg_rms_norm_backward(
-        *_ptrs(dY, H, rstd, W, dR, dX, dW, workspace),
-        workspace_bytes, M, K, _stream(stream)))
+    _check(_ops().rms_norm_backward(
+        dY, H, rstd, W, dR, dX, dW, workspace, workspace_bytes, M, K, _stream(stream)))
 
 
 def swiglu_quantize_fp8_1x128(GU, Y, Q, sa, CQ, csa, num_groups, M, I, ld_sa, masked_m=None,
@@ -347,48 +353,45 @@ def swiglu_quantize_fp8_1x128(GU, Y, Q, sa, CQ, csa, num_groups, M, I, ld_sa, ma
     (bf16), Q, sa (e4m3, fp32 [G,I/128,ld_sa]) and the 8-bit checkpoint CQ, csa of
     GU ([G,M,2I], fp32 [G,2I/128,ld_sa]), each or None; masked_m int32 [G] on the
     device limits the rows."""
-    _check(lib().dg_swiglu_quantize_fp8_1x128(
-        *_ptrs(GU, Y, Q, sa, CQ, csa, masked_m), num_groups, M,
-        I, ld_sa, _stream(stream)))
+    _check(_ops().swiglu_quantize_fp8_1x128(
+        GU, Y, Q, sa, CQ, csa, masked_m, num_groups, M, I, ld_sa, _stream(stream)))
 
 
 def swiglu_quantize_fp8_1x128_ue8m0(GU, Y, Q, sfa, CQ, csa, num_groups, M, I, ld_sfa,
                                     masked_m=None, stream=None):
     """The gated activation with packed UE8M0 scales sfa int32 [G,ceil(I/512),ld_sfa]
     of Q (the checkpoint's scales stay fp32)."""
-    _check(lib().dg_swiglu_quantize_fp8_1x128_ue8m0(
-        *_ptrs(GU, Y, Q, sfa, CQ, csa, masked_m), num_groups, M,
-        I, ld_sfa, _stream(stream)))
+    _check(_ops().swiglu_quantize_fp8_1x128_ue8m0(
+        GU, Y, Q, sfa, CQ, csa, masked_m, num_groups, M, I, ld_sfa, _stream(stream)))
 
 
 def swiglu_backward_fp8_1x128(CQ, csa, dY, dGU, Y, num_groups, M, I, ld_csa, masked_m=None,
                               stream=None):
     """Gradient dGU bf16 [G,M,2I] of the gated activation from its checkpoint, and
     the activation Y bf16 [G,M,I] again (or None)."""
-    _check(lib().dg_swiglu_backward_fp8_1x128(
-        *_ptrs(CQ, csa, dY, dGU, Y, masked_m), num_groups, M, I,
-        ld_csa, _stream(stream)))
+    _check(_ops().swiglu_backward_fp8_1x128(
+        CQ, csa, dY, dGU, Y, masked_m, num_groups, M, I, ld_csa, _stream(stream)))
 
 
 def m_grouped_gemm_bf16_nt_ragged(A, B, D, ms, M_total, N, K, num_groups, stream=None):
     """D[t] = A[t] B[g]^T for the rows t of group g: bf16 A [M_total,K], B [G,N,K],
     D [M_total,N]; ms int32 [G] on the device, any sizes."""
-    _check(lib().dg_m_grouped_gemm_bf16_nt_ragged(*_ptrs(A, B, D, ms), M_total, N,
-                                                  K, num_groups, _stream(stream)))
+    _check(_ops().m_grouped_gemm_bf16_nt_ragged(
+        A, B, D, ms, M_total, N, K, num_groups, _stream(stream)))
 
 
 def m_grouped_gemm_bf16_nn_ragged(A, B, D, ms, M_total, N, K, num_groups, stream=None):
     """D[t] = A[t] B[g] for the rows t of group g: bf16 A [M_total,K], B [G,K,N],
     D [M_total,N]; ms int32 [G] on the device, any sizes."""
-    _check(lib().dg_m_grouped_gemm_bf16_nn_ragged(*_ptrs(A, B, D, ms), M_total, N,
-                                                  K, num_groups, _stream(stream)))
+    _check(_ops().m_grouped_gemm_bf16_nn_ragged(
+        A, B, D, ms, M_total, N, K, num_groups, _stream(stream)))
 
 
 def k_grouped_gemm_bf16_tn_ragged(A, B, D, ks, num_groups, M, N, K_total, C=None, stream=None):
     """D[g] = C[g] + A_g^T B_g over each group's rows: bf16 A [K_total,M], B
     [K_total,N], D (and C) [G,M,N]; ks int32 [G] on the device, any sizes."""
-    _check(lib().dg_k_grouped_gemm_bf16_tn_ragged(*_ptrs(A, B, C, D, ks),
-                                                  num_groups, M, N, K_total, _stream(stream)))
+    _check(_ops().k_grouped_gemm_bf16_tn_ragged(
+        A, B, C, D, ks, num_groups, M, N, K_total, _stream(stream)))
 
 
 def get_num_sms():

@@ -1,5 +1,6 @@
 """Builds the C-ABI library `libdg.so` (the CUDA kernels and their host
-launcher) for sm_103a with nvcc, in the package directory.
+launcher) for sm_103a with nvcc, and the CPython module `_binding.so` that calls
+some of its entry points, in the package directory.
 
 `python -m moe_grouped_gemm_bf16_gb300._build` or `build()`.  The translation
 units compile in parallel; the result links the CUDA runtime statically so the
@@ -9,6 +10,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdg.so")
 LIB_DEBUG = os.path.join(HERE, "libdg_debug.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 SOURCES = ["dg_host.cu", "dg_inst_dense.cu", "dg_inst_contiguous.cu", "dg_inst_masked.cu", "dg_inst_mn.cu", "dg_inst_ue8m0.cu", "dg_inst_ue8m0_mn.cu", "dg_inst_bs.cu",
            "dg_inst_bs_mn.cu", "dg_quant.cu", "dg_norm.cu", "dg_swiglu.cu", "dg_bf16.cu",
@@ -36,12 +39,28 @@ def _deps():
     return max(os.path.getmtime(f) for f in files)
 
 
+def _build_binding(force):
+    """The CPython module (host code only; it opens the library at run time)."""
+    src = os.path.join(CSRC, "dg_ops_binding.cpp")
+    deps = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "dg.h")))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= deps:
+        return
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-Wall", "-fPIC", "-shared", "-I",
+           INCLUDE, "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force=False, verbose=False, debug=False):
-    """Compile the library.  debug=True builds the checked library
+    """Compile the library and the CPython module.  debug=True builds the checked library
     libdg_debug.so instead (every kernel compiled with -DDG_DEBUG=1: bounds
     checks before each TMA load and plain global store, fill checks after
     each ring wait, failures reported in the device status word)."""
     lib = LIB_DEBUG if debug else LIB
+    _build_binding(force)
     if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps():
         return lib
     bdir = os.path.join(BUILD, "debug") if debug else BUILD

@@ -142,3 +142,43 @@ def test_forced_plan_refusals(plan, code):
         assert status(lambda: dg.debug_force_ragged_plan(*plan), {}) == code
     finally:
         dg.debug_force_ragged_plan()
+
+
+class Tensor:
+    def __init__(self, address):
+        self.address = address
+
+    def data_ptr(self):
+        if isinstance(self.address, Exception):
+            raise self.address
+        return self.address
+
+
+@pytest.mark.parametrize("kw,error", [
+    (dict(X=1.5), AttributeError), (dict(X=Tensor(1.5)), TypeError),
+    (dict(X=Tensor(KeyError("x"))), KeyError), (dict(X=1 << 70), OverflowError),
+    (dict(M=2.0), TypeError), (dict(M=None), TypeError), (dict(M=1 << 31), OverflowError),
+    (dict(M=-(1 << 31) - 1), OverflowError), (dict(K=1 << 70), OverflowError),
+    (dict(eps="small"), TypeError), (dict(rstd="x"), AttributeError)])
+def test_arguments_of_other_types(kw, error):
+    with pytest.raises(error):
+        dg.rms_norm_quantize_fp8_1x128(**{**NORM, "sa": P, "ld_sa": 8, **kw})
+
+
+def test_arguments_reach_the_entry_points():
+    # tensors, addresses, None; whole numbers of other types; a stream's address
+    class Eight:
+        def __index__(self):
+            return 8
+    kw = {**NORM, "sa": Tensor(P), "ld_sa": Eight(), "X": Tensor(P), "M": Eight(), "eps": 1}
+    assert status(dg.rms_norm_quantize_fp8_1x128, {**kw, "W": Tensor(0)}) == INVALID
+    assert status(dg.rms_norm_quantize_fp8_1x128, {**kw, "W": Tensor(P + 8)}) == MISALIGNED
+    assert status(dg.rms_norm_quantize_fp8_1x128, {**kw, "M": 0, "stream": P}) == OK
+
+
+@pytest.mark.parametrize("given", [0, 12, 14])
+def test_number_of_arguments(given):
+    from moe_grouped_gemm_bf16_gb300 import _binding
+    dg.lib()
+    with pytest.raises(TypeError, match="takes 13 arguments"):
+        _binding.rms_norm_quantize_fp8_1x128(*[0] * given)
