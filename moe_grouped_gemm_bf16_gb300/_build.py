@@ -22,7 +22,7 @@ LIB_DEBUG = os.path.join(HERE, "libdg_debug.so")
 BINDING = os.path.join(HERE, "_binding.so")
 
 SOURCES = ["dg_host.cu", "dg_inst_dense.cu", "dg_inst_contiguous.cu", "dg_inst_masked.cu", "dg_inst_mn.cu", "dg_inst_ue8m0.cu", "dg_inst_ue8m0_mn.cu", "dg_inst_bs.cu",
-           "dg_inst_bs_mn.cu", "dg_quant.cu", "dg_norm.cu", "dg_swiglu.cu", "dg_bf16.cu",
+           "dg_inst_bs_mn.cu", "dg_quant.cu", "dg_norm.cu", "dg_swiglu.cu", "dg_bf16.cu", "dg_bf16_few.cu",
            "dg_ops_host.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -40,7 +40,8 @@
 // groups: 156 us (6.0 TB/s); nt 61 rows on 6 of 8 groups, 4096 x 7168: 58 us (6.1
 // TB/s).
 //
-// Every wait is bounded, as in the FP8 kernels.
+// Every wait is bounded, as in the FP8 kernels.  Calls of a few rows in all take
+// dg_bf16_few.cu instead.
 #include <algorithm>
 #include <cmath>
 

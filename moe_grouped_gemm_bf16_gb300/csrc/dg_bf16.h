@@ -45,4 +45,9 @@ cudaError_t bf16_set_up();
 cudaError_t launch_bf16_grouped(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode,
                                 int num_sms, cudaStream_t stream);
 
+// The form for a few rows in all (dg_bf16_few.cu): whether it takes the call, and
+// its launch.
+bool bf16_few_rows(const BfCall& c);
+cudaError_t launch_bf16_few(const BfCall& c, int num_sms, cudaStream_t stream);
+
 }  // namespace dgk

@@ -148,8 +148,15 @@ dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void
         c.forced.split * (c.forced.pair ? 2 : 1) > st.sms)
       return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "no kernel for the forced plan");
   }
-  const cudaError_t e =
-      dgk::launch_bf16_grouped(c, st.encode, st.sms, static_cast<cudaStream_t>(stream));
+  cudaError_t e = cudaSuccess;
+  int all_sms = 0;
+  // (a grid of many small blocks: not under a limit on the SMs)
+  if (dgk::bf16_few_rows(c) &&
+      cudaDeviceGetAttribute(&all_sms, cudaDevAttrMultiProcessorCount, st.device) == cudaSuccess &&
+      st.sms >= all_sms)
+    e = dgk::launch_bf16_few(c, st.sms, static_cast<cudaStream_t>(stream));
+  else
+    e = dgk::launch_bf16_grouped(c, st.encode, st.sms, static_cast<cudaStream_t>(stream));
   if (e == cudaErrorInvalidValue) {
     cudaGetLastError();
     return host_fail(DG_ERR_CUDA, "ragged bf16 product: tensor map or launch rejected");
