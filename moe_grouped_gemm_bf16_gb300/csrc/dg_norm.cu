@@ -20,7 +20,8 @@
 //    shared memory (the gradient: each keeps its share of the weight's in
 //    registers, and a second kernel adds the shares).
 // Measured: 4096 x 7168 forward 45 us (5.9 TB/s; one block per row 47 us),
-// 8192 x 7168 backward 77 us (6.1 TB/s; the one-launch form 171 us).
+// 8192 x 7168 backward 77 us (6.1 TB/s; the one-launch form 171 us), without dR
+// 61 us (5.8 TB/s), 8192 x 4224 40 us.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -318,6 +319,11 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
   load_weight<VPT>(a.W, nv, w);
   __syncthreads();
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  // With one vector a thread keeps what it has read of a row for the output; with
+  // two (which 64 registers do not hold) it reads the slot again, which then is
+  // free a row later.
+  constexpr bool KEEP = VPT == 1;
+  const int ahead = (KEEP ? stages : stages - 1) * step;
   Pairs dw[VPT] = {};
   int s = 0, par = 0;
   uint32_t ph = 0;
@@ -333,18 +339,25 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
     for (int i = 0; i < VPT; ++i) {
       const int v = i * T + threadIdx.x;
       const bool on = v < nv && ok;
-      r[i] = on && a.dR ? x[2 * nv + v] : zero;
+      if (KEEP) r[i] = on && a.dR ? x[2 * nv + v] : zero;
       dot += grad_sums(on ? x[v] : zero, on ? x[nv + v] : zero, w[i], rs, g[i], xh[i], dw[i]);
     }
     const float mean = block_sum(dot, red[par]) * (1.0f / static_cast<float>(a.K));
-    // (as in the forward kernel)
+    // every thread has read the slot (two vectors: the one before) for the last
+    // time; after a failed wait nothing more is loaded or stored
     const bool go = *abort_flag == 0;
-    if (threadIdx.x == 0 && go && m + static_cast<long long>(stages) * step < a.M)
-      ring.fill(static_cast<int>(m) + stages * step, s);
+    if (threadIdx.x == 0 && go && (KEEP || m != blockIdx.x) && m + ahead < a.M)
+      ring.fill(static_cast<int>(m) + ahead, KEEP ? s : (s == 0 ? stages : s) - 1);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * T + threadIdx.x;
-      if (v < nv && go) static_cast<uint4*>(a.dX)[base + v] = grad_row(g[i], xh[i], rs, mean, r[i]);
+      if (v >= nv || !go) continue;
+      if (!KEEP) {
+        Pairs unused = {};
+        grad_sums(x[v], x[nv + v], w[i], rs, g[i], xh[i], unused);
+        r[i] = a.dR ? x[2 * nv + v] : zero;
+      }
+      static_cast<uint4*>(a.dX)[base + v] = grad_row(g[i], xh[i], rs, mean, r[i]);
     }
     if (++s == stages) { s = 0; ph ^= 1; }
   }
@@ -391,7 +404,8 @@ RingShape ring_shape(int M, int K, int ops, int vpt, int num_sms, int max_blocks
   r.threads = row_threads(K, vpt);
   const int slot = 2 * K * ops;
   const int per_sm = std::max(1, std::min(1024 / r.threads, ring_bytes(1) / (3 * slot)));
-  r.stages = std::max(1, std::min(kMaxRing, ring_bytes(per_sm) / slot));
+  // (two slots of the longest rows fit; the gradient's two-vector form needs them)
+  r.stages = std::max(2, std::min(kMaxRing, ring_bytes(per_sm) / slot));
   r.blocks = std::min(std::min(M, per_sm * num_sms), max_blocks);
   r.smem = r.stages * slot;
   return r;
@@ -454,9 +468,19 @@ cudaError_t launch_rms_norm_backward(const NormBwd& a, int num_sms, cudaStream_t
     return vpt == 1 ? launch_dependent(rms_norm_backward_kernel<1>, grid, threads, stream, smem, a)
                     : launch_dependent(rms_norm_backward_kernel<2>, grid, threads, stream, smem, a);
   }
-  const RingShape r = ring_shape(a.M, a.K, a.dR ? 3 : 2, vpt, num_sms, kNormBwdBlocks);
-  const cudaError_t e = vpt == 1 ? launch_ring(rms_norm_backward_ring_kernel<1>, r, stream, a)
-                                 : launch_ring(rms_norm_backward_ring_kernel<2>, r, stream, a);
+  // Two vectors a thread also where that makes two blocks per SM, each with three
+  // slots, of rows that otherwise take one alone, whose barriers then leave the SM
+  // idle (8192 rows: K = 4224 57 to 40 us, 7168 without dR 71 to 61; with dR, two
+  // slots each, 77 to 78); not worth a longer start for a few rows (614 rows, K =
+  // 5120: 8.7 to 10.7, 1254 rows 16.4 to 15.5).
+  const int ops = a.dR ? 3 : 2;
+  const bool split = a.K > 4096 && a.K <= 8192 && a.M > 6 * num_sms &&
+                     ring_bytes(2) >= 3 * 2 * a.K * ops;
+  const int per_thread = split ? 2 : vpt;
+  const RingShape r = ring_shape(a.M, a.K, ops, per_thread, num_sms, kNormBwdBlocks);
+  const cudaError_t e = per_thread == 1
+                            ? launch_ring(rms_norm_backward_ring_kernel<1>, r, stream, a)
+                            : launch_ring(rms_norm_backward_ring_kernel<2>, r, stream, a);
   if (e != cudaSuccess) return e;
   return launch_dependent(rms_norm_weight_grad_kernel, dim3(a.K / 32), 1024, stream, 0,
                           static_cast<const float*>(a.part), a.dW, r.blocks, a.K);

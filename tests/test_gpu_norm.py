@@ -210,6 +210,28 @@ def test_norm_gradient_in_place_and_few_sms():
     check_backward(dY, H, rstd, W, keep, dX, dW, "in place")
 
 
+@pytest.mark.parametrize("shape,sms", [((1000, 4224), 0), ((930, 6400), 0), ((950, 8192), 0),
+                                       ((100, 5120), 3), ((31, 8064), 1), ((20, 16384), 3),
+                                       ((23, 12416), 1)],
+                         ids=lambda s: "x".join(map(str, s)) if isinstance(s, tuple) else f"{s}sms")
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_gradient_of_long_rows(shape, sms, residual):
+    """Rows that take two vectors a thread, many rows per block (every slot of
+    the ring several times), dX in place of dR."""
+    M, K = shape
+    H, W = normal(M, K, seed=M, scale=2.0), normal(K, seed=K, scale=0.5)
+    dY = normal(M, K, seed=M + 1, scale=0.03)
+    dR = normal(M, K, seed=M + 2, scale=0.03) if residual else None
+    rstd = torch.rsqrt(H.float().square().mean(-1) + EPS)
+    keep = dR.clone() if residual else None
+    dg.set_num_sms(sms)
+    try:
+        dX, dW = backward(dY, H, rstd, W, dR, dX=dR)
+    finally:
+        dg.set_num_sms(0)
+    check_backward(dY, H, rstd, W, keep, dX, dW, f"{shape}")
+
+
 def test_norm_gradient_of_no_rows():
     dW = torch.full((256,), float("nan"), device="cuda")
     dg.rms_norm_backward(None, None, None, None, None, None, dW, None, 0, 0, 256)
