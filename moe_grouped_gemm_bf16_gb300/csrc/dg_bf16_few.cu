@@ -324,14 +324,17 @@ __global__ void __launch_bounds__(TN_THREADS) few_tn_kernel(const FewParams p) {
 // knows the total only: nt and nn up to the FEW_ROWS that one pass over the
 // weights takes (in us, the tensor cores' kernel and this one: nt 1 row of 3496 x
 // 1392 7.7, 3.6; 4 rows in one group, 7792 x 872 7.1, 7.2, in two of 784 x 4592
-// 10.0, 5.2; 8 in 19 groups, 944 x 7400 25, 25; nn 2 rows in 46 groups, 648 x 2128
+// 10.0, 5.2; 8 in 19 groups, 944 x 7400 25, 25; two passes over weights of a few
+// MB, 5 rows of 424 x 5144 13.2, 4.9, 7 of 2744 x 720 6.0, 5.3, but 6 of 3120 x 5216
+// 21.7, 24.6; nn 2 rows in 46 groups, 648 x 2128
 // 9.6, 4.9, in one of 8136 x 1024 7.3, 4.9; with 5 in one group of 5640 x 7880 24,
 // 78), more where many groups share them.  tn reads each row once: 3 rows in one
 // group, 6496 x 568 7.6, 4.3; 5 in 30 groups, 1872 x 5320 115, 90 (88 at the copy
 // rate); 8 in one of two, 6816 x 576 8.7, 7.4; 21 in one of two, 304 x 5488 6.1,
 // 7.6.  At most 32 in all, should one group have them.
 bool bf16_few_rows(const BfCall& c) {
-  const int most = c.form == kBfTN ? 8 + c.G / 2 : FEW_ROWS + c.G / 4;
+  const bool twice = c.form == kBfNT && static_cast<long long>(c.N) * c.K <= 4 << 20;
+  const int most = c.form == kBfTN ? 8 + c.G / 2 : (twice ? 2 : 1) * FEW_ROWS + c.G / 4;
   return c.forced.lanes == 0 && c.rows <= std::min(32, most) && c.M <= 64 * 65535;
 }
 
