@@ -190,6 +190,52 @@ __device__ __forceinline__ void store_four(const BfParams& p, size_t at, float4 
   *reinterpret_cast<uint2*>(p.D + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
+// A CTA's share of a split tile's rows: the ranks' partials added up in the order
+// of the ranks (`has`: those that have one).  A warp takes 8 / S rows at a time,
+// a lane four columns of each, and asks for all S partials of them before it adds
+// (rank by rank, with the ranks' flags before, 13 rows split in 8 took 3.8 us, so
+// 1.0).  Nothing is stored where a rank gave up a wait (`ok`: this thread knows of
+// none; lane r asks rank r's `flag`, while the partials are on their way).
+template <bool PAIR, int BC, bool TN, int S>
+__device__ __forceinline__ void add_partials(const BfParams& p, const BfTile& T, uint32_t sbase,
+                                             uint32_t has, uint32_t flag, bool ok, int krank,
+                                             uint32_t side, int halves) {
+  constexpr int U = 8 / S;
+  const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5) - 4;
+  const int l_end = min(p.N, T.l0 + p.lanes);
+  const int c0 = U * (p.split * warp + krank);
+  if (c0 >= T.cols) return;
+  uint32_t gave_up = 0;
+  if (lane < p.split) gave_up = ld_cluster_u32(map_cluster(flag, PAIR ? 2 * lane + side : lane));
+  for (int a = 0; a < halves; ++a) {
+    const int l = T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + 4 * lane;
+    for (int c = c0; c < T.cols; c += U * BF_EPI * p.split) {
+      const int rows = l < l_end ? min(U, T.cols - c) : 0;   // (l_end is a multiple of 8)
+      float4 x[S][U];
+      const uint32_t at = sbase + ((a * BC + c) * 128 + 4 * lane) * 4;
+#pragma unroll
+      for (int r = 0; r < S; ++r) {
+        const int n = (has >> r) & 1u ? rows : 0;
+        const int rank = min(r, p.split - 1);
+        const uint32_t from = map_cluster(at, PAIR ? 2 * rank + side : rank);
+#pragma unroll
+        for (int j = 0; j < U; ++j) x[r][j] = ld_cluster_v4_if(from + j * 512, j < n);
+      }
+      if (!__all_sync(0xffffffffu, ok && gave_up == 0)) return;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < S; ++r) {
+          sum.x += x[r][j].x; sum.y += x[r][j].y; sum.z += x[r][j].z; sum.w += x[r][j].w;
+        }
+        if (j < rows)
+          store_four(p, ((TN ? static_cast<size_t>(T.g) * p.M : 0) + T.q0 + c + j) * p.N + l, sum);
+      }
+    }
+  }
+}
+
 // BC: capacity of an accumulator in rows of D (`bc` at most).
 template <bool PAIR, int BC, int FORM>
 __global__ void __launch_bounds__(BF_THREADS, 1)
@@ -286,9 +332,9 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // the peers signal this CTA's barriers from here on (their initialisation
+  // a pair's CTAs signal each other's barriers from here on (their initialisation
   // was made visible to the cluster by thread 0's fence)
-  if (cluster > 1) {
+  if constexpr (PAIR) {
     cluster_arrive_relaxed();
     cluster_wait();
   }
@@ -660,43 +706,14 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     __syncwarp();
     cluster_sync();
     if (warp >= 4 && mine) {
-      // ranks that had slots of the reduction; nothing is stored where one of
-      // them gave up a wait
-      uint32_t has = 0;
-      for (int r = 0; r < p.split; ++r) {
-        const long long nk = T.nk;
-        if (nk * r / p.split < nk * (r + 1) / p.split) has |= 1u << r;
-        const uint32_t flag = map_cluster(smem_u32(misc + 1), PAIR ? 2 * r + side : r);
-        ok = ok && ld_cluster_u32(flag) == 0;
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      // a warp adds up four rows at a time, a lane four columns of each
-      constexpr int U = 4;
-      for (int a = 0; ok && a < halves; ++a) {
-        const int l = T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + 4 * lane;
-        const int l_end = min(p.N, T.l0 + p.lanes);
-        for (int c = U * (BF_EPI * krank + warp - 4); c < T.cols; c += U * BF_EPI * p.split) {
-          float4 sum[U] = {};
-          const uint32_t at = sbase + ((a * BC + c) * 128 + 4 * lane) * 4;
-          for (int r = 0; r < p.split; ++r) {
-            if (!((has >> r) & 1u)) continue;
-            const uint32_t from = map_cluster(at, PAIR ? 2 * r + side : r);
-            float4 x[U];
-#pragma unroll
-            for (int j = 0; j < U; ++j) x[j] = ld_cluster_v4(from + j * 512);
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-              sum[j].x += x[j].x; sum[j].y += x[j].y; sum[j].z += x[j].z; sum[j].w += x[j].w;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < U; ++j) {
-            if (c + j >= T.cols || l >= l_end) continue;   // (l_end is a multiple of 8)
-            store_four(p, ((TN ? static_cast<size_t>(T.g) * p.M : 0) + T.q0 + c + j) * p.N + l,
-                       sum[j]);
-          }
-        }
-      }
+      // ranks that had slots of the reduction
+      const long long nk = T.nk;
+      const uint32_t has = __ballot_sync(
+          0xffffffffu, lane < p.split && nk * lane / p.split < nk * (lane + 1) / p.split);
+      const uint32_t flag = smem_u32(misc + 1);
+      if (p.split <= 2) add_partials<PAIR, BC, TN, 2>(p, T, sbase, has, flag, ok, krank, side, halves);
+      else if (p.split <= 4) add_partials<PAIR, BC, TN, 4>(p, T, sbase, has, flag, ok, krank, side, halves);
+      else add_partials<PAIR, BC, TN, 8>(p, T, sbase, has, flag, ok, krank, side, halves);
     }
     __syncwarp();
   }
@@ -708,47 +725,50 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     if constexpr (PAIR) tmem_dealloc_pair(tmem, 2 * ACC);
     else tmem_dealloc(tmem, 2 * ACC);
   }
-  // no CTA leaves while a peer may still signal it or read its shared memory
+  // no CTA leaves while a peer may still signal it or read its shared memory: the
+  // arrival is a release, which a read of a peer's partial or flag comes before
+  // even where nothing has used its value yet
   if (cluster > 1) {
     __syncwarp();
-    cluster_sync_relaxed();
+    cluster_sync();
   }
 }
 
 // Estimated time of a plan beyond the launch (us), for the choice between
 // plans only.  The groups' sizes are on the device: one group stands for all, at
-// 1.4 times the average rows (some get none).  Constants fitted to timings of
-// every plan below on 800 shapes drawn over 1 to 64 groups, 1 to 32647 rows and
-// widths of 256 to 8192, all forms: the choice is 3.1% slower than the best plan
-// on average (fixed rules on the group's rows and the tile count: 11%).
-//  * a slot costs a pair 0.33 us (64 deep), the single form (128 deep) 2.7 ns per
-//    lane and 2.3 ns per row of A: what they take to load;
+// 1.3 times the average rows (some get none).  Constants fitted to timings of
+// every plan below on 3700 shapes drawn over 1 to 64 groups, 1 to 32647 rows and
+// widths of 256 to 8192, all forms: the choice is 3.6% slower than the best plan
+// on average, on as many others too (splits of 3, 5 and 6 as well would gain 0.2%).
+//  * a slot costs a pair 0.33 us (64 deep), the single form (128 deep) 0.08 us, 2.6
+//    ns per lane and 2 ns per row of A: what they take to load;
 //  * a tile's epilogue 3.7 ns per row of D and 128 lanes, hidden behind the next
 //    tile but for the last one;
-//  * a split adds 1.9 us (two cluster barriers) and 0.37 ns per partial sum a
-//    thread's CTA reads from the others, and large clusters leave SMs empty;
+//  * a split adds 2.2 us (partials written, a cluster barrier, a round of reads)
+//    and 0.2 ns per partial that a CTA reads from the others, and large clusters
+//    leave SMs empty;
 //  * memory 8.3 TB/s over what is read and written once (weights in L2 count in).
 double bf_cost(const BfCall& c, const BfPlan& f, int num_sms) {
   const bool tn = c.form == kBfTN;
-  const double groups = tn ? c.G : std::min(c.G, c.rows), fill = groups > 1 ? 1.4 : 1.0;
+  const double groups = tn ? c.G : std::min(c.G, c.rows), fill = groups > 1 ? 1.3 : 1.0;
   const double per = tn ? c.M : fill * c.rows / groups;       // rows of D in a group
   const double depth = tn ? fill * c.rows / c.G : c.K;
   const int cluster = (f.pair ? 2 : 1) * f.split;
   const double room = std::max(
-      1.0, std::floor(num_sms * (cluster >= 8 ? 0.4 : cluster >= 4 ? 0.86 : 1.0) / cluster));
+      1.0, std::floor(num_sms * (cluster >= 8 ? 0.55 : cluster >= 4 ? 0.8 : 1.0) / cluster));
   const double tiles = groups * std::ceil(per / f.bc) * ((c.N + f.lanes - 1) / f.lanes);
   const double waves = std::max(1.0, std::ceil(tiles / room));
   const int halves = f.pair ? 1 : (f.lanes + 127) / 128;
   const double cols = std::min<double>(f.bc, per);
   const double slots = std::max(1.0, std::ceil(depth / bf_bk(f.pair) / f.split));
-  const double main = slots * (f.pair ? 0.33 : 0.0027 * f.lanes + 0.0023 * f.bc);
+  const double main = slots * (f.pair ? 0.33 : 0.08 + 0.0026 * f.lanes + 0.002 * f.bc);
   const double epilogue = 0.0037 * cols * halves;
   const double run = main + epilogue + (waves - 1) * std::max(main, epilogue);
   const double N = c.N, K = c.K, M = c.M, T = c.rows;
   const double memory =
       2 * (tn ? c.G * M * N + T * (M + N) : groups * N * K + T * (N + K)) / 8.3e6;
-  return std::max(run, memory) + 0.19 * std::min(run, memory) +
-         (f.split > 1 ? 1.9 + 3.7e-4 * 128 * halves * cols * (f.split - 1) / f.split : 0.0);
+  return std::max(run, memory) + 0.12 * std::min(run, memory) +
+         (f.split > 1 ? 2.2 + 2e-4 * 128 * halves * cols * (f.split - 1) / f.split : 0.0);
 }
 
 BfPlan bf_plan(const BfCall& c, int num_sms) {

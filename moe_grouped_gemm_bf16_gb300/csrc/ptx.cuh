@@ -528,11 +528,18 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+// Four floats where `on`, else zeros (predicated: several in a row stay in flight).
+__device__ __forceinline__ float4 ld_cluster_v4_if(uint32_t addr, bool on) {
   float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "setp.ne.u32 p, %5, 0;\n\t"
+               "mov.f32 %0, 0f00000000;\n\t"
+               "mov.f32 %1, 0f00000000;\n\t"
+               "mov.f32 %2, 0f00000000;\n\t"
+               "mov.f32 %3, 0f00000000;\n\t"
+               "@p ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+               : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w)
+               : "r"(addr), "r"(static_cast<uint32_t>(on))
                : "memory");
   return v;
 }
