@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
   __shared__ uint32_t aborted;
   volatile uint32_t* abort_flag = &aborted;
   const int T = blockDim.x, nv = a.K >> 3, step = gridDim.x;
-  ChunkRing ring{{a.X, a.R, nullptr}, smem, full, stages, a.R ? 2 : 1, a.K * 2, 0, 0};
+  ChunkRing ring{{a.X, a.R, nullptr}, smem, full, stages, a.R ? 2 : 1, a.K * 2, a.debug_flags, 0, 0};
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(full + s), 1);
     aborted = 0;
@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
   int s = 0, par = 0;
   uint32_t ph = 0;
   for (long long m = blockIdx.x; m < a.M; m += step, par ^= 1) {
-    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a);
+    // (once a wait has failed a later turn of the ring may look complete)
+    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) && *abort_flag == 0;
     const size_t base = static_cast<size_t>(m) * nv;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
     Pairs h[VPT] = {};
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
   __shared__ uint32_t aborted;
   volatile uint32_t* abort_flag = &aborted;
   const int T = blockDim.x, nv = a.K >> 3, step = gridDim.x;
-  ChunkRing ring{{a.dY, a.H, a.dR}, smem, full, stages, a.dR ? 3 : 2, a.K * 2, 0, 0};
+  ChunkRing ring{{a.dY, a.H, a.dR}, smem, full, stages, a.dR ? 3 : 2, a.K * 2, a.debug_flags, 0, 0};
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(full + s), 1);
     aborted = 0;
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
   uint32_t ph = 0;
   for (long long m = blockIdx.x; m < a.M; m += step, par ^= 1) {
     const float rs = __ldg(a.rstd + m);
-    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a);
+    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) && *abort_flag == 0;
     const size_t base = static_cast<size_t>(m) * nv;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
     Pairs g[VPT], xh[VPT];

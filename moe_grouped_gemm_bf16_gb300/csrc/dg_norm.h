@@ -21,6 +21,7 @@ struct NormFwd {
   float eps;
   unsigned int* status;           // device status word and the waits' limit
   unsigned long long timeout_ns;
+  unsigned int debug_flags;
 };
 
 struct NormBwd {
@@ -35,6 +36,7 @@ struct NormBwd {
   int M, K;
   unsigned int* status;
   unsigned long long timeout_ns;
+  unsigned int debug_flags;
 };
 
 // The caller has validated the arguments (K % 128 == 0, K <= kNormMaxK,

@@ -63,6 +63,7 @@ dg_status rms_norm(const dgk::NormFwd& a0, void* stream, bool ue8m0) {
   if (s != DG_OK) return s;
   a.status = st.status;
   a.timeout_ns = st.timeout_ns;
+  a.debug_flags = st.debug_flags;
   const cudaError_t e =
       dgk::launch_rms_norm(a, ue8m0, st.sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "norm launch") : host_ok();
@@ -93,6 +94,7 @@ dg_status swiglu(const dgk::SwigluFwd& a0, void* stream, bool ue8m0) {
   if (s != DG_OK) return s;
   a.status = st.status;
   a.timeout_ns = st.timeout_ns;
+  a.debug_flags = st.debug_flags;
   const cudaError_t e = dgk::launch_swiglu(a, ue8m0, st.sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "swiglu launch") : host_ok();
 }
@@ -170,14 +172,14 @@ extern "C" {
 dg_status dg_rms_norm_quantize_fp8_1x128(const void* X, const void* R, const void* W, void* H,
                                          void* Y, void* Q, float* sa, float* rstd, int M, int K,
                                          int ld_sa, float eps, void* stream) {
-  return rms_norm(dgk::NormFwd{X, R, W, H, Y, Q, sa, rstd, M, K, ld_sa, eps, nullptr, 0}, stream,
+  return rms_norm(dgk::NormFwd{X, R, W, H, Y, Q, sa, rstd, M, K, ld_sa, eps, nullptr, 0, 0}, stream,
                   false);
 }
 
 dg_status dg_rms_norm_quantize_fp8_1x128_ue8m0(const void* X, const void* R, const void* W, void* H,
                                                void* Y, void* Q, int32_t* sfa, float* rstd, int M,
                                                int K, int ld_sfa, float eps, void* stream) {
-  return rms_norm(dgk::NormFwd{X, R, W, H, Y, Q, sfa, rstd, M, K, ld_sfa, eps, nullptr, 0}, stream,
+  return rms_norm(dgk::NormFwd{X, R, W, H, Y, Q, sfa, rstd, M, K, ld_sfa, eps, nullptr, 0, 0}, stream,
                   true);
 }
 
@@ -208,7 +210,7 @@ dg_status dg_rms_norm_backward(const void* dY, const void* H, const float* rstd,
   if (s != DG_OK) return s;
   const cudaError_t e = dgk::launch_rms_norm_backward(
       dgk::NormBwd{dY, H, rstd, W, dR, dX, dW, static_cast<float*>(workspace), M, K, st.status,
-                   st.timeout_ns},
+                   st.timeout_ns, st.debug_flags},
       st.sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "norm gradient launch") : host_ok();
 }
@@ -216,7 +218,7 @@ dg_status dg_rms_norm_backward(const void* dY, const void* H, const float* rstd,
 dg_status dg_swiglu_quantize_fp8_1x128(const void* GU, void* Y, void* Q, float* sa, void* CQ,
                                        float* csa, const int32_t* masked_m, int num_groups, int M,
                                        int I, int ld_sa, void* stream) {
-  return swiglu(dgk::SwigluFwd{GU, Y, Q, sa, CQ, csa, masked_m, num_groups, M, I, ld_sa, nullptr, 0},
+  return swiglu(dgk::SwigluFwd{GU, Y, Q, sa, CQ, csa, masked_m, num_groups, M, I, ld_sa, nullptr, 0, 0},
                 stream, false);
 }
 
@@ -224,7 +226,7 @@ dg_status dg_swiglu_quantize_fp8_1x128_ue8m0(const void* GU, void* Y, void* Q, i
                                              void* CQ, float* csa, const int32_t* masked_m,
                                              int num_groups, int M, int I, int ld_sfa,
                                              void* stream) {
-  return swiglu(dgk::SwigluFwd{GU, Y, Q, sfa, CQ, csa, masked_m, num_groups, M, I, ld_sfa, nullptr, 0},
+  return swiglu(dgk::SwigluFwd{GU, Y, Q, sfa, CQ, csa, masked_m, num_groups, M, I, ld_sfa, nullptr, 0, 0},
                 stream, true);
 }
 

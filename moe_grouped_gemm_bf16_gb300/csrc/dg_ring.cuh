@@ -23,6 +23,7 @@ struct ChunkRing {
   uint8_t* smem;
   uint64_t* full;          // a barrier per slot
   int stages, ops, bytes;
+  uint32_t debug_flags;
   uint32_t issued, phase;  // filling thread: slots with a load, and that load's phase
 
   __device__ __forceinline__ uint8_t* slot(int s) const { return smem + s * ops * bytes; }
@@ -30,6 +31,7 @@ struct ChunkRing {
   // Chunk i into slot s; `part` bytes of it, where it is the operands' last and
   // shorter (16-byte multiples).
   __device__ __forceinline__ void fill(int i, int s, int part) {
+    if (debug_flags & DBG_SKIP_PRODUCER) return;
     const uint32_t dst = smem_u32(slot(s)), bar = smem_u32(full + s);
     mbar_arrive_expect_tx(bar, ops * part);
     for (int j = 0; j < ops; ++j)

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(SG_THREADS) swiglu_ring_kernel(const SwigluFwd
   __shared__ uint32_t aborted;
   volatile uint32_t* abort_flag = &aborted;
   const int lanes = a.I >> 4, total = a.G * a.M;   // lanes per row, rows
-  ChunkRing ring{{a.GU, nullptr, nullptr}, smem, full, stages, 1, rows * a.I * 4, 0, 0};
+  ChunkRing ring{{a.GU, nullptr, nullptr}, smem, full, stages, 1, rows * a.I * 4, a.debug_flags, 0, 0};
   auto fill = [&](int c, int s) { ring.fill(c, s, min(rows, total - c * rows) * a.I * 4); };
   const int chunks = (total + rows - 1) / rows;
   if (threadIdx.x == 0) {
@@ -242,7 +242,11 @@ __global__ void __launch_bounds__(SG_THREADS) swiglu_ring_kernel(const SwigluFwd
   int s = 0;
   uint32_t ph = 0;
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a);
+    // the warp's lanes agree (forward_group exchanges values among all 32, and a
+    // wait that gives up may do so in some lanes only); after a failed wait
+    // nothing more is loaded or stored
+    const bool ok = __all_sync(0xffffffffu, wait_bar(smem_u32(full + s), ph, abort_flag, a) &&
+                                                *abort_flag == 0);
     const int n = ok ? min(rows, total - c * rows) * lanes : 0;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
     int r = r0, q = q0;

@@ -18,6 +18,7 @@ struct SwigluFwd {
   int G, M, I, ld;
   unsigned int* status;           // device status word and the waits' limit
   unsigned long long timeout_ns;
+  unsigned int debug_flags;
 };
 
 struct SwigluBwd {
