@@ -262,8 +262,10 @@ dg_status dg_quantize_fp8_1x128_ue8m0(const void* X, void* Q, int32_t* sfa, int 
  * row m, in fp32:
  *   h = X[m,k] + R[m,k];  rstd[m] = 1 / sqrt(mean_k(h^2) + eps);
  *   y = h * rstd[m] * W[k];  H = bf16(h);  Y = bf16(y);
- *   Q, sa = the 1x128 quantisation of y (of the fp32 value, not of Y)
- *   X   bf16 [M][K]; R bf16 [M][K] or null (h = X); W bf16 [K]; finite values
+ *   Q, sa = the 1x128 quantisation of y (of the fp32 value, not of Y; a value
+ *           past fp32's range counts as its largest number)
+ *   X   bf16 [M][K]; R bf16 [M][K] or null (h = X); W bf16 [K]; finite values,
+ *       |h| below 2^56 (its squares are added up in fp32)
  *   H   bf16 [M][K] or null (not written; needs R): may be X or R itself
  *   Y   bf16 [M][K] or null; Q e4m3 [M][K] or null: one of them at least
  *   sa  fp32 [K/128][ld_sa] with Q: columns m < M are written
@@ -305,7 +307,7 @@ long long dg_rms_norm_backward_workspace_bytes(int M, int K);
  * output quantised 1x128, and an 8-bit checkpoint of its input.  A row of GU
  * holds the I gate columns, then the I up columns.  In fp32:
  *   s = 1 / (1 + exp(-g));  y = g * s * u;  Y = bf16(y);
- *   Q, sa = the 1x128 quantisation of y;  CQ, csa = that of GU (exactly what
+ *   Q, sa = the 1x128 quantisation of y (as the norm's);  CQ, csa = that of GU (exactly what
  *   dg_quantize_fp8_1x128 writes for GU as a matrix of K = 2 I columns)
  *   GU  bf16 [num_groups][M][2 I], finite values
  *   Y   bf16 [num_groups][M][I] or null; Q e4m3 [num_groups][M][I] or null, with

@@ -9,6 +9,9 @@
 namespace dgk {
 
 constexpr float kScaleFloor = 1e-4f;  // smallest group maximum a scale is made from
+// largest one: values computed from bf16 ones (a norm's, an activation's) may pass
+// fp32; with it a scale stays finite and they get the largest code of their sign
+constexpr float kScaleTop = 3.402823466e38f;
 
 // two fp32 -> two e4m3 codes (round to nearest even, saturating to +-448),
 // `lo` in the low byte
@@ -146,14 +149,14 @@ __device__ __forceinline__ float bf16x8_amax(const uint4& w) {
 }
 
 // The factor a group's values are multiplied by before the conversion to
-// e4m3, from its maximum a (floored): 448 / a, or with UE8M0 scales 1 / s with
+// e4m3, from its maximum a (floored, finite): 448 / a, or with UE8M0 scales 1 / s with
 // s the smallest power of two >= a / 448, whose exponent code is e8.
 template <bool UE8M0>
 __device__ __forceinline__ void group_factor(float a, float& factor, uint32_t& e8) {
   e8 = 0;
   if constexpr (UE8M0) {
-    // t = a / 448 is a normal fp32 number here (a >= 1e-4, a <= bf16's largest);
-    // its power-of-two ceiling is 2^(E - 127) when the mantissa is zero, else
+    // t = a / 448 is a normal fp32 number here (1e-4 <= a <= the largest finite
+    // fp32 number, so e8 <= 247); its power-of-two ceiling is 2^(E - 127) when the mantissa is zero, else
     // 2^(E - 126), E the biased exponent; the factor 1 / s is exact
     const uint32_t tb = __float_as_uint(__fdiv_rn(a, 448.0f));
     e8 = ((tb >> 23) & 0xFFu) + ((tb & 0x7FFFFFu) != 0u ? 1u : 0u);

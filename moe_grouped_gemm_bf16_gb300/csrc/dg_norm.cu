@@ -74,7 +74,7 @@ __device__ __forceinline__ void norm_output(const NormFwd& a, int m, int nv, Pai
     float amax = pairs_amax(h[i]);
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    amax = fmaxf(amax, kScaleFloor);
+    amax = fminf(fmaxf(amax, kScaleFloor), kScaleTop);
     if constexpr (UE8M0) {
       float f;
       uint32_t e8;

@@ -105,7 +105,7 @@ __device__ __forceinline__ void forward_group(const SwigluFwd& a, const Place& p
     Y[8] = pairs_to_bf16x8(y[1]);
   }
   float ay = kScaleFloor, ag = kScaleFloor, au = kScaleFloor;
-  if (a.Q) ay = lanes_max(fmaxf(pairs_amax(y[0]), pairs_amax(y[1])));
+  if (a.Q) ay = fminf(lanes_max(fmaxf(pairs_amax(y[0]), pairs_amax(y[1]))), kScaleTop);
   if (a.CQ) {
     ag = lanes_max(fmaxf(bf16x8_amax(v[0]), bf16x8_amax(v[1])));
     au = lanes_max(fmaxf(bf16x8_amax(v[2]), bf16x8_amax(v[3])));
