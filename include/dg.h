@@ -263,7 +263,8 @@ dg_status dg_quantize_fp8_1x128_ue8m0(const void* X, void* Q, int32_t* sfa, int 
  *   h = X[m,k] + R[m,k];  rstd[m] = 1 / sqrt(mean_k(h^2) + eps);
  *   y = h * rstd[m] * W[k];  H = bf16(h);  Y = bf16(y);
  *   Q, sa = the 1x128 quantisation of y (of the fp32 value, not of Y; a value
- *           past fp32's range counts as its largest number)
+ *           past fp32 gets the largest code of its sign, and a group's maximum
+ *           counts as the largest fp32 number at most)
  *   X   bf16 [M][K]; R bf16 [M][K] or null (h = X); W bf16 [K]; finite values,
  *       |h| below 2^56 (its squares are added up in fp32)
  *   H   bf16 [M][K] or null (not written; needs R): may be X or R itself

@@ -23,13 +23,15 @@ def built():
 
 def check(Q, scale, y):
     """Q [K], scale [K/128] of the 64-bit y [K]."""
-    y = y.clamp(-TOP, TOP)
-    a = R.group_amax(y)
+    past = y.abs() > TOP
+    assert past.any() and (Q[past] == torch.where(y[past] > 0, 0x7E, 0xFE)).all()
+    a = R.group_amax(y).clamp_max(TOP)
     assert torch.isfinite(scale).all()
     # (two rounded factors before the product, one quotient: 2^-20 is ample; a
     # power of two not below it)
     assert (scale >= a / 448 * (1 - 2.0 ** -20)).all() and (scale <= a / 224).all()
-    R.check_codes(Q[None], scale[None], y[None], 2.0 ** -18, "codes")
+    kept = ~past
+    R.check_codes((Q * kept)[None], scale[None], (y * kept)[None], 2.0 ** -18, "codes")
 
 
 @pytest.mark.parametrize("ue8m0", [False, True])
@@ -39,7 +41,9 @@ def test_activation(ue8m0):
     GU[0, 0, 5], GU[0, 0, I + 5] = 1e30, 1e30            # + inf in fp32
     GU[0, 1, 200], GU[0, 1, I + 200] = 2e38, -3e38       # - inf, in the second group
     GU[0, 1, 201], GU[0, 1, I + 201] = 1e19, 1e19        # 1e38: keeps its code
-    GU[0, 2, 7], GU[0, 2, I + 7] = 1e19, 3e19            # near the top, finite
+    GU[0, 2, 7], GU[0, 2, I + 7] = -3e38, 1e30           # (a gate that far below: zero)
+    GU[0, 2, 9], GU[0, 2, I + 9] = 3e38, 1e30
+    GU[0, 2, 8], GU[0, 2, I + 8] = 1e19, 3e19            # near the top, finite
     Y = torch.zeros(1, M, I, dtype=torch.bfloat16, device="cuda")
     Q = torch.zeros(1, M, I, dtype=torch.uint8, device="cuda")
     sa = torch.zeros(1, 1 if ue8m0 else I // 128, 4, dtype=torch.int32 if ue8m0 else torch.float32,
