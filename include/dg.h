@@ -478,8 +478,9 @@ dg_status dg_debug_force_block_scaled(int mode);
  * CTAs (lanes: columns of D per tile, 64..256; rows: rows of D per tile, 16..128;
  * both multiples of 16, of 64 where the form's operand is read in 64-wide boxes,
  * else the calls return DG_ERR_UNSUPPORTED_SHAPE; split: CTAs sharing a tile's
- * reduction, 1..8; calls of a few rows are tiled then, too).  lanes = 0 leaves the
- * choice to the library. */
+ * reduction, 1..8; calls of a few rows are tiled then, too; a plan of more CTAs
+ * than a limit on the SMs allows is refused likewise).  lanes = 0 leaves the choice
+ * to the library. */
 dg_status dg_debug_force_ragged_plan(int pair, int lanes, int rows, int split);
 
 #ifdef __cplusplus

@@ -771,6 +771,13 @@ double bf_cost(const BfCall& c, const BfPlan& f, int num_sms) {
          (f.split > 1 ? 2.2 + 2e-4 * 128 * halves * cols * (f.split - 1) / f.split : 0.0);
 }
 
+// Tiles of `lanes` columns and `bc` rows of D that the call can have at most.
+long long bf_most_tiles(const BfCall& c, int lanes, int bc) {
+  const long long nl = (c.N + lanes - 1) / lanes;
+  return nl * (c.form == kBfTN ? static_cast<long long>(c.G) * ((c.M + bc - 1) / bc)
+                               : std::min<long long>(c.G, c.rows) + c.rows / bc);
+}
+
 BfPlan bf_plan(const BfCall& c, int num_sms) {
   const bool tn = c.form == kBfTN;
   const int per = tn ? c.M : (c.rows + std::min(c.G, c.rows) - 1) / std::max(1, std::min(c.G, c.rows));
@@ -782,6 +789,7 @@ BfPlan bf_plan(const BfCall& c, int num_sms) {
     for (int split = 1; split * width <= kBfMaxCluster && (split == 1 || depth >= 128 * split); split *= 2) {
       if (split * width > num_sms) break;   // (a limit on the SMs may leave fewer)
       const BfPlan f{pair, lanes, bc, split};
+      if (c.limited && bf16_grid(c, f, num_sms) > num_sms) break;   // (a cluster per tile)
       const double t = bf_cost(c, f, num_sms);
       if (t < least) {
         least = t;
@@ -865,14 +873,9 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
           : operand(maps.q, &p.q_whole, c.A, false, 1, rows, c.K, q_rows));
   if (!good) return cudaErrorInvalidValue;
 
-  // as many CTAs (pairs) as there can be tiles, at most one per SM; with a
-  // split reduction a cluster for each of them
-  const long long most = tn ? static_cast<long long>(c.G) * p.nc * p.nl
-                            : (std::min<long long>(c.G, c.rows) + c.rows / bc) * p.nl;
   const int cluster = (PAIR ? 2 : 1) * split;
-  const long long units = split > 1 ? most : std::min<long long>(most, num_sms / cluster);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, units) * cluster), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(bf16_grid(c, plan, num_sms)), 1, 1);
   cfg.blockDim = dim3(BF_THREADS, 1, 1);
   cfg.dynamicSmemBytes = p.stages * (p.p_bytes + p.q_bytes) + BfSmem::fixed(c.G);
   cfg.stream = stream;
@@ -914,6 +917,14 @@ cudaError_t launch_form(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encod
 }
 
 }  // namespace
+
+// As many CTAs (pairs) as there can be tiles, at most one per SM; with a split
+// reduction a cluster for each of them.
+long long bf16_grid(const BfCall& c, const BfPlan& f, int num_sms) {
+  const long long most = bf_most_tiles(c, f.lanes, f.bc);
+  const int width = f.pair ? 2 : 1;
+  return std::max(1ll, f.split > 1 ? most : std::min<long long>(most, num_sms / width)) * width * f.split;
+}
 
 cudaError_t bf16_set_up() {
   cudaError_t e = set_up_form<kBfNT>();

@@ -35,6 +35,7 @@ struct BfCall {
   unsigned int* status;
   unsigned long long timeout_ns;
   unsigned int debug_flags;
+  bool limited;          // fewer SMs than the device has: no grid of more CTAs
   BfPlan forced;         // lanes > 0: this plan (tests)
 };
 
@@ -44,6 +45,9 @@ cudaError_t bf16_set_up();
 // tensor map could not be encoded.
 cudaError_t launch_bf16_grouped(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode,
                                 int num_sms, cudaStream_t stream);
+
+// CTAs of the plan's grid.
+long long bf16_grid(const BfCall& c, const BfPlan& plan, int num_sms);
 
 // The form for a few rows in all (dg_bf16_few.cu): whether it takes the call, and
 // its launch.

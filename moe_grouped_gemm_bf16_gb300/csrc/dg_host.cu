@@ -655,6 +655,7 @@ dg_status host_state(HostState* out) {
   if (s != DG_OK) return s;
   out->device = dev;
   out->sms = sms_in_use(*st);
+  out->device_sms = st->sms;
   out->status = st->status;
   out->timeout_ns = g_timeout_ns.load();
   out->debug_flags = g_skip_producer.load() ? DBG_SKIP_PRODUCER : 0u;

@@ -14,6 +14,7 @@ constexpr int kHostMaxDevices = 64;
 struct HostState {
   int device;                     // index, below kHostMaxDevices
   int sms;                        // SMs the kernels may use
+  int device_sms;                 // SMs of the device (above sms under a limit)
   unsigned int* status;           // device status word
   unsigned long long timeout_ns;  // limit of every wait inside a kernel
   unsigned int debug_flags;

@@ -142,23 +142,21 @@ dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void
   c.status = st.status;
   c.timeout_ns = st.timeout_ns;
   c.debug_flags = st.debug_flags;
+  c.limited = st.sms < st.device_sms;
   if (const unsigned long long f = g_ragged_plan.load()) {
     c.forced = {(f >> 48) != 0, static_cast<int>(f >> 32 & 0xFFFF), static_cast<int>(f >> 16 & 0xFFFF),
                 static_cast<int>(f & 0xFFFF)};
     // boxes of an MN-major operand are 64 wide (nn, tn: B's; tn: A's)
     if ((!c.forced.pair && ((form != dgk::kBfNT && c.forced.lanes % 64) || (tn && c.forced.bc % 64))) ||
-        c.forced.split * (c.forced.pair ? 2 : 1) > st.sms)
+        c.forced.split * (c.forced.pair ? 2 : 1) > st.sms ||
+        (c.limited && dgk::bf16_grid(c, c.forced, st.sms) > st.sms))
       return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "no kernel for the forced plan");
   }
-  cudaError_t e = cudaSuccess;
-  int all_sms = 0;
-  // (a grid of many small blocks: not under a limit on the SMs)
-  if (dgk::bf16_few_rows(c) &&
-      cudaDeviceGetAttribute(&all_sms, cudaDevAttrMultiProcessorCount, st.device) == cudaSuccess &&
-      st.sms >= all_sms)
-    e = dgk::launch_bf16_few(c, st.sms, static_cast<cudaStream_t>(stream));
-  else
-    e = dgk::launch_bf16_grouped(c, st.encode, st.sms, static_cast<cudaStream_t>(stream));
+  // (few rows: a grid of many small blocks, not under a limit on the SMs)
+  const cudaError_t e =
+      dgk::bf16_few_rows(c) && !c.limited
+          ? dgk::launch_bf16_few(c, st.sms, static_cast<cudaStream_t>(stream))
+          : dgk::launch_bf16_grouped(c, st.encode, st.sms, static_cast<cudaStream_t>(stream));
   if (e == cudaErrorInvalidValue) {
     cudaGetLastError();
     return host_fail(DG_ERR_CUDA, "ragged bf16 product: tensor map or launch rejected");
