@@ -19,6 +19,9 @@
 //  * persistent blocks fed by bulk copies, several rows ahead, into a ring in
 //    shared memory (the gradient: each keeps its share of the weight's in
 //    registers, and a second kernel adds the shares).
+// Under a limit on the SMs a grid has one block per SM, whose threads are teams that
+// stand in for such blocks (132 of the 152 SMs: 4096 x 2048 forward 17.8 us, with all
+// 13.4; backward 27.6 and 24.8).
 // Measured: 4096 x 7168 forward 45 us (5.9 TB/s; one block per row 47 us),
 // 8192 x 7168 backward 77 us (6.1 TB/s; the one-launch form 171 us), without dR
 // 61 us (5.8 TB/s), 8192 x 4224 40 us.
@@ -42,28 +45,57 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the block of up to 32 warps; `red` is 32 floats that the previous
+// The threads that take a row together, whole warps: a block or, with FOLD, one of
+// several teams of a block (under a limit on the SMs, where a grid has one block
+// per SM).  tid: thread of the team, rank: the team among all in the grid.
+constexpr int kMaxTeams = 15;   // of a block: a named barrier each, 1 .. 15
+constexpr int kTeamsBytes = 6144;   // what their sums and barriers take from the rings at most
+
+template <bool FOLD>
+struct Team {
+  int tid, size, id, rank;
+  __device__ __forceinline__ explicit Team(int threads) {
+    if constexpr (FOLD) {
+      id = threadIdx.x / threads;
+      tid = threadIdx.x - id * threads;
+      size = threads;
+      rank = id * gridDim.x + blockIdx.x;
+    } else {
+      id = 0;
+      tid = threadIdx.x;
+      size = blockDim.x;
+      rank = blockIdx.x;
+    }
+  }
+  __device__ __forceinline__ void sync() const {
+    if constexpr (FOLD) named_bar_sync(1 + id, size);
+    else __syncthreads();
+  }
+};
+
+// Sum over the team of up to 32 warps; `red` is 32 floats that the previous
 // call did not use (one barrier per call).
-__device__ __forceinline__ float block_sum(float v, float* red) {
+template <bool FOLD>
+__device__ __forceinline__ float team_sum(const Team<FOLD>& t, float v, float* red) {
   v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int warps = (blockDim.x + 31) >> 5;
-  v = (threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f;
+  if ((t.tid & 31) == 0) red[t.tid >> 5] = v;
+  t.sync();
+  const int warps = (t.size + 31) >> 5;
+  v = (t.tid & 31) < warps ? red[t.tid & 31] : 0.f;
   return warp_sum(v);
 }
 
 // Output of a normalised row: the thread's VPT vectors h (w: the weight's,
 // packed), those below nv stored.
 template <int VPT, bool UE8M0>
-__device__ __forceinline__ void norm_output(const NormFwd& a, int m, int nv, Pairs (&h)[VPT], float rs,
-                                            const uint4 (&w)[VPT]) {
-  const int T = blockDim.x, kb = a.K >> 7;
+__device__ __forceinline__ void norm_output(const NormFwd& a, int m, int nv, int tid, int T,
+                                            Pairs (&h)[VPT], float rs, const uint4 (&w)[VPT]) {
+  const int kb = a.K >> 7;
   const size_t base = static_cast<size_t>(m) * (a.K >> 3);
   const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v = i * T + threadIdx.x;
+    const int v = i * T + tid;
     const Pairs wp = bf16x8_to_pairs(w[i]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[i].v[j] = mul2(mul2(h[i].v[j], rs2), wp.v[j]);
@@ -98,10 +130,10 @@ __device__ __forceinline__ void norm_output(const NormFwd& a, int m, int nv, Pai
 }
 
 template <int VPT>
-__device__ __forceinline__ void load_weight(const void* W, int nv, uint4 (&w)[VPT]) {
+__device__ __forceinline__ void load_weight(const void* W, int nv, int tid, int T, uint4 (&w)[VPT]) {
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v = i * blockDim.x + threadIdx.x;
+    const int v = i * T + tid;
     w[i] = v < nv ? __ldg(static_cast<const uint4*>(W) + v) : make_uint4(0, 0, 0, 0);
   }
 }
@@ -122,37 +154,57 @@ __device__ __forceinline__ float add_residual(const NormFwd& a, size_t at, const
   return ss.x + ss.y;
 }
 
-template <int VPT, bool UE8M0>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormFwd a) {
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  __shared__ float red[32];
-  const int T = blockDim.x, nv = a.K >> 3, m = blockIdx.x;
+// One row by a team, loads straight to registers.
+template <int VPT, bool UE8M0, bool FOLD>
+__device__ __forceinline__ void norm_row(const NormFwd& a, const Team<FOLD>& t, int m, float* red) {
+  const int T = t.size, nv = a.K >> 3;
   const uint4* X = static_cast<const uint4*>(a.X);
   const uint4* R = static_cast<const uint4*>(a.R);
   const size_t base = static_cast<size_t>(m) * nv;
   uint4 x[VPT], r[VPT], w[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v = i * T + threadIdx.x;
+    const int v = i * T + t.tid;
     x[i] = r[i] = make_uint4(0, 0, 0, 0);
     if (v < nv) {
       x[i] = ld_stream_v4(X + base + v);
       if (R) r[i] = ld_stream_v4(R + base + v);
     }
   }
-  load_weight<VPT>(a.W, nv, w);
+  load_weight<VPT>(a.W, nv, t.tid, T, w);
   Pairs h[VPT] = {};
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v = i * T + threadIdx.x;
+    const int v = i * T + t.tid;
     if (v < nv) ss += add_residual(a, base + v, x[i], r[i], h[i]);
   }
-  ss = block_sum(ss, red);
+  ss = team_sum(t, ss, red);
   const float rs = __frsqrt_rn(ss / static_cast<float>(a.K) + a.eps);
-  if (threadIdx.x == 0 && a.rstd) a.rstd[m] = rs;
-  norm_output<VPT, UE8M0>(a, m, nv, h, rs, w);
+  if (t.tid == 0 && a.rstd) a.rstd[m] = rs;
+  norm_output<VPT, UE8M0>(a, m, nv, t.tid, T, h, rs, w);
+}
+
+template <int VPT, bool UE8M0>
+__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormFwd a) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  __shared__ float red[32];
+  const Team<false> t(0);
+  norm_row<VPT, UE8M0>(a, t, t.rank, red);
+}
+
+// The same by teams of `threads` threads, which take row after row.
+template <int VPT, bool UE8M0>
+__global__ void __launch_bounds__(1024) rms_norm_teams_kernel(const NormFwd a, int threads) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  __shared__ float red[kMaxTeams][2][32];
+  const Team<true> t(threads);
+  const int step = gridDim.x * (blockDim.x / threads);
+  int par = 0;
+  for (long long m = t.rank; m < a.M; m += step, par ^= 1)
+    norm_row<VPT, UE8M0>(a, t, static_cast<int>(m), red[t.id][par]);
 }
 
 template <int VPT, bool UE8M0>
@@ -174,8 +226,9 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
   if (threadIdx.x == 0)
     for (int s = 0; s < stages && blockIdx.x + static_cast<long long>(s) * step < a.M; ++s)
       ring.fill(blockIdx.x + s * step, s);
+  const Team<false> t(0);
   uint4 w[VPT];
-  load_weight<VPT>(a.W, nv, w);
+  load_weight<VPT>(a.W, nv, t.tid, T, w);
   __syncthreads();
   int s = 0, par = 0;
   uint32_t ph = 0;
@@ -191,7 +244,7 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
       const int v = i * T + threadIdx.x;
       if (v < nv && ok) ss += add_residual(a, base + v, x[v], a.R ? x[nv + v] : x[v], h[i]);
     }
-    ss = block_sum(ss, red[par]);
+    ss = team_sum(t, ss, red[par]);
     // every thread has read the slot: the row `stages` turns ahead may follow
     // (after a failed wait nothing more is loaded or stored)
     const bool go = *abort_flag == 0;
@@ -199,7 +252,7 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
       ring.fill(static_cast<int>(m) + stages * step, s);
     const float rs = __frsqrt_rn(ss / static_cast<float>(a.K) + a.eps);
     if (threadIdx.x == 0 && a.rstd && go) a.rstd[m] = rs;
-    norm_output<VPT, UE8M0>(a, static_cast<int>(m), go ? nv : 0, h, rs, w);
+    norm_output<VPT, UE8M0>(a, static_cast<int>(m), go ? nv : 0, t.tid, T, h, rs, w);
     if (++s == stages) { s = 0; ph ^= 1; }
   }
   if (threadIdx.x == 0 && *abort_flag) ring.drain(a);
@@ -259,12 +312,13 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_kernel(const NormBwd a
         if (dR) r[i] = ld_stream_v4(dR + base + v);
       }
     }
-    load_weight<VPT>(a.W, nv, w);
+    const Team<false> t(0);
+    load_weight<VPT>(a.W, nv, t.tid, T, w);
     Pairs g[VPT], xh[VPT], dw = {};
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) dot += grad_sums(dy[i], hv[i], w[i], rs, g[i], xh[i], dw);
-    const float mean = block_sum(dot, red) * (1.0f / static_cast<float>(a.K));
+    const float mean = team_sum(t, dot, red) * (1.0f / static_cast<float>(a.K));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * T + threadIdx.x;
@@ -297,28 +351,37 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_kernel(const NormBwd a
   }
 }
 
-template <int VPT>
-__global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const NormBwd a, int stages) {
+// Rows by `teams` teams (FOLD; else a block each), with a ring each.
+template <int VPT, bool FOLD>
+__global__ void __launch_bounds__(1024)
+rms_norm_backward_ring_kernel(const NormBwd a, int threads, int teams, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float red[2][32];
-  __shared__ __align__(8) uint64_t full[kMaxRing];
-  __shared__ uint32_t aborted;
-  volatile uint32_t* abort_flag = &aborted;
-  const int T = blockDim.x, nv = a.K >> 3, step = gridDim.x;
-  ChunkRing ring{{a.dY, a.H, a.dR}, smem, full, stages, a.dR ? 3 : 2, a.K * 2, a.debug_flags, 0, 0};
-  if (threadIdx.x == 0) {
+  constexpr int TEAMS = FOLD ? kMaxTeams : 1;
+  __shared__ float reds[TEAMS][2][32];
+  __shared__ __align__(8) uint64_t fulls[TEAMS][kMaxRing];
+  __shared__ uint32_t aborts[TEAMS];
+  const Team<FOLD> t(threads);
+  float(*red)[32] = reds[t.id];
+  uint64_t* full = fulls[t.id];
+  volatile uint32_t* abort_flag = &aborts[t.id];
+  const int T = t.size, nv = a.K >> 3, step = FOLD ? teams : static_cast<int>(gridDim.x);
+  const int ops = a.dR ? 3 : 2, bytes = a.K * 2;
+  ChunkRing ring{{a.dY, a.H, a.dR}, smem + t.id * stages * ops * bytes, full, stages, ops, bytes,
+                 a.debug_flags, 0, 0};
+  if (t.tid == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(full + s), 1);
-    aborted = 0;
+    *abort_flag = 0;
     fence_mbarrier_init();
   }
   grid_dep_wait();
   grid_dep_launch_dependents();
-  if (threadIdx.x == 0)
-    for (int s = 0; s < stages && blockIdx.x + static_cast<long long>(s) * step < a.M; ++s)
-      ring.fill(blockIdx.x + s * step, s);
+  if (FOLD && t.rank >= teams) return;   // (the last block's; from here on a team is by itself)
+  if (t.tid == 0)
+    for (int s = 0; s < stages && t.rank + static_cast<long long>(s) * step < a.M; ++s)
+      ring.fill(t.rank + s * step, s);
   uint4 w[VPT];
-  load_weight<VPT>(a.W, nv, w);
-  __syncthreads();
+  load_weight<VPT>(a.W, nv, t.tid, T, w);
+  t.sync();
   const uint4 zero = make_uint4(0, 0, 0, 0);
   // With one vector a thread keeps what it has read of a row for the output; with
   // two (which 64 registers do not hold) it reads the slot again, which then is
@@ -328,7 +391,7 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
   Pairs dw[VPT] = {};
   int s = 0, par = 0;
   uint32_t ph = 0;
-  for (long long m = blockIdx.x; m < a.M; m += step, par ^= 1) {
+  for (long long m = t.rank; m < a.M; m += step, par ^= 1) {
     const float rs = __ldg(a.rstd + m);
     const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) && *abort_flag == 0;
     const size_t base = static_cast<size_t>(m) * nv;
@@ -338,20 +401,20 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
     uint4 r[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = i * T + threadIdx.x;
+      const int v = i * T + t.tid;
       const bool on = v < nv && ok;
       if (KEEP) r[i] = on && a.dR ? x[2 * nv + v] : zero;
       dot += grad_sums(on ? x[v] : zero, on ? x[nv + v] : zero, w[i], rs, g[i], xh[i], dw[i]);
     }
-    const float mean = block_sum(dot, red[par]) * (1.0f / static_cast<float>(a.K));
+    const float mean = team_sum(t, dot, red[par]) * (1.0f / static_cast<float>(a.K));
     // every thread has read the slot (two vectors: the one before) for the last
     // time; after a failed wait nothing more is loaded or stored
     const bool go = *abort_flag == 0;
-    if (threadIdx.x == 0 && go && (KEEP || m != blockIdx.x) && m + ahead < a.M)
+    if (t.tid == 0 && go && (KEEP || m != t.rank) && m + ahead < a.M)
       ring.fill(static_cast<int>(m) + ahead, KEEP ? s : (s == 0 ? stages : s) - 1);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = i * T + threadIdx.x;
+      const int v = i * T + t.tid;
       if (v >= nv || !go) continue;
       if (!KEEP) {
         Pairs unused = {};
@@ -364,38 +427,45 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_ring_kernel(const Norm
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v = i * T + threadIdx.x;
+    const int v = i * T + t.tid;
     if (v >= nv) continue;
-    float4* out = reinterpret_cast<float4*>(a.part + static_cast<size_t>(blockIdx.x) * a.K) + 2 * v;
+    float4* out = reinterpret_cast<float4*>(a.part + static_cast<size_t>(t.rank) * a.K) + 2 * v;
     out[0] = make_float4(dw[i].v[0].x, dw[i].v[0].y, dw[i].v[1].x, dw[i].v[1].y);
     out[1] = make_float4(dw[i].v[2].x, dw[i].v[2].y, dw[i].v[3].x, dw[i].v[3].y);
   }
-  if (threadIdx.x == 0 && *abort_flag) ring.drain(a);
+  if (t.tid == 0 && *abort_flag) ring.drain(a);
 }
 
-// dW[k] = sum of the blocks' partial sums, in a fixed order (32 columns per
-// block, 32 chains over the partials).
+// dW[k] = sum of the blocks' (teams') partial sums, in a fixed order: 32 columns
+// per block (WALK: at a time), 32 chains over the partials.
+template <bool WALK>
 __global__ void __launch_bounds__(1024)
 rms_norm_weight_grad_kernel(const float* __restrict__ part, float* __restrict__ dW, int blocks,
                             int K) {
   grid_dep_wait();
   grid_dep_launch_dependents();
   __shared__ float s[32][33];
-  const int c = threadIdx.x & 31, r = threadIdx.x >> 5, k = blockIdx.x * 32 + c;
-  float acc = 0.f;
-  for (int b = r; b < blocks; b += 32) acc += part[static_cast<size_t>(b) * K + k];
-  s[r][c] = acc;
-  __syncthreads();
-  // (transposed: warp r now sums the chains of column r)
-  const float sum = warp_sum(s[c][r]);
-  if (c == 0) dW[blockIdx.x * 32 + r] = sum;
+  const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+  for (int k0 = blockIdx.x * 32; k0 < K; k0 += gridDim.x * 32) {
+    const int k = k0 + c;
+    float acc = 0.f;
+    for (int b = r; b < blocks; b += 32) acc += part[static_cast<size_t>(b) * K + k];
+    s[r][c] = acc;
+    __syncthreads();
+    // (transposed: warp r now sums the chains of column r)
+    const float sum = warp_sum(s[c][r]);
+    if (c == 0) dW[k0 + r] = sum;
+    if (!WALK) return;
+    __syncthreads();   // the sums have been read
+  }
 }
 
 // Threads of a block whose rows of K columns take `vpt` vectors per thread.
 int row_threads(int K, int vpt) { return ((K / 8 + vpt - 1) / vpt + 31) / 32 * 32; }
 
+// threads: of a team (a block, or with `teams` > 0 one of that many over the blocks)
 struct RingShape {
-  int blocks, threads, stages, smem;
+  int blocks, threads, stages, smem, teams, per_block;
 };
 
 // A ring per block, as many blocks per SM as a thousand threads make (their
@@ -409,6 +479,23 @@ RingShape ring_shape(int M, int K, int ops, int vpt, int num_sms, int max_blocks
   r.stages = std::max(2, std::min(kMaxRing, ring_bytes(per_sm) / slot));
   r.blocks = std::min(std::min(M, per_sm * num_sms), max_blocks);
   r.smem = r.stages * slot;
+  r.teams = 0;
+  r.per_block = 1;
+  return r;
+}
+
+// The same folded into one block per SM: teams in place of the blocks that share
+// an SM.
+RingShape ring_fold(int M, int K, int ops, int vpt, int num_sms, int max_teams) {
+  RingShape r;
+  r.threads = row_threads(K, vpt);
+  const int slot = 2 * K * ops, room = ring_bytes(1) - kTeamsBytes;
+  const int most = std::max(1, std::min(std::min(kMaxTeams, 1024 / r.threads), room / (3 * slot)));
+  r.teams = std::min(std::min(M, most * num_sms), max_teams);
+  r.blocks = std::min(r.teams, num_sms);
+  r.per_block = (r.teams + r.blocks - 1) / r.blocks;
+  r.stages = std::max(2, std::min(kMaxRing, room / r.per_block / slot));
+  r.smem = r.per_block * r.stages * slot;
   return r;
 }
 
@@ -418,7 +505,7 @@ cudaError_t launch_ring(void (*kernel)(P...), const RingShape& r, cudaStream_t s
 }
 
 template <bool UE8M0>
-cudaError_t launch_fwd(const NormFwd& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_fwd(const NormFwd& a, int num_sms, bool limited, cudaStream_t stream) {
   const int vpt = a.K <= 8192 ? 1 : 2;
   // Long rows leave room for one or two blocks per SM, which wait for their
   // loads in turn: the ring is ahead from some 12 rows per SM (2432 x 7168: 27.7
@@ -430,6 +517,14 @@ cudaError_t launch_fwd(const NormFwd& a, int num_sms, cudaStream_t stream) {
                     : launch_ring(rms_norm_ring_kernel<2, UE8M0>, r, stream, a);
   }
   const int threads = row_threads(a.K, vpt);
+  if (limited && a.M > num_sms) {
+    const int teams = std::min(kMaxTeams, 1024 / threads);
+    const dim3 grid(std::min(num_sms, a.M));
+    return vpt == 1 ? launch_dependent(rms_norm_teams_kernel<1, UE8M0>, grid, teams * threads, stream, 0, a,
+                                       threads)
+                    : launch_dependent(rms_norm_teams_kernel<2, UE8M0>, grid, teams * threads, stream, 0, a,
+                                       threads);
+  }
   return vpt == 1 ? launch_dependent(rms_norm_kernel<1, UE8M0>, dim3(a.M), threads, stream, 0, a)
                   : launch_dependent(rms_norm_kernel<2, UE8M0>, dim3(a.M), threads, stream, 0, a);
 }
@@ -441,27 +536,35 @@ cudaError_t norm_set_up() {
                            reinterpret_cast<const void*>(rms_norm_ring_kernel<2, false>),
                            reinterpret_cast<const void*>(rms_norm_ring_kernel<1, true>),
                            reinterpret_cast<const void*>(rms_norm_ring_kernel<2, true>),
-                           reinterpret_cast<const void*>(rms_norm_backward_ring_kernel<1>),
-                           reinterpret_cast<const void*>(rms_norm_backward_ring_kernel<2>)};
-  for (const void* k : kernels) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(1));
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+                           reinterpret_cast<const void*>(rms_norm_backward_ring_kernel<1, false>),
+                           reinterpret_cast<const void*>(rms_norm_backward_ring_kernel<2, false>)};
+  const void* teams[] = {reinterpret_cast<const void*>(rms_norm_backward_ring_kernel<1, true>),
+                         reinterpret_cast<const void*>(rms_norm_backward_ring_kernel<2, true>)};
+  auto opt_in = [](const void* k, int bytes) {
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  cudaError_t e = cudaSuccess;
+  for (const void* k : kernels)
+    if (e == cudaSuccess) e = opt_in(k, ring_bytes(1));
+  for (const void* k : teams)
+    if (e == cudaSuccess) e = opt_in(k, ring_bytes(1) - kTeamsBytes);
+  return e;
 }
 
-cudaError_t launch_rms_norm(const NormFwd& a, bool ue8m0, int num_sms, cudaStream_t stream) {
-  return ue8m0 ? launch_fwd<true>(a, num_sms, stream) : launch_fwd<false>(a, num_sms, stream);
+cudaError_t launch_rms_norm(const NormFwd& a, bool ue8m0, int num_sms, bool limited,
+                            cudaStream_t stream) {
+  return ue8m0 ? launch_fwd<true>(a, num_sms, limited, stream)
+               : launch_fwd<false>(a, num_sms, limited, stream);
 }
 
-cudaError_t launch_rms_norm_backward(const NormBwd& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rms_norm_backward(const NormBwd& a, int num_sms, bool limited,
+                                     cudaStream_t stream) {
   const int vpt = a.K <= 8192 ? 1 : 2;
   // The one-launch form reads its rows a second time, in chains that grow with
   // M; the ring pays a second kernel (about 1.5 us).  Measured with both, 456
   // rows of 512, 2048, 7168 columns: 5.0, 5.5, 9.3 us in one launch, 5.0, 6.7,
   // 8.8 us with the ring; 608 rows: 6.0, 7.2, 11.9 and 5.4, 7.1, 10.1 us.
-  if (a.M <= 3 * num_sms) {
+  if (limited ? a.M + a.K / 64 <= num_sms : a.M <= 3 * num_sms) {
     // (at least 32 chains of rows in a block of dW's columns)
     const int threads = std::max(256, row_threads(a.K, vpt));
     const dim3 grid(a.M + a.K / 64);
@@ -478,13 +581,26 @@ cudaError_t launch_rms_norm_backward(const NormBwd& a, int num_sms, cudaStream_t
   const bool split = a.K > 4096 && a.K <= 8192 && a.M > 6 * num_sms &&
                      ring_bytes(2) >= 3 * 2 * a.K * ops;
   const int per_thread = split ? 2 : vpt;
+  auto launch = [&](auto kernel, const RingShape& r) {
+    return launch_dependent(kernel, dim3(r.blocks), r.per_block * r.threads, stream, r.smem, a, r.threads,
+                            r.teams, r.stages);
+  };
+  auto add_up = [&](auto kernel, int parts, int blocks) {
+    return launch_dependent(kernel, dim3(blocks), 1024, stream, 0, static_cast<const float*>(a.part), a.dW,
+                            parts, a.K);
+  };
+  if (limited) {
+    const int sums = std::min(num_sms, a.K / 32);
+    if (a.M == 0) return add_up(rms_norm_weight_grad_kernel<true>, 0, sums);
+    const RingShape r = ring_fold(a.M, a.K, ops, per_thread, num_sms, kNormBwdBlocks);
+    const cudaError_t e = per_thread == 1 ? launch(rms_norm_backward_ring_kernel<1, true>, r)
+                                          : launch(rms_norm_backward_ring_kernel<2, true>, r);
+    return e != cudaSuccess ? e : add_up(rms_norm_weight_grad_kernel<true>, r.teams, sums);
+  }
   const RingShape r = ring_shape(a.M, a.K, ops, per_thread, num_sms, kNormBwdBlocks);
-  const cudaError_t e = per_thread == 1
-                            ? launch_ring(rms_norm_backward_ring_kernel<1>, r, stream, a)
-                            : launch_ring(rms_norm_backward_ring_kernel<2>, r, stream, a);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(rms_norm_weight_grad_kernel, dim3(a.K / 32), 1024, stream, 0,
-                          static_cast<const float*>(a.part), a.dW, r.blocks, a.K);
+  const cudaError_t e = per_thread == 1 ? launch(rms_norm_backward_ring_kernel<1, false>, r)
+                                        : launch(rms_norm_backward_ring_kernel<2, false>, r);
+  return e != cudaSuccess ? e : add_up(rms_norm_weight_grad_kernel<false>, r.blocks, a.K / 32);
 }
 
 }  // namespace dgk

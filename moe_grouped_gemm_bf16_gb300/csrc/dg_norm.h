@@ -42,7 +42,10 @@ struct NormBwd {
 // The caller has validated the arguments (K % 128 == 0, K <= kNormMaxK,
 // 16-byte aligned tensors).
 cudaError_t norm_set_up();  // opts the kernels into their shared memory (once per device)
-cudaError_t launch_rms_norm(const NormFwd& a, bool ue8m0, int num_sms, cudaStream_t stream);
-cudaError_t launch_rms_norm_backward(const NormBwd& a, int num_sms, cudaStream_t stream);
+// limited: fewer SMs than the device has, so no grid of more blocks.
+cudaError_t launch_rms_norm(const NormFwd& a, bool ue8m0, int num_sms, bool limited,
+                            cudaStream_t stream);
+cudaError_t launch_rms_norm_backward(const NormBwd& a, int num_sms, bool limited,
+                                     cudaStream_t stream);
 
 }  // namespace dgk

@@ -65,7 +65,7 @@ dg_status rms_norm(const dgk::NormFwd& a0, void* stream, bool ue8m0) {
   a.timeout_ns = st.timeout_ns;
   a.debug_flags = st.debug_flags;
   const cudaError_t e =
-      dgk::launch_rms_norm(a, ue8m0, st.sms, static_cast<cudaStream_t>(stream));
+      dgk::launch_rms_norm(a, ue8m0, st.sms, st.sms < st.device_sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "norm launch") : host_ok();
 }
 
@@ -209,7 +209,7 @@ dg_status dg_rms_norm_backward(const void* dY, const void* H, const float* rstd,
   const cudaError_t e = dgk::launch_rms_norm_backward(
       dgk::NormBwd{dY, H, rstd, W, dR, dX, dW, static_cast<float*>(workspace), M, K, st.status,
                    st.timeout_ns, st.debug_flags},
-      st.sms, static_cast<cudaStream_t>(stream));
+      st.sms, st.sms < st.device_sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "norm gradient launch") : host_ok();
 }
 

@@ -5,9 +5,12 @@ import torch
 
 import moe_grouped_gemm_bf16_gb300 as dg
 from moe_grouped_gemm_bf16_gb300 import _build
+from tests import operators_ref as R
 from tests import test_gpu_bf16_ragged as P
+from tests import test_gpu_norm as N
 from tests.launches import launched
 from tests.test_gpu_bf16_ragged import ints
+from tests.test_gpu_swiglu import normal
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +75,49 @@ def test_forced_tilings_past_the_limit_are_refused():
         dg.debug_force_ragged_plan()
         dg.set_num_sms(0)
     P.check("nt", A, B, sizes, D, "forced")
+
+
+@pytest.mark.parametrize("shape", [(1, 7168), (7, 1536), (200, 128), (150, 384), (700, 2048), (40, 8320),
+                                   (300, 6144), (1500, 512), (45, 16384), (400, 7168)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("ue8m0", [False, True])
+@pytest.mark.parametrize("sms", LIMITS)
+def test_norm(shape, ue8m0, sms):
+    M, K = shape
+    ld = (M + 3) // 4 * 4
+    X, Rs, W = normal(M, K, seed=M), normal(M, K, seed=K, scale=3.0), normal(K, seed=sms)
+    H, Y, Q, sa, rstd = got = N.buffers(M, K, ld, ue8m0)
+    fn = dg.rms_norm_quantize_fp8_1x128_ue8m0 if ue8m0 else dg.rms_norm_quantize_fp8_1x128
+    within(sms, lambda s: fn(X, Rs, W, H, Y, Q, sa, rstd, M, K, ld, N.EPS, stream=s))
+    N.check(X, Rs, W, got, M, K, ue8m0, "HYQr", f"{shape} on {sms} SMs")
+    assert dg.get_device_status() == 0
+
+
+@pytest.mark.parametrize("shape", [(0, 256), (1, 7168), (2, 256), (33, 640), (150, 2048), (305, 1024),
+                                   (611, 384), (9, 8320), (45, 16384), (2500, 512), (200, 128),
+                                   (460, 7168), (300, 5120)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("sms", LIMITS)
+def test_norm_gradient(shape, residual, sms):
+    M, K = shape
+    H, W = normal(M, K, seed=M, scale=2.0), normal(K, seed=K, scale=0.5)
+    dY = normal(M, K, seed=M + 1, scale=0.03)
+    dR = normal(M, K, seed=M + 2, scale=0.03) if residual else None
+    rstd = torch.rsqrt(H.float().square().mean(-1) + N.EPS)
+    n = dg.rms_norm_backward_workspace_bytes(M, K)
+    work = torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    dX = torch.full((M, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dW = torch.full((K,), float("nan"), device="cuda")
+    within(sms, lambda s: dg.rms_norm_backward(dY, H, rstd, W, dR, dX, dW, work, n, M, K, stream=s))
+    if M == 0:
+        assert (dW == 0).all()
+        return
+    # (as N.check_backward, whose bound for dW supposes the rows to be spread over
+    # the blocks: here one block may add up a chain of M / sms rows)
+    dx, dw = R.norm_backward(dY, H, rstd, W, dR)
+    xh, g = H.double() * rstd.double()[:, None], dY.double() * W.double()
+    mag = rstd.double()[:, None] * (g.abs() + xh.abs() * (g * xh).abs().mean(-1, keepdim=True))
+    R.check_close(dX, dx, N.REL * (mag + (dR.double().abs() if residual else 0.0)), "dX")
+    lim = (64 + M / min(sms, 16)) * 2 * R.U32 * (dY.double() * xh).abs().sum(0)
+    assert ((dW.double() - dw).abs() <= lim).all(), "dW"
+    assert dg.get_device_status() == 0
