@@ -375,7 +375,9 @@ dg_status dg_k_grouped_gemm_bf16_tn_ragged(const void* A, const void* B, const v
 /* Maximum number of SMs the kernels may use (DeepGEMM set_num_sms / get_num_sms,
  * es.news.hada.io/topic?id=19459, "Utilidades y variables de entorno").
  * dg_set_num_sms(0) restores "all SMs of the device"; a value above the device's
- * SM count is rejected with DG_ERR_INVALID_ARG when a device is present.
+ * SM count is rejected with DG_ERR_INVALID_ARG when a device is present.  Below the
+ * device's count no grid has more blocks than the limit, but for the two
+ * quantisers', whose grids go by their rows.
  * dg_get_num_sms() returns the limit in force (the device's SM count by default,
  * 0 when no device is present and no limit was set). */
 int dg_get_num_sms(void);

@@ -95,7 +95,8 @@ dg_status swiglu(const dgk::SwigluFwd& a0, void* stream, bool ue8m0) {
   a.status = st.status;
   a.timeout_ns = st.timeout_ns;
   a.debug_flags = st.debug_flags;
-  const cudaError_t e = dgk::launch_swiglu(a, ue8m0, st.sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = dgk::launch_swiglu(a, ue8m0, st.sms, st.sms < st.device_sms,
+                                           static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "swiglu launch") : host_ok();
 }
 
@@ -250,7 +251,7 @@ dg_status dg_swiglu_backward_fp8_1x128(const void* CQ, const float* csa, const v
   if (s != DG_OK) return s;
   const cudaError_t e = dgk::launch_swiglu_backward(
       dgk::SwigluBwd{CQ, csa, dY, dGU, Y, masked_m, num_groups, M, I, ld_csa, st.status},
-      static_cast<cudaStream_t>(stream));
+      st.sms, st.sms < st.device_sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "swiglu gradient launch") : host_ok();
 }
 

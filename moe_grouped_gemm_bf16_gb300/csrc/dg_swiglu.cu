@@ -18,10 +18,14 @@
 //  * persistent blocks fed by bulk copies of whole rows into a ring in shared
 //    memory, for many rows (registers alone do not keep enough loads in
 //    flight).
+// Under a limit on the SMs either form has one block per SM, of the threads that
+// otherwise share one (132 of the 152 SMs, 32647 rows, I = 2048, with checkpoint: 87
+// us, with all 75; the gradient 118 and 104).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "dg_fp8.cuh"
 #include "dg_launch.h"
@@ -33,6 +37,7 @@ namespace dgk {
 namespace {
 
 constexpr int SG_THREADS = 256;   // direct form: 32 rows of one 128-column group
+constexpr int SG_WALK = 1024;     // under a limit on the SMs: 128 rows at a time
 
 // 1 / (1 + exp(-g)) with the hardware's exponential and reciprocal; a gate whose
 // exponential is not finite gives 0 (below -88) or 1.
@@ -171,14 +176,13 @@ __device__ __forceinline__ void backward_group(const SwigluBwd& a, const Place& 
   }
 }
 
+// Rows m0 .. of batch z, as many as eight threads each make; group `grp` of each.
 template <bool UE8M0>
-__global__ void __launch_bounds__(SG_THREADS, 4) swiglu_kernel(const SwigluFwd a) {
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  const int m = blockIdx.x * 32 + (threadIdx.x >> 3), z = blockIdx.z;
+__device__ __forceinline__ void forward_block(const SwigluFwd& a, int m0, int grp, int z) {
+  const int m = m0 + (threadIdx.x >> 3);
   const int rows = valid_rows(a.masked_m, z, a.M, a.status);
-  if (static_cast<int>(blockIdx.x) * 32 >= rows) return;
-  const Place p(z, m, blockIdx.y, threadIdx.x & 7, a.M, a.I);
+  if (m0 >= rows) return;
+  const Place p(z, m, grp, threadIdx.x & 7, a.M, a.I);
   const bool on = m < rows;
   uint4 v[4] = {};
   if (on) {
@@ -191,12 +195,10 @@ __global__ void __launch_bounds__(SG_THREADS, 4) swiglu_kernel(const SwigluFwd a
   forward_group<UE8M0>(a, p, v, on);
 }
 
-__global__ void __launch_bounds__(SG_THREADS) swiglu_backward_kernel(const SwigluBwd a) {
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  const int m = blockIdx.x * 32 + (threadIdx.x >> 3), z = blockIdx.z, kb = a.I >> 7;
+__device__ __forceinline__ void backward_block(const SwigluBwd& a, int m0, int grp, int z) {
+  const int m = m0 + (threadIdx.x >> 3), kb = a.I >> 7;
   if (m >= valid_rows(a.masked_m, z, a.M, a.status)) return;
-  const Place p(z, m, blockIdx.y, threadIdx.x & 7, a.M, a.I);
+  const Place p(z, m, grp, threadIdx.x & 7, a.M, a.I);
   const uint2* CQ = static_cast<const uint2*>(a.CQ);
   const uint4* dY = static_cast<const uint4*>(a.dY);
   const uint2 c[4] = {__ldg(CQ + p.gate), __ldg(CQ + p.gate + 8), __ldg(CQ + p.up),
@@ -207,11 +209,47 @@ __global__ void __launch_bounds__(SG_THREADS) swiglu_backward_kernel(const Swigl
                  __ldg(cs + static_cast<size_t>(kb + p.grp) * a.ld), d);
 }
 
+template <bool UE8M0>
+__global__ void __launch_bounds__(SG_THREADS, 4) swiglu_kernel(const SwigluFwd a) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  forward_block<UE8M0>(a, blockIdx.x * 32, blockIdx.y, blockIdx.z);
+}
+
+__global__ void __launch_bounds__(SG_THREADS) swiglu_backward_kernel(const SwigluBwd a) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  backward_block(a, blockIdx.x * 32, blockIdx.y, blockIdx.z);
+}
+
+// Under a limit on the SMs: one block after the other of G x I / 128 x M / 128.
+template <class F>
+__device__ __forceinline__ void walk_blocks(int G, int M, int I, F f) {
+  const int mb = (M + SG_WALK / 8 - 1) / (SG_WALK / 8), kb = I >> 7;
+  for (long long u = blockIdx.x; u < static_cast<long long>(mb) * kb * G; u += gridDim.x) {
+    const long long zg = u / mb;
+    f(static_cast<int>(u - zg * mb) * (SG_WALK / 8), static_cast<int>(zg % kb), static_cast<int>(zg / kb));
+  }
+}
+
+template <bool UE8M0>
+__global__ void __launch_bounds__(SG_WALK) swiglu_walk_kernel(const SwigluFwd a) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  walk_blocks(a.G, a.M, a.I, [&](int m0, int grp, int z) { forward_block<UE8M0>(a, m0, grp, z); });
+}
+
+__global__ void __launch_bounds__(SG_WALK) swiglu_backward_walk_kernel(const SwigluBwd a) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  walk_blocks(a.G, a.M, a.I, [&](int m0, int grp, int z) { backward_block(a, m0, grp, z); });
+}
+
 // Ring form: a chunk is `rows` whole rows, of which a thread takes one lane's
 // share of a group at a time.
-template <bool UE8M0>
-__global__ void __launch_bounds__(SG_THREADS) swiglu_ring_kernel(const SwigluFwd a, int rows,
-                                                                 int stages) {
+template <bool UE8M0, int THREADS>
+__global__ void __launch_bounds__(THREADS) swiglu_ring_kernel(const SwigluFwd a, int rows,
+                                                              int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kMaxRing];
   __shared__ uint32_t aborted;
@@ -233,7 +271,7 @@ __global__ void __launch_bounds__(SG_THREADS) swiglu_ring_kernel(const SwigluFwd
   __syncthreads();
   // this thread's first unit of a chunk (row, lane of the row), and the next
   const int r0 = threadIdx.x / lanes, q0 = threadIdx.x - r0 * lanes;
-  const int dr = SG_THREADS / lanes, dq = SG_THREADS - dr * lanes;
+  const int dr = THREADS / lanes, dq = THREADS - dr * lanes;
   auto advance = [&](int& r, int& q) {
     r += dr;
     q += dq;
@@ -250,7 +288,7 @@ __global__ void __launch_bounds__(SG_THREADS) swiglu_ring_kernel(const SwigluFwd
     const int n = ok ? min(rows, total - c * rows) * lanes : 0;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
     int r = r0, q = q0;
-    for (int u0 = threadIdx.x & ~31; u0 < n; u0 += SG_THREADS, advance(r, q)) {
+    for (int u0 = threadIdx.x & ~31; u0 < n; u0 += THREADS, advance(r, q)) {
       const int row = c * rows + r, z = a.G > 1 ? row / a.M : 0;
       const Place p(z, row - z * a.M, q >> 3, q & 7, a.M, a.I);
       const uint4* g = x + r * (a.I >> 2) + p.grp * 16 + p.lane8;
@@ -273,6 +311,10 @@ __global__ void __launch_bounds__(SG_THREADS) swiglu_ring_kernel(const SwigluFwd
 }
 
 dim3 grid_of(int G, int M, int I) { return dim3((M + 31) / 32, I / 128, G); }
+dim3 walk_grid(int G, int M, int I, int num_sms) {
+  const long long blocks = static_cast<long long>(G) * (I / 128) * ((M + SG_WALK / 8 - 1) / (SG_WALK / 8));
+  return dim3(static_cast<unsigned>(std::min<long long>(num_sms, blocks)));
+}
 
 // Ring: two blocks per SM (112 registers a thread; a third block, or a ring in
 // smaller chunks, was slower), chunks of about 48 KB, which are three units of
@@ -280,38 +322,60 @@ dim3 grid_of(int G, int M, int I) { return dim3((M + 31) / 32, I / 128, G); }
 // chunks of 16 KB 83 us, three blocks of 85 registers each 91 us; loads straight
 // to registers 90-101 us.  (The gradient, with two thirds of the instructions
 // per byte, runs at 96% of the copy rate without a ring.)
+// Under a limit on the SMs one block of twice the threads and chunks.
 constexpr int kRingPerSm = 2, kChunk = 49152;
 
-}  // namespace
-
-cudaError_t swiglu_set_up() {
-  const cudaError_t e = cudaFuncSetAttribute(swiglu_ring_kernel<false>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             ring_bytes(kRingPerSm));
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(swiglu_ring_kernel<true>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 ring_bytes(kRingPerSm));
-}
-
-cudaError_t launch_swiglu(const SwigluFwd& a, bool ue8m0, int num_sms, cudaStream_t stream) {
+template <bool UE8M0>
+cudaError_t launch_fwd(const SwigluFwd& a, int num_sms, bool limited, cudaStream_t stream) {
   const long long total = static_cast<long long>(a.G) * a.M;
-  const int row = 4 * a.I, rows = std::max(1, kChunk / row);
-  const int stages = std::min(kMaxRing, ring_bytes(kRingPerSm) / (rows * row));
-  const int blocks = kRingPerSm * num_sms;
+  const int per_sm = limited ? 1 : kRingPerSm;
+  const int row = 4 * a.I, rows = std::max(1, kRingPerSm / per_sm * kChunk / row);
+  const int stages = std::min(kMaxRing, ring_bytes(per_sm) / (rows * row));
+  const int blocks = per_sm * num_sms;
   // whole rows only (no masked layout), and enough chunks for every block to
   // make up for the ring's 2 us of start (measured both ways, I = 256 to 4096:
   // with a checkpoint the ring is ahead from about 6 chunks per block, 46 to 41
   // us at 16384 x 2048, without one from 14, 61 to 58 us at 32647 x 2048)
   if (!a.masked_m && stages >= 2 && total < (1ll << 31) &&
       total >= (a.CQ ? 6ll : 14ll) * blocks * rows)
-    return launch_dependent(ue8m0 ? swiglu_ring_kernel<true> : swiglu_ring_kernel<false>,
-                            dim3(blocks), SG_THREADS, stream, stages * rows * row, a, rows, stages);
-  return launch_dependent(ue8m0 ? swiglu_kernel<true> : swiglu_kernel<false>,
-                          grid_of(a.G, a.M, a.I), SG_THREADS, stream, 0, a);
+    return launch_dependent(limited ? swiglu_ring_kernel<UE8M0, kRingPerSm * SG_THREADS>
+                                    : swiglu_ring_kernel<UE8M0, SG_THREADS>,
+                            dim3(blocks), kRingPerSm / per_sm * SG_THREADS, stream, stages * rows * row, a,
+                            rows, stages);
+  if (limited)
+    return launch_dependent(swiglu_walk_kernel<UE8M0>, walk_grid(a.G, a.M, a.I, num_sms), SG_WALK, stream, 0,
+                            a);
+  return launch_dependent(swiglu_kernel<UE8M0>, grid_of(a.G, a.M, a.I), SG_THREADS, stream, 0, a);
 }
 
-cudaError_t launch_swiglu_backward(const SwigluBwd& a, cudaStream_t stream) {
+}  // namespace
+
+cudaError_t swiglu_set_up() {
+  constexpr int two = kRingPerSm * SG_THREADS;
+  const std::pair<const void*, int> kernels[] = {
+      {reinterpret_cast<const void*>(swiglu_ring_kernel<false, SG_THREADS>), kRingPerSm},
+      {reinterpret_cast<const void*>(swiglu_ring_kernel<true, SG_THREADS>), kRingPerSm},
+      {reinterpret_cast<const void*>(swiglu_ring_kernel<false, two>), 1},
+      {reinterpret_cast<const void*>(swiglu_ring_kernel<true, two>), 1}};
+  for (const auto& [k, per_sm] : kernels) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(per_sm));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_swiglu(const SwigluFwd& a, bool ue8m0, int num_sms, bool limited,
+                          cudaStream_t stream) {
+  return ue8m0 ? launch_fwd<true>(a, num_sms, limited, stream)
+               : launch_fwd<false>(a, num_sms, limited, stream);
+}
+
+cudaError_t launch_swiglu_backward(const SwigluBwd& a, int num_sms, bool limited,
+                                   cudaStream_t stream) {
+  if (limited)
+    return launch_dependent(swiglu_backward_walk_kernel, walk_grid(a.G, a.M, a.I, num_sms), SG_WALK, stream,
+                            0, a);
   return launch_dependent(swiglu_backward_kernel, grid_of(a.G, a.M, a.I), SG_THREADS, stream, 0, a);
 }
 

@@ -32,10 +32,13 @@ struct SwigluBwd {
   unsigned int* status;
 };
 
-// The caller has validated the arguments (I % 128 == 0, I / 128 and G <=
-// 65535, 16-byte aligned tensors, ld >= M).
+// The caller has validated the arguments (I % 128 == 0, I / 128 <= 32767, G <=
+// 65535, 16-byte aligned tensors, ld >= M).  limited: fewer SMs than the device
+// has, so no grid of more blocks.
 cudaError_t swiglu_set_up();  // opts the kernels into their shared memory (once per device)
-cudaError_t launch_swiglu(const SwigluFwd& a, bool ue8m0, int num_sms, cudaStream_t stream);
-cudaError_t launch_swiglu_backward(const SwigluBwd& a, cudaStream_t stream);
+cudaError_t launch_swiglu(const SwigluFwd& a, bool ue8m0, int num_sms, bool limited,
+                          cudaStream_t stream);
+cudaError_t launch_swiglu_backward(const SwigluBwd& a, int num_sms, bool limited,
+                                   cudaStream_t stream);
 
 }  // namespace dgk

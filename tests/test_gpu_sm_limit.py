@@ -11,6 +11,7 @@ from tests import test_gpu_norm as N
 from tests.launches import launched
 from tests.test_gpu_bf16_ragged import ints
 from tests.test_gpu_swiglu import normal
+from tests.test_gpu_swiglu_ring import Activation
 
 pytestmark = pytest.mark.gpu
 
@@ -120,4 +121,52 @@ def test_norm_gradient(shape, residual, sms):
     R.check_close(dX, dx, N.REL * (mag + (dR.double().abs() if residual else 0.0)), "dX")
     lim = (64 + M / min(sms, 16)) * 2 * R.U32 * (dY.double() * xh).abs().sum(0)
     assert ((dW.double() - dw).abs() <= lim).all(), "dW"
+    assert dg.get_device_status() == 0
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 128), (1, 37, 256), (1, 200, 2048), (1, 4111, 640), (3, 57, 384),
+                                   (2, 301, 4224), (1, 60, 16384)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("ue8m0,outs", [(False, "YQC"), (True, "Q")])
+@pytest.mark.parametrize("sms", LIMITS)
+def test_activation(shape, ue8m0, outs, sms):
+    a = Activation(*shape, ue8m0, outs, seed=sum(shape))
+    within(sms, a)
+    a.check()
+
+
+MASKED = [(3, 64, 512, [64, 0, 33]), (8, 650, 384, [650, 3, 0, 0, 129, 640, 32, 1]), (2, 40, 256, [0, 0])]
+
+
+@pytest.mark.parametrize("G,M,I,rows", MASKED)
+@pytest.mark.parametrize("ue8m0", [False, True])
+@pytest.mark.parametrize("sms", LIMITS)
+def test_masked_activation(G, M, I, rows, ue8m0, sms):
+    from tests.test_gpu_swiglu import check
+    a = Activation(G, M, I, ue8m0, "YQC", seed=M)
+    for z, n in enumerate(rows):
+        a.GU[z, n:] = float("nan")
+    mm = ints(rows)
+    fn = dg.swiglu_quantize_fp8_1x128_ue8m0 if ue8m0 else dg.swiglu_quantize_fp8_1x128
+    within(sms, lambda s: fn(a.GU, a.Y, a.Q, a.sa, a.CQ, a.csa, G, M, I, a.ld, masked_m=mm, stream=s))
+    check(a.GU, (a.Y, a.Q, a.sa, a.CQ, a.csa), rows, ue8m0, f"masked on {sms} SMs")
+    assert dg.get_device_status() == 0
+
+
+@pytest.mark.parametrize("G,M,I,rows", MASKED + [(1, 700, 2048, None)])
+@pytest.mark.parametrize("sms", LIMITS)
+def test_activation_gradient(G, M, I, rows, sms):
+    """The same bits as without a limit."""
+    GU, dY = normal(G, M, 2 * I, seed=M, scale=1.5), normal(G, M, I, seed=I, scale=0.05)
+    ld = (M + 3) // 4 * 4
+    CQ = torch.zeros(G, M, 2 * I, dtype=torch.uint8, device="cuda")
+    csa = torch.zeros(G, 2 * I // 128, ld, device="cuda")
+    dg.quantize_fp8_1x128(GU, CQ, csa, G, M, 2 * I, ld)
+    mm = None if rows is None else ints(rows)
+    outs = [[torch.full((G, M, w * I), -3.0, dtype=torch.bfloat16, device="cuda") for w in (2, 1)]
+            for _ in range(2)]
+    call = lambda o, s: dg.swiglu_backward_fp8_1x128(CQ, csa, dY, o[0], o[1], G, M, I, ld, masked_m=mm,
+                                                     stream=s)
+    call(outs[0], None)
+    within(sms, lambda s: call(outs[1], s))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
     assert dg.get_device_status() == 0

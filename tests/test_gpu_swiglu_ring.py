@@ -76,7 +76,7 @@ class Activation:
 SHAPES = [(1, 11003, 2048, 0), (1, 34700, 640, 0), (3, 3651, 2048, 0), (1, 1833, 8192, 0),
           (1, 175200, 128, 0), (2, 1831, 6144, 0),
           (1, 2701, 128, 1), (1, 601, 640, 1), (1, 401, 2048, 2), (5, 83, 2048, 2), (3, 47, 4224, 3),
-          (1, 151, 8192, 2)]
+          (1, 151, 8192, 2), (1, 60, 16384, 2)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
