@@ -353,8 +353,9 @@ dg_status dg_swiglu_backward_fp8_1x128(const void* CQ, const float* csa, const v
  * zero and the total is clamped to M_total; both are reported as
  * DG_ERR_KS_RANGE by dg_get_device_status.  Sums in fp32, one rounding.
  * N and K positive multiples of 8 (else DG_ERR_UNSUPPORTED_SHAPE); 1 <=
- * num_groups <= 1024; tensors 16-byte, sizes 4-byte aligned.  M_total == 0 is
- * a no-op. */
+ * num_groups <= 1024; tensors 16-byte, sizes 4-byte aligned.  Refused as too large
+ * (DG_ERR_UNSUPPORTED_SHAPE): N of 2^23 or more, M_total or K within 8192 of 2^31,
+ * weights of 2^34 elements a group, 2^38 of A or D.  M_total == 0 is a no-op. */
 dg_status dg_m_grouped_gemm_bf16_nt_ragged(const void* A, const void* B, void* D, const int32_t* ms,
                                            int M_total, int N, int K, int num_groups,
                                            void* stream);
@@ -366,8 +367,8 @@ dg_status dg_m_grouped_gemm_bf16_nn_ragged(const void* A, const void* B, void* D
  *   A  bf16 [K_total][M], B bf16 [K_total][N], ks int32 [num_groups] on the
  *   device (as ms above), C bf16 [num_groups][M][N] or null (may be D itself),
  *   D  bf16 [num_groups][M][N]: all of it is written, a group without rows as C
- *   or +0.  M and N multiples of 8.  M == 0 is a no-op; with K_total == 0, A and
- *   B may be null. */
+ *   or +0.  M and N multiples of 8 (too large as above, of K_total and M).  M == 0
+ *   is a no-op; with K_total == 0, A and B may be null. */
 dg_status dg_k_grouped_gemm_bf16_tn_ragged(const void* A, const void* B, const void* C, void* D,
                                            const int32_t* ks, int num_groups, int M, int N,
                                            int K_total, void* stream);

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "dg.h"
 #include "dg_bf16.h"
@@ -113,7 +114,9 @@ dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void
   if (N < 8 || N % 8 != 0 || (!tn && (K < 8 || K % 8 != 0)) || (tn && M % 8 != 0))
     return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "N=%d, %s=%d: need positive multiples of 8", N,
                 tn ? "M" : "K", tn ? M : K);
-  if (N >= (1 << 23) || (long long)N * K >= (1ll << 34) || (long long)N * M >= (1ll << 34) ||
+  // (the kernels' 32-bit counters step past these extents by less than 8192)
+  constexpr int kMostExtent = INT_MAX - 8192;
+  if (std::max(std::max(rows, K), M) > kMostExtent || N >= (1 << 23) || (long long)N * K >= (1ll << 34) || (long long)N * M >= (1ll << 34) ||
       ((long long)rows / 16 + G) * (N / 64 + 1) >= (1ll << 31) ||
       (long long)G * (M / 16 + 1) * (N / 64 + 1) >= (1ll << 31) ||
       (long long)rows * std::max(std::max(N, K), M) >= (1ll << 38))
