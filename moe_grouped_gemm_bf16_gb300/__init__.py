@@ -196,8 +196,12 @@ def _stream(s):
             torch = sys.modules.get("torch")   # (a process that never imported it has no torch stream)
             if torch is None or not torch.cuda.is_initialized():
                 return None
-            # (raw handles take 0.2 us; a Stream object costs 3 us)
-            _torch_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+            # (raw handles take 0.2 us, but their names are private; a Stream object
+            # costs 3 us)
+            raw = [getattr(torch._C, f, None) for f in ("_cuda_getDevice", "_cuda_getCurrentRawStream")]
+            if None in raw:
+                raw = [lambda: None, lambda device: int(torch.cuda.current_stream().cuda_stream)]
+            _torch_stream = tuple(raw)
         device, stream = _torch_stream
         return stream(device())
     if isinstance(s, int):
