@@ -10,6 +10,7 @@ loaded, else the legacy default stream).
 There is no fallback: if the library has not been built, `lib()` raises.
 """
 import ctypes
+import importlib.machinery
 import os
 import sys
 
@@ -37,8 +38,9 @@ LIB_PATH = os.path.join(HERE, "libdg.so")
 #: the checked build (bounds and ring-fill checks in every kernel), loaded in
 #: place of libdg.so when the environment sets DG_DEBUG=1
 LIB_DEBUG_PATH = os.path.join(HERE, "libdg_debug.so")
-#: CPython module through which the operators around the GEMMs are called
-BINDING_PATH = os.path.join(HERE, "_binding.so")
+#: CPython module through which the operators around the GEMMs are called (of this
+#: interpreter: its tag is in the name)
+BINDING_PATH = os.path.join(HERE, "_binding" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 STATUS_NAMES = {
     0: "DG_OK", 1: "DG_ERR_INVALID_ARG", 2: "DG_ERR_UNSUPPORTED_SHAPE", 3: "DG_ERR_MISALIGNED",
@@ -87,20 +89,23 @@ class DGConfig(ctypes.Structure):
 
 
 _LIB = None
-_calls = None   # the CPython module _binding, opened with the library (csrc/dg_ops_binding.cpp)
+_calls = None   # the CPython module _binding, once opened (csrc/dg_ops_binding.cpp)
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 
 
+def _needed(path):
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with "
+                           "`python -m moe_grouped_gemm_bf16_gb300._build`")
+
+
 def lib():
     """The loaded library.  Raises if it has not been built (no fallback)."""
-    global _LIB, _calls
+    global _LIB
     if _LIB is None:
         path = LIB_DEBUG_PATH if os.environ.get("DG_DEBUG", "0") not in ("", "0") else LIB_PATH
-        for built in (path, BINDING_PATH):
-            if not os.path.exists(built):
-                raise RuntimeError(f"{built} is missing: build it with "
-                                   "`python -m moe_grouped_gemm_bf16_gb300._build`")
+        _needed(path)
         L = ctypes.CDLL(path)
         L.dg_gemm_fp8_fp8_bf16_nt.argtypes = [_vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp]
         L.dg_gemm_fp8_fp8_bf16_nt_add_c.argtypes = [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i,
@@ -163,17 +168,20 @@ def lib():
             if f not in ("dg_last_error_string", "dg_num_output_tiles",
                          "dg_rms_norm_backward_workspace_bytes"):
                 getattr(L, f).restype = _i
-        from . import _binding
-        _binding.open(path)
-        _LIB, _calls = L, _binding
+        _LIB = L
     return _LIB
 
 
 def _ops():
     """The entry points of the operators around the GEMMs, with _ptr done on
     their arguments."""
+    global _calls
     if _calls is None:
-        lib()
+        path = lib()._name
+        _needed(BINDING_PATH)
+        from . import _binding
+        _binding.open(path)
+        _calls = _binding
     return _calls
 
 

@@ -1,5 +1,5 @@
 """Builds the C-ABI library `libdg.so` (the CUDA kernels and their host
-launcher) for sm_103a with nvcc, and the CPython module `_binding.so` that calls
+launcher) for sm_103a with nvcc, and the CPython module `_binding` that calls
 some of its entry points, in the package directory.
 
 `python -m moe_grouped_gemm_bf16_gb300._build` or `build()`.  The translation
@@ -7,10 +7,12 @@ units compile in parallel; the result links the CUDA runtime statically so the
 library does not depend on which libcudart the process loaded first.
 """
 import concurrent.futures as cf
+import importlib.machinery
 import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdg.so")
 LIB_DEBUG = os.path.join(HERE, "libdg_debug.so")
-BINDING = os.path.join(HERE, "_binding.so")
+# (another interpreter, whose tag differs, builds and loads its own)
+BINDING = os.path.join(HERE, "_binding" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 SOURCES = ["dg_host.cu", "dg_inst_dense.cu", "dg_inst_contiguous.cu", "dg_inst_masked.cu", "dg_inst_mn.cu", "dg_inst_ue8m0.cu", "dg_inst_ue8m0_mn.cu", "dg_inst_bs.cu",
            "dg_inst_bs_mn.cu", "dg_quant.cu", "dg_norm.cu", "dg_swiglu.cu", "dg_bf16.cu", "dg_bf16_few.cu",
@@ -40,7 +43,9 @@ def _deps():
 
 
 def _build_binding(force):
-    """The CPython module (host code only; it opens the library at run time)."""
+    """The CPython module (host code only; it opens the library at run time).  It
+    needs a C++ compiler and Python's headers; without them the library, which
+    needs neither, is still of use: a warning says what is missing."""
     src = os.path.join(CSRC, "dg_ops_binding.cpp")
     deps = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "dg.h")))
     if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= deps:
@@ -48,9 +53,17 @@ def _build_binding(force):
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-Wall", "-fPIC", "-shared", "-I",
            INCLUDE, "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-ldl"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        log = None if r.returncode == 0 else r.stdout + r.stderr
+    except OSError as e:
+        log = str(e)
+    if log is not None:
+        if os.path.exists(BINDING):   # (of an older header)
+            os.remove(BINDING)
+        warnings.warn(f"{os.path.basename(BINDING)} was not built, the operators around the GEMMs cannot "
+                      f"be called from Python ({cmd[0]} failed for {src}):\n{log}", RuntimeWarning)
+        return
     os.replace(tmp, BINDING)
 
 
@@ -60,9 +73,14 @@ def build(force=False, verbose=False, debug=False):
     checks before each TMA load and plain global store, fill checks after
     each ring wait, failures reported in the device status word)."""
     lib = LIB_DEBUG if debug else LIB
+    _build_library(lib, force, verbose, debug)
     _build_binding(force)
+    return lib
+
+
+def _build_library(lib, force, verbose, debug):
     if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps():
-        return lib
+        return
     bdir = os.path.join(BUILD, "debug") if debug else BUILD
     os.makedirs(bdir, exist_ok=True)
     cc = nvcc()
@@ -92,7 +110,6 @@ def build(force=False, verbose=False, debug=False):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":
