@@ -232,22 +232,31 @@ def _code_only(text):
     return " ".join(text.split())
 
 
-def kernel_source_hash(workload):
-    """Hash of the code a workload's kernels and launch choices come from:
-    the quantiser's own files for quantize_act, the FP8 GEMMs' for the GEMM
-    workloads (the host code, which plans and launches both, in each; the
-    files of the operators around them in none); comments and blank space do
-    not count."""
-    h = hashlib.sha256()
+def kernel_sources(workload):
+    """The files a workload's kernels and launch choices come from: its
+    translation units (the quantiser's, or the FP8 GEMMs' instances) with all
+    that they include, and the host code, which plans and launches both."""
     csrc = os.path.join(ROOT, "moe_grouped_gemm_bf16_gb300", "csrc")
-    quant = workload == "quantize_act"
-    for f in sorted(os.listdir(csrc)):
-        if f.startswith(("dg_norm", "dg_swiglu", "dg_bf16", "dg_ops")):
+    there = os.listdir(csrc)
+    left = [f for f in there if f.endswith(".cu") and
+            f.startswith("dg_quant" if workload == "quantize_act" else "dg_inst_")]
+    found = {"dg_host.cu"}
+    while left:
+        f = left.pop()
+        if f in found or f not in there:
             continue
-        if f != "dg_host.cu" and f.startswith("dg_quant") != quant:
-            continue
+        found.add(f)
         with open(os.path.join(csrc, f), encoding="utf-8") as fh:
-            h.update(f.encode())
+            left += re.findall(r'^\s*#include "([^"]+)"', fh.read(), flags=re.M)
+    return [os.path.join(csrc, f) for f in sorted(found)]
+
+
+def kernel_source_hash(workload):
+    """Hash of kernel_sources(workload); comments and blank space do not count."""
+    h = hashlib.sha256()
+    for path in kernel_sources(workload):
+        with open(path, encoding="utf-8") as fh:
+            h.update(os.path.basename(path).encode())
             h.update(_code_only(fh.read()).encode())
     return h.hexdigest()[:16]
 
