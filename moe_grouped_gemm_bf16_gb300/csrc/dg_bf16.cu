@@ -98,7 +98,9 @@ struct BfSmem {
                        T_FULL = 3 * BF_MAX_STAGES, T_EMPTY = T_FULL + 2, MMA_DONE = T_EMPTY + 2,
                        NUM_BARS = MMA_DONE + 1;
   static constexpr int MISC = NUM_BARS * 8;
-  static constexpr int TAB = (MISC + 8 + 15) / 16 * 16;
+  // (checked build: fill counters of the lane and the column operand's slots)
+  static constexpr int FILLS = MISC + 8;
+  static constexpr int TAB = (FILLS + (kDebug ? 2 * BF_MAX_STAGES * 4 : 0) + 15) / 16 * 16;
   __host__ __device__ static constexpr int fixed(int G) { return 1024 + TAB + 2 * (G + 1) * 4; }
 };
 
@@ -178,8 +180,13 @@ __device__ __forceinline__ BfTile bf_tile(int t, const BfParams& p, const int* f
   return T;
 }
 
+__device__ __forceinline__ size_t bf_elements(const BfParams& p, bool tn) {
+  return (tn ? static_cast<size_t>(p.G) * p.M : static_cast<size_t>(p.rows)) * p.N;
+}
+
 // Four columns of a row of D: the addend in fp32, then one rounding.
-__device__ __forceinline__ void store_four(const BfParams& p, size_t at, float4 v) {
+__device__ __forceinline__ void store_four(const BfParams& p, bool tn, size_t at, float4 v) {
+  if (!in_bounds(p, at, 4, bf_elements(p, tn))) return;
   if (p.C) {
     const uint2 c = *reinterpret_cast<const uint2*>(p.C + at);
     v.x += __uint_as_float(c.x << 16);
@@ -230,7 +237,7 @@ __device__ __forceinline__ void add_partials(const BfParams& p, const BfTile& T,
           sum.x += x[r][j].x; sum.y += x[r][j].y; sum.z += x[r][j].z; sum.w += x[r][j].w;
         }
         if (j < rows)
-          store_four(p, ((TN ? static_cast<size_t>(T.g) * p.M : 0) + T.q0 + c + j) * p.N + l, sum);
+          store_four(p, TN, ((TN ? static_cast<size_t>(T.g) * p.M : 0) + T.q0 + c + j) * p.N + l, sum);
       }
     }
   }
@@ -255,6 +262,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
   auto bar = [&](int i) -> uint32_t { return sbase + ring + 8 * i; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + ring + L::MISC);
   volatile uint32_t* abort_flag = misc + 1;
+  volatile uint32_t* fills = reinterpret_cast<uint32_t*>(smem + ring + L::FILLS);
   int* first = reinterpret_cast<int*>(smem + ring + L::TAB);
   int* blk = first + p.G + 1;
   const int cluster = (PAIR ? 2 : 1) * p.split;
@@ -277,6 +285,8 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     }
     mbar_init(bar(L::MMA_DONE), 1);
     misc[1] = 0;
+    if constexpr (kDebug)
+      for (int i = 0; i < 2 * BF_MAX_STAGES; ++i) fills[i] = 0;
     fence_mbarrier_init();
     prefetch_tmap(&maps.p[0]);
     prefetch_tmap(&maps.q[0]);
@@ -393,6 +403,8 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
               dbg_fail(p, ST_DEBUG_BOUNDS, abort_flag);
               go = false;
             }
+            const int slot = lanes_op ? s : BF_MAX_STAGES + s;
+            if (go) fills[slot] = fills[slot] + 1;
           }
           if (go) {
             const uint32_t dst = base + s * bytes;
@@ -465,6 +477,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       const uint16_t mask = static_cast<uint16_t>(PAIR ? 0x3u << leader : 0x1u);
       int s = 0, b = 0;
       uint32_t ph = 0, bph = 0;
+      uint32_t turn = 1;   // checked build: the fill that a slot has to hold
       for (int t = unit; t < tiles; t += units) {
         const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank, group);
         if (T.kbeg == T.kend) continue;
@@ -484,6 +497,12 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
           ok = (PAIR && tail ? wait_bar<true>(bar(L::FULL + s), ph, abort_flag, p)
                              : wait_bar(bar(L::FULL + s), ph, abort_flag, p)) && ok;
           tc_fence_after();
+          if constexpr (kDebug) {
+            if (ok && (fills[s] != turn || fills[BF_MAX_STAGES + s] != turn)) {
+              dbg_fail(p, ST_DEBUG_PHASE, abort_flag);
+              ok = false;
+            }
+          }
           if (issuer && ok) {
             const uint32_t ps = sbase + s * p.p_bytes, qs = sbase + q_off + s * p.q_bytes;
             const uint64_t pd = P_MN ? smem_desc_sw128_mnmajor(ps, ATOM) : smem_desc_sw128_kmajor(ps);
@@ -517,7 +536,11 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
             }
           }
           __syncwarp();
-          if (++s == p.stages) { s = 0; ph ^= 1; }
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1;
+            if constexpr (kDebug) ++turn;
+          }
         }
         b ^= 1;
         if (b == 0) bph ^= 1;
@@ -646,6 +669,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
             const int r = u / per, l = l0 + 8 * (u - r * per);
             if (l >= l_end) continue;
             const size_t at = (static_cast<size_t>(T.g) * p.M + T.q0 + r) * p.N + l;
+            if (!in_bounds(p, at, 8, bf_elements(p, TN))) continue;
             *reinterpret_cast<uint4*>(p.D + at) =
                 p.C ? *reinterpret_cast<const uint4*>(p.C + at) : make_uint4(0, 0, 0, 0);
           }

@@ -91,8 +91,11 @@ __device__ __forceinline__ FewGroup few_group(const FewParams& p, int z, bool re
   return f;
 }
 
-__device__ __forceinline__ uint16_t to_bf16(float x) {
-  return static_cast<uint16_t>(pack_bf16x2(x, 0.f));
+// nt, nn: a value of D.
+__device__ __forceinline__ void store_one(const FewParams& p, int t, int n, float sum) {
+  const size_t at = static_cast<size_t>(t) * p.N + n;
+  if (in_bounds(p, at, 1, static_cast<size_t>(p.rows) * p.N))
+    p.D[at] = static_cast<uint16_t>(pack_bf16x2(sum, 0.f));
 }
 
 // One step of adding up V values over the lanes of a warp: with V > 1 the lanes of
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(NT_THREADS, NT_PER_SM) few_nt_kernel(const Few
       float sum = 0.f;
       for (int w = 0; w < split; ++w)
         sum += red[turn][((c / NT_COLS) * split + w) * (FEW_ROWS * NT_COLS) + r * NT_COLS + c % NT_COLS];
-      p.D[static_cast<size_t>(f.first + r0 + r) * p.N + n] = to_bf16(sum);
+      store_one(p, f.first + r0 + r, n, sum);
     }
   }
 }
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(NN_THREADS, 2) few_nn_kernel(const FewParams p
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) sum += red[(w * FEW_ROWS + r) * COLS + c];
-      p.D[static_cast<size_t>(f.first + r0 + r) * p.N + n0 + c] = to_bf16(sum);
+      store_one(p, f.first + r0 + r, n0 + c, sum);
     }
   }
 }
@@ -314,7 +317,8 @@ __global__ void __launch_bounds__(TN_THREADS) few_tn_kernel(const FewParams p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i].v[j] = add2(acc[i].v[j], c.v[j]);
     }
-    *reinterpret_cast<uint4*>(p.D + at + static_cast<size_t>(i) * p.N) = pairs_to_bf16x8(acc[i]);
+    if (in_bounds(p, at + static_cast<size_t>(i) * p.N, 8, static_cast<size_t>(p.G) * p.M * p.N))
+      *reinterpret_cast<uint4*>(p.D + at + static_cast<size_t>(i) * p.N) = pairs_to_bf16x8(acc[i]);
   }
 }
 

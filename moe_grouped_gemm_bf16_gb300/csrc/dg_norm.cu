@@ -85,6 +85,12 @@ __device__ __forceinline__ float team_sum(const Team<FOLD>& t, float v, float* r
   return warp_sum(v);
 }
 
+// Checked build: vector `at` of a tensor [M][K].
+template <class P>
+__device__ __forceinline__ bool in_tensor(const P& a, size_t at) {
+  return in_bounds(a, at, 1, static_cast<size_t>(a.M) * (a.K >> 3));
+}
+
 // Output of a normalised row: the thread's VPT vectors h (w: the weight's,
 // packed), those below nv stored.
 template <int VPT, bool UE8M0>
@@ -99,7 +105,8 @@ __device__ __forceinline__ void norm_output(const NormFwd& a, int m, int nv, int
     const Pairs wp = bf16x8_to_pairs(w[i]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[i].v[j] = mul2(mul2(h[i].v[j], rs2), wp.v[j]);
-    if (a.Y && v < nv) static_cast<uint4*>(a.Y)[base + v] = pairs_to_bf16x8(h[i]);
+    if (a.Y && v < nv && in_tensor(a, base + v))
+      static_cast<uint4*>(a.Y)[base + v] = pairs_to_bf16x8(h[i]);
     if (!a.Q) continue;
     // a 128-column group is 16 consecutive lanes (T is a multiple of 32); its
     // even lanes compute 448 / a, which all take, its odd ones the scale a / 448
@@ -111,19 +118,21 @@ __device__ __forceinline__ void norm_output(const NormFwd& a, int m, int nv, int
       float f;
       uint32_t e8;
       group_factor<true>(amax, f, e8);
-      if (v < nv) {
+      if (v < nv && in_tensor(a, base + v)) {
         static_cast<uint2*>(a.Q)[base + v] = pairs_to_e4m3x8(h[i], f);
-        if ((v & 15) == 1)
+        if ((v & 15) == 1 &&
+            in_bounds(a, static_cast<size_t>(v >> 6) * a.ld_sa + m, 1, static_cast<size_t>((kb + 3) >> 2) * a.ld_sa))
           store_scale<true>(static_cast<float*>(a.sa), 0, kb, a.ld_sa, v >> 4, m, amax, e8);
       }
     } else {
       const bool odd = v & 1;
       const float quot = __fdiv_rn(odd ? amax : 448.0f, odd ? 448.0f : amax);
       const float f = __shfl_sync(0xffffffffu, quot, threadIdx.x & 30);
-      if (v < nv) {
+      if (v < nv && in_tensor(a, base + v)) {
         static_cast<uint2*>(a.Q)[base + v] = pairs_to_e4m3x8(h[i], f);
-        if ((v & 15) == 1)
-          static_cast<float*>(a.sa)[static_cast<size_t>(v >> 4) * a.ld_sa + m] = quot;
+        const size_t at = static_cast<size_t>(v >> 4) * a.ld_sa + m;
+        if ((v & 15) == 1 && in_bounds(a, at, 1, static_cast<size_t>(kb) * a.ld_sa))
+          static_cast<float*>(a.sa)[at] = quot;
       }
     }
   }
@@ -146,7 +155,7 @@ __device__ __forceinline__ float add_residual(const NormFwd& a, size_t at, const
     const Pairs rp = bf16x8_to_pairs(r);
 #pragma unroll
     for (int j = 0; j < 4; ++j) h.v[j] = add2(h.v[j], rp.v[j]);
-    if (a.H) static_cast<uint4*>(a.H)[at] = pairs_to_bf16x8(h);
+    if (a.H && in_tensor(a, at)) static_cast<uint4*>(a.H)[at] = pairs_to_bf16x8(h);
   }
   float2 ss = mul2(h.v[0], h.v[0]);
 #pragma unroll
@@ -181,7 +190,7 @@ __device__ __forceinline__ void norm_row(const NormFwd& a, const Team<FOLD>& t, 
   }
   ss = team_sum(t, ss, red);
   const float rs = __frsqrt_rn(ss / static_cast<float>(a.K) + a.eps);
-  if (t.tid == 0 && a.rstd) a.rstd[m] = rs;
+  if (t.tid == 0 && a.rstd && in_bounds(a, m, 1, a.M)) a.rstd[m] = rs;
   norm_output<VPT, UE8M0>(a, m, nv, t.tid, T, h, rs, w);
 }
 
@@ -212,15 +221,12 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2][32];
   __shared__ __align__(8) uint64_t full[kMaxRing];
-  __shared__ uint32_t aborted;
+  __shared__ uint32_t aborted, fills[kDebugRing];
   volatile uint32_t* abort_flag = &aborted;
   const int T = blockDim.x, nv = a.K >> 3, step = gridDim.x;
-  ChunkRing ring{{a.X, a.R, nullptr}, smem, full, stages, a.R ? 2 : 1, a.K * 2, a.debug_flags, 0, 0};
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) mbar_init(smem_u32(full + s), 1);
-    aborted = 0;
-    fence_mbarrier_init();
-  }
+  ChunkRing ring{{a.X, a.R, nullptr}, smem, full, stages, a.R ? 2 : 1, a.K * 2,
+                 {static_cast<size_t>(a.M) * a.K * 2, a.status, abort_flag, fills}, a.debug_flags, 0, 0};
+  if (threadIdx.x == 0) ring.init(abort_flag);
   grid_dep_wait();
   grid_dep_launch_dependents();
   if (threadIdx.x == 0)
@@ -234,7 +240,8 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
   uint32_t ph = 0;
   for (long long m = blockIdx.x; m < a.M; m += step, par ^= 1) {
     // (once a wait has failed a later turn of the ring may look complete)
-    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) && *abort_flag == 0;
+    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) && *abort_flag == 0 &&
+                    ring.holds(s, (m - blockIdx.x) / step / stages + 1);
     const size_t base = static_cast<size_t>(m) * nv;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
     Pairs h[VPT] = {};
@@ -251,7 +258,7 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
     if (threadIdx.x == 0 && go && m + static_cast<long long>(stages) * step < a.M)
       ring.fill(static_cast<int>(m) + stages * step, s);
     const float rs = __frsqrt_rn(ss / static_cast<float>(a.K) + a.eps);
-    if (threadIdx.x == 0 && a.rstd && go) a.rstd[m] = rs;
+    if (threadIdx.x == 0 && a.rstd && go && in_bounds(a, m, 1, a.M)) a.rstd[m] = rs;
     norm_output<VPT, UE8M0>(a, static_cast<int>(m), go ? nv : 0, t.tid, T, h, rs, w);
     if (++s == stages) { s = 0; ph ^= 1; }
   }
@@ -322,7 +329,8 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_kernel(const NormBwd a
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * T + threadIdx.x;
-      if (v < nv) static_cast<uint4*>(a.dX)[base + v] = grad_row(g[i], xh[i], rs, mean, r[i]);
+      if (v < nv && in_tensor(a, base + v))
+        static_cast<uint4*>(a.dX)[base + v] = grad_row(g[i], xh[i], rs, mean, r[i]);
     }
     return;
   }
@@ -347,7 +355,8 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_kernel(const NormBwd a
   for (int k = threadIdx.x; k < 64; k += T) {
     float sum = 0.f;
     for (int i = 0; i < chains; ++i) sum += part[i * 64 + k];
-    a.dW[(blockIdx.x - a.M) * 64 + k] = sum;
+    const int at = (blockIdx.x - a.M) * 64 + k;
+    if (in_bounds(a, at, 1, a.K)) a.dW[at] = sum;
   }
 }
 
@@ -359,7 +368,7 @@ rms_norm_backward_ring_kernel(const NormBwd a, int threads, int teams, int stage
   constexpr int TEAMS = FOLD ? kMaxTeams : 1;
   __shared__ float reds[TEAMS][2][32];
   __shared__ __align__(8) uint64_t fulls[TEAMS][kMaxRing];
-  __shared__ uint32_t aborts[TEAMS];
+  __shared__ uint32_t aborts[TEAMS], fills[TEAMS][kDebugRing];
   const Team<FOLD> t(threads);
   float(*red)[32] = reds[t.id];
   uint64_t* full = fulls[t.id];
@@ -367,12 +376,9 @@ rms_norm_backward_ring_kernel(const NormBwd a, int threads, int teams, int stage
   const int T = t.size, nv = a.K >> 3, step = FOLD ? teams : static_cast<int>(gridDim.x);
   const int ops = a.dR ? 3 : 2, bytes = a.K * 2;
   ChunkRing ring{{a.dY, a.H, a.dR}, smem + t.id * stages * ops * bytes, full, stages, ops, bytes,
-                 a.debug_flags, 0, 0};
-  if (t.tid == 0) {
-    for (int s = 0; s < stages; ++s) mbar_init(smem_u32(full + s), 1);
-    *abort_flag = 0;
-    fence_mbarrier_init();
-  }
+                 {static_cast<size_t>(a.M) * bytes, a.status, abort_flag, fills[t.id]}, a.debug_flags, 0,
+                 0};
+  if (t.tid == 0) ring.init(abort_flag);
   grid_dep_wait();
   grid_dep_launch_dependents();
   if (FOLD && t.rank >= teams) return;   // (the last block's; from here on a team is by itself)
@@ -393,7 +399,8 @@ rms_norm_backward_ring_kernel(const NormBwd a, int threads, int teams, int stage
   uint32_t ph = 0;
   for (long long m = t.rank; m < a.M; m += step, par ^= 1) {
     const float rs = __ldg(a.rstd + m);
-    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) && *abort_flag == 0;
+    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) && *abort_flag == 0 &&
+                    ring.holds(s, (m - t.rank) / step / stages + 1);
     const size_t base = static_cast<size_t>(m) * nv;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
     Pairs g[VPT], xh[VPT];
@@ -415,7 +422,7 @@ rms_norm_backward_ring_kernel(const NormBwd a, int threads, int teams, int stage
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * T + t.tid;
-      if (v >= nv || !go) continue;
+      if (v >= nv || !go || !in_tensor(a, base + v)) continue;
       if (!KEEP) {
         Pairs unused = {};
         grad_sums(x[v], x[nv + v], w[i], rs, g[i], xh[i], unused);
@@ -428,20 +435,25 @@ rms_norm_backward_ring_kernel(const NormBwd a, int threads, int teams, int stage
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = i * T + t.tid;
-    if (v >= nv) continue;
-    float4* out = reinterpret_cast<float4*>(a.part + static_cast<size_t>(t.rank) * a.K) + 2 * v;
+    const size_t at = static_cast<size_t>(t.rank) * a.K + 8 * v;
+    if (v >= nv || !in_bounds(a, at, 8, static_cast<size_t>(min(a.M, kNormBwdBlocks)) * a.K)) continue;
+    float4* out = reinterpret_cast<float4*>(a.part + at);
     out[0] = make_float4(dw[i].v[0].x, dw[i].v[0].y, dw[i].v[1].x, dw[i].v[1].y);
     out[1] = make_float4(dw[i].v[2].x, dw[i].v[2].y, dw[i].v[3].x, dw[i].v[3].y);
   }
   if (t.tid == 0 && *abort_flag) ring.drain(a);
 }
 
+struct StatusWord {
+  unsigned int* status;
+};
+
 // dW[k] = sum of the blocks' (teams') partial sums, in a fixed order: 32 columns
 // per block (WALK: at a time), 32 chains over the partials.
 template <bool WALK>
 __global__ void __launch_bounds__(1024)
 rms_norm_weight_grad_kernel(const float* __restrict__ part, float* __restrict__ dW, int blocks,
-                            int K) {
+                            int K, const StatusWord word) {
   grid_dep_wait();
   grid_dep_launch_dependents();
   __shared__ float s[32][33];
@@ -454,7 +466,7 @@ rms_norm_weight_grad_kernel(const float* __restrict__ part, float* __restrict__ 
     __syncthreads();
     // (transposed: warp r now sums the chains of column r)
     const float sum = warp_sum(s[c][r]);
-    if (c == 0) dW[k0 + r] = sum;
+    if (c == 0 && in_bounds(word, k0 + r, 1, K)) dW[k0 + r] = sum;
     if (!WALK) return;
     __syncthreads();   // the sums have been read
   }
@@ -587,7 +599,7 @@ cudaError_t launch_rms_norm_backward(const NormBwd& a, int num_sms, bool limited
   };
   auto add_up = [&](auto kernel, int parts, int blocks) {
     return launch_dependent(kernel, dim3(blocks), 1024, stream, 0, static_cast<const float*>(a.part), a.dW,
-                            parts, a.K);
+                            parts, a.K, StatusWord{a.status});
   };
   if (limited) {
     const int sums = std::min(num_sms, a.K / 32);

@@ -83,6 +83,14 @@ struct Place {
     gate = row * (I >> 2) + grp * 16 + j;
     up = gate + (I >> 3);
   }
+  // Checked build: the places lie in tensors of G batches, the row in its scales'.
+  template <class P>
+  __device__ __forceinline__ bool inside(const P& a) const {
+    const size_t rows = static_cast<size_t>(a.G) * a.M;
+    return in_bounds(a, at, 9, rows * (a.I >> 3)) && in_bounds(a, gate, 9, rows * (a.I >> 2)) &&
+           in_bounds(a, up, 9, rows * (a.I >> 2)) && in_bounds(a, grp, 1, a.I >> 7) &&
+           in_bounds(a, z, 1, a.G) && in_bounds(a, m, 1, a.M);
+  }
 };
 
 // One lane's share of a group, forward: v = {gate, gate + 8, up, up + 8}.
@@ -104,6 +112,7 @@ __device__ __forceinline__ void forward_group(const SwigluFwd& a, const Place& p
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       y[h].v[i] = mul2(mul2(g[h].v[i], sigmoid2(g[h].v[i])), u[h].v[i]);
+  on = on && p.inside(a);
   if (a.Y && on) {
     uint4* Y = static_cast<uint4*>(a.Y) + p.at;
     Y[0] = pairs_to_bf16x8(y[0]);
@@ -156,6 +165,7 @@ __device__ __forceinline__ void forward_group(const SwigluFwd& a, const Place& p
 __device__ __forceinline__ void backward_group(const SwigluBwd& a, const Place& p,
                                                const uint2 (&c)[4], float sg, float su,
                                                const uint4 (&dv)[2]) {
+  if (!p.inside(a)) return;
   uint4* dGU = static_cast<uint4*>(a.dGU);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -252,17 +262,14 @@ __global__ void __launch_bounds__(THREADS) swiglu_ring_kernel(const SwigluFwd a,
                                                               int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kMaxRing];
-  __shared__ uint32_t aborted;
+  __shared__ uint32_t aborted, fills[kDebugRing];
   volatile uint32_t* abort_flag = &aborted;
   const int lanes = a.I >> 4, total = a.G * a.M;   // lanes per row, rows
-  ChunkRing ring{{a.GU, nullptr, nullptr}, smem, full, stages, 1, rows * a.I * 4, a.debug_flags, 0, 0};
+  ChunkRing ring{{a.GU, nullptr, nullptr}, smem, full, stages, 1, rows * a.I * 4,
+                 {static_cast<size_t>(total) * a.I * 4, a.status, abort_flag, fills}, a.debug_flags, 0, 0};
   auto fill = [&](int c, int s) { ring.fill(c, s, min(rows, total - c * rows) * a.I * 4); };
   const int chunks = (total + rows - 1) / rows;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) mbar_init(smem_u32(full + s), 1);
-    aborted = 0;
-    fence_mbarrier_init();
-  }
+  if (threadIdx.x == 0) ring.init(abort_flag);
   grid_dep_wait();
   grid_dep_launch_dependents();
   if (threadIdx.x == 0)
@@ -284,7 +291,8 @@ __global__ void __launch_bounds__(THREADS) swiglu_ring_kernel(const SwigluFwd a,
     // wait that gives up may do so in some lanes only); after a failed wait
     // nothing more is loaded or stored
     const bool ok = __all_sync(0xffffffffu, wait_bar(smem_u32(full + s), ph, abort_flag, a) &&
-                                                *abort_flag == 0);
+                                                *abort_flag == 0 &&
+                                                ring.holds(s, (c - blockIdx.x) / gridDim.x / stages + 1));
     const int n = ok ? min(rows, total - c * rows) * lanes : 0;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
     int r = r0, q = q0;

@@ -22,6 +22,19 @@ __device__ __forceinline__ void dbg_fail(const P& p, unsigned int code,
   *abort_flag = 1;
 }
 
+// Checked build: whether [at, at + n) lies in a tensor of `extent` elements (else
+// the access is to be skipped, and is reported).  Nothing in the regular build.
+template <class P>
+__device__ __forceinline__ bool in_bounds(const P& p, size_t at, size_t n, size_t extent) {
+  if constexpr (kDebug) {
+    if (at > extent || n > extent - at) {
+      raise_status(p, ST_DEBUG_BOUNDS);
+      return false;
+    }
+  }
+  return true;
+}
+
 // Bounded mbarrier wait.  Returns false (without waiting) once the CTA has
 // aborted, or after `timeout_ns`, in which case it records the timeout and
 // aborts the CTA.
