@@ -238,9 +238,10 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
   __syncthreads();
   int s = 0, par = 0;
   uint32_t ph = 0;
+  bool go = true;
   for (long long m = blockIdx.x; m < a.M; m += step, par ^= 1) {
     // (once a wait has failed a later turn of the ring may look complete)
-    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) && *abort_flag == 0 &&
+    const bool ok = go && wait_bar(smem_u32(full + s), ph, abort_flag, a) &&
                     ring.holds(s, (m - blockIdx.x) / step / stages + 1);
     const size_t base = static_cast<size_t>(m) * nv;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
     ss = team_sum(t, ss, red[par]);
     // every thread has read the slot: the row `stages` turns ahead may follow
     // (after a failed wait nothing more is loaded or stored)
-    const bool go = *abort_flag == 0;
+    go = *abort_flag == 0;
     if (threadIdx.x == 0 && go && m + static_cast<long long>(stages) * step < a.M)
       ring.fill(static_cast<int>(m) + stages * step, s);
     const float rs = __frsqrt_rn(ss / static_cast<float>(a.K) + a.eps);
@@ -399,7 +400,7 @@ rms_norm_backward_ring_kernel(const NormBwd a, int threads, int teams, int stage
   uint32_t ph = 0;
   for (long long m = t.rank; m < a.M; m += step, par ^= 1) {
     const float rs = __ldg(a.rstd + m);
-    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) && *abort_flag == 0 &&
+    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) &&
                     ring.holds(s, (m - t.rank) / step / stages + 1);
     const size_t base = static_cast<size_t>(m) * nv;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
@@ -458,7 +459,7 @@ rms_norm_weight_grad_kernel(const float* __restrict__ part, float* __restrict__ 
   grid_dep_launch_dependents();
   __shared__ float s[32][33];
   const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
-  for (int k0 = blockIdx.x * 32; k0 < K; k0 += gridDim.x * 32) {
+  auto sum_up = [&](int k0) {
     const int k = k0 + c;
     float acc = 0.f;
     for (int b = r; b < blocks; b += 32) acc += part[static_cast<size_t>(b) * K + k];
@@ -467,8 +468,14 @@ rms_norm_weight_grad_kernel(const float* __restrict__ part, float* __restrict__ 
     // (transposed: warp r now sums the chains of column r)
     const float sum = warp_sum(s[c][r]);
     if (c == 0 && in_bounds(word, k0 + r, 1, K)) dW[k0 + r] = sum;
-    if (!WALK) return;
-    __syncthreads();   // the sums have been read
+  };
+  if constexpr (WALK) {
+    for (int k0 = blockIdx.x * 32; k0 < K; k0 += gridDim.x * 32) {
+      sum_up(k0);
+      __syncthreads();   // the chains have been read
+    }
+  } else {
+    sum_up(blockIdx.x * 32);
   }
 }
 
