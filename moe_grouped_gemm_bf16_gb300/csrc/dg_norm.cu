@@ -22,9 +22,9 @@
 // Under a limit on the SMs a grid has one block per SM, whose threads are teams that
 // stand in for such blocks (132 of the 152 SMs: 4096 x 2048 forward 17.8 us, with all
 // 13.4; backward 27.6 and 24.8).
-// Measured: 4096 x 7168 forward 45 us (5.9 TB/s; one block per row 47 us),
-// 8192 x 7168 backward 77 us (6.1 TB/s; the one-launch form 171 us), without dR
-// 61 us (5.8 TB/s), 8192 x 4224 40 us.
+// Measured: 4096 x 7168 forward 45 us (5.9 TB/s; one block per row 47 us), 3333 x
+// 6656 without a residual 27 us; 8192 x 7168 backward 77 us (6.1 TB/s; the
+// one-launch form 171 us), without dR 61 us (5.8 TB/s), 8192 x 4224 40 us.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(1024) rms_norm_ring_kernel(const NormFwd a, in
   bool go = true;
   for (long long m = blockIdx.x; m < a.M; m += step, par ^= 1) {
     // (once a wait has failed a later turn of the ring may look complete)
-    const bool ok = go && wait_bar(smem_u32(full + s), ph, abort_flag, a) &&
+    const bool ok = wait_bar(smem_u32(full + s), ph, abort_flag, a) && go &&
                     ring.holds(s, (m - blockIdx.x) / step / stages + 1);
     const size_t base = static_cast<size_t>(m) * nv;
     const uint4* x = reinterpret_cast<const uint4*>(ring.slot(s));
