@@ -36,9 +36,12 @@
 //
 // Measured: nt 32647 rows in 4 groups, 4096 x 7168: 1135-1170 us (1640-1690
 // TFLOP/s under the power cap, 1.43 GHz; the tensor pipe 94% active), tn 16391
-// rows 2048 x 7168: 257 us alone, 294 us in a loop; nn 5003 rows in 29 of 32
-// groups: 156 us (6.0 TB/s); nt 61 rows on 6 of 8 groups, 4096 x 7168: 58 us (6.1
-// TB/s).
+// rows 2048 x 7168: 251 us alone, 290 us in a loop (with an addend, read four bytes
+// at a time between the stores, 445 us; 8192 rows in 8 groups, 2048 x 2048: 43 us, with
+// one 263); nn 5003 rows in 29 of 32 groups: 156 us (6.0 TB/s); nt 61 rows on 6 of 8
+// groups, 4096 x 7168: 58 us (6.1 TB/s).  Far from these where groups are uneven or
+// empty, or a width is a little above whole tiles (tn 12818 rows in one of two groups,
+// 1816 x 352: 51 us, the floor 9).
 //
 // Every wait is bounded, as in the FP8 kernels.  Calls of a few rows in all take
 // dg_bf16_few.cu instead.
