@@ -114,9 +114,11 @@ def quantize_weight(x):
 
 
 def decode_step(w, w1q, w2q, x, residual, top_k, max_m):
-    """One decoding step in FP8 (w1q, w2q: quantize_weight of the experts); at
-    most max_m rows per expert."""
+    """One decoding step in FP8 (w1q, w2q: quantize_weight of the experts), with
+    room for max_m rows per expert: as many as tokens, which may all choose one."""
     T, H, I, G = x.shape[0], w.hidden, w.inter, w.experts
+    if T > max_m:
+        raise ValueError(f"{T} tokens, room for {max_m} rows per expert")
     ld = dg.get_tma_aligned_size(T, 4)
     h, y = _empty(T, H), _empty(T, H)
     q, sa = _empty(T, H, dtype=torch.uint8), _empty(H // 128, ld, dtype=torch.float32)
