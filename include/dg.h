@@ -446,7 +446,8 @@ long long dg_num_output_tiles(int m, int n, int block_m, int block_n);
 dg_status dg_set_wait_timeout_ns(unsigned long long ns);
 
 /* Test hook for the failure path: when nonzero, the next launches run with the
- * TMA producer switched off, so that their waits run out (DG_ERR_TIMEOUT).  Use
+ * TMA producer (the norm's and the activation's rings: the bulk copies) switched
+ * off, so that their waits run out (DG_ERR_TIMEOUT).  Use
  * only together with a short dg_set_wait_timeout_ns(). */
 dg_status dg_debug_set_skip_producer(int on);
 
