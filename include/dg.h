@@ -373,6 +373,110 @@ dg_status dg_k_grouped_gemm_bf16_tn_ragged(const void* A, const void* B, const v
                                            const int32_t* ks, int num_groups, int M, int N,
                                            int K_total, void* stream);
 
+/* Routing of tokens to experts.  Per token, of its num_experts logits x:
+ *   s = softmax(x), or 1 / (1 + exp(-x)) with sigmoid != 0;  c = s + bias (null: c = s)
+ *   the experts lie in num_groups groups of consecutive ones; a group's value is
+ *   the sum of its group_best (1 or 2) largest c, and the top_groups groups of the
+ *   largest values stay (top_groups == num_groups: all)
+ *   experts[t][j] = the expert of the j-th largest c among those that stay,
+ *   j < top_k; equal values, of experts and of groups, go to the lowest index
+ *   weights[t][j] = scale * s, of that expert; with renormalize != 0 divided by the
+ *   sum of the chosen s (sigmoid: plus 1e-20)
+ * The bias moves the choice only, for an even load.  The choice is that of the
+ * formulas in 64 bits, whatever is rounded on the way (where all biases are equal and
+ * no sum of two decides, it is made by the logits, which both scores rise with).  An expert whose logit is -infinity or NaN is not available; where
+ * fewer than top_k are, the entries left over are expert -1, weight 0 (a token
+ * whose experts are all masked has no row and no weight).  A logit of +infinity
+ * counts as the largest number.
+ *   logits fp32 or bf16 [T][num_experts], bias fp32 [num_experts] or null,
+ *   experts int32 [T][top_k], weights fp32 [T][top_k]
+ * 1 <= num_experts <= 1024 in groups of equal size, num_groups <= 32, 1 <= top_k <=
+ * 32 and at most the experts that stay; tensors aligned to their elements.
+ * T == 0 is a no-op. */
+dg_status dg_route_top_k_fp32(const float* logits, const float* bias, int32_t* experts, float* weights,
+                              int T, int num_experts, int top_k, int sigmoid, int num_groups,
+                              int top_groups, int group_best, int renormalize, float scale,
+                              void* stream);
+dg_status dg_route_top_k_bf16(const void* logits, const float* bias, int32_t* experts, float* weights,
+                              int T, int num_experts, int top_k, int sigmoid, int num_groups,
+                              int top_groups, int group_best, int renormalize, float scale,
+                              void* stream);
+/* Gradient of the logits from that of the weights, for the choice made (bias and
+ * groups have none): d_logits as the logits, all of it written.  An entry -1 of
+ * experts has no weight; one outside [-1, num_experts) counts as -1 and is reported
+ * as DG_ERR_EXPERT_RANGE.  An expert that is named twice gets both gradients. */
+dg_status dg_route_top_k_backward_fp32(const float* logits, const int32_t* experts,
+                                       const float* d_weights, float* d_logits, int T,
+                                       int num_experts, int top_k, int sigmoid, int renormalize,
+                                       float scale, void* stream);
+dg_status dg_route_top_k_backward_bf16(const void* logits, const int32_t* experts,
+                                       const float* d_weights, void* d_logits, int T,
+                                       int num_experts, int top_k, int sigmoid, int renormalize,
+                                       float scale, void* stream);
+
+/* Where the rows of the tokens' choices lie in the experts' operands: rows[t][j] is
+ * the row of choice j of token t, in the order of the experts and, of one expert,
+ * of the choices (t first).  -1: no row (expert -1, or no room).
+ *   ragged      the experts' rows one after the other: ms is the sizes argument of
+ *               the ragged products (M_total: T * top_k, or any more)
+ *   contiguous  each expert's rows begin at a multiple of 128; m_indices [M_total] is
+ *               written as the contiguous GEMMs take it, -1 behind an expert's rows
+ *               and behind the last expert (T * top_k + 127 * num_groups rows, rounded
+ *               up to 128, always suffice; a choice past M_total gets no row, which
+ *               is reported as DG_ERR_KS_RANGE); ms counts all choices
+ *   masked      max_m rows for each expert, its first at expert * max_m: masked_m is
+ *               the masked GEMMs' argument (a choice past max_m gets no row, which is
+ *               reported as DG_ERR_MASK_RANGE)
+ *   experts int32 [T][top_k]: -1, or below num_groups (another value counts as -1
+ *   and is reported as DG_ERR_EXPERT_RANGE); rows int32 [T][top_k]; ms, masked_m
+ *   int32 [num_groups]
+ * top_k <= 32, num_groups <= 1024, T * top_k < 2^30; contiguous: M_total a multiple
+ * of 128; masked: num_groups * max_m < 2^31.  With T == 0 sizes of 0 are written. */
+dg_status dg_expert_rows_ragged(const int32_t* experts, int32_t* ms, int32_t* rows, int T, int top_k,
+                                int num_groups, void* stream);
+dg_status dg_expert_rows_contiguous(const int32_t* experts, int32_t* ms, int32_t* rows,
+                                    int32_t* m_indices, int T, int top_k, int num_groups, int M_total,
+                                    void* stream);
+dg_status dg_expert_rows_masked(const int32_t* experts, int32_t* masked_m, int32_t* rows, int T,
+                                int top_k, int num_groups, int max_m, void* stream);
+
+/* Dispatch: D[rows[t][j]] = X[t] for every choice with a row; the other rows of D are
+ * left as they were.  (Its gradient is dg_combine_rows without weights.)
+ *   bf16       X [T][K], D [num_rows][K]; K a multiple of 8
+ *   fp8_1x128  Q e4m3 [T][K] with scales sa [K/128][ld_sa] (packed UE8M0:
+ *              [ceil(K/512)][ld_sfa]), as the quantisers write them, into A
+ *              [num_groups][max_m][K] with sa_out [num_groups][K/128][ld_out]
+ *              (num_groups = 1, max_m = M_total: the contiguous layout); K a
+ *              multiple of 128, ld_sa >= T and ld_out >= max_m multiples of 4
+ * A row outside [-1, num_rows) is left out and reported as DG_ERR_EXPERT_RANGE.
+ * Tensors 16-byte, rows 4-byte aligned; D overlaps nothing else.  T == 0 is a no-op. */
+dg_status dg_dispatch_rows_bf16(const void* X, const int32_t* rows, void* D, int T, int K, int top_k,
+                                int num_rows, void* stream);
+dg_status dg_dispatch_rows_fp8_1x128(const void* Q, const float* sa, int ld_sa, const int32_t* rows,
+                                     void* A, float* sa_out, int ld_out, int T, int K, int top_k,
+                                     int num_groups, int max_m, void* stream);
+dg_status dg_dispatch_rows_fp8_1x128_ue8m0(const void* Q, const int32_t* sfa, int ld_sfa,
+                                           const int32_t* rows, void* A, int32_t* sfa_out, int ld_out,
+                                           int T, int K, int top_k, int num_groups, int max_m,
+                                           void* stream);
+
+/* Combine: the experts' output rows back to their tokens, in fp32 with one rounding:
+ *   out[t] = bf16( R[t] + sum_j weights[t][j] * Y[rows[t][j]] )
+ * over the choices with a row, in their order.
+ *   Y bf16 [num_rows][K]; weights fp32 [T][top_k] or null (all 1); R bf16 [T][K] or
+ *   null (none); out bf16 [T][K], may be R itself
+ * and its gradient, with dO that of out (R's is dO itself):
+ *   dY[rows[t][j]] = bf16( weights[t][j] * dO[t] );  the other rows are left as they were
+ *   d_weights[t][j] = sum_k dO[t][k] * Y[rows[t][j]][k]  (fp32; null: not computed, Y
+ *   is not read); 0 for a choice without a row
+ * K a multiple of 8; rows and errors as for dispatch.  Two choices share no row.
+ * T == 0 is a no-op. */
+dg_status dg_combine_rows(const void* Y, const int32_t* rows, const float* weights, const void* R,
+                          void* out, int T, int K, int top_k, int num_rows, void* stream);
+dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t* rows,
+                                   const float* weights, void* dY, float* d_weights, int T, int K,
+                                   int top_k, int num_rows, void* stream);
+
 /* Maximum number of SMs the kernels may use (DeepGEMM set_num_sms / get_num_sms,
  * es.news.hada.io/topic?id=19459, "Utilidades y variables de entorno").
  * dg_set_num_sms(0) restores "all SMs of the device"; a value above the device's

@@ -31,6 +31,10 @@ __all__ = [
     "swiglu_quantize_fp8_1x128_ue8m0", "swiglu_backward_fp8_1x128",
     "m_grouped_gemm_bf16_nt_ragged", "m_grouped_gemm_bf16_nn_ragged",
     "k_grouped_gemm_bf16_tn_ragged", "debug_force_ragged_plan",
+    "route_top_k_fp32", "route_top_k_bf16", "route_top_k_backward_fp32", "route_top_k_backward_bf16",
+    "expert_rows_ragged", "expert_rows_contiguous", "expert_rows_masked", "dispatch_rows_bf16",
+    "dispatch_rows_fp8_1x128", "dispatch_rows_fp8_1x128_ue8m0", "combine_rows",
+    "combine_rows_backward",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -72,6 +76,10 @@ EXPORTED_SYMBOLS = [
     "dg_swiglu_backward_fp8_1x128", "dg_m_grouped_gemm_bf16_nt_ragged",
     "dg_m_grouped_gemm_bf16_nn_ragged", "dg_k_grouped_gemm_bf16_tn_ragged",
     "dg_debug_force_ragged_plan",
+    "dg_route_top_k_fp32", "dg_route_top_k_bf16", "dg_route_top_k_backward_fp32",
+    "dg_route_top_k_backward_bf16", "dg_expert_rows_ragged", "dg_expert_rows_contiguous",
+    "dg_expert_rows_masked", "dg_dispatch_rows_bf16", "dg_dispatch_rows_fp8_1x128",
+    "dg_dispatch_rows_fp8_1x128_ue8m0", "dg_combine_rows", "dg_combine_rows_backward",
 ]
 
 
@@ -164,6 +172,19 @@ def lib():
         L.dg_k_grouped_gemm_bf16_tn_ragged.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
                                                        _vp]
         L.dg_debug_force_ragged_plan.argtypes = [_i, _i, _i, _i]
+        _f = ctypes.c_float
+        for x in ("fp32", "bf16"):
+            getattr(L, "dg_route_top_k_" + x).argtypes = [_vp] * 4 + [_i] * 8 + [_f, _vp]
+            getattr(L, "dg_route_top_k_backward_" + x).argtypes = [_vp] * 4 + [_i] * 5 + [_f, _vp]
+        L.dg_expert_rows_ragged.argtypes = [_vp] * 3 + [_i] * 3 + [_vp]
+        L.dg_expert_rows_contiguous.argtypes = [_vp] * 4 + [_i] * 4 + [_vp]
+        L.dg_expert_rows_masked.argtypes = [_vp] * 3 + [_i] * 4 + [_vp]
+        L.dg_dispatch_rows_bf16.argtypes = [_vp] * 3 + [_i] * 4 + [_vp]
+        for suffix in ("", "_ue8m0"):
+            getattr(L, "dg_dispatch_rows_fp8_1x128" + suffix).argtypes = [
+                _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]
+        L.dg_combine_rows.argtypes = [_vp] * 5 + [_i] * 4 + [_vp]
+        L.dg_combine_rows_backward.argtypes = [_vp] * 6 + [_i] * 4 + [_vp]
         for f in EXPORTED_SYMBOLS:
             if f not in ("dg_last_error_string", "dg_num_output_tiles",
                          "dg_rms_norm_backward_workspace_bytes"):
@@ -404,6 +425,92 @@ def k_grouped_gemm_bf16_tn_ragged(A, B, D, ks, num_groups, M, N, K_total, C=None
     [K_total,N], D (and C) [G,M,N]; ks int32 [G] on the device, any sizes."""
     _check(_ops().k_grouped_gemm_bf16_tn_ragged(
         A, B, C, D, ks, num_groups, M, N, K_total, _stream(stream)))
+
+
+def route_top_k_fp32(logits, bias, experts, weights, T, num_experts, top_k, sigmoid=False,
+                     num_groups=1, top_groups=1, group_best=2, renormalize=True, scale=1.0,
+                     stream=None):
+    """The top_k experts (int32 [T,top_k]) and weights (fp32 [T,top_k]) of each token from its
+    logits fp32 [T,num_experts]: softmax or sigmoid scores, an optional bias fp32 [num_experts]
+    for the choice, optionally the best top_groups of num_groups groups."""
+    _check(_ops().route_top_k_fp32(logits, bias, experts, weights, T, num_experts, top_k, sigmoid,
+                                   num_groups, top_groups, group_best, renormalize, scale,
+                                   _stream(stream)))
+
+
+def route_top_k_bf16(logits, bias, experts, weights, T, num_experts, top_k, sigmoid=False,
+                     num_groups=1, top_groups=1, group_best=2, renormalize=True, scale=1.0,
+                     stream=None):
+    """route_top_k_fp32 of bf16 logits."""
+    _check(_ops().route_top_k_bf16(logits, bias, experts, weights, T, num_experts, top_k, sigmoid,
+                                   num_groups, top_groups, group_best, renormalize, scale,
+                                   _stream(stream)))
+
+
+def route_top_k_backward_fp32(logits, experts, d_weights, d_logits, T, num_experts, top_k,
+                              sigmoid=False, renormalize=True, scale=1.0, stream=None):
+    """Gradient d_logits fp32 [T,num_experts] of the logits from that of the weights."""
+    _check(_ops().route_top_k_backward_fp32(logits, experts, d_weights, d_logits, T, num_experts,
+                                            top_k, sigmoid, renormalize, scale, _stream(stream)))
+
+
+def route_top_k_backward_bf16(logits, experts, d_weights, d_logits, T, num_experts, top_k,
+                              sigmoid=False, renormalize=True, scale=1.0, stream=None):
+    """route_top_k_backward_fp32 of bf16 logits, d_logits bf16."""
+    _check(_ops().route_top_k_backward_bf16(logits, experts, d_weights, d_logits, T, num_experts,
+                                            top_k, sigmoid, renormalize, scale, _stream(stream)))
+
+
+def expert_rows_ragged(experts, ms, rows, T, top_k, num_groups, stream=None):
+    """The row of each choice (rows int32 [T,top_k]) and each expert's count (ms int32
+    [num_groups]) in the layout of the ragged products, from experts int32 [T,top_k]."""
+    _check(_ops().expert_rows_ragged(experts, ms, rows, T, top_k, num_groups, _stream(stream)))
+
+
+def expert_rows_contiguous(experts, ms, rows, m_indices, T, top_k, num_groups, M_total,
+                           stream=None):
+    """The same in the contiguous layout of M_total rows, with m_indices int32 [M_total]."""
+    _check(_ops().expert_rows_contiguous(experts, ms, rows, m_indices, T, top_k, num_groups,
+                                         M_total, _stream(stream)))
+
+
+def expert_rows_masked(experts, masked_m, rows, T, top_k, num_groups, max_m, stream=None):
+    """The same in the masked layout of max_m rows per expert."""
+    _check(_ops().expert_rows_masked(experts, masked_m, rows, T, top_k, num_groups, max_m,
+                                     _stream(stream)))
+
+
+def dispatch_rows_bf16(X, rows, D, T, K, top_k, num_rows, stream=None):
+    """D[rows[t,j]] = X[t]: bf16 X [T,K], D [num_rows,K]."""
+    _check(_ops().dispatch_rows_bf16(X, rows, D, T, K, top_k, num_rows, _stream(stream)))
+
+
+def dispatch_rows_fp8_1x128(Q, sa, ld_sa, rows, A, sa_out, ld_out, T, K, top_k, num_groups, max_m,
+                            stream=None):
+    """A[rows[t,j]] = Q[t] with their scales: e4m3 Q [T,K], sa fp32 [K/128,ld_sa] into A
+    [num_groups,max_m,K], sa_out [num_groups,K/128,ld_out]."""
+    _check(_ops().dispatch_rows_fp8_1x128(Q, sa, ld_sa, rows, A, sa_out, ld_out, T, K, top_k,
+                                          num_groups, max_m, _stream(stream)))
+
+
+def dispatch_rows_fp8_1x128_ue8m0(Q, sfa, ld_sfa, rows, A, sfa_out, ld_out, T, K, top_k,
+                                  num_groups, max_m, stream=None):
+    """The same with packed UE8M0 scales int32 [ceil(K/512),ld_sfa]."""
+    _check(_ops().dispatch_rows_fp8_1x128_ue8m0(Q, sfa, ld_sfa, rows, A, sfa_out, ld_out, T, K,
+                                                top_k, num_groups, max_m, _stream(stream)))
+
+
+def combine_rows(Y, rows, weights, R, out, T, K, top_k, num_rows, stream=None):
+    """out[t] = R[t] + sum_j weights[t,j] Y[rows[t,j]]: bf16 Y [num_rows,K], R (or None) and
+    out [T,K]; weights fp32 [T,top_k] or None (the gradient of dispatch)."""
+    _check(_ops().combine_rows(Y, rows, weights, R, out, T, K, top_k, num_rows, _stream(stream)))
+
+
+def combine_rows_backward(dO, Y, rows, weights, dY, d_weights, T, K, top_k, num_rows, stream=None):
+    """dY[rows[t,j]] = weights[t,j] dO[t] (bf16 [num_rows,K]) and d_weights fp32 [T,top_k] (or
+    None)."""
+    _check(_ops().combine_rows_backward(dO, Y, rows, weights, dY, d_weights, T, K, top_k, num_rows,
+                                        _stream(stream)))
 
 
 def get_num_sms():

@@ -101,7 +101,19 @@ PyObject* call(Entry<A...> f, const char* name, PyObject* const* args, Py_ssize_
   X(swiglu_backward_fp8_1x128)              \
   X(m_grouped_gemm_bf16_nt_ragged)          \
   X(m_grouped_gemm_bf16_nn_ragged)          \
-  X(k_grouped_gemm_bf16_tn_ragged)
+  X(k_grouped_gemm_bf16_tn_ragged)          \
+  X(route_top_k_fp32)                       \
+  X(route_top_k_bf16)                       \
+  X(route_top_k_backward_fp32)              \
+  X(route_top_k_backward_bf16)              \
+  X(expert_rows_ragged)                     \
+  X(expert_rows_contiguous)                 \
+  X(expert_rows_masked)                     \
+  X(dispatch_rows_bf16)                     \
+  X(dispatch_rows_fp8_1x128)                \
+  X(dispatch_rows_fp8_1x128_ue8m0)          \
+  X(combine_rows)                           \
+  X(combine_rows_backward)
 
 #define DG_FUNCTION(name)                                                        \
   decltype(&dg_##name) p_##name;                                                 \

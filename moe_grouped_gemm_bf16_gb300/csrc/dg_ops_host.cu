@@ -13,33 +13,20 @@
 #include "dg_bf16.h"
 #include "dg_host.h"
 #include "dg_norm.h"
+#include "dg_ops_util.h"
 #include "dg_swiglu.h"
 
 namespace {
 
+using dgk::aligned;
+using dgk::aligned16;
+using dgk::cuda_fail;
 using dgk::host_fail;
 using dgk::host_ok;
-
-dg_status cuda_fail(cudaError_t e, const char* what) {
-  return host_fail(DG_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+using dgk::set_up_once;
 
 // dg_debug_force_ragged_plan: pair, lanes, rows, split packed; 0: the heuristic.
 std::atomic<unsigned long long> g_ragged_plan{0};
-
-// Opts an operator's kernels into their shared memory, once per device.
-template <cudaError_t (*SET_UP)()>
-dg_status set_up_once(int device) {
-  static std::atomic<bool> done[dgk::kHostMaxDevices];
-  if (done[device].load(std::memory_order_acquire)) return DG_OK;
-  const cudaError_t e = SET_UP();
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory)");
-  done[device].store(true, std::memory_order_release);
-  return DG_OK;
-}
 
 dg_status rms_norm(const dgk::NormFwd& a0, void* stream, bool ue8m0) {
   dgk::NormFwd a = a0;
