@@ -477,6 +477,41 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
                                    const float* weights, void* dY, float* d_weights, int T, int K,
                                    int top_k, int num_rows, void* stream);
 
+/* Softmax cross entropy of a product over a vocabulary, without its logits in
+ * memory: the loss behind a model's last norm.  With z = X W^T in fp32 and y the
+ * target of token t:
+ *   lse[t] = log sum_v exp(z[t][v]);  loss[t] = lse[t] - z[t][y]
+ * A token whose target is outside [0, V) (-1, say: padding) has loss 0.
+ *   X bf16 [T][K] and W bf16 [V][K], finite values; targets int32 [T]; loss, lse fp32
+ *   [T], one of them may be null (lse: for the gradient)
+ *   workspace  at least dg_linear_cross_entropy_workspace_bytes(T, V, K) bytes,
+ *              16-byte aligned; its contents need not be kept.  It belongs to one
+ *              call at a time: calls on different streams, and graphs that may run
+ *              at the same time, each need their own
+ * and its gradient, with d_loss fp32 [T] that of loss:
+ *   p = (exp(z[t][v] - lse[t]) - [v = y]) * d_loss[t], rounded to bf16 (0 for a token
+ *       without a target, whose d_loss is not read)
+ *   dX = p W, bf16 [T][K];  dW = p^T X, bf16 [V][K]: sums in fp32, one rounding; one
+ *   of them may be null (not computed)
+ *   lse        what the forward call wrote for these X and W
+ *   workspace  dg_linear_cross_entropy_backward_workspace_bytes(T, V, K) bytes, as above
+ *              (a piece of p: 96 MB, or 4096 words of each token, at most; and dX in
+ *              fp32 where there is more than one piece)
+ * The sums run in a fixed order: the same inputs give the same bits on the same
+ * number of SMs.  K a multiple of 8; too large (DG_ERR_UNSUPPORTED_SHAPE): T or K of 2^23
+ * or more, V within 8192 of 2^31, X or W of 2^34 elements, T * V of 2^38.  X, W, dX
+ * and dW 16-byte, the others 4-byte aligned.  T == 0: dW = 0, nothing else. */
+dg_status dg_linear_cross_entropy(const void* X, const void* W, const int32_t* targets, float* loss,
+                                  float* lse, void* workspace, long long workspace_bytes, int T, int V,
+                                  int K, void* stream);
+dg_status dg_linear_cross_entropy_backward(const void* X, const void* W, const int32_t* targets,
+                                           const float* lse, const float* d_loss, void* dX, void* dW,
+                                           void* workspace, long long workspace_bytes, int T, int V,
+                                           int K, void* stream);
+/* Bytes of workspace of the two (-1 for negative sizes). */
+long long dg_linear_cross_entropy_workspace_bytes(int T, int V, int K);
+long long dg_linear_cross_entropy_backward_workspace_bytes(int T, int V, int K);
+
 /* Maximum number of SMs the kernels may use (DeepGEMM set_num_sms / get_num_sms,
  * es.news.hada.io/topic?id=19459, "Utilidades y variables de entorno").
  * dg_set_num_sms(0) restores "all SMs of the device"; a value above the device's

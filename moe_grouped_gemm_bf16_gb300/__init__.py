@@ -34,7 +34,8 @@ __all__ = [
     "route_top_k_fp32", "route_top_k_bf16", "route_top_k_backward_fp32", "route_top_k_backward_bf16",
     "expert_rows_ragged", "expert_rows_contiguous", "expert_rows_masked", "dispatch_rows_bf16",
     "dispatch_rows_fp8_1x128", "dispatch_rows_fp8_1x128_ue8m0", "combine_rows",
-    "combine_rows_backward",
+    "combine_rows_backward", "linear_cross_entropy", "linear_cross_entropy_backward",
+    "linear_cross_entropy_workspace_bytes", "linear_cross_entropy_backward_workspace_bytes",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -80,6 +81,8 @@ EXPORTED_SYMBOLS = [
     "dg_route_top_k_backward_bf16", "dg_expert_rows_ragged", "dg_expert_rows_contiguous",
     "dg_expert_rows_masked", "dg_dispatch_rows_bf16", "dg_dispatch_rows_fp8_1x128",
     "dg_dispatch_rows_fp8_1x128_ue8m0", "dg_combine_rows", "dg_combine_rows_backward",
+    "dg_linear_cross_entropy", "dg_linear_cross_entropy_backward",
+    "dg_linear_cross_entropy_workspace_bytes", "dg_linear_cross_entropy_backward_workspace_bytes",
 ]
 
 
@@ -185,9 +188,15 @@ def lib():
                 _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]
         L.dg_combine_rows.argtypes = [_vp] * 5 + [_i] * 4 + [_vp]
         L.dg_combine_rows_backward.argtypes = [_vp] * 6 + [_i] * 4 + [_vp]
+        L.dg_linear_cross_entropy.argtypes = [_vp] * 6 + [ctypes.c_longlong] + [_i] * 3 + [_vp]
+        L.dg_linear_cross_entropy_backward.argtypes = [_vp] * 8 + [ctypes.c_longlong] + [_i] * 3 + [_vp]
+        sizes = ["dg_rms_norm_backward_workspace_bytes", "dg_linear_cross_entropy_workspace_bytes",
+                 "dg_linear_cross_entropy_backward_workspace_bytes"]
+        for name in sizes[1:]:
+            getattr(L, name).argtypes = [_i] * 3
+            getattr(L, name).restype = ctypes.c_longlong
         for f in EXPORTED_SYMBOLS:
-            if f not in ("dg_last_error_string", "dg_num_output_tiles",
-                         "dg_rms_norm_backward_workspace_bytes"):
+            if f not in ("dg_last_error_string", "dg_num_output_tiles", *sizes):
                 getattr(L, f).restype = _i
         _LIB = L
     return _LIB
@@ -511,6 +520,31 @@ def combine_rows_backward(dO, Y, rows, weights, dY, d_weights, T, K, top_k, num_
     None)."""
     _check(_ops().combine_rows_backward(dO, Y, rows, weights, dY, d_weights, T, K, top_k, num_rows,
                                         _stream(stream)))
+
+
+def linear_cross_entropy_workspace_bytes(T, V, K):
+    """Bytes of device workspace linear_cross_entropy needs."""
+    return int(lib().dg_linear_cross_entropy_workspace_bytes(int(T), int(V), int(K)))
+
+
+def linear_cross_entropy(X, W, targets, loss, lse, workspace, workspace_bytes, T, V, K, stream=None):
+    """Softmax cross entropy of X W^T (bf16 X [T,K], W [V,K]) with int32 targets [T] (outside
+    [0, V): no loss): loss and lse fp32 [T], one of them may be None."""
+    _check(_ops().linear_cross_entropy(X, W, targets, loss, lse, workspace, workspace_bytes, T, V,
+                                       K, _stream(stream)))
+
+
+def linear_cross_entropy_backward_workspace_bytes(T, V, K):
+    """Bytes of device workspace linear_cross_entropy_backward needs."""
+    return int(lib().dg_linear_cross_entropy_backward_workspace_bytes(int(T), int(V), int(K)))
+
+
+def linear_cross_entropy_backward(X, W, targets, lse, d_loss, dX, dW, workspace, workspace_bytes, T,
+                                  V, K, stream=None):
+    """Its gradients dX bf16 [T,K] and dW bf16 [V,K] (one may be None) from d_loss fp32 [T]
+    and the forward call's lse."""
+    _check(_ops().linear_cross_entropy_backward(X, W, targets, lse, d_loss, dX, dW, workspace,
+                                                workspace_bytes, T, V, K, _stream(stream)))
 
 
 def get_num_sms():

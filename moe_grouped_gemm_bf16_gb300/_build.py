@@ -26,7 +26,8 @@ BINDING = os.path.join(HERE, "_binding" + importlib.machinery.EXTENSION_SUFFIXES
 
 SOURCES = ["dg_host.cu", "dg_inst_dense.cu", "dg_inst_contiguous.cu", "dg_inst_masked.cu", "dg_inst_mn.cu", "dg_inst_ue8m0.cu", "dg_inst_ue8m0_mn.cu", "dg_inst_bs.cu",
            "dg_inst_bs_mn.cu", "dg_quant.cu", "dg_norm.cu", "dg_swiglu.cu", "dg_bf16.cu", "dg_bf16_few.cu",
-           "dg_ops_host.cu", "dg_route.cu", "dg_rows.cu", "dg_moe_host.cu"]
+           "dg_ops_host.cu", "dg_route.cu", "dg_rows.cu", "dg_loss.cu",
+           "dg_moe_host.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

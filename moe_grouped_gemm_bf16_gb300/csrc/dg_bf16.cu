@@ -7,9 +7,9 @@ namespace {
 
 template <int FORM>
 cudaError_t set_up_form() {
-  const void* kernels[] = {reinterpret_cast<const void*>(bf16_grouped_kernel<true, 256, FORM>),
-                           reinterpret_cast<const void*>(bf16_grouped_kernel<false, 128, FORM>),
-                           reinterpret_cast<const void*>(bf16_grouped_kernel<false, 64, FORM>)};
+  const void* kernels[] = {reinterpret_cast<const void*>(bf16_grouped_kernel<true, 256, FORM, kBfPlain>),
+                           reinterpret_cast<const void*>(bf16_grouped_kernel<false, 128, FORM, kBfPlain>),
+                           reinterpret_cast<const void*>(bf16_grouped_kernel<false, 64, FORM, kBfPlain>)};
   for (const void* k : kernels) {
     const cudaError_t e =
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBfMaxSmem);

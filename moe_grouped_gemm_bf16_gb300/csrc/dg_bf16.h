@@ -14,6 +14,29 @@ enum BfForm : int { kBfNT = 0, kBfNN = 1, kBfTN = 2 };
 
 constexpr int kBfMaxGroups = 1024;
 
+// What becomes of a tile's sums: D itself, or, of the loss over a vocabulary, the
+// logits' largest values and sums (nt), the gradient of the logits (nt), or a sum
+// over pieces of the vocabulary (nn).
+enum BfEpilogue : int { kBfPlain = 0, kBfStats = 1, kBfGrad = 2, kBfSum = 3 };
+
+struct BfLoss {
+  // nt: the rows of A are the words word0 .. of `words`, the rows of B tokens
+  const int32_t* targets;   // [N]: a word, or outside [0, words)
+  int words, word0;
+  // stats: per half of a tile's words and token the largest logit times log2(e) and
+  // the sum of 2^(z log2(e) - it); the target's logit where there is a target
+  float2* part;             // [parts][N]
+  float* hit;               // [N]
+  int parts;
+  // gradient: D = (softmax - 1 at the target) * d_loss, rows of `pitch` words
+  const float* lse;         // [N]
+  const float* d_loss;      // [N]
+  int pitch;
+  // sum: fp32, shaped like D; first: nothing before, last: D is written
+  float* sum;
+  bool first, last;
+};
+
 // How a call is tiled: CTA pairs or single CTAs, columns and rows of D per tile,
 // CTAs (pairs) that share a tile's reduction.
 struct BfPlan {
@@ -27,11 +50,14 @@ struct BfCall {
   const void* B;
   const void* C;         // tn: addend shaped like D, or null
   void* D;
-  const int32_t* sizes;  // [G] rows of each group
+  const int32_t* sizes;  // [G] rows of each group (null: G = 1, all rows)
   int G;
   int rows;              // rows of A (all groups)
   int M;                 // tn: rows of each D[e]
   int N, K;              // K unused by tn (its reduction runs over the rows)
+  int pitch;             // elements from row to row of A (0: K, tn: M), a multiple of 8
+  BfEpilogue epilogue;
+  BfLoss loss;
   unsigned int* status;
   unsigned long long timeout_ns;
   unsigned int debug_flags;

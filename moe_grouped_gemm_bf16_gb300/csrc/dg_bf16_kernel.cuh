@@ -81,9 +81,10 @@ struct BfParams {
   int q_bytes;     // bytes of a slot's column operand (per CTA)
   int p_whole;     // extent of the operands' whole 64-wide pieces (see `operand` below)
   int q_whole;
-  const int32_t* sizes;
+  const int32_t* sizes;   // null: one group of all rows
   uint16_t* D;
   const uint16_t* C;
+  BfLoss loss;     // (of the epilogues of the loss)
   unsigned int* status;
   unsigned long long timeout_ns;
   unsigned int debug_flags;
@@ -189,8 +190,20 @@ __device__ __forceinline__ size_t bf_elements(const BfParams& p, bool tn) {
 }
 
 // Four columns of a row of D: the addend in fp32, then one rounding.
+template <int EPI>
 __device__ __forceinline__ void store_four(const BfParams& p, bool tn, size_t at, float4 v) {
   if (!in_bounds(p, at, 4, bf_elements(p, tn))) return;
+  if constexpr (EPI == kBfSum) {
+    float4* sum = reinterpret_cast<float4*>(p.loss.sum + at);
+    if (!p.loss.first) {
+      const float4 x = *sum;
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    if (!p.loss.last) {
+      *sum = v;
+      return;
+    }
+  }
   if (p.C) {
     const uint2 c = *reinterpret_cast<const uint2*>(p.C + at);
     v.x += __uint_as_float(c.x << 16);
@@ -207,7 +220,7 @@ __device__ __forceinline__ void store_four(const BfParams& p, bool tn, size_t at
 // (rank by rank, with the ranks' flags before, 13 rows split in 8 took 3.8 us, so
 // 1.0).  Nothing is stored where a rank gave up a wait (`ok`: this thread knows of
 // none; lane r asks rank r's `flag`, while the partials are on their way).
-template <bool PAIR, int BC, bool TN, int S>
+template <bool PAIR, int BC, bool TN, int EPI, int S>
 __device__ __forceinline__ void add_partials(const BfParams& p, const BfTile& T, uint32_t sbase,
                                              uint32_t has, uint32_t flag, bool ok, int krank,
                                              uint32_t side, int halves) {
@@ -241,14 +254,57 @@ __device__ __forceinline__ void add_partials(const BfParams& p, const BfTile& T,
           sum.x += x[r][j].x; sum.y += x[r][j].y; sum.z += x[r][j].z; sum.w += x[r][j].w;
         }
         if (j < rows)
-          store_four(p, TN, ((TN ? static_cast<size_t>(T.g) * p.M : 0) + T.q0 + c + j) * p.N + l, sum);
+          store_four<EPI>(p, TN, ((TN ? static_cast<size_t>(T.g) * p.M : 0) + T.q0 + c + j) * p.N + l, sum);
       }
     }
   }
 }
 
+// The loss over a vocabulary: its epilogues (dg_loss.cu).  Lanes are tokens, the
+// accumulator's columns words, so that a lane has 32 of a token's logits at a time.
+
+// ex2.approx, off by 2^-22 of itself; 0 for -infinity.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 32 logits of a token, words c .. of a tile of `cols` words, into the largest
+// logit seen so far, times log2(e) (`top`), and the sum of 2^(z log2(e) - top).
+__device__ __forceinline__ void add_logits(const uint32_t (&v)[32], int c, int cols, float& top,
+                                           float& sum) {
+  float m = __uint_as_float(v[0]);
+  if (c + 32 <= cols) {
+#pragma unroll
+    for (int j = 1; j < 32; ++j) m = fmaxf(m, __uint_as_float(v[j]));
+  } else {
+#pragma unroll
+    for (int j = 1; j < 32; ++j) m = c + j < cols ? fmaxf(m, __uint_as_float(v[j])) : m;
+  }
+  m *= kLog2e;
+  if (m > top) {
+    // (the first time: 0 times 0)
+    sum *= exp2_fast(top - m);
+    top = m;
+  }
+  const float shift = top == -INFINITY ? 0.f : -top;
+  float s[4] = {};
+  if (c + 32 <= cols) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, shift));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (c + j < cols) s[j & 3] += exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, shift));
+  }
+  sum += (s[0] + s[1]) + (s[2] + s[3]);
+}
+
 // BC: capacity of an accumulator in rows of D (`bc` at most).
-template <bool PAIR, int BC, int FORM>
+template <bool PAIR, int BC, int FORM, int EPI>
 __global__ void __launch_bounds__(BF_THREADS, 1)
 bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
   using L = BfSmem;
@@ -313,7 +369,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     bool bad = false;
     for (int base = 0; base < p.G; base += 32) {
       const int g = base + lane;
-      int v = g < p.G ? __ldg(p.sizes + g) : 0;
+      int v = g >= p.G ? 0 : p.sizes ? __ldg(p.sizes + g) : p.rows;
       if (v < 0) { bad = true; v = 0; }
       if (v > p.rows) { bad = true; v = p.rows; }
       // the running total in 64 bits: 32 sizes may pass 2^31
@@ -653,12 +709,115 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       }
     }
   };
+  // Rows c .. c + 31 of the tile added to the fp32 sums before them (a lane one
+  // column), which are kept unless these are the last.
+  auto add_rows = [&](const BfTile& T, int l, int c, uint32_t (&v)[32]) {
+    const int n = l < min(p.N, T.l0 + p.lanes) ? min(32, T.cols - c) : 0;
+    const size_t at = static_cast<size_t>(T.q0 + c) * p.N + l;
+    if (n == 0 || !in_bounds(p, at, static_cast<size_t>(n - 1) * p.N + 1, bf_elements(p, TN))) return;
+    float* sum = p.loss.sum + at;
+    if (!p.loss.first) {
+      float old[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) old[j] = j < n ? sum[static_cast<size_t>(j) * p.N] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + old[j]);
+    }
+    if (!p.loss.last) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < n) sum[static_cast<size_t>(j) * p.N] = __uint_as_float(v[j]);
+    }
+  };
   // first column of the thread's pair of columns of D, in half `a` of the lanes
   auto column = [&](const BfTile& T, int a) {
     return T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + q * 32 + (lane & ~1);
   };
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16);
-  if (p.split == 1) {
+  if constexpr (EPI == kBfStats || EPI == kBfGrad) {
+    if (warp >= 4) {
+      const BfLoss& x = p.loss;
+      int b = 0;
+      uint32_t bph = 0;
+      for (int t = unit; t < tiles; t += units) {
+        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, 0, group);
+        // (asked for before the wait)
+        int target[2];      // of the thread's token in each half of the lanes, from the tile's first word
+        float lse[2], scale[2];
+#pragma unroll
+        for (int a = 0; a < (PAIR ? 1 : 2); ++a) {
+          const int l = T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + q * 32 + lane;
+          const bool on = a < halves && l < p.N;
+          target[a] = on ? __ldg(x.targets + l) : -1;
+          if (EPI == kBfGrad) {
+            const bool there = target[a] >= 0 && target[a] < x.words;
+            scale[a] = there ? __ldg(x.d_loss + l) : 0.f;
+            lse[a] = there ? -kLog2e * __ldg(x.lse + l) : -INFINITY;
+          }
+          // (0 .. : in this tile or a later one; a word before the piece is negative)
+          target[a] = target[a] >= 0 && target[a] < x.words ? target[a] - x.word0 - T.q0 : -1;
+        }
+        const bool ok =
+            __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
+        tc_fence_after();
+#pragma unroll
+        for (int a = 0; a < (PAIR ? 1 : 2); ++a) {
+          if (a >= halves) break;
+          const int l = T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + q * 32 + lane;
+          const bool on = ok && l < min(p.N, T.l0 + p.lanes);
+          float top = -INFINITY, sum = 0.f;
+          for (int c = 32 * eh; c < T.cols; c += 64) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
+            tmem_wait_ld(v);
+            const int hit = target[a] - c;   // the target is the chunk's word of this number
+            if constexpr (EPI == kBfStats) {
+              add_logits(v, c, T.cols, top, sum);
+              if (on && hit >= 0 && hit < min(32, T.cols - c)) {
+                float z = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) z = j == hit ? __uint_as_float(v[j]) : z;
+                x.hit[l] = z;
+              }
+            } else {
+              // (softmax - 1 at the target) * d_loss (what lies past the piece's last word is
+              // not read again)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float s = exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, lse[a]));
+                v[j] = __float_as_uint(scale[a] * (j == hit ? s - 1.f : s));
+              }
+              const size_t at = static_cast<size_t>(l) * x.pitch + T.q0 + c;
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                // (the pitch is a multiple of 8: whole vectors up to it)
+                if (on && c + j < T.cols && in_bounds(p, at + j, 8, static_cast<size_t>(p.N) * x.pitch)) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    w[i] = pack_bf16x2(__uint_as_float(v[j + 2 * i]), __uint_as_float(v[j + 2 * i + 1]));
+                  *reinterpret_cast<uint4*>(p.D + at + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+            }
+          }
+          if constexpr (EPI == kBfStats) {
+            const size_t at = (static_cast<size_t>(T.q0 / p.bc) * 2 + eh) * p.N + l;
+            if (on && in_bounds(p, at, 1, static_cast<size_t>(x.parts) * p.N))
+              x.part[at] = make_float2(top, sum);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR && side != 0) mbar_arrive_remote_relaxed(bar(L::T_EMPTY + b), leader);
+          else mbar_arrive(bar(L::T_EMPTY + b));
+        }
+        b ^= 1;
+        if (b == 0) bph ^= 1;
+      }
+    }
+  } else if (p.split == 1) {
     if (warp >= 4) {
       int b = 0;
       uint32_t bph = 0;
@@ -694,6 +853,12 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
             if (more) tmem_ld_32x32b_x32(at + 64, w);
             tmem_wait_ld(v);
             if (more) tmem_wait_ld(w);
+            if constexpr (EPI == kBfSum) {
+              // (l: the even column of the lane's pair; it holds that of its own)
+              if (ok) add_rows(T, l + (lane & 1), c, v);
+              if (ok && more) add_rows(T, l + (lane & 1), c + 64, w);
+              if (!p.loss.last) continue;
+            }
             if (ok) {
               store_rows(T, l, c, v);
               if (more) store_rows(T, l, c + 64, w);
@@ -739,9 +904,9 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       const uint32_t has = __ballot_sync(
           0xffffffffu, lane < p.split && nk * lane / p.split < nk * (lane + 1) / p.split);
       const uint32_t flag = smem_u32(misc + 1);
-      if (p.split <= 2) add_partials<PAIR, BC, TN, 2>(p, T, sbase, has, flag, ok, krank, side, halves);
-      else if (p.split <= 4) add_partials<PAIR, BC, TN, 4>(p, T, sbase, has, flag, ok, krank, side, halves);
-      else add_partials<PAIR, BC, TN, 8>(p, T, sbase, has, flag, ok, krank, side, halves);
+      if (p.split <= 2) add_partials<PAIR, BC, TN, EPI, 2>(p, T, sbase, has, flag, ok, krank, side, halves);
+      else if (p.split <= 4) add_partials<PAIR, BC, TN, EPI, 4>(p, T, sbase, has, flag, ok, krank, side, halves);
+      else add_partials<PAIR, BC, TN, EPI, 8>(p, T, sbase, has, flag, ok, krank, side, halves);
     }
     __syncwarp();
   }
@@ -815,6 +980,7 @@ BfPlan bf_plan(const BfCall& c, int num_sms) {
   auto consider = [&](bool pair, int lanes, int bc) {
     const int width = pair ? 2 : 1;
     for (int split = 1; split * width <= kBfMaxCluster && (split == 1 || depth >= 128 * split); split *= 2) {
+      if (split > 1 && (c.epilogue == kBfStats || c.epilogue == kBfGrad)) break;   // (whole logits)
       if (split * width > num_sms) break;   // (a limit on the SMs may leave fewer)
       const BfPlan f{pair, lanes, bc, split};
       if (c.limited && bf16_grid(c, f, num_sms) > num_sms) break;   // (a cluster per tile)
@@ -834,7 +1000,7 @@ BfPlan bf_plan(const BfCall& c, int num_sms) {
   return best;
 }
 
-template <bool PAIR, int BC, int FORM>
+template <bool PAIR, int BC, int FORM, int EPI = kBfPlain>
 cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode,
                          const BfPlan& plan, int num_sms, cudaStream_t stream) {
   constexpr bool tn = FORM == kBfTN;
@@ -861,6 +1027,7 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
   p.sizes = c.sizes;
   p.D = static_cast<uint16_t*>(c.D);
   p.C = static_cast<const uint16_t*>(c.C);
+  p.loss = c.loss;
   p.status = c.status;
   p.timeout_ns = c.timeout_ns;
   p.debug_flags = c.debug_flags;
@@ -879,17 +1046,19 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
   // (width) x BK rows of K.  One load takes them all, with the pieces as the third
   // dimension of a map of the whole pieces; where the extent is no multiple of
   // 64, its edge needs the other map, a load per piece.
+  // pitch: elements from row to row of x (0: its rows lie side by side).
   auto operand = [&](CUtensorMap* m, int* whole, const void* x, bool mn, uint64_t z, uint64_t rows,
-                     uint64_t k, uint32_t box) {
-    const uint64_t wide = mn ? rows : k, deep = mn ? k : rows, all = 2 * wide * deep;
+                     uint64_t k, uint32_t box, uint64_t pitch = 0) {
+    const uint64_t wide = mn ? rows : k, deep = mn ? k : rows;
+    const uint64_t row = 2 * (pitch ? pitch : wide), all = row * deep;
     const uint32_t pieces = mn ? box / 64 : BK / 64, height = mn ? BK : box;
     *whole = static_cast<int>(wide / 64 * 64);
-    if (!map(m + 1, x, {wide, deep, 1, z}, {2 * wide, all, all}, {64, height, 1, 1})) return false;
+    if (!map(m + 1, x, {wide, deep, 1, z}, {row, all, all}, {64, height, 1, 1})) return false;
     if (*whole == 0) {
       m[0] = m[1];   // (never used)
       return true;
     }
-    return map(m, x, {64, deep, wide / 64, z}, {2 * wide, 128, all}, {64, height, pieces, 1});
+    return map(m, x, {64, deep, wide / 64, z}, {row, 128, all}, {64, height, pieces, 1});
   };
   BfMaps maps;
   // (a reduction without rows loads nothing; its maps still need an extent)
@@ -897,8 +1066,8 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
   const bool good =
       (tn ? operand(maps.p, &p.p_whole, c.B, true, 1, c.N, rows, p_rows)
           : operand(maps.p, &p.p_whole, c.B, FORM == kBfNN, c.G, c.N, c.K, p_rows)) &&
-      (tn ? operand(maps.q, &p.q_whole, c.A, true, 1, c.M, rows, q_rows)
-          : operand(maps.q, &p.q_whole, c.A, false, 1, rows, c.K, q_rows));
+      (tn ? operand(maps.q, &p.q_whole, c.A, true, 1, c.M, rows, q_rows, c.pitch)
+          : operand(maps.q, &p.q_whole, c.A, false, 1, rows, c.K, q_rows, c.pitch));
   if (!good) return cudaErrorInvalidValue;
 
   const int cluster = (PAIR ? 2 : 1) * split;
@@ -919,7 +1088,7 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
     cfg.numAttrs = 2;
   }
   cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, bf16_grouped_kernel<PAIR, BC, FORM>, maps, p);
+  return cudaLaunchKernelEx(&cfg, bf16_grouped_kernel<PAIR, BC, FORM, EPI>, maps, p);
 }
 
 }  // namespace

@@ -1,11 +1,16 @@
-// Entry points of the operators between the products of an expert layer
-// (include/dg.h): routing, the experts' rows, dispatch and combine.  Validation on
-// the host, then one launch; errors as in dg_host.cu.
+// Entry points of the operators between the products of an expert layer, and of
+// the loss (include/dg.h): routing, the experts' rows, dispatch, combine, softmax
+// cross entropy.  Validation on the host, then one launch (the loss: two, or three
+// per piece of the vocabulary); errors as in dg_host.cu.
 #include <cuda_runtime.h>
 
 #include <climits>
 
+#include <algorithm>
+
 #include "dg.h"
+#include "dg_bf16.h"
+#include "dg_loss.h"
 #include "dg_ops_util.h"
 #include "dg_route.h"
 #include "dg_rows.h"
@@ -149,6 +154,46 @@ dg_status check_rows(const char* name, int T, int K, int top_k, int num_rows) {
   return DG_OK;
 }
 
+// T tokens, V words, K columns: the limits of the bf16 products' kernel.
+dg_status check_vocabulary(const char* name, int T, int V, int K) {
+  if (T < 0 || V < 1 || K < 1) return host_fail(DG_ERR_INVALID_ARG, "%s: T=%d V=%d K=%d", name, T, V, K);
+  if (K % 8 != 0) return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: K=%d (a multiple of 8)", name, K);
+  const long long t = T, v = V, k = K;
+  if (V > INT_MAX - 8192 || T >= (1 << 23) || K >= (1 << 23) || v * k >= (1ll << 34) || t * k >= (1ll << 34) ||
+      t * v >= (1ll << 38) || (v / 16 + 1) * (t / 64 + 1) >= (1ll << 31))
+    return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: T=%d V=%d K=%d: too large", name, T, V, K);
+  return DG_OK;
+}
+
+dg_status check_workspace(const char* name, const void* workspace, long long bytes, long long need) {
+  if (!workspace || bytes < need)
+    return host_fail(DG_ERR_INVALID_ARG, "%s: %lld bytes of workspace, %lld needed", name,
+                     workspace ? bytes : 0ll, need);
+  return DG_OK;
+}
+
+dg_status loss_state(dgk::LossCall* a, int* sms) {
+  dgk::HostState st;
+  dg_status s = dgk::host_state(&st);
+  if (s == DG_OK) s = dgk::set_up_once<dgk::loss_set_up>(st.device);
+  if (s != DG_OK) return s;
+  a->status = st.status;
+  a->timeout_ns = st.timeout_ns;
+  a->debug_flags = st.debug_flags;
+  a->limited = st.sms < st.device_sms;
+  a->encode = st.encode;
+  *sms = st.sms;
+  return DG_OK;
+}
+
+dg_status loss_result(cudaError_t e) {
+  if (e == cudaErrorInvalidValue) {
+    cudaGetLastError();
+    return host_fail(DG_ERR_CUDA, "cross entropy: tensor map or launch rejected");
+  }
+  return e != cudaSuccess ? cuda_fail(e, "cross entropy launch") : host_ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -272,6 +317,85 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
       dgk::CombineBwd{dO, Y, rows, weights, dY, d_weights, T, K, top_k, num_rows, st.status}, st.sms,
       st.sms < st.device_sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "combine gradient launch") : host_ok();
+}
+
+long long dg_linear_cross_entropy_workspace_bytes(int T, int V, int K) {
+  return T < 0 || V < 0 || K < 0 ? -1 : dgk::loss_workspace(T, V);
+}
+
+dg_status dg_linear_cross_entropy(const void* X, const void* W, const int32_t* targets, float* loss,
+                                  float* lse, void* workspace, long long workspace_bytes, int T, int V,
+                                  int K, void* stream) {
+  const char* name = "dg_linear_cross_entropy";
+  dg_status s = check_vocabulary(name, T, V, K);
+  if (s != DG_OK) return s;
+  if (T == 0) return host_ok();
+  if (!X || !W || !targets || (!loss && !lse))
+    return host_fail(DG_ERR_INVALID_ARG, "%s: null pointer (X, W, targets, one of loss and lse)", name);
+  s = check_workspace(name, workspace, workspace_bytes, dgk::loss_workspace(T, V));
+  if (s != DG_OK) return s;
+  if (!aligned16(X) || !aligned16(W) || !aligned16(workspace) || !aligned(targets, 4) || !aligned(loss, 4) ||
+      !aligned(lse, 4))
+    return host_fail(DG_ERR_MISALIGNED, "%s: X, W and workspace 16-byte, the others 4-byte aligned", name);
+  dgk::LossCall a{};
+  a.X = X;
+  a.W = W;
+  a.targets = targets;
+  a.loss = loss;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.T = T;
+  a.V = V;
+  a.K = K;
+  int sms = 0;
+  s = loss_state(&a, &sms);
+  if (s != DG_OK) return s;
+  return loss_result(dgk::launch_loss(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+long long dg_linear_cross_entropy_backward_workspace_bytes(int T, int V, int K) {
+  return T < 0 || V < 0 || K < 0 ? -1 : dgk::loss_backward_workspace(T, V, K);
+}
+
+dg_status dg_linear_cross_entropy_backward(const void* X, const void* W, const int32_t* targets,
+                                           const float* lse, const float* d_loss, void* dX, void* dW,
+                                           void* workspace, long long workspace_bytes, int T, int V,
+                                           int K, void* stream) {
+  const char* name = "dg_linear_cross_entropy_backward";
+  dg_status s = check_vocabulary(name, T, V, K);
+  if (s != DG_OK) return s;
+  if ((!dX && !dW) || (T > 0 && (!X || !W || !targets || !lse || !d_loss)))
+    return host_fail(DG_ERR_INVALID_ARG,
+                     "%s: null pointer (X, W, targets, lse, d_loss, one of dX and dW)", name);
+  if (T > 0) {
+    s = check_workspace(name, workspace, workspace_bytes, dgk::loss_backward_workspace(T, V, K));
+    if (s != DG_OK) return s;
+  }
+  if (!aligned16(X) || !aligned16(W) || !aligned16(dX) || !aligned16(dW) || !aligned16(workspace) ||
+      !aligned(targets, 4) || !aligned(lse, 4) || !aligned(d_loss, 4))
+    return host_fail(DG_ERR_MISALIGNED,
+                     "%s: X, W, dX, dW and workspace 16-byte, the others 4-byte aligned", name);
+  if (T == 0 && !dW) return host_ok();
+  dgk::LossCall a{};
+  a.X = X;
+  a.W = W;
+  a.targets = targets;
+  a.lse = const_cast<float*>(lse);
+  a.d_loss = d_loss;
+  a.dX = dX;
+  a.dW = dW;
+  a.workspace = workspace;
+  a.T = T;
+  a.V = V;
+  a.K = K;
+  int sms = 0;
+  s = loss_state(&a, &sms);
+  if (s != DG_OK) return s;
+  if (T == 0) {   // no tokens: dW is 0
+    const cudaError_t e = cudaMemsetAsync(dW, 0, 2ull * V * K, static_cast<cudaStream_t>(stream));
+    return e != cudaSuccess ? cuda_fail(e, "cross entropy: clearing dW") : host_ok();
+  }
+  return loss_result(dgk::launch_loss_backward(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -113,7 +113,9 @@ PyObject* call(Entry<A...> f, const char* name, PyObject* const* args, Py_ssize_
   X(dispatch_rows_fp8_1x128)                \
   X(dispatch_rows_fp8_1x128_ue8m0)          \
   X(combine_rows)                           \
-  X(combine_rows_backward)
+  X(combine_rows_backward)                  \
+  X(linear_cross_entropy)                   \
+  X(linear_cross_entropy_backward)
 
 #define DG_FUNCTION(name)                                                        \
   decltype(&dg_##name) p_##name;                                                 \

@@ -1,0 +1,208 @@
+"""Softmax cross entropy of a product over a vocabulary, and its gradients, against
+the definition in 64 bits (bounds: loss_ref.py)."""
+import pytest
+import torch
+
+import moe_grouped_gemm_bf16_gb300 as dg
+from moe_grouped_gemm_bf16_gb300 import _build
+from tests import loss_ref as L
+from tests.launches import launched
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+KEEP = -7.0   # what no call may write
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    _build.build()
+    torch.cuda.init()
+    dg.get_device_status()
+    yield
+    assert dg.get_device_status() == 0
+
+
+def inputs(T, V, K, seed, ignored=0.2, scale=2.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    X = torch.randn(T, K, generator=g, device="cuda").to(BF16)
+    W = (torch.randn(V, K, generator=g, device="cuda") * scale * K ** -0.5).to(BF16)
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    skip = torch.rand(T, generator=g, device="cuda") < ignored
+    t = torch.where(skip, torch.where(t % 2 == 0, -1, V), t).to(torch.int32)
+    return X, W, t, torch.randn(T, generator=g, device="cuda")
+
+
+def guarded(*shape, dtype=BF16):
+    """A tensor with rows behind it that nothing may touch."""
+    x = torch.full((shape[0] + 3, *shape[1:]), KEEP, dtype=dtype, device="cuda")
+    return x[:shape[0]], x[shape[0]:]
+
+
+def workspace(n):
+    return torch.full((max(n, 16) + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+def forward(X, W, t, stream=None):
+    (T, K), V = X.shape, W.shape[0]
+    n = dg.linear_cross_entropy_workspace_bytes(T, V, K)
+    work = workspace(n)
+    (loss, lg), (lse, sg) = guarded(T, dtype=torch.float32), guarded(T, dtype=torch.float32)
+    dg.linear_cross_entropy(X, W, t, loss, lse, work, n, T, V, K, stream=stream)
+    torch.cuda.synchronize()
+    assert (lg == KEEP).all() and (sg == KEEP).all() and (work[n:] == 0xFF).all()
+    return loss, lse
+
+
+def backward(X, W, t, lse, d, want_x=True, want_w=True, stream=None):
+    (T, K), V = X.shape, W.shape[0]
+    n = dg.linear_cross_entropy_backward_workspace_bytes(T, V, K)
+    work = workspace(n)
+    (dX, xg), (dW, wg) = guarded(T, K), guarded(V, K)
+    dg.linear_cross_entropy_backward(X, W, t, lse, d, dX if want_x else None, dW if want_w else None, work, n, T,
+                                     V, K, stream=stream)
+    torch.cuda.synchronize()
+    assert (xg == KEEP).all() and (wg == KEEP).all() and (work[n:] == 0xFF).all()
+    return dX, dW
+
+
+def check_forward(X, W, t, loss, lse):
+    want, want_lse = L.loss(X, W, t)
+    e, es = L.slack(X, W)
+    assert ((lse.double() - want_lse).abs() <= es).all(), (lse.double() - want_lse).abs().max()
+    lim = torch.where(L.there(t, W.shape[0]), e + es + 2 * L.U * want.abs(), 0.0)
+    assert ((loss.double() - want).abs() <= lim).all(), (loss.double() - want).abs().max()
+
+
+def check_backward(X, W, t, lse, d, dX, dW):
+    p = L.probabilities(X, W, t, lse, d)
+    e, es = L.slack(X, W)
+    # each p: a relative error of its exponential, its rounding; (s - 1 is off by what s is)
+    s = (p / d.double()[:, None].where(d[:, None] != 0, 1.0)).abs()
+    at = L.there(t, W.shape[0]).nonzero()[:, 0]
+    s[at, t[at].long()] = 1.0
+    off = s * d.double().abs()[:, None] * (2 * (e + es) + 2.0 ** -20)[:, None] + L.BF16_ROUND * p.abs()
+    off = torch.where(L.there(t, W.shape[0])[:, None], off, 0.0)
+    for name, got, want, mag, err in (
+            ("dX", dX, p @ W.double(), p.abs() @ W.double().abs(), off @ W.double().abs()),
+            ("dW", dW, p.t() @ X.double(), p.t().abs() @ X.double().abs(), off.t() @ X.double().abs())):
+        lim = L.BF16_ROUND * (1 + L.BF16_ROUND) * want.abs() + 1e-5 * mag + err * 1.01 + 1e-38
+        bad = ~((got.double() - want).abs() <= lim)
+        assert not bad.any(), (name, int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+SHAPES = [(1, 1, 8), (1, 1000, 256), (3, 17, 8), (61, 130, 64), (128, 128, 128), (130, 2051, 264), (257, 513, 72),
+          (40, 32003, 512), (700, 5000, 136), (300, 257, 1032), (2, 50003, 2048)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_loss_and_gradients(shape):
+    T, V, K = shape
+    X, W, t, d = inputs(T, V, K, seed=T + V)
+    loss, lse = forward(X, W, t)
+    check_forward(X, W, t, loss, lse)
+    dX, dW = backward(X, W, t, lse, d)
+    check_backward(X, W, t, lse, d, dX, dW)
+    # either gradient alone
+    assert torch.equal(backward(X, W, t, lse, d, want_w=False)[0], dX)
+    assert torch.equal(backward(X, W, t, lse, d, want_x=False)[1], dW)
+
+
+@pytest.mark.parametrize("shape", [(12300, 9001, 64), (6000, 20011, 256), (13000, 4097, 8)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_pieces_of_the_vocabulary(shape):
+    T, V, K = shape
+    assert dg.linear_cross_entropy_backward_workspace_bytes(T, V, K) < 2 * T * V   # more than one piece
+    X, W, t, d = inputs(T, V, K, seed=1)
+    t[0], t[1], t[2], t[3] = V - 1, 4096, 4095, 0    # (at the borders)
+    loss, lse = forward(X, W, t)
+    check_forward(X, W, t, loss, lse)
+    check_backward(X, W, t, lse, d, *backward(X, W, t, lse, d))
+
+
+def test_no_target_at_all():
+    X, W, t, d = inputs(20, 300, 64, seed=2)
+    t[:] = -1
+    d[:] = float("nan")   # (not read)
+    loss, lse = forward(X, W, t)
+    check_forward(X, W, t, loss, lse)
+    assert (loss == 0).all()
+    dX, dW = backward(X, W, t, lse, d)
+    assert (dX == 0).all() and (dW == 0).all()
+
+
+def test_no_tokens():
+    X, W, t, d = inputs(0, 300, 64, seed=2)
+    dX, dW = backward(X, W, t, d, d)
+    assert (dW == 0).all()
+    dg.linear_cross_entropy(None, W, None, None, None, None, 0, 0, 300, 64)
+
+
+@pytest.mark.parametrize("scale", [0.0, 30.0, 2000.0])
+def test_flat_and_peaked(scale):
+    # all logits equal; logits of a hundred, of thousands (one word has it all)
+    X, W, t, d = inputs(90, 3001, 128, seed=3, scale=scale)
+    loss, lse = forward(X, W, t)
+    assert torch.isfinite(loss).all() and torch.isfinite(lse).all()
+    check_forward(X, W, t, loss, lse)
+    dX, dW = backward(X, W, t, lse, d)
+    assert torch.isfinite(dX).all() and torch.isfinite(dW).all()
+    if scale <= 30.0:
+        check_backward(X, W, t, lse, d, dX, dW)
+
+
+def test_one_output_only():
+    X, W, t, _ = inputs(70, 900, 64, seed=4)
+    loss, lse = forward(X, W, t)
+    n = dg.linear_cross_entropy_workspace_bytes(70, 900, 64)
+    for i, want in ((0, loss), (1, lse)):
+        out = torch.zeros(70, device="cuda")
+        args = (out, None) if i == 0 else (None, out)
+        dg.linear_cross_entropy(X, W, t, *args, workspace(n), n, 70, 900, 64)
+        assert torch.equal(out, want)
+
+
+def test_streams_graphs_and_limits():
+    T, V, K = 300, 20000, 512
+    X, W, t, d = inputs(T, V, K, seed=5)
+    loss, lse = forward(X, W, t)
+    dX, dW = backward(X, W, t, lse, d)
+    want = [x.clone() for x in (loss, lse, dX, dW)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = (*forward(X, W, t, stream=side), *backward(X, W, t, lse, d, stream=side))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    nf, nb = (f(T, V, K) for f in (dg.linear_cross_entropy_workspace_bytes,
+                                   dg.linear_cross_entropy_backward_workspace_bytes))
+    work = workspace(max(nf, nb))
+    outs = [torch.zeros_like(x) for x in want]
+
+    def both(stream=None):
+        dg.linear_cross_entropy(X, W, t, outs[0], outs[1], work, nf, T, V, K, stream=stream)
+        dg.linear_cross_entropy_backward(X, W, t, outs[1], d, outs[2], outs[3], work, nb, T, V, K, stream=stream)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        both()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    # new inputs through the same graph
+    X2, W2, t2, d2 = inputs(T, V, K, seed=6)
+    for a, b in zip((X, W, t, d), (X2, W2, t2, d2)):
+        a.copy_(b)
+    g.replay()
+    torch.cuda.synchronize()
+    check_forward(X, W, t, outs[0], outs[1])
+    check_backward(X, W, t, outs[1], d, outs[2], outs[3])
+    for sms in (1, 3, 132):
+        dg.set_num_sms(sms)
+        try:
+            for o in outs:
+                o.zero_()
+            both()
+            torch.cuda.synchronize()
+            assert all(b <= sms for b, _, _ in launched(both))
+        finally:
+            dg.set_num_sms(0)
+        check_forward(X, W, t, outs[0], outs[1])
+        check_backward(X, W, t, outs[1], d, outs[2], outs[3])

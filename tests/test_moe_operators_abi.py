@@ -123,3 +123,43 @@ SUM_BWD = dict(dO=P, Y=P, rows=P, weights=P, dY=P, d_weights=P, T=5, K=256, top_
     (dict(dY=P + 8), MISALIGNED), (dict(d_weights=P + 2), MISALIGNED), (dict(T=0), OK)])
 def test_combine_gradient_refusals(kw, code):
     assert status(dg.combine_rows_backward, {**SUM_BWD, **kw}) == code
+
+
+LOSS = dict(X=P, W=P, targets=P, loss=P, lse=P, workspace=P, workspace_bytes=1 << 40, T=5, V=1000, K=256)
+LOSS_COMMON = [(dict(X=None), INVALID), (dict(W=None), INVALID), (dict(targets=None), INVALID),
+               (dict(workspace=None), INVALID), (dict(workspace_bytes=64), INVALID), (dict(T=-1), INVALID),
+               (dict(V=0), INVALID), (dict(K=0), INVALID), (dict(K=12), SHAPE), (dict(V=2 ** 31 - 1), SHAPE),
+               (dict(T=1 << 23), SHAPE), (dict(V=1 << 27, K=128), SHAPE), (dict(T=1 << 20, V=1 << 20), SHAPE),
+               (dict(X=P + 8), MISALIGNED), (dict(W=P + 2), MISALIGNED), (dict(workspace=P + 4), MISALIGNED),
+               (dict(targets=P + 2), MISALIGNED), (dict(lse=P + 2), MISALIGNED)]
+
+
+@pytest.mark.parametrize("kw,code", LOSS_COMMON + [
+    (dict(loss=None, lse=None), INVALID), (dict(loss=P + 1), MISALIGNED),
+    (dict(T=0, X=None, W=None, targets=None, loss=None, lse=None, workspace=None), OK)])
+def test_loss_refusals(kw, code):
+    assert status(dg.linear_cross_entropy, {**LOSS, **kw}) == code
+
+
+LOSS_BWD = dict(X=P, W=P, targets=P, lse=P, d_loss=P, dX=P, dW=P, workspace=P, workspace_bytes=1 << 40, T=5,
+                V=1000, K=256)
+
+
+@pytest.mark.parametrize("kw,code", LOSS_COMMON + [
+    (dict(lse=None), INVALID), (dict(d_loss=None), INVALID), (dict(dX=None, dW=None), INVALID),
+    (dict(dX=P + 8), MISALIGNED), (dict(dW=P + 8), MISALIGNED), (dict(d_loss=P + 2), MISALIGNED),
+    (dict(T=0, dW=None), OK)])
+def test_loss_gradient_refusals(kw, code):
+    assert status(dg.linear_cross_entropy_backward, {**LOSS_BWD, **kw}) == code
+
+
+def test_loss_workspaces():
+    f, b = dg.linear_cross_entropy_workspace_bytes, dg.linear_cross_entropy_backward_workspace_bytes
+    for n in (f, b):
+        assert n(0, 1000, 256) == 0 and n(-1, 5, 8) == -1 and n(5, -1, 8) == -1 and n(5, 5, -1) == -1
+    for T, V in ((1, 1), (1, 131072), (4096, 131072), (100000, 50003)):
+        K = 2048
+        # far below the logits', where there are many
+        assert f(T, V, K) <= T * (V / 4 + 200) and f(T, V, K) >= 8 * T
+        words = b(T, V, K) // (2 * T)
+        assert b(T, V, K) <= max(2 * T * 4352, 100 << 20) + 4 * T * K + 256 and words >= min(V, 4096)
