@@ -489,8 +489,8 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
  *              call at a time: calls on different streams, and graphs that may run
  *              at the same time, each need their own
  * and its gradient, with d_loss fp32 [T] that of loss:
- *   p = (exp(z[t][v] - lse[t]) - [v = y]) * d_loss[t], rounded to bf16 (0 for a token
- *       without a target, whose d_loss is not read)
+ *   p = (exp(z[t][v] - lse[t]) - [v = y]) * d_loss[t] (0 for a token without a target,
+ *       whose d_loss is not read), rounded to bf16 relative to the largest |d_loss|
  *   dX = p W, bf16 [T][K];  dW = p^T X, bf16 [V][K]: sums in fp32, one rounding; one
  *   of them may be null (not computed)
  *   lse        what the forward call wrote for these X and W
@@ -622,8 +622,9 @@ dg_status dg_debug_force_block_scaled(int mode);
  * both multiples of 16, of 64 where the form's operand is read in 64-wide boxes,
  * else the calls return DG_ERR_UNSUPPORTED_SHAPE; split: CTAs sharing a tile's
  * reduction, 1..8; calls of a few rows are tiled then, too; a plan of more CTAs
- * than a limit on the SMs allows is refused likewise).  lanes = 0 leaves the choice
- * to the library. */
+ * than a limit on the SMs allows is refused likewise).  It goes for the products of
+ * the cross entropy as well (lanes and rows multiples of 64; its logits' products take
+ * no split).  lanes = 0 leaves the choice to the library. */
 dg_status dg_debug_force_ragged_plan(int pair, int lanes, int rows, int split);
 
 #ifdef __cplusplus

@@ -15,8 +15,8 @@ enum BfForm : int { kBfNT = 0, kBfNN = 1, kBfTN = 2 };
 constexpr int kBfMaxGroups = 1024;
 
 // What becomes of a tile's sums: D itself, or, of the loss over a vocabulary, the
-// logits' largest values and sums (nt), the gradient of the logits (nt), or a sum
-// over pieces of the vocabulary (nn).
+// logits' largest values and sums (nt), the gradient of the logits (nt), or a
+// multiple of them, added up over pieces of the vocabulary (nn, tn).
 enum BfEpilogue : int { kBfPlain = 0, kBfStats = 1, kBfGrad = 2, kBfSum = 3 };
 
 struct BfLoss {
@@ -30,10 +30,11 @@ struct BfLoss {
   int parts;
   // gradient: D = (softmax - 1 at the target) * d_loss, rows of `pitch` words
   const float* lse;         // [N]
-  const float* d_loss;      // [N]
+  const float* d_loss;      // [N], taken relative to *unit
   int pitch;
-  // sum: fp32, shaped like D; first: nothing before, last: D is written
+  // sum: fp32, shaped like D; first: nothing before, last: D = *unit times it is written
   float* sum;
+  const float* unit;
   bool first, last;
 };
 
@@ -71,6 +72,9 @@ cudaError_t bf16_set_up();
 // tensor map could not be encoded.
 cudaError_t launch_bf16_grouped(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 encode,
                                 int num_sms, cudaStream_t stream);
+
+// The plan that dg_debug_force_ragged_plan asks for (lanes = 0: none).
+BfPlan bf16_forced_plan();
 
 // CTAs of the plan's grid.
 long long bf16_grid(const BfCall& c, const BfPlan& plan, int num_sms);

@@ -203,6 +203,8 @@ __device__ __forceinline__ void store_four(const BfParams& p, bool tn, size_t at
       *sum = v;
       return;
     }
+    const float u = __ldg(p.loss.unit);
+    v.x *= u; v.y *= u; v.z *= u; v.w *= u;
   }
   if (p.C) {
     const uint2 c = *reinterpret_cast<const uint2*>(p.C + at);
@@ -710,11 +712,11 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     }
   };
   // Rows c .. c + 31 of the tile added to the fp32 sums before them (a lane one
-  // column), which are kept unless these are the last.
+  // column), which are kept, or the last time multiplied by the unit for D.
   auto add_rows = [&](const BfTile& T, int l, int c, uint32_t (&v)[32]) {
     const int n = l < min(p.N, T.l0 + p.lanes) ? min(32, T.cols - c) : 0;
     const size_t at = static_cast<size_t>(T.q0 + c) * p.N + l;
-    if (n == 0 || !in_bounds(p, at, static_cast<size_t>(n - 1) * p.N + 1, bf_elements(p, TN))) return;
+    if (n > 0 && !in_bounds(p, at, static_cast<size_t>(n - 1) * p.N + 1, bf_elements(p, TN))) return;
     float* sum = p.loss.sum + at;
     if (!p.loss.first) {
       float old[32];
@@ -727,6 +729,10 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         if (j < n) sum[static_cast<size_t>(j) * p.N] = __uint_as_float(v[j]);
+    } else {
+      const float u = __ldg(p.loss.unit);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(u * __uint_as_float(v[j]));
     }
   };
   // first column of the thread's pair of columns of D, in half `a` of the lanes
@@ -751,7 +757,8 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
           target[a] = on ? __ldg(x.targets + l) : -1;
           if (EPI == kBfGrad) {
             const bool there = target[a] >= 0 && target[a] < x.words;
-            scale[a] = there ? __ldg(x.d_loss + l) : 0.f;
+            const float unit = __ldg(x.unit);
+            scale[a] = there && unit != 0.f ? __fdiv_rn(__ldg(x.d_loss + l), unit) : 0.f;
             lse[a] = there ? -kLog2e * __ldg(x.lse + l) : -INFINITY;
           }
           // (0 .. : in this tile or a later one; a word before the piece is negative)
@@ -780,8 +787,8 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
                 x.hit[l] = z;
               }
             } else {
-              // (softmax - 1 at the target) * d_loss (what lies past the piece's last word is
-              // not read again)
+              // (softmax - 1 at the target) * d_loss / unit (what lies past the piece's last
+              // word is not read again)
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 const float s = exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, lse[a]));

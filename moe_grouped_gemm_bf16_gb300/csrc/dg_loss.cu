@@ -11,11 +11,15 @@
 // it; a second kernel joins the tiles' pairs.  The logits never leave tensor memory.
 //
 // Backward: per piece of the vocabulary the logits again, whose epilogue writes p in
-// bf16 (one rounding: each p is off by 2^-9 of itself at most, as every operand of
-// these products), then the piece's rows of dW (form tn) and its share of dX (form
-// nn), which is added up in fp32 over the pieces and rounded once with the last.  A
-// piece is as wide as makes p about 96 MB, which L2 holds until both products have
-// read it.
+// bf16 (as every operand of these products; one rounding, by 2^-9 of itself at most),
+// then the piece's rows of dW (form tn) and its share of dX (form nn), which is added
+// up in fp32 over the pieces and rounded once with the last.  p is written relative
+// to the largest |d_loss|, the unit, and the products' sums are multiplied by it: with
+// the same d_loss for all tokens, as in a mean, its rounding then is none of p's, and
+// the -1 at the targets, the largest entries of all, stay near -1 (with d_loss in p,
+// 1 / T rounded to bf16 in every token's largest entry: dX and dW off by up to 0.0037
+// of themselves, so 0.0017, which is their own rounding).  A piece is as wide as makes
+// p about 96 MB, which L2 holds until both products have read it.
 //
 // Bounded by the tensor cores; with few tokens by reading W (and writing dW).
 #include <algorithm>
@@ -44,11 +48,14 @@ long long piece_words(long long T, long long V) {
 // words (16 in a vocabulary of up to 128).
 long long most_parts(long long V) { return 2 * ((V + 63) / 64 + 8); }
 
+constexpr long long kHead = 256;   // bytes of the backward workspace before p: the unit
+
 template <bool PAIR, int BC>
 cudaError_t opt_in() {
   const void* kernels[] = {reinterpret_cast<const void*>(bf16_grouped_kernel<PAIR, BC, kBfNT, kBfStats>),
                            reinterpret_cast<const void*>(bf16_grouped_kernel<PAIR, BC, kBfNT, kBfGrad>),
-                           reinterpret_cast<const void*>(bf16_grouped_kernel<PAIR, BC, kBfNN, kBfSum>)};
+                           reinterpret_cast<const void*>(bf16_grouped_kernel<PAIR, BC, kBfNN, kBfSum>),
+                           reinterpret_cast<const void*>(bf16_grouped_kernel<PAIR, BC, kBfTN, kBfSum>)};
   for (const void* k : kernels) {
     const cudaError_t e =
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBfMaxSmem);
@@ -60,7 +67,8 @@ cudaError_t opt_in() {
 template <int FORM, int EPI>
 cudaError_t launch_product(BfCall& c, const LossCall& a, int num_sms, cudaStream_t stream) {
   c.epilogue = static_cast<BfEpilogue>(EPI);
-  const BfPlan f = bf_plan(c, num_sms);
+  BfPlan f = a.forced.lanes > 0 ? a.forced : bf_plan(c, num_sms);
+  if (FORM == kBfNT) f.split = 1;
   c.loss.parts = 2 * ((c.rows + f.bc - 1) / f.bc);
   return f.pair       ? launch_tiles<true, 256, FORM, EPI>(c, a.encode, f, num_sms, stream)
          : f.bc <= 64 ? launch_tiles<false, 64, FORM, EPI>(c, a.encode, f, num_sms, stream)
@@ -137,20 +145,44 @@ loss_end_kernel(const LossEnd a) {
   }
 }
 
+// The unit: the largest |d_loss| of the tokens with a target (one block).
+constexpr int UNIT_THREADS = 1024;
+
+__global__ void __launch_bounds__(UNIT_THREADS)
+loss_unit_kernel(const float* d_loss, const int32_t* targets, float* unit, int T, int V) {
+  __shared__ float share[UNIT_THREADS / 32];
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  float m = 0.f;
+#pragma unroll 4
+  for (int t = threadIdx.x; t < T; t += UNIT_THREADS) {
+    const int y = __ldg(targets + t);
+    if (y >= 0 && y < V) m = fmaxf(m, fabsf(__ldg(d_loss + t)));
+  }
+  // (not negative: in the order of their bits)
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  if ((threadIdx.x & 31) == 0) share[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(share[threadIdx.x])));
+    if (threadIdx.x == 0) *unit = m;
+  }
+}
+
 }  // namespace
 
 long long loss_workspace(long long T, long long V) { return T * (8 * most_parts(V) + 4); }
 
 long long loss_backward_workspace(long long T, long long V, long long K) {
+  if (T == 0) return 0;
   const long long words = piece_words(T, V);
-  return round_up(2 * T * words, 256) + (words < V ? 4 * T * K : 0);
+  return kHead + round_up(2 * T * words, 256) + (words < V ? 4 * T * K : 0);
 }
 
 cudaError_t loss_set_up() {
   cudaError_t e = opt_in<true, 256>();
   if (e == cudaSuccess) e = opt_in<false, 128>();
   if (e == cudaSuccess) e = opt_in<false, 64>();
-  if (e == cudaSuccess) e = bf16_set_up();
   return e;
 }
 
@@ -170,8 +202,12 @@ cudaError_t launch_loss(const LossCall& a, int num_sms, cudaStream_t stream) {
 
 cudaError_t launch_loss_backward(const LossCall& a, int num_sms, cudaStream_t stream) {
   const int words = static_cast<int>(piece_words(a.T, a.V));
-  uint8_t* p = static_cast<uint8_t*>(a.workspace);
+  float* unit = static_cast<float*>(a.workspace);
+  uint8_t* p = static_cast<uint8_t*>(a.workspace) + kHead;
   float* sum = reinterpret_cast<float*>(p + round_up(2ll * a.T * words, 256));
+  cudaError_t e = launch_dependent(loss_unit_kernel, dim3(1), UNIT_THREADS, stream, 0, a.d_loss, a.targets,
+                                   unit, a.T, a.V);
+  if (e != cudaSuccess) return e;
   for (long long w0 = 0; w0 < a.V; w0 += words) {
     const int n = static_cast<int>(std::min<long long>(words, a.V - w0));
     const uint8_t* W = static_cast<const uint8_t*>(a.W) + 2 * w0 * a.K;
@@ -181,24 +217,24 @@ cudaError_t launch_loss_backward(const LossCall& a, int num_sms, cudaStream_t st
     c.loss.word0 = static_cast<int>(w0);
     c.loss.lse = a.lse;
     c.loss.d_loss = a.d_loss;
+    c.loss.unit = unit;
     c.loss.pitch = words;
-    cudaError_t e = launch_product<kBfNT, kBfGrad>(c, a, num_sms, stream);
+    e = launch_product<kBfNT, kBfGrad>(c, a, num_sms, stream);
     if (e == cudaSuccess && a.dW) {
       c = product(a, kBfTN, p, a.X, static_cast<uint8_t*>(a.dW) + 2 * w0 * a.K, a.T, n, a.K, 0);
       c.pitch = words;
-      e = launch_bf16_grouped(c, a.encode, num_sms, stream);
+      c.loss.unit = unit;
+      c.loss.first = c.loss.last = true;
+      e = launch_product<kBfTN, kBfSum>(c, a, num_sms, stream);
     }
     if (e == cudaSuccess && a.dX) {
       c = product(a, kBfNN, p, W, a.dX, a.T, 0, a.K, n);
       c.pitch = words;
-      if (words < a.V) {
-        c.loss.sum = sum;
-        c.loss.first = w0 == 0;
-        c.loss.last = a.V - w0 <= words;
-        e = launch_product<kBfNN, kBfSum>(c, a, num_sms, stream);
-      } else {
-        e = launch_bf16_grouped(c, a.encode, num_sms, stream);
-      }
+      c.loss.sum = sum;
+      c.loss.unit = unit;
+      c.loss.first = w0 == 0;
+      c.loss.last = a.V - w0 <= words;
+      e = launch_product<kBfNN, kBfSum>(c, a, num_sms, stream);
     }
     if (e != cudaSuccess) return e;
   }

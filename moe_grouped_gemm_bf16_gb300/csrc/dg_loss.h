@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "dg_bf16.h"
+
 namespace dgk {
 
 struct LossCall {
@@ -23,6 +25,7 @@ struct LossCall {
   unsigned int debug_flags;
   bool limited;             // fewer SMs than the device has: no grid of more CTAs
   PFN_cuTensorMapEncodeTiled_v12000 encode;
+  BfPlan forced;            // lanes > 0: this plan (tests; the logits' product without a split)
 };
 
 // Workspace of a call, in bytes.

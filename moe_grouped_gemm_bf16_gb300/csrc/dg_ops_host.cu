@@ -134,9 +134,8 @@ dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void
   c.timeout_ns = st.timeout_ns;
   c.debug_flags = st.debug_flags;
   c.limited = st.sms < st.device_sms;
-  if (const unsigned long long f = g_ragged_plan.load()) {
-    c.forced = {(f >> 48) != 0, static_cast<int>(f >> 32 & 0xFFFF), static_cast<int>(f >> 16 & 0xFFFF),
-                static_cast<int>(f & 0xFFFF)};
+  c.forced = dgk::bf16_forced_plan();
+  if (c.forced.lanes > 0) {
     // boxes of an MN-major operand are 64 wide (nn, tn: B's; tn: A's)
     if ((!c.forced.pair && ((form != dgk::kBfNT && c.forced.lanes % 64) || (tn && c.forced.bc % 64))) ||
         c.forced.split * (c.forced.pair ? 2 : 1) > st.sms ||
@@ -155,6 +154,12 @@ dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void
   return e != cudaSuccess ? cuda_fail(e, "ragged bf16 product launch") : host_ok();
 }
 }  // namespace
+
+dgk::BfPlan dgk::bf16_forced_plan() {
+  const unsigned long long f = g_ragged_plan.load();
+  return {(f >> 48) != 0, static_cast<int>(f >> 32 & 0xFFFF), static_cast<int>(f >> 16 & 0xFFFF),
+          static_cast<int>(f & 0xFFFF)};
+}
 
 extern "C" {
 

@@ -206,3 +206,46 @@ def test_streams_graphs_and_limits():
             dg.set_num_sms(0)
         check_forward(X, W, t, outs[0], outs[1])
         check_backward(X, W, t, outs[1], d, outs[2], outs[3])
+
+
+@pytest.mark.parametrize("plan", [(True, 256, 256, 1), (True, 256, 256, 2), (True, 256, 256, 4), (False, 64, 64, 1),
+                                  (False, 64, 64, 8), (False, 128, 64, 2), (False, 192, 64, 4),
+                                  (False, 256, 128, 1), (False, 128, 128, 3), (False, 256, 128, 8)],
+                         ids=lambda p: "x".join(str(int(v)) for v in p))
+@pytest.mark.parametrize("shape", [(200, 3001, 264), (61, 700, 1024), (13000, 4500, 72)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_every_tiling(plan, shape):
+    X, W, t, d = inputs(*shape, seed=9)
+    dg.debug_force_ragged_plan(*plan)
+    try:
+        loss, lse = forward(X, W, t)
+        dX, dW = backward(X, W, t, lse, d)
+    finally:
+        dg.debug_force_ragged_plan()
+    check_forward(X, W, t, loss, lse)
+    check_backward(X, W, t, lse, d, dX, dW)
+
+
+def test_a_mean_loses_no_precision():
+    # the same d_loss for all tokens, no power of two: p is rounded near -1, not near -d
+    X, W, t, _ = inputs(45, 20000, 256, seed=7, ignored=0.0)
+    d = torch.full((45,), 1 / 45.35, device="cuda")
+    loss, lse = forward(X, W, t)
+    dX, dW = backward(X, W, t, lse, d)
+    for got, want in zip((dX, dW), L.gradients(X, W, t, lse, d)):
+        # a rounding to bf16 is uniform in half a step, a step 2^-7 of values from 1 to 2: at most
+        # 2^-8 / sqrt(3) of them in the mean square; p's own rounding, of single words' small shares
+        # and by 2^-9 of the -1's, adds less than half of that
+        assert (got.double() - want).norm() <= 1.2 * 2.0 ** -8 / 3 ** 0.5 * want.norm()
+
+
+def test_forced_tilings_that_the_products_lack_are_refused():
+    X, W, t, d = inputs(20, 300, 64, seed=2)
+    for plan in ((False, 144, 64, 1), (False, 128, 48, 1)):
+        dg.debug_force_ragged_plan(*plan)
+        try:
+            with pytest.raises(dg.DGError) as e:
+                forward(X, W, t)
+        finally:
+            dg.debug_force_ragged_plan()
+        assert e.value.status == 2
