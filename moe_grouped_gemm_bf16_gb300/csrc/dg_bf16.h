@@ -20,21 +20,26 @@ constexpr int kBfMaxGroups = 1024;
 enum BfEpilogue : int { kBfPlain = 0, kBfStats = 1, kBfGrad = 2, kBfSum = 3 };
 
 struct BfLoss {
-  // nt: the rows of A are the words word0 .. of `words`, the rows of B tokens
-  const int32_t* targets;   // [N]: a word, or outside [0, words)
-  int words, word0;
-  // stats: per half of a tile's words and token the largest logit times log2(e) and
+  // nt: the rows of A are the words word0 .. of `words` and the rows of B tokens, or
+  // (words_on_lanes) the other way round
+  bool words_on_lanes;
+  const int32_t* targets;   // [tokens]: a word, or outside [0, words)
+  int words, word0, tokens;
+  // stats: per share of a tile's words and token the largest logit times log2(e) and
   // the sum of 2^(z log2(e) - it); the target's logit where there is a target
-  float2* part;             // [parts][N]
-  float* hit;               // [N]
-  int parts;
-  // gradient: D = (softmax - 1 at the target) * d_loss, rows of `pitch` words
-  const float* lse;         // [N]
-  const float* d_loss;      // [N], taken relative to *unit
+  float2* pair;             // [pairs][tokens]
+  float* hit;               // [tokens]
+  int pairs;
+  // gradient: D [tokens][pitch] = (softmax - 1 at the target) * d_loss
+  const float* lse;         // [tokens]
+  const float* d_loss;      // [tokens], taken relative to *unit
   int pitch;
   // sum: fp32, shaped like D; first: nothing before, last: D = *unit times it is written
+  // (first of a gradient: *unit is found and written).  With parts > 1 (nn): parts of the
+  // reduction, `depth` deep, a sum for each
   float* sum;
-  const float* unit;
+  float* unit;
+  int parts, depth;
   bool first, last;
 };
 

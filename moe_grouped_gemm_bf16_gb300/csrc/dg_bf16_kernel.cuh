@@ -106,7 +106,8 @@ struct BfSmem {
   // (checked build: fill counters of the lane and the column operand's slots)
   static constexpr int FILLS = MISC + 8;
   static constexpr int TAB = (FILLS + (kDebug ? 2 * BF_MAX_STAGES * 4 : 0) + 15) / 16 * 16;
-  __host__ __device__ static constexpr int fixed(int G) { return 1024 + TAB + 2 * (G + 1) * 4; }
+  // (the last: a word per epilogue warp)
+  __host__ __device__ static constexpr int fixed(int G) { return 1024 + TAB + 2 * (G + 1) * 4 + BF_EPI * 4; }
 };
 
 // Reduction depth of a slot.
@@ -136,11 +137,17 @@ __device__ __forceinline__ int bf_div(int x, unsigned long long inv) {
 
 // Tile t; `from`: a group at or before the tile's (a role's tiles come in
 // rising order), replaced by the tile's.  (350 to 500 cycles so.)
-template <int BK, int FORM>
+template <int BK, int FORM, int EPI>
 __device__ __forceinline__ BfTile bf_tile(int t, const BfParams& p, const int* first,
                                           const int* blk, int krank, int& from) {
   BfTile T;
-  int nc;
+  int nc, part = 0;
+  if (EPI == kBfSum && FORM == kBfNN && p.loss.parts > 1) {
+    // part by part of the reduction
+    const int per = blk[1] * p.nl;
+    part = t / per;
+    t -= part * per;
+  }
   if (FORM == kBfTN) {
     T.g = bf_div(t, p.inv_per);
     t -= T.g * (p.nc * p.nl);
@@ -174,6 +181,10 @@ __device__ __forceinline__ BfTile bf_tile(int t, const BfParams& p, const int* f
     T.q0 = first[T.g] + c0;
     T.k0 = 0;
     T.kn = p.K;
+    if (EPI == kBfSum && FORM == kBfNN && p.loss.parts > 1) {
+      T.k0 = part * p.loss.depth;
+      T.kn = min(p.loss.depth, p.K - T.k0);
+    }
   }
   T.nk = (T.kn + BK - 1) / BK;
   T.kbeg = 0;
@@ -262,8 +273,9 @@ __device__ __forceinline__ void add_partials(const BfParams& p, const BfTile& T,
   }
 }
 
-// The loss over a vocabulary: its epilogues (dg_loss.cu).  Lanes are tokens, the
-// accumulator's columns words, so that a lane has 32 of a token's logits at a time.
+// The loss over a vocabulary: its epilogues (dg_loss.cu).  A lane has 32 logits of one
+// token at a time: as they come where the accumulator's lanes are tokens and its
+// columns words, exchanged between the lanes where it is the other way round.
 
 // ex2.approx, off by 2^-22 of itself; 0 for -infinity.
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -274,35 +286,49 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 32 logits of a token, words c .. of a tile of `cols` words, into the largest
-// logit seen so far, times log2(e) (`top`), and the sum of 2^(z log2(e) - top).
-__device__ __forceinline__ void add_logits(const uint32_t (&v)[32], int c, int cols, float& top,
-                                           float& sum) {
+// 32 logits of a token, of which the first n are there, into the largest logit seen
+// so far, times log2(e) (`top`), and the sum of 2^(z log2(e) - top).
+__device__ __forceinline__ void add_logits(const uint32_t (&v)[32], int n, float& top, float& sum) {
   float m = __uint_as_float(v[0]);
-  if (c + 32 <= cols) {
+  if (n >= 32) {
 #pragma unroll
     for (int j = 1; j < 32; ++j) m = fmaxf(m, __uint_as_float(v[j]));
   } else {
 #pragma unroll
-    for (int j = 1; j < 32; ++j) m = c + j < cols ? fmaxf(m, __uint_as_float(v[j])) : m;
+    for (int j = 1; j < 32; ++j) m = j < n ? fmaxf(m, __uint_as_float(v[j])) : m;
   }
   m *= kLog2e;
   if (m > top) {
-    // (the first time: 0 times 0)
-    sum *= exp2_fast(top - m);
+    sum *= exp2_fast(top - m);   // (the first time 0)
     top = m;
   }
   const float shift = top == -INFINITY ? 0.f : -top;
   float s[4] = {};
-  if (c + 32 <= cols) {
+  if (n >= 32) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) s[j & 3] += exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, shift));
   } else {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (c + j < cols) s[j & 3] += exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, shift));
+      if (j < n) s[j & 3] += exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, shift));
   }
   sum += (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// v[j] of lane i to v[i] of lane j: blocks of 16, 8, .. 1 rows and columns change places
+__device__ __forceinline__ void transpose_32x32(uint32_t (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) {
+    const bool high = (lane & s) != 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j & s) continue;
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? v[j] : v[j | s], s);
+      if (high) v[j] = got;
+      else v[j | s] = got;
+    }
+  }
 }
 
 // BC: capacity of an accumulator in rows of D (`bc` at most).
@@ -411,7 +437,8 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     cluster_wait();
   }
   const uint32_t tmem = misc[0];
-  const int tiles = TN ? p.G * p.nc * p.nl : blk[p.G] * p.nl;
+  const int tiles = (TN ? p.G * p.nc * p.nl : blk[p.G] * p.nl) *
+                    (EPI == kBfSum && FORM == kBfNN ? p.loss.parts : 1);
   // the MMA's N: whole instruction steps; a pair's CTA holds half of the
   // columns each (tn: in whole 64-wide boxes)
   auto mma_n = [&](int cols) {
@@ -420,7 +447,8 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
   int group = 0;   // this thread's place in the groups (bf_tile)
   // the tile's last slot needs zeroed rows, and is this CTA's
   auto ragged = [&](const BfTile& T) {
-    return TN && (T.kn & 15) != 0 && T.kend == T.nk && T.kbeg < T.kend;
+    // (behind the rows of a single group there are none: zeros are loaded)
+    return TN && p.sizes && (T.kn & 15) != 0 && T.kend == T.nk && T.kbeg < T.kend;
   };
 
   if (warp == 0 || warp == 2) {
@@ -444,7 +472,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0, tails = 0, tail_par = 0;
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank, group);
+        const BfTile T = bf_tile<BK, FORM, EPI>(t, p, first, blk, krank, group);
         const int half = lanes_op ? 128 : mma_n(T.cols) / 2;   // from one CTA of a pair to the other
         const int at = (lanes_op ? T.l0 : T.q0) + static_cast<int>(side) * half;
         const uint32_t piece_bytes = bytes / pieces;
@@ -541,7 +569,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       uint32_t ph = 0, bph = 0;
       uint32_t turn = 1;   // checked build: the fill that a slot has to hold
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank, group);
+        const BfTile T = bf_tile<BK, FORM, EPI>(t, p, first, blk, krank, group);
         if (T.kbeg == T.kend) continue;
         const uint32_t idesc = idesc_bf16_f32(PAIR ? 256 : 128, mma_n(T.cols), P_MN, TN);
         const uint32_t d = tmem + static_cast<uint32_t>(b * ACC);
@@ -620,7 +648,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       int s = 0;
       uint32_t par = 0;
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, krank, group);
+        const BfTile T = bf_tile<BK, FORM, EPI>(t, p, first, blk, krank, group);
         if (ragged(T)) {
           // all 32 lanes: wait for this CTA's two loads, then zero the rows
           // behind the group's last one, up to the next multiple of 16 (a row
@@ -715,8 +743,10 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
   // column), which are kept, or the last time multiplied by the unit for D.
   auto add_rows = [&](const BfTile& T, int l, int c, uint32_t (&v)[32]) {
     const int n = l < min(p.N, T.l0 + p.lanes) ? min(32, T.cols - c) : 0;
-    const size_t at = static_cast<size_t>(T.q0 + c) * p.N + l;
-    if (n > 0 && !in_bounds(p, at, static_cast<size_t>(n - 1) * p.N + 1, bf_elements(p, TN))) return;
+    // (each part of the reduction has sums of its own)
+    const size_t rows = p.loss.parts > 1 ? static_cast<size_t>(T.k0 / p.loss.depth) * p.rows : 0;
+    const size_t at = (rows + T.q0 + c) * p.N + l;
+    if (n > 0 && !in_bounds(p, at, static_cast<size_t>(n - 1) * p.N + 1, bf_elements(p, TN) * p.loss.parts)) return;
     float* sum = p.loss.sum + at;
     if (!p.loss.first) {
       float old[32];
@@ -745,73 +775,129 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       const BfLoss& x = p.loss;
       int b = 0;
       uint32_t bph = 0;
-      for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, 0, group);
-        // (asked for before the wait)
-        int target[2];      // of the thread's token in each half of the lanes, from the tile's first word
-        float lse[2], scale[2];
-#pragma unroll
-        for (int a = 0; a < (PAIR ? 1 : 2); ++a) {
-          const int l = T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + q * 32 + lane;
-          const bool on = a < halves && l < p.N;
-          target[a] = on ? __ldg(x.targets + l) : -1;
-          if (EPI == kBfGrad) {
-            const bool there = target[a] >= 0 && target[a] < x.words;
-            const float unit = __ldg(x.unit);
-            scale[a] = there && unit != 0.f ? __fdiv_rn(__ldg(x.d_loss + l), unit) : 0.f;
-            lse[a] = there ? -kLog2e * __ldg(x.lse + l) : -INFINITY;
+      // The unit: the largest |d_loss| of the tokens with a target.  Every CTA of the
+      // first piece's launch finds it while its first tile's operands are loaded (a
+      // launch of its own took 3 us); the later launches read it.
+      float unit_d = 0.f;
+      if (EPI == kBfGrad) {
+        if (x.first) {
+          uint32_t* warps = reinterpret_cast<uint32_t*>(blk + p.G + 1);
+          for (int l = static_cast<int>(threadIdx.x) - 128; l < x.tokens; l += 32 * BF_EPI) {
+            const int y = __ldg(x.targets + l);
+            if (y >= 0 && y < x.words) unit_d = fmaxf(unit_d, fabsf(__ldg(x.d_loss + l)));
           }
-          // (0 .. : in this tile or a later one; a word before the piece is negative)
-          target[a] = target[a] >= 0 && target[a] < x.words ? target[a] - x.word0 - T.q0 : -1;
+          // (not negative: in the order of their bits)
+          const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(unit_d));
+          if (lane == 0) warps[warp - 4] = most;
+          named_bar_sync(1, 32 * BF_EPI);
+          unit_d = __uint_as_float(__reduce_max_sync(0xffffffffu, warps[lane % BF_EPI]));
+          if (blockIdx.x == 0 && threadIdx.x == 128) *x.unit = unit_d;
+        } else {
+          unit_d = *x.unit;
         }
-        const bool ok =
-            __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
-        tc_fence_after();
+      }
+      // 32 logits of token l, of the piece's words w .. (n of them there), into top and
+      // sum, or into D
+      struct Token {
+        int l;            // -1: none
+        int target;       // a word of the piece, or outside it
+        float lse, scale; // -log2(e) lse; d_loss / unit
+        float top, sum;
+      };
+      auto token = [&](int l, bool on) {
+        Token k{on ? l : -1, -1, -INFINITY, 0.f, -INFINITY, 0.f};
+        if (!on) return k;
+        const int y = __ldg(x.targets + l);
+        const bool there = y >= 0 && y < x.words;
+        if (there) k.target = y - x.word0;
+        if (EPI == kBfGrad && there) {
+          if (unit_d != 0.f) k.scale = __fdiv_rn(__ldg(x.d_loss + l), unit_d);
+          k.lse = -kLog2e * __ldg(x.lse + l);
+        }
+        return k;
+      };
+      auto take = [&](Token& k, uint32_t (&v)[32], int w, int n) {
+        // (the target's word is number `hit` of these; one behind them is of a later
+        // tile or piece)
+        const int hit = k.target - w;
+        if constexpr (EPI == kBfStats) {
+          add_logits(v, n, k.top, k.sum);
+          if (k.l >= 0 && hit >= 0 && hit < min(32, n)) {
+            float z = 0.f;
 #pragma unroll
-        for (int a = 0; a < (PAIR ? 1 : 2); ++a) {
-          if (a >= halves) break;
-          const int l = T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + q * 32 + lane;
-          const bool on = ok && l < min(p.N, T.l0 + p.lanes);
-          float top = -INFINITY, sum = 0.f;
-          for (int c = 32 * eh; c < T.cols; c += 64) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
-            tmem_wait_ld(v);
-            const int hit = target[a] - c;   // the target is the chunk's word of this number
-            if constexpr (EPI == kBfStats) {
-              add_logits(v, c, T.cols, top, sum);
-              if (on && hit >= 0 && hit < min(32, T.cols - c)) {
-                float z = 0.f;
+            for (int j = 0; j < 32; ++j) z = j == hit ? __uint_as_float(v[j]) : z;
+            x.hit[k.l] = z;
+          }
+        } else {
+          // (softmax - 1 at the target) * d_loss / unit (what lies past the piece's last
+          // word is not read again)
 #pragma unroll
-                for (int j = 0; j < 32; ++j) z = j == hit ? __uint_as_float(v[j]) : z;
-                x.hit[l] = z;
-              }
-            } else {
-              // (softmax - 1 at the target) * d_loss / unit (what lies past the piece's last
-              // word is not read again)
+          for (int j = 0; j < 32; ++j) {
+            const float s = exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, k.lse));
+            v[j] = __float_as_uint(k.scale * (j == hit ? s - 1.f : s));
+          }
+          const size_t at = static_cast<size_t>(k.l) * x.pitch + w;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float s = exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, lse[a]));
-                v[j] = __float_as_uint(scale[a] * (j == hit ? s - 1.f : s));
-              }
-              const size_t at = static_cast<size_t>(l) * x.pitch + T.q0 + c;
+          for (int j = 0; j < 32; j += 8) {
+            // (the pitch is a multiple of 8: whole vectors up to it)
+            if (k.l >= 0 && j < n && in_bounds(p, at + j, 8, static_cast<size_t>(x.tokens) * x.pitch)) {
+              uint32_t o[4];
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                // (the pitch is a multiple of 8: whole vectors up to it)
-                if (on && c + j < T.cols && in_bounds(p, at + j, 8, static_cast<size_t>(p.N) * x.pitch)) {
-                  uint32_t w[4];
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    w[i] = pack_bf16x2(__uint_as_float(v[j + 2 * i]), __uint_as_float(v[j + 2 * i + 1]));
-                  *reinterpret_cast<uint4*>(p.D + at + j) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-              }
+              for (int i = 0; i < 4; ++i)
+                o[i] = pack_bf16x2(__uint_as_float(v[j + 2 * i]), __uint_as_float(v[j + 2 * i + 1]));
+              *reinterpret_cast<uint4*>(p.D + at + j) = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
-          if constexpr (EPI == kBfStats) {
-            const size_t at = (static_cast<size_t>(T.q0 / p.bc) * 2 + eh) * p.N + l;
-            if (on && in_bounds(p, at, 1, static_cast<size_t>(x.parts) * p.N))
-              x.part[at] = make_float2(top, sum);
+        }
+      };
+      auto leave = [&](const Token& k, int i) {
+        const size_t at = static_cast<size_t>(i) * x.tokens + k.l;
+        if (EPI == kBfStats && k.l >= 0 && in_bounds(p, at, 1, static_cast<size_t>(x.pairs) * x.tokens))
+          x.pair[at] = make_float2(k.top, k.sum);
+      };
+      for (int t = unit; t < tiles; t += units) {
+        const BfTile T = bf_tile<BK, FORM, EPI>(t, p, first, blk, 0, group);
+        const int l_end = min(p.N, T.l0 + p.lanes);
+        // first lane of the warp's quarter, in half a
+        auto quarter = [&](int a) { return T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + q * 32; };
+        if (x.words_on_lanes) {
+          // (a first chunk's tokens are asked for before the wait)
+          Token k = token(T.q0 + 32 * eh + lane, 32 * eh + lane < T.cols);
+          const bool ok =
+              __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
+          tc_fence_after();
+          for (int c = 32 * eh; c < T.cols; c += 64) {
+            if (c >= 64) k = token(T.q0 + c + lane, c + lane < T.cols);
+            if (!ok) k.l = -1;
+            for (int a = 0; a < halves; ++a) {
+              if (quarter(a) >= l_end) break;
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
+              tmem_wait_ld(v);
+              transpose_32x32(v);
+              take(k, v, quarter(a), l_end - quarter(a));
+            }
+            leave(k, (T.l0 / p.lanes * (PAIR ? 2 : 1) + static_cast<int>(side)) * 4 + q);
+          }
+        } else {
+          Token k[2];
+#pragma unroll
+          for (int a = 0; a < (PAIR ? 1 : 2); ++a)
+            k[a] = token(quarter(a) + lane, a < halves && quarter(a) + lane < l_end);
+          const bool ok =
+              __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
+          tc_fence_after();
+#pragma unroll
+          for (int a = 0; a < (PAIR ? 1 : 2); ++a) {
+            if (a >= halves) break;
+            if (!ok) k[a].l = -1;
+            for (int c = 32 * eh; c < T.cols; c += 64) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
+              tmem_wait_ld(v);
+              take(k[a], v, T.q0 + c, T.cols - c);
+            }
+            leave(k[a], T.q0 / p.bc * 2 + eh);
           }
         }
         tc_fence_before();
@@ -829,7 +915,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
       int b = 0;
       uint32_t bph = 0;
       for (int t = unit; t < tiles; t += units) {
-        const BfTile T = bf_tile<BK, FORM>(t, p, first, blk, 0, group);
+        const BfTile T = bf_tile<BK, FORM, EPI>(t, p, first, blk, 0, group);
         const int l_end = min(p.N, T.l0 + p.lanes);
         if (T.nk == 0) {
           // tn, a group without rows: its block of D is C, or zero
@@ -887,7 +973,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     // is complete: the ring now holds the partial [half][row][128] in fp32.
     const bool mine = unit < tiles;
     BfTile T{};
-    if (mine) T = bf_tile<BK, FORM>(unit, p, first, blk, krank, group);
+    if (mine) T = bf_tile<BK, FORM, EPI>(unit, p, first, blk, krank, group);
     float* part = reinterpret_cast<float*>(smem);
     bool ok = true;
     if (warp >= 4 && mine && T.kbeg < T.kend) {
@@ -952,11 +1038,12 @@ double bf_cost(const BfCall& c, const BfPlan& f, int num_sms) {
   const bool tn = c.form == kBfTN;
   const double groups = tn ? c.G : std::min(c.G, c.rows), fill = groups > 1 ? 1.3 : 1.0;
   const double per = tn ? c.M : fill * c.rows / groups;       // rows of D in a group
-  const double depth = tn ? fill * c.rows / c.G : c.K;
+  const double parts = std::max(1, c.loss.parts);
+  const double depth = (tn ? fill * c.rows / c.G : c.K) / parts;
   const int cluster = (f.pair ? 2 : 1) * f.split;
   const double room = std::max(
       1.0, std::floor(num_sms * (cluster >= 8 ? 0.55 : cluster >= 4 ? 0.8 : 1.0) / cluster));
-  const double tiles = groups * std::ceil(per / f.bc) * ((c.N + f.lanes - 1) / f.lanes);
+  const double tiles = groups * std::ceil(per / f.bc) * ((c.N + f.lanes - 1) / f.lanes) * parts;
   const double waves = std::max(1.0, std::ceil(tiles / room));
   const int halves = f.pair ? 1 : (f.lanes + 127) / 128;
   const double cols = std::min<double>(f.bc, per);
@@ -974,8 +1061,9 @@ double bf_cost(const BfCall& c, const BfPlan& f, int num_sms) {
 // Tiles of `lanes` columns and `bc` rows of D that the call can have at most.
 long long bf_most_tiles(const BfCall& c, int lanes, int bc) {
   const long long nl = (c.N + lanes - 1) / lanes;
-  return nl * (c.form == kBfTN ? static_cast<long long>(c.G) * ((c.M + bc - 1) / bc)
-                               : std::min<long long>(c.G, c.rows) + c.rows / bc);
+  return nl * std::max(1, c.loss.parts) *
+         (c.form == kBfTN ? static_cast<long long>(c.G) * ((c.M + bc - 1) / bc)
+                          : std::min<long long>(c.G, c.rows) + c.rows / bc);
 }
 
 BfPlan bf_plan(const BfCall& c, int num_sms) {
@@ -987,7 +1075,8 @@ BfPlan bf_plan(const BfCall& c, int num_sms) {
   auto consider = [&](bool pair, int lanes, int bc) {
     const int width = pair ? 2 : 1;
     for (int split = 1; split * width <= kBfMaxCluster && (split == 1 || depth >= 128 * split); split *= 2) {
-      if (split > 1 && (c.epilogue == kBfStats || c.epilogue == kBfGrad)) break;   // (whole logits)
+      // (whole logits; a reduction in parts is split already)
+      if (split > 1 && (c.epilogue == kBfStats || c.epilogue == kBfGrad || c.loss.parts > 1)) break;
       if (split * width > num_sms) break;   // (a limit on the SMs may leave fewer)
       const BfPlan f{pair, lanes, bc, split};
       if (c.limited && bf16_grid(c, f, num_sms) > num_sms) break;   // (a cluster per tile)

@@ -156,10 +156,13 @@ def test_loss_gradient_refusals(kw, code):
 def test_loss_workspaces():
     f, b = dg.linear_cross_entropy_workspace_bytes, dg.linear_cross_entropy_backward_workspace_bytes
     for n in (f, b):
+        assert n(0, 0, 0) == 0 and n(5, 0, 8) >= 0 and n(5, 7, 0) >= 0
         assert n(0, 1000, 256) == 0 and n(-1, 5, 8) == -1 and n(5, -1, 8) == -1 and n(5, 5, -1) == -1
     for T, V in ((1, 1), (1, 131072), (4096, 131072), (100000, 50003)):
         K = 2048
         # far below the logits', where there are many
-        assert f(T, V, K) <= T * (V / 4 + 200) and f(T, V, K) >= 8 * T
+        assert f(T, V, K) <= T * (V / (2 if T <= 64 else 4) + 300) and f(T, V, K) >= 8 * T
         words = b(T, V, K) // (2 * T)
-        assert b(T, V, K) <= max(2 * T * 4352, 100 << 20) + 4 * T * K + 256 and words >= min(V, 4096)
+        # a piece of the gradient of the logits; dX in fp32, of a few tokens in parts
+        assert b(T, V, K) <= max(2 * T * 4352, 100 << 20) + max(4 * T * K, 64 << 20) + 1024
+        assert words >= min(V, 4096)
