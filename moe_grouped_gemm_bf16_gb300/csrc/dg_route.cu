@@ -7,9 +7,9 @@
 //   the k largest c among them are chosen, equal ones by their index
 //   w_j = scale s_j, or scale s_j / (sum of the chosen s)
 //
-// A warp takes a token, a lane every 32nd expert: the k largest are k rounds of
-// a maximum over the warp (redux on the values' order as unsigned integers, then
-// on the index among the lanes that hold it).
+// A warp takes a token (or several of few experts), a lane NPL consecutive experts: the
+// k largest are k rounds of a maximum over the lanes, on the values' order as unsigned
+// integers, which the first lane that holds it takes out.
 //
 // The choice is that of the formulas in 64 bits, whatever the rounding here: where all
 // biases are equal it is made by the logits themselves (both scores rise with
@@ -67,199 +67,402 @@ __device__ __forceinline__ double warp_sum(double v) {
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
   return v;
 }
-__device__ __forceinline__ double warp_max(double v) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = fmax(v, __shfl_xor_sync(ALL, v, o));
-  return v;
-}
-
 // (by exp(-|x|), which does not overflow)
 __device__ __forceinline__ float sigmoid(float x) {
   const float e = expf(-fabsf(x));
   return __fdiv_rn(x < 0.f ? e : 1.f, 1.f + e);
 }
 
-// Largest (value, lowest index) over the warp; -1 where all are -infinity.
-__device__ __forceinline__ int warp_argmax(double v, int index) {
-  const double top = warp_max(v);
-  return top == -INFINITY ? -1
-                          : static_cast<int>(__reduce_min_sync(
-                                ALL, v == top ? static_cast<unsigned>(index) : 0x7fffffffu));
+// Unsigned integers in the order of the doubles, none of them NaN; 0 stands below
+// them all.  (Compared as such: FP64 instructions are issued every 16 cycles.)
+__device__ __forceinline__ uint64_t order_of(double x) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x));
+  return u ^ (static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double double_of(uint64_t o) {
+  return __longlong_as_double(
+      static_cast<long long>((o & 0x8000000000000000ull) ? o ^ 0x8000000000000000ull : ~o));
+}
+__device__ __forceinline__ uint64_t warp_most(uint64_t v) {
+  const uint32_t high = __reduce_max_sync(ALL, static_cast<uint32_t>(v >> 32));
+  const uint32_t low = __reduce_max_sync(ALL, static_cast<uint32_t>(v >> 32) == high ? static_cast<uint32_t>(v) : 0);
+  return static_cast<uint64_t>(high) << 32 | low;
 }
 
-// The token's choice in 64 bits: lane j returns the j-th expert.
+// What the choice in fp32 leaves open, in 64 bits.  row: the token's values as
+// order_of(c) in fp32 (0: not available), whose differences are off by less than
+// `margin`; only the values that this leaves in doubt are computed, a lane one of its
+// own at a time (few lanes have more than one).  Returns the j-th choice in lane j.
+// (All values in 64 bits took 7 us for a token of 128 experts, 13 of 384.)
 template <class X, int NPL>
-__device__ __noinline__ int choose_exact(const RouteFwd& a, const X* logits) {
-  const int lane = threadIdx.x & 31;
-  double c[NPL];
-  double top = -INFINITY;
+__device__ __noinline__ int choose_exact(const RouteFwd a, const X* logits, const uint32_t* row,
+                                         float margin) {
+  const int lane = threadIdx.x & 31, e0 = lane * NPL;
+  uint32_t key[NPL];
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = lane + 32 * i;
-    c[i] = e < a.G ? static_cast<double>(clean(read_logit(logits + e))) : -INFINITY;
-    top = fmax(top, c[i]);
-  }
+  for (int i = 0; i < NPL; ++i) key[i] = e0 + i < a.G ? row[e0 + i] : 0;
+  uint64_t c[NPL];   // order of the exact values; 0: not needed
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) c[i] = 0;
+  double top = 0, sum = 1;
   if (!a.sigmoid) {
-    top = warp_max(top);
-    double sum = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (c[i] != -INFINITY) sum += exp(c[i] - top);
-    sum = warp_sum(sum);
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (c[i] != -INFINITY) c[i] = exp(c[i] - top) / sum;
-  } else {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (c[i] != -INFINITY) c[i] = 1.0 / (1.0 + exp(-c[i]));
-  }
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = lane + 32 * i;
-    if (a.bias && e < a.G) c[i] += static_cast<double>(__ldg(a.bias + e));
-    if (!(c[i] > -INFINITY)) c[i] = -INFINITY;
-  }
-  if (a.groups > a.top_groups) {
-    const int per = a.G / a.groups;
-    double mine = -INFINITY;   // lane g: group g's value
-    for (int g = 0; g < a.groups; ++g) {
-      double one = -INFINITY, two = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 32 * i;
-        if (e >= g * per && e < (g + 1) * per) {
-          two = fmax(two, fmin(one, c[i]));
-          one = fmax(one, c[i]);
-        }
-      }
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) {
-        const double p = __shfl_xor_sync(ALL, one, o), q = __shfl_xor_sync(ALL, two, o);
-        two = fmax(fmax(two, q), fmin(one, p));
-        one = fmax(one, p);
-      }
-      if (lane == g) mine = a.best == 2 && two != -INFINITY ? one + two : one;
+    float m = -INFINITY;
+    for (int e = lane; e < a.G; e += 32) m = fmaxf(m, clean(read_logit(logits + e)));
+    top = static_cast<double>(float_of(__reduce_max_sync(ALL, order_of(m))));
+    sum = 0;
+    for (int e = lane; e < a.G; e += 32) {
+      const float x = clean(read_logit(logits + e));
+      if (x > -INFINITY) sum += exp(static_cast<double>(x) - top);
     }
-    uint32_t keep = 0;
-    for (int n = 0; n < a.top_groups; ++n) {
-      const int g = warp_argmax((keep >> lane) & 1u || lane >= a.groups ? -INFINITY : mine, lane);
-      if (g < 0) break;
-      keep |= 1u << g;
+    sum = warp_sum(sum);
+  }
+  // computes the values in `want` (a bit per value of the lane)
+  auto compute = [&](uint32_t want) {
+    while (__any_sync(ALL, want != 0)) {
+      const int at = want ? __ffs(want) - 1 : 0;
+      uint64_t v = 0;
+      if (want) {
+        const double x = clean(read_logit(logits + e0 + at));
+        double s = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum;
+        if (a.bias) s += static_cast<double>(__ldg(a.bias + e0 + at));
+        v = order_of(s);
+      }
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (want && i == at) c[i] = v;
+      want &= want - 1;
+    }
+  };
+  uint32_t done = 0;
+  if (a.groups > a.top_groups) {
+    // the values that may be among their group's `best`: not below its best-th in fp32
+    // by more than the margin
+    const int per = a.G / a.groups;
+    uint64_t mine = 0;   // lane g: group g's value
+    uint32_t edge = 0;   // lane g: group g's best-th
+    if (lane < a.groups) {
+      uint32_t one = 0, two = 0;
+      for (int e = 0; e < per; ++e) {
+        const uint32_t v = row[lane * per + e];
+        two = max(two, min(one, v));
+        one = max(one, v);
+      }
+      edge = a.best == 2 && two ? two : one;
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < a.G && !((keep >> (e / per)) & 1u)) c[i] = -INFINITY;
+      const uint32_t limit = __shfl_sync(ALL, edge, min((e0 + i) / per, 31));
+      if (key[i] && float_of(key[i]) >= float_of(limit) - margin) done |= 1u << i;
     }
+    compute(done);
+    for (int g = 0; g < a.groups; ++g) {
+      uint64_t one = 0, two = 0;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (c[i] && e0 + i >= g * per && e0 + i < (g + 1) * per) {
+          if (c[i] > one) { two = one; one = c[i]; }
+          else if (c[i] > two) two = c[i];
+        }
+      const uint64_t first = warp_most(one);
+      // (the first lane that holds the largest gives its second)
+      const int owner = __ffs(__ballot_sync(ALL, one == first)) - 1;
+      const uint64_t second = warp_most(lane == owner ? two : one);
+      if (lane == g) {
+        mine = first;
+        if (a.best == 2 && second) mine = order_of(double_of(first) + double_of(second));
+      }
+    }
+    uint32_t keep = 0;
+    for (int n = 0; n < a.top_groups; ++n) {
+      const uint64_t left = (keep >> lane) & 1u ? 0 : mine;
+      const uint64_t v = warp_most(left);
+      if (v == 0) break;
+      keep |= 1u << (__ffs(__ballot_sync(ALL, left == v)) - 1);
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (!((keep >> min((e0 + i) / per, 31)) & 1u)) key[i] = c[i] = 0;
   }
-  int chosen = -1;
+  // the values that may be among the k largest: not below the k-th in fp32 by more
+  // than the margin
+  uint32_t left[NPL], edge = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) left[i] = key[i];
   for (int j = 0; j < a.k; ++j) {
-    double v = -INFINITY;
+    uint32_t v = 0;
     int at = 0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-      if (c[i] > v) { v = c[i]; at = lane + 32 * i; }
-    const int e = warp_argmax(v, at);
+      if (left[i] > v) { v = left[i]; at = i; }
+    const uint32_t best = __reduce_max_sync(ALL, v);
+    if (best) edge = best;
+    const int owner = __ffs(__ballot_sync(ALL, v == best)) - 1;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (lane == owner && i == at) left[i] = 0;
+  }
+  uint32_t want = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    if (key[i] && float_of(key[i]) >= float_of(edge) - margin) {
+      if (!((done >> i) & 1u)) want |= 1u << i;
+    } else {
+      c[i] = 0;
+    }
+  }
+  compute(want);
+  int chosen = -1;
+  for (int j = 0; j < a.k; ++j) {
+    uint64_t v = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (c[i] > v) { v = c[i]; at = i; }
+    const uint64_t best = warp_most(v);
+    if (best == 0) break;
+    const int owner = __ffs(__ballot_sync(ALL, v == best)) - 1;
+    const int e = __shfl_sync(ALL, e0 + at, owner);
     if (lane == j) chosen = e;
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-      if (e == lane + 32 * i) c[i] = -INFINITY;
+      if (lane == owner && i == at) c[i] = 0;
   }
   return chosen;
 }
 
+// ex2 and rcp approximated (2^-22 and 2^-23 of the result): for the choice, where what
+// they are off by is counted; the weights are computed with expf and division.
+__device__ __forceinline__ float exp_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // More than what the difference of two c near `c` may be off by in fp32, `bias`
-// the largest bias' magnitude.  A sigmoid: 2^-22 of 1 (expf, the sum, the quotient)
-// each.  A softmax's s: expf by 2^-22 of itself and by |x - max| 2^-24 (its
-// argument's rounding, |x - max| at most 88, and at most -ln s), the sum, common to
-// both, by 44 2^-24 (its roundings and its terms').  Each c: 2^-24 of itself.
+// the largest bias' magnitude; u = 2^-24.
+// A sigmoid: e by (4 + 1.5 |x|) u of itself (ex2.approx, its argument), s = 1 / (1 + e)
+// by a quarter of that at most and |x| s (1 - s) < 0.23, sum, reciprocal and product by
+// 4 u: below 2^-21 each.
+// A softmax's s: e by (4 + 2.5 d) u of itself, d = |x - max| at most ln(1 / s) and 104
+// (below which e is 0); the sum, common to both, by (4 + 2.5 ln(1024)) u for its terms
+// and 40 u for its additions and its reciprocal: with s d < 0.37 below 2^-17 in all, with
+// d < 104 below 2^-14 of s.
+// Each c: u of itself.
 __device__ __forceinline__ float doubt(bool sigmoid, float c, float bias) {
-  const float s = sigmoid ? 0x1p-20f : fminf(0x1p-18f, 0x1p-16f * (fabsf(c) + bias));
+  const float s = sigmoid ? 0x1p-19f : fminf(0x1p-17f, 0x1p-14f * (fabsf(c) + bias));
   return s + 0x1p-22f * fabsf(c);
 }
 
-// NPL: experts per lane.
+// A lane's NPL consecutive logits (or biases) from e0 on, -infinity behind the last.
+// `whole`: the row lies on 16 bytes, or on as many as a lane's elements take.
+template <int NPL>
+__device__ __forceinline__ void read_row(const float* p, int e0, int G, bool whole, float (&x)[NPL]) {
+  if (whole && NPL >= 4) {
+#pragma unroll
+    for (int i = 0; i < NPL; i += 4) {
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (e0 + i < G) v = __ldg(reinterpret_cast<const float4*>(p + e0 + i));
+      x[i] = v.x;
+      x[i + 1 < NPL ? i + 1 : i] = v.y;
+      x[i + 2 < NPL ? i + 2 : i] = v.z;
+      x[i + 3 < NPL ? i + 3 : i] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) x[i] = e0 + i < G ? __ldg(p + e0 + i) : -INFINITY;
+  }
+}
+template <int NPL>
+__device__ __forceinline__ void read_row(const __nv_bfloat16* p, int e0, int G, bool whole,
+                                         float (&x)[NPL]) {
+  constexpr uint32_t kNone = 0xff80ff80u;   // -infinity twice
+  if (whole && NPL >= 4) {
+    constexpr int STEP = NPL >= 8 ? 8 : 4;
+#pragma unroll
+    for (int i = 0; i < NPL; i += STEP) {
+      uint32_t v[4] = {kNone, kNone, kNone, kNone};
+      if (e0 + i < G) {
+        if constexpr (STEP == 8) {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(p + e0 + i));
+          v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+        } else {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(p + e0 + i));
+          v[0] = w.x; v[1] = w.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < STEP && i + j < NPL; ++j)
+        x[i + j] = __uint_as_float(j & 1 ? v[j >> 1] & 0xFFFF0000u : v[j >> 1] << 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) x[i] = e0 + i < G ? read_logit(p + e0 + i) : -INFINITY;
+  }
+}
+
+// Whether every row of G elements at p lies as read_row's whole rows do.
 template <class X, int NPL>
-__global__ void __launch_bounds__(32 * RT_WARPS)
-route_kernel(const RouteFwd a) {
+bool whole_rows(const void* p, int G) {
+  constexpr int step = NPL * static_cast<int>(sizeof(X)) >= 16 ? 16 / sizeof(X) : NPL;
+  return NPL >= 4 && G % step == 0 && (reinterpret_cast<uintptr_t>(p) & (step * sizeof(X) - 1)) == 0;
+}
+
+template <int NPL>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&key)[NPL]) {
+  uint32_t v[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) v[i] = key[i];
+#pragma unroll
+  for (int n = NPL / 2; n >= 1; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < NPL / 2; ++i)
+      if (i < n) v[i] = max(v[i], v[i + n]);
+  return v[0];
+}
+
+// Over the LANES lanes of a token.
+template <int LANES>
+__device__ __forceinline__ uint32_t team_max(uint32_t v) {
+  if constexpr (LANES == 32) {
+    return __reduce_max_sync(ALL, v);
+  } else {
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o >>= 1) v = max(v, __shfl_xor_sync(ALL, v, o));
+    return v;
+  }
+}
+template <int LANES>
+__device__ __forceinline__ float team_sum(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
+  return v;
+}
+// The first lane of the token (counted in it) that has `p`; -1: none.
+template <int LANES>
+__device__ __forceinline__ int team_first(bool p, int team) {
+  uint32_t b = __ballot_sync(ALL, p);
+  if (LANES < 32) b = b >> (team * LANES) & ((1u << (LANES & 31)) - 1);
+  return __ffs(b) - 1;
+}
+
+// What the host works out once.
+struct RoutePlan {
+  int per;             // experts of a group
+  uint32_t per_inv;    // x / per = __umulhi(x, per_inv) for x < 2^16 (per = 1: 0)
+  bool grouped;        // groups are left out
+  bool whole, whole_bias;
+};
+
+// NPL: experts per lane, LANES: lanes per token (the others of the warp take further
+// tokens: 9268 tokens of 16 experts took 9 us with a warp each).
+template <class X, int NPL, int LANES>
+__global__ void __launch_bounds__(32 * RT_WARPS, NPL <= 4 ? 5 : NPL == 8 ? 4 : NPL == 16 ? 2 : 1)
+route_kernel(const RouteFwd a, const RoutePlan plan) {
+  constexpr int TEAMS = 32 / LANES;
   extern __shared__ uint32_t route_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t* row = route_smem + warp * a.G;   // (with groups) the values' order
+  const int team = lane / LANES, member = lane % LANES, e0 = member * NPL;
+  uint32_t* rows = route_smem + warp * TEAMS * a.G;   // the tokens' values in order (if kept)
+  uint32_t* row = rows + team * a.G;
   grid_dep_wait();
   grid_dep_launch_dependents();
+  const int first_t = (blockIdx.x * RT_WARPS + warp) * TEAMS;
+  // (a token behind the last is read as the last, and not written)
+  auto logits_of = [&](int t) {
+    return static_cast<const X*>(a.logits) + static_cast<size_t>(min(t, a.T - 1)) * a.G;
+  };
+  float x[NPL];
+  // (the first row and the biases asked for together)
+  if (first_t < a.T) read_row<NPL>(logits_of(first_t + team), e0, a.G, plan.whole, x);
   // all biases equal: the choice is by the logits
   bool even = true;
   float bias_most = 0.f;
   if (a.bias) {
-    const float first = __ldg(a.bias);
-    bool same = first > -INFINITY;
-    for (int e = lane; e < a.G; e += 32) {
-      const float b = __ldg(a.bias + e);
-      same = same && b == first;
-      bias_most = fmaxf(bias_most, fabsf(b));
-    }
-    even = __all_sync(ALL, same);
+    float b[NPL];
+    read_row<NPL>(a.bias, e0, a.G, plan.whole_bias, b);
+    const float first = __shfl_sync(ALL, b[0], 0);
+    even = first > -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (e0 + i < a.G) {
+        even = even && b[i] == first;
+        bias_most = fmaxf(bias_most, fabsf(b[i]));
+      }
+    even = __all_sync(ALL, even);
     bias_most = __uint_as_float(__reduce_max_sync(ALL, __float_as_uint(bias_most)));
   }
-  const bool grouped = a.groups > a.top_groups;
+  const bool grouped = plan.grouped;
   const bool by_logit = even && (!grouped || a.best == 1);
-  const int per = a.G / a.groups;
-  for (int t = blockIdx.x * RT_WARPS + warp; t < a.T; t += gridDim.x * RT_WARPS) {
-    const X* logits = static_cast<const X*>(a.logits) + static_cast<size_t>(t) * a.G;
-    float x[NPL];
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = lane + 32 * i;
-      x[i] = e < a.G ? clean(read_logit(logits + e)) : -INFINITY;
-    }
+  for (int t0 = first_t; t0 < a.T; t0 += gridDim.x * RT_WARPS * TEAMS) {
+    const int t = t0 + team;
+    const X* logits = logits_of(t);
+    if (t0 != first_t) read_row<NPL>(logits, e0, a.G, plan.whole, x);
     uint32_t key[NPL];   // order of c, or of the logit; 0: not available
-    uint32_t key_top = 0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      key[i] = x[i] > -INFINITY ? order_of(x[i]) : 0;
-      key_top = max(key_top, key[i]);
+      // (NaN compares false)
+      key[i] = x[i] > -INFINITY ? order_of(fminf(x[i], FLT_MAX) + 0.f) : 0;
+      x[i] = key[i] ? fminf(x[i], FLT_MAX) : -INFINITY;
     }
     // the scores are needed in full for c, or for a softmax's sum
     float top = 0.f, sum = 1.f;
     if (!a.sigmoid && !(by_logit && a.renormalize)) {
-      key_top = __reduce_max_sync(ALL, key_top);
-      top = key_top ? float_of(key_top) : 0.f;
+      const uint32_t most = team_max<LANES>(largest<NPL>(key));
+      top = most ? float_of(most) : 0.f;
       sum = 0.f;
+      if (!a.renormalize) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const float s = expf(x[i] - top);   // (0 for -infinity)
-        sum += s;
-        if (!by_logit) x[i] = key[i] ? s : -INFINITY;
+        for (int i = 0; i < NPL; ++i) {
+          x[i] = expf(x[i] - top);   // (0 for -infinity)
+          sum += x[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          x[i] = exp_fast(x[i] - top);
+          sum += x[i];
+        }
       }
-      sum = warp_sum(sum);
+      sum = team_sum<LANES>(sum);
     } else if (!by_logit) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) x[i] = key[i] ? sigmoid(x[i]) : -INFINITY;
+      for (int i = 0; i < NPL; ++i) {
+        const float e = exp_fast(-fabsf(x[i]));
+        x[i] = (x[i] < 0.f ? e : 1.f) * rcp_fast(1.f + e);
+      }
     }
     if (!by_logit) {
-      const float share = a.sigmoid ? 1.f : __frcp_rn(sum);
+      const float share = a.sigmoid ? 1.f : rcp_fast(sum);
+      float b[NPL] = {};
+      if (a.bias) read_row<NPL>(a.bias, e0, a.G, plan.whole_bias, b);   // (in L1)
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 32 * i;
-        const float c = e < a.G ? fmaf(x[i], share, a.bias ? __ldg(a.bias + e) : 0.f) : -INFINITY;
-        key[i] = c > -INFINITY ? order_of(c) : 0;
+        const float c = fmaf(x[i], share, b[i]);
+        key[i] = key[i] && c > -INFINITY ? order_of(c) : 0;
       }
     }
     bool sure = true;
-    if (grouped) {
-      // 32 / groups lanes (a power of two) to a group's two largest values
+    if (grouped || !by_logit) {
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
-        if (lane + 32 * i < a.G) row[lane + 32 * i] = key[i];
+        if (e0 + i < a.G) row[e0 + i] = key[i];
       __syncwarp();
-      const int width = 1 << (31 - __clz(32 / a.groups));
-      const int g = lane / width;
+    }
+    if (grouped) {
+      // LANES / groups lanes (a power of two) to a group's two largest values
+      const int shift = 31 - __clz(LANES / a.groups), width = 1 << shift;
+      const int g = member >> shift;
       uint32_t one = 0, two = 0;
       if (g < a.groups)
-        for (int e = lane & (width - 1); e < per; e += width) {
-          const uint32_t v = row[g * per + e];
+#pragma unroll 4
+        for (int e = member & (width - 1); e < plan.per; e += width) {
+          const uint32_t v = row[g * plan.per + e];
           two = max(two, min(one, v));
           one = max(one, v);
         }
@@ -270,71 +473,81 @@ route_kernel(const RouteFwd a) {
       }
       uint32_t value = one;
       if (a.best == 2 && two) value = order_of(float_of(one) + float_of(two));
-      uint32_t keep = 0;
-      const bool mine = g < a.groups && (lane & (width - 1)) == 0;
-      uint32_t last = 0, left = mine ? value : 0;
-      for (int n = 0; n < a.top_groups; ++n) {
-        const uint32_t v = __reduce_max_sync(ALL, left);
-        if (v == 0) break;
-        const unsigned who = __reduce_min_sync(ALL, left == v ? static_cast<unsigned>(lane) : 32u);
-        keep |= 1u << (who / width);
-        if (lane == static_cast<int>(who)) left = 0;
-        last = v;
+      // a group's rank: the groups of a larger value, and of the same before it
+      const bool mine = g < a.groups;
+      value = mine ? value : 0;
+      int rank = 0;
+      for (int h = 0; h < a.groups; ++h) {
+        const uint32_t v = __shfl_sync(ALL, value, team * LANES + (h << shift));
+        rank += v > value || (v == value && h < g);
       }
-      const uint32_t next = __reduce_max_sync(ALL, left);
+      const bool stays = mine && value && rank < a.top_groups;
+      const uint32_t lanes = __ballot_sync(ALL, stays) >> (team * LANES);
+      const uint32_t last = ~team_max<LANES>(stays ? ~value : 0);
+      const uint32_t next = team_max<LANES>(stays ? 0 : value);
       if (!by_logit && next) {
         const float l = float_of(last), n = float_of(next);
         sure = l - n > 2.f * doubt(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most);
       }
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 32 * i;
-        if (e < a.G && !((keep >> (e / per)) & 1u)) key[i] = 0;
+        const uint32_t of = plan.per_inv ? __umulhi(e0 + i, plan.per_inv) : e0 + i;
+        if (!((lanes >> (of << shift & 31)) & 1u)) key[i] = 0;
       }
     }
     // k rounds, and one more for what the last choice was close to
     int chosen = -1;
     const int rounds = by_logit ? a.k : a.k + 1;
-    uint32_t before = 0;
+    float before = 0.f;
     for (int j = 0; j < rounds; ++j) {
-      uint32_t v = 0;
+      const uint32_t v = largest<NPL>(key);
+      const uint32_t best = team_max<LANES>(v);
+      if (!by_logit && best) {
+        const float n = float_of(best);
+        if (j > 0) sure = sure && before - n > doubt(a.sigmoid, fmaxf(fabsf(before), fabsf(n)), bias_most);
+        before = n;
+      }
+      const int owner = team_first<LANES>(v == best, team);
       int at = 0;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (key[i] > v) { v = key[i]; at = i; }
-      const uint32_t best = __reduce_max_sync(ALL, v);
-      if (best == 0) break;
-      if (!by_logit && j > 0) {
-        const float l = float_of(before), n = float_of(best);
-        sure = sure && l - n > doubt(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most);
-      }
-      before = best;
-      const unsigned e =
-          __reduce_min_sync(ALL, v == best ? static_cast<unsigned>(lane + 32 * at) : 0x7fffffffu);
-      if (lane == j && j < a.k) chosen = static_cast<int>(e);
+      for (int i = NPL - 1; i >= 1; --i) at = key[i] == best ? i : at;
+      if (NPL > 1) at = key[0] == best ? 0 : at;
+      const int e = __shfl_sync(ALL, e0 + at, team * LANES + owner);
+      if (member == j && j < a.k && best) chosen = e;
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
-        if (e == static_cast<unsigned>(lane + 32 * i)) key[i] = 0;
+        if (member == owner && i == at) key[i] = 0;
     }
-    if (!sure) chosen = choose_exact<X, NPL>(a, logits);
+    if (!__all_sync(ALL, sure)) {
+      // (|c| at most that of the scores and the biases; an infinite bias decides by
+      // itself).  All lanes take one token at a time.
+      const uint32_t open = __ballot_sync(ALL, !sure);
+      const float margin = 2.f * doubt(a.sigmoid, 1.f + (bias_most < INFINITY ? bias_most : 0.f), bias_most);
+      for (int i = 0; i < TEAMS; ++i) {
+        if (!((open >> (i * LANES)) & 1u)) continue;
+        const int e = choose_exact<X, (NPL * LANES + 31) / 32>(a, logits_of(t0 + i), rows + i * a.G, margin);
+        const int mine = __shfl_sync(ALL, e, member);
+        if (team == i) chosen = mine;
+      }
+    }
     // weights: lane j that of the j-th choice
-    const bool there = lane < a.k && chosen >= 0;
+    const bool there = member < a.k && chosen >= 0;
     const float y = there ? clean(read_logit(logits + chosen)) : -INFINITY;
     float s;
     if (a.sigmoid) {
       s = there ? sigmoid(y) : 0.f;
-      if (a.renormalize) s = __fdiv_rn(s, warp_sum(s) + kLeast);
+      if (a.renormalize) s = __fdiv_rn(s, team_sum<LANES>(s) + kLeast);
     } else if (a.renormalize) {
       // (relative to the largest chosen: no underflow of them all)
-      const uint32_t m = __reduce_max_sync(ALL, there ? order_of(y) : 0);
+      const uint32_t m = team_max<LANES>(there ? order_of(y) : 0);
       s = there ? expf(y - float_of(m)) : 0.f;
-      const float total = warp_sum(s);
+      const float total = team_sum<LANES>(s);
       s = there ? __fdiv_rn(s, total) : 0.f;
     } else {
       s = there ? __fdiv_rn(expf(y - top), sum) : 0.f;
     }
-    if (lane < a.k) {
-      const size_t at = static_cast<size_t>(t) * a.k + lane;
+    if (member < a.k && t < a.T) {
+      const size_t at = static_cast<size_t>(t) * a.k + member;
       a.experts[at] = chosen;
       a.weights[at] = s * a.scale;
     }
@@ -349,9 +562,75 @@ __device__ __forceinline__ void write_logit(__nv_bfloat16* p, float v) { *p = __
 //   renormalised: ds_j = (d_j - sum_i d_i s_i / S) / S, S the sum of the chosen s
 //   sigmoid: dx = ds s (1 - s);  softmax: dx_e = s_e (ds_e - sum_i ds_i s_i)
 // In the renormalised softmax the last sum vanishes, so that, as with sigmoid
-// scores, only the chosen logits have a gradient and only they are read.  The row
-// is put together in shared memory (an expert that is named twice gets both
-// contributions, in order).
+// scores, only the chosen logits have a gradient and only they are read: a token takes
+// LANES lanes, one for each choice, which write zeros and then the chosen ones'.
+template <class X, int LANES>
+__global__ void __launch_bounds__(32 * RT_WARPS)
+route_backward_few_kernel(const RouteBwd a, bool whole) {
+  constexpr int TEAMS = 32 / LANES, STEP = 16 / sizeof(X);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = lane / LANES, member = lane % LANES;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  for (int t0 = (blockIdx.x * RT_WARPS + warp) * TEAMS; t0 < a.T; t0 += gridDim.x * RT_WARPS * TEAMS) {
+    const int t = t0 + team;
+    const X* logits = static_cast<const X*>(a.logits) + static_cast<size_t>(t) * a.G;
+    X* out = static_cast<X*>(a.d_logits) + static_cast<size_t>(t) * a.G;
+    const size_t pair = static_cast<size_t>(t) * a.k + member;
+    int e = -1;
+    float d = 0.f;
+    if (member < a.k && t < a.T) {
+      e = __ldg(a.experts + pair);
+      d = __ldg(a.d_weights + pair) * a.scale;
+      if (e >= a.G || e < -1) {
+        atomicCAS(a.status, 0u, ST_EXPERT_RANGE);
+        e = -1;
+      }
+    }
+    const float x = e >= 0 ? clean(read_logit(logits + e)) : -INFINITY;
+    const bool there = x > -INFINITY;
+    if (t < a.T) {
+      if (whole) {
+        for (int i = member * STEP; i < a.G; i += LANES * STEP)
+          *reinterpret_cast<uint4*>(out + i) = make_uint4(0, 0, 0, 0);
+      } else {
+        for (int i = member; i < a.G; i += LANES) write_logit(out + i, 0.f);
+      }
+    }
+    if (!there) d = 0.f;
+    float s, g;
+    if (a.sigmoid) {
+      s = there ? sigmoid(x) : 0.f;
+      if (a.renormalize) {
+        const float total = team_sum<LANES>(s) + kLeast;
+        d = __fdiv_rn(d - team_sum<LANES>(d * __fdiv_rn(s, total)), total);
+      }
+      g = there ? d * s * sigmoid(-x) : 0.f;   // (1 - s without cancellation)
+    } else {
+      const uint32_t m = team_max<LANES>(there ? order_of(x) : 0);
+      s = there ? expf(x - float_of(m)) : 0.f;
+      const float total = team_sum<LANES>(s);
+      s = there ? __fdiv_rn(s, total) : 0.f;
+      g = s * (d - team_sum<LANES>(d * s));
+    }
+    // an expert that is named twice gets both, in order (the choices before a lane's own)
+    bool first = true;
+    float sum = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      const int ej = __shfl_sync(ALL, e, team * LANES + j);
+      const float gj = __shfl_sync(ALL, g, team * LANES + j);
+      if (ej == e) {
+        sum += gj;
+        first = first && j >= member;
+      }
+    }
+    __syncwarp();   // (the zeros come before the values)
+    if (e >= 0 && first) write_logit(out + e, sum);
+  }
+}
+
+// A softmax that is not renormalised: a warp a token, the row put together in shared
+// memory.
 template <class X>
 __global__ void __launch_bounds__(32 * RT_WARPS)
 route_backward_kernel(const RouteBwd a) {
@@ -360,9 +639,9 @@ route_backward_kernel(const RouteBwd a) {
   float* row = route_rows + warp * a.G;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const bool few = a.sigmoid || a.renormalize;
   for (int t = blockIdx.x * RT_WARPS + warp; t < a.T; t += gridDim.x * RT_WARPS) {
     const X* logits = static_cast<const X*>(a.logits) + static_cast<size_t>(t) * a.G;
+    X* out = static_cast<X*>(a.d_logits) + static_cast<size_t>(t) * a.G;
     const size_t pair = static_cast<size_t>(t) * a.k + lane;
     int e = -1;
     float d = 0.f;
@@ -374,75 +653,84 @@ route_backward_kernel(const RouteBwd a) {
         e = -1;
       }
     }
-    for (int i = lane; i < a.G; i += 32) row[i] = 0.f;
-    float x = e >= 0 ? clean(read_logit(logits + e)) : -INFINITY;
+    const float x = e >= 0 ? clean(read_logit(logits + e)) : -INFINITY;
     const bool there = x > -INFINITY;
     if (!there) d = 0.f;
-    float s = 0.f, g, top = 0.f, share = 0.f;
-    if (a.sigmoid) {
-      s = there ? sigmoid(x) : 0.f;
-      if (a.renormalize) {
-        const float total = warp_sum(s) + kLeast;
-        d = __fdiv_rn(d - warp_sum(d * __fdiv_rn(s, total)), total);
-      }
-      g = there ? d * s * sigmoid(-x) : 0.f;   // (1 - s without cancellation)
-    } else if (a.renormalize) {
-      const uint32_t m = __reduce_max_sync(ALL, there ? order_of(x) : 0);
-      s = there ? expf(x - float_of(m)) : 0.f;
-      const float total = warp_sum(s);
-      s = there ? __fdiv_rn(s, total) : 0.f;
-      g = s * (d - warp_sum(d * s));
-    } else {
-      uint32_t m = 0;
-      for (int i = lane; i < a.G; i += 32) {
-        const float v = clean(read_logit(logits + i));
-        if (v > -INFINITY) m = max(m, order_of(v));
-      }
-      m = __reduce_max_sync(ALL, m);
-      top = m ? float_of(m) : 0.f;
-      float sum = 0.f;
-      for (int i = lane; i < a.G; i += 32) sum += expf(clean(read_logit(logits + i)) - top);
-      sum = warp_sum(sum);
-      share = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
-      s = there ? expf(x - top) * share : 0.f;
-      g = d;   // ds: the row's other term follows below
+    uint32_t m = 0;
+    for (int i = lane; i < a.G; i += 32) {
+      const float v = clean(read_logit(logits + i));
+      if (v > -INFINITY) m = max(m, order_of(v));
+      row[i] = 0.f;
     }
-    const float dot = few ? 0.f : warp_sum(d * s);
+    m = __reduce_max_sync(ALL, m);
+    const float top = m ? float_of(m) : 0.f;
+    float sum = 0.f;
+    for (int i = lane; i < a.G; i += 32) sum += expf(clean(read_logit(logits + i)) - top);
+    sum = warp_sum(sum);
+    const float share = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
+    const float dot = warp_sum(there ? d * (expf(x - top) * share) : 0.f);
     __syncwarp();
     for (int j = 0; j < a.k; ++j) {
       const int ej = __shfl_sync(ALL, e, j);
-      const float gj = __shfl_sync(ALL, g, j);
+      const float dj = __shfl_sync(ALL, d, j);
       // (the same lane for the same expert: its additions are in order)
-      if (ej >= 0 && (ej & 31) == lane) row[ej] += gj;
+      if (ej >= 0 && (ej & 31) == lane) row[ej] += dj;
     }
     __syncwarp();
-    X* out = static_cast<X*>(a.d_logits) + static_cast<size_t>(t) * a.G;
-    for (int i = lane; i < a.G; i += 32) {
-      float v = row[i];
-      if (!few) v = expf(clean(read_logit(logits + i)) - top) * share * (v - dot);
-      write_logit(out + i, v);
-    }
+    for (int i = lane; i < a.G; i += 32)
+      write_logit(out + i, expf(clean(read_logit(logits + i)) - top) * share * (row[i] - dot));
     __syncwarp();
   }
 }
 
-int route_grid(int T, int num_sms, bool limited) {
-  const int blocks = (T - 1) / RT_WARPS + 1;
-  return limited ? std::min(blocks, num_sms) : std::min(blocks, 8 * num_sms);
+// Blocks for T tokens, `teams` of them to a warp.
+int route_grid(int T, int teams, int num_sms, bool limited) {
+  const int each = RT_WARPS * teams, blocks = (T - 1) / each + 1;
+  return limited ? std::min(blocks, num_sms) : blocks;
+}
+
+template <class X, int NPL, int LANES>
+cudaError_t launch_fwd(const RouteFwd& a, int num_sms, bool limited, cudaStream_t stream) {
+  constexpr int TEAMS = 32 / LANES;
+  RoutePlan p{};
+  p.per = a.G / a.groups;
+  p.per_inv = p.per > 1 ? 0xffffffffu / p.per + 1 : 0;
+  p.grouped = a.groups > a.top_groups;
+  p.whole = whole_rows<X, NPL>(a.logits, a.G);
+  p.whole_bias = whole_rows<float, NPL>(a.bias, a.G);
+  const int smem = p.grouped || a.bias ? RT_WARPS * TEAMS * a.G * 4 : 0;
+  return launch_dependent(route_kernel<X, NPL, LANES>, dim3(route_grid(a.T, TEAMS, num_sms, limited)),
+                          32 * RT_WARPS, stream, smem, a, p);
 }
 
 template <class X>
 cudaError_t launch_fwd(const RouteFwd& a, int num_sms, bool limited, cudaStream_t stream) {
-  const dim3 grid(route_grid(a.T, num_sms, limited));
-  const int smem = a.groups > a.top_groups ? RT_WARPS * a.G * 4 : 0;
-  auto go = [&](auto kernel) { return launch_dependent(kernel, grid, 32 * RT_WARPS, stream, smem, a); };
-  // registers for the row of logits: as many as its length needs
-  if (a.G <= 32) return go(route_kernel<X, 1>);
-  if (a.G <= 64) return go(route_kernel<X, 2>);
-  if (a.G <= 128) return go(route_kernel<X, 4>);
-  if (a.G <= 256) return go(route_kernel<X, 8>);
-  if (a.G <= 512) return go(route_kernel<X, 16>);
-  return go(route_kernel<X, 32>);
+  // a lane for each choice and each group at least; as few lanes, and registers for the
+  // row of logits, as its length needs
+  const int least = std::max(a.k, a.groups);
+  if (a.G <= 8 && least <= 8) return launch_fwd<X, 1, 8>(a, num_sms, limited, stream);
+  if (a.G <= 16 && least <= 8) return launch_fwd<X, 2, 8>(a, num_sms, limited, stream);
+  if (a.G <= 32 && least <= 8) return launch_fwd<X, 4, 8>(a, num_sms, limited, stream);
+  if (a.G <= 64 && least <= 16) return launch_fwd<X, 4, 16>(a, num_sms, limited, stream);
+  if (a.G <= 64) return launch_fwd<X, 2, 32>(a, num_sms, limited, stream);
+  if (a.G <= 128) return launch_fwd<X, 4, 32>(a, num_sms, limited, stream);
+  if (a.G <= 256) return launch_fwd<X, 8, 32>(a, num_sms, limited, stream);
+  if (a.G <= 512) return launch_fwd<X, 16, 32>(a, num_sms, limited, stream);
+  return launch_fwd<X, 32, 32>(a, num_sms, limited, stream);
+}
+
+template <class X>
+cudaError_t launch_bwd(const RouteBwd& a, int num_sms, bool limited, cudaStream_t stream) {
+  if (!a.sigmoid && !a.renormalize)
+    return launch_dependent(route_backward_kernel<X>, dim3(route_grid(a.T, 1, num_sms, limited)),
+                            32 * RT_WARPS, stream, RT_WARPS * a.G * 4, a);
+  const bool whole = a.G % (16 / sizeof(X)) == 0 && (reinterpret_cast<uintptr_t>(a.d_logits) & 15) == 0;
+  const int lanes = a.k <= 8 ? 8 : a.k <= 16 ? 16 : 32;
+  const dim3 grid(route_grid(a.T, 32 / lanes, num_sms, limited));
+  auto go = [&](auto kernel) { return launch_dependent(kernel, grid, 32 * RT_WARPS, stream, 0, a, whole); };
+  return lanes == 8    ? go(route_backward_few_kernel<X, 8>)
+         : lanes == 16 ? go(route_backward_few_kernel<X, 16>)
+                       : go(route_backward_few_kernel<X, 32>);
 }
 
 }  // namespace
@@ -454,10 +742,8 @@ cudaError_t launch_route(const RouteFwd& a, bool bf16, int num_sms, bool limited
 
 cudaError_t launch_route_backward(const RouteBwd& a, bool bf16, int num_sms, bool limited,
                                   cudaStream_t stream) {
-  const dim3 grid(route_grid(a.T, num_sms, limited));
-  const int smem = RT_WARPS * a.G * 4;
-  return bf16 ? launch_dependent(route_backward_kernel<__nv_bfloat16>, grid, 32 * RT_WARPS, stream, smem, a)
-              : launch_dependent(route_backward_kernel<float>, grid, 32 * RT_WARPS, stream, smem, a);
+  return bf16 ? launch_bwd<__nv_bfloat16>(a, num_sms, limited, stream)
+              : launch_bwd<float>(a, num_sms, limited, stream);
 }
 
 }  // namespace dgk

@@ -23,13 +23,15 @@ namespace {
 constexpr unsigned ALL = 0xffffffffu;
 
 // ------------------------------------------------------------ the sort ----
-constexpr int SORT_THREADS = 1024, SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_CLUSTER = 8;
+constexpr int SORT_BATCH = 8;   // pairs of a lane asked for at a time
 constexpr int kSegment = 128;   // contiguous layout: an expert's segment in whole blocks
 
-// Shared memory of a block: a count per warp and expert; the block's count, all
-// blocks' count and the first row of each expert; the totals of the scan's warps.
-int sort_smem(int G) { return (SORT_WARPS * G + 3 * G + 1 + 32) * 4; }
+// Shared memory of a block: a count per warp and expert (rows of an odd length: the
+// warps' counts of an expert lie in different banks); the block's count, all blocks'
+// count, the block's first row and the first row of each expert; the totals of the
+// scan's warps.
+int sort_smem(int warps, int G) { return (warps * (G | 1) + 4 * G + 1 + 32) * 4; }
 
 __device__ __forceinline__ int expert_of(const RowsCall& a, int pair, bool& bad) {
   const int e = __ldg(a.experts + pair);
@@ -37,129 +39,166 @@ __device__ __forceinline__ int expert_of(const RowsCall& a, int pair, bool& bad)
   return e >= 0 && e < a.G ? e : -1;
 }
 
-// One cluster sorts.  The blocks share the pairs in order, a block's warps its
-// share; a warp takes 32 pairs at a time, where __match_any gives each lane the
-// lanes of the same expert.  Two passes: each warp's counts, from which follow
-// (over the warps, over the blocks, over the experts) the first row of each warp's
-// pairs of each expert; then the rows themselves.
-template <int LAYOUT>
-__global__ void __launch_bounds__(SORT_THREADS)
-expert_rows_kernel(const RowsCall a, int cluster, int chunk) {
-  extern __shared__ int sort_mem[];
-  int* count = sort_mem;                      // [warp][expert]
-  int* total = count + SORT_WARPS * a.G;      // [expert], read by the cluster
-  int* have = total + a.G;                    // [expert]
-  int* first = have + a.G;                    // [expert + 1]
-  int* part = first + a.G + 1;                // [32]
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  for (int i = tid; i < SORT_WARPS * a.G; i += SORT_THREADS) count[i] = 0;
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  __syncthreads();
+// The lanes with the same expert (of `bits` bits; -1: none) as the lane's own: by a
+// ballot for each bit (__match_any_sync, on the SM's one unit for it, made up most of a
+// sort of 16384 pairs).
+__device__ __forceinline__ unsigned peers(int e, int bits) {
+  unsigned m = __ballot_sync(ALL, e >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool set = (e >> b) & 1;
+    const unsigned v = __ballot_sync(ALL, set);
+    m &= set ? v : ~v;
+  }
+  return m;
+}
 
-  // `chunk` pairs a warp (a multiple of 32)
-  const long long from = (static_cast<long long>(rank) * SORT_WARPS + warp) * chunk;
-  const int begin = static_cast<int>(min(from, static_cast<long long>(a.pairs)));
-  const int end = static_cast<int>(min(from + chunk, static_cast<long long>(a.pairs)));
-  int* mine = count + warp * a.G;
-  bool bad = false;
-  for (int p = begin; p < end; p += 32) {
-    const int e = p + lane < end ? expert_of(a, p + lane, bad) : -1;
-    const unsigned same = __match_any_sync(ALL, e);
-    if (e >= 0 && (same & ((1u << lane) - 1)) == 0) mine[e] += __popc(same);
-    __syncwarp();
-  }
-  __syncthreads();
-  // counts of the warps before, of the block, of the blocks before, of all
-  int sum = 0, before = 0, all = 0;
-  if (tid < a.G) {
-#pragma unroll 8
-    for (int w = 0; w < SORT_WARPS; ++w) {
-      const int n = count[w * a.G + tid];
-      count[w * a.G + tid] = sum;
-      sum += n;
-    }
-    total[tid] = sum;
-  }
-  if (cluster > 1) {
-    cluster_sync();
-    if (tid < a.G)
-#pragma unroll
-      for (int r = 0; r < SORT_CLUSTER; ++r)
-        if (r < cluster) {
-          const int n = static_cast<int>(ld_cluster_u32(map_cluster(smem_u32(total + tid), r)));
-          if (r < rank) before += n;
-          all += n;
-        }
-  } else {
-    all = sum;
-  }
-  // first rows: a scan over the experts
-  int room = LAYOUT == kRowsContiguous ? (all + kSegment - 1) / kSegment * kSegment : all;
-  int x = room;
+// Inclusive sum over the warp's lanes up to each.
+__device__ __forceinline__ int scan(int x) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(ALL, x, o);
-    if (lane >= o) x += y;
+    if ((threadIdx.x & 31) >= o) x += y;
   }
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int y = part[lane];
+  return x;
+}
+
+// One cluster sorts.  The blocks share the pairs in order, a block's warps its
+// share; a warp takes 32 pairs at a time, of which each lane finds those of the same
+// expert.  Two passes: each warp's counts, from which follow
+// (over the warps, over the blocks, over the experts) the first row of each warp's
+// pairs of each expert; then the rows themselves.
+template <int LAYOUT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
+expert_rows_kernel(const RowsCall a, int cluster, int chunk, int bits) {
+  constexpr int THREADS = 32 * WARPS;
+  extern __shared__ int sort_mem[];
+  const int pitch = a.G | 1;
+  int* count = sort_mem;                      // [warp][expert]
+  int* total = count + WARPS * pitch;         // [expert], read by the cluster
+  int* have = total + a.G;                    // [expert]
+  int* start = have + a.G;                    // [expert]
+  int* first = start + a.G;                   // [expert + 1]
+  int* part = first + a.G + 1;                // [32]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  for (int i = tid; i < WARPS * pitch; i += THREADS) count[i] = 0;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+
+  // `chunk` pairs a warp (a multiple of 32)
+  const long long from = (static_cast<long long>(rank) * WARPS + warp) * chunk;
+  const int begin = static_cast<int>(min(from, static_cast<long long>(a.pairs)));
+  const int end = static_cast<int>(min(from + chunk, static_cast<long long>(a.pairs)));
+  int* mine = count + warp * pitch;
+  bool bad = false;
+  int e[SORT_BATCH];
+  unsigned same[SORT_BATCH];   // of the first batch, for the second pass
+  auto ask = [&](int p) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int z = __shfl_up_sync(ALL, y, o);
-      if (lane >= o) y += z;
+    for (int i = 0; i < SORT_BATCH; ++i) e[i] = p + 32 * i + lane < end ? expert_of(a, p + 32 * i + lane, bad) : -1;
+  };
+  ask(begin);
+  __syncthreads();
+  for (int p = begin; p < end; p += 32 * SORT_BATCH) {
+    if (p != begin) ask(p);
+#pragma unroll
+    for (int i = 0; i < SORT_BATCH; ++i) {
+      if (p + 32 * i >= end) break;
+      same[i] = peers(e[i], bits);
+      if (e[i] >= 0 && (same[i] & ((1u << lane) - 1)) == 0) mine[e[i]] += __popc(same[i]);
+      __syncwarp();
     }
-    part[lane] = y;
   }
   __syncthreads();
-  x += warp > 0 ? part[warp - 1] : 0;
-  if (tid < a.G) {
-    first[tid + 1] = x;
-    if (tid == 0) first[0] = 0;
-    have[tid] = all;
-    const int start = (LAYOUT == kRowsMasked ? 0 : x - room) + before;
-#pragma unroll 8
-    for (int w = 0; w < SORT_WARPS; ++w) count[w * a.G + tid] += start;
-    if (rank == 0) {
-      int n = all;
-      if (LAYOUT == kRowsMasked && n > a.room) {
-        raise_status(a, ST_MASK_RANGE);
-        n = a.room;
+  // each expert's counts of the warps before (a warp an expert, a lane a warp)
+  for (int x = warp; x < a.G; x += WARPS) {
+    const int n = lane < WARPS ? count[lane * pitch + x] : 0;
+    const int sum = scan(n);
+    if (lane < WARPS) count[lane * pitch + x] = sum - n;
+    if (lane == 31) total[x] = sum;
+  }
+  if (cluster > 1) {
+    __syncwarp();
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  // of the blocks before, and of all; then the experts' first rows
+  int base = 0;   // rows of the experts up to those of this round
+  for (int x0 = 0; x0 < a.G; x0 += THREADS) {
+    const int x = x0 + tid;
+    int before = 0, all = 0;
+    if (x < a.G) {
+      if (cluster > 1) {
+#pragma unroll
+        for (int r = 0; r < SORT_CLUSTER; ++r)
+          if (r < cluster) {
+            const int n = static_cast<int>(ld_cluster_u32(map_cluster(smem_u32(total + x), r)));
+            if (r < rank) before += n;
+            all += n;
+          }
+      } else {
+        all = total[x];
       }
-      if (LAYOUT == kRowsContiguous && x - room + all > a.room) raise_status(a, ST_KS_RANGE);
-      a.sizes[tid] = n;
     }
+    const int room = LAYOUT == kRowsContiguous ? (all + kSegment - 1) / kSegment * kSegment : all;
+    int end_row = scan(room);
+    if (lane == 31) part[warp] = end_row;
+    __syncthreads();
+    if (warp == 0) {
+      const int n = lane < WARPS ? part[lane] : 0;
+      const int sum = scan(n);
+      if (lane < WARPS) part[lane] = sum;
+    }
+    __syncthreads();
+    end_row += base + (warp > 0 ? part[warp - 1] : 0);
+    base += part[WARPS - 1];
+    if (x < a.G) {
+      const int first_row = end_row - room;
+      first[x] = first_row;
+      have[x] = all;
+      start[x] = (LAYOUT == kRowsMasked ? 0 : first_row) + before;
+      if (rank == 0) {
+        int n = all;
+        if (LAYOUT == kRowsMasked && n > a.room) {
+          raise_status(a, ST_MASK_RANGE);
+          n = a.room;
+        }
+        if (LAYOUT == kRowsContiguous && first_row + all > a.room) raise_status(a, ST_KS_RANGE);
+        a.sizes[x] = n;
+      }
+    }
+    if (tid == 0) first[a.G] = base;   // (the last round's)
+    __syncthreads();
   }
-  __syncthreads();
-  for (int p = begin; p < end; p += 32) {
-    const bool on = p + lane < end;
-    const int e = on ? expert_of(a, p + lane, bad) : -1;
-    const unsigned same = __match_any_sync(ALL, e);
-    int row = -1;
-    if (e >= 0) row = mine[e] + __popc(same & ((1u << lane) - 1));
-    __syncwarp();
-    if (e >= 0 && (same & ((1u << lane) - 1)) == 0) mine[e] += __popc(same);
-    __syncwarp();
-    if (LAYOUT != kRowsRagged && row >= a.room) row = -1;
-    if (LAYOUT == kRowsMasked && row >= 0) row += e * a.room;
-    if (on) a.rows[p + lane] = row;
+  for (int p = begin; p < end; p += 32 * SORT_BATCH) {
+    const bool again = chunk > 32 * SORT_BATCH;
+    if (again) ask(p);
+#pragma unroll
+    for (int i = 0; i < SORT_BATCH; ++i) {
+      const int at = p + 32 * i + lane;
+      if (p + 32 * i >= end) break;
+      const int x = e[i];
+      const unsigned all_same = again ? peers(x, bits) : same[i], less = all_same & ((1u << lane) - 1);
+      int row = -1;
+      if (x >= 0) row = start[x] + mine[x] + __popc(less);
+      __syncwarp();
+      if (x >= 0 && less == 0) mine[x] += __popc(all_same);
+      __syncwarp();
+      if (LAYOUT != kRowsRagged && row >= a.room) row = -1;
+      if (LAYOUT == kRowsContiguous && row >= 0) a.m_indices[row] = x;
+      if (LAYOUT == kRowsMasked && row >= 0) row += x * a.room;
+      if (at < end) a.rows[at] = row;
+    }
   }
   if (bad) raise_status(a, ST_EXPERT_RANGE);
   if (LAYOUT == kRowsContiguous) {
-    // the expert of each row: the last that starts at or before it, where it has
-    // that many rows
-    for (long long r = rank * SORT_THREADS + tid; r < a.room; r += cluster * SORT_THREADS) {
-      int lo = 0, hi = a.G;   // first[lo] <= r < first[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first[mid] <= r) lo = mid;
-        else hi = mid;
-      }
-      a.m_indices[r] = r - first[lo] < have[lo] ? lo : -1;
-    }
+    // -1 behind each expert's rows (a warp an expert), and behind the last expert
+    for (int x = rank * WARPS + warp; x < a.G; x += cluster * WARPS)
+      for (int r = first[x] + have[x] + lane; r < min(first[x + 1], a.room); r += 32) a.m_indices[r] = -1;
+    for (long long r = static_cast<long long>(first[a.G]) + rank * THREADS + tid; r < a.room;
+         r += cluster * THREADS)
+      a.m_indices[r] = -1;
   }
   // (a peer may still read this block's counts)
   __syncwarp();
@@ -237,31 +276,48 @@ dispatch_kernel(const DispatchCall a) {
 }
 
 // ---------------------------------------------------------- weighted sum ----
-constexpr int SUM_THREADS = 256;
+constexpr int SUM_THREADS = 256, SUM_PER_SM = 4;
 constexpr int SUM_ROWS = 8;   // rows of a token in flight at a time
 
 // A warp takes 256 columns of a token, a lane eight of them, of all its rows:
 // products and sum in fp32 in the order of the choices, the residual added first.
-__global__ void __launch_bounds__(SUM_THREADS)
+// The next token's rows and weights are on their way meanwhile.
+__global__ void __launch_bounds__(SUM_THREADS, SUM_PER_SM)
 combine_kernel(const CombineCall a) {
   const int lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int vecs = a.K >> 3, pieces = (vecs + 31) / 32;
-  const long long units = static_cast<long long>(a.T) * pieces;
   const uint4* Y = static_cast<const uint4*>(a.Y);
-  const long long stride = static_cast<long long>(gridDim.x) * (SUM_THREADS / 32);
-  for (long long u = static_cast<long long>(blockIdx.x) * (SUM_THREADS / 32) + (threadIdx.x >> 5);
-       u < units; u += stride) {
-    const int t = static_cast<int>(u / pieces);
-    const int v = static_cast<int>(u - static_cast<long long>(t) * pieces) * 32 + lane;
+  const unsigned warps = gridDim.x * (SUM_THREADS / 32), w0 = blockIdx.x * (SUM_THREADS / 32) + (threadIdx.x >> 5);
+  // (the warp's first unit, and the step from one to the next, without a division each)
+  int t = w0 / pieces, piece = w0 - t * pieces;
+  const int step_t = warps / pieces, step_p = warps - step_t * pieces;
+  int mine = -1;
+  float weight = 0.f;
+  auto ask = [&](int t, int& mine, float& weight) {
+    const size_t pair = static_cast<size_t>(t) * a.k + lane;
+    const bool on = t < a.T && lane < a.k;
+    mine = row_of(a.rows, pair, on, a.num_rows, a.status);
+    weight = !on ? 0.f : a.weights ? __ldg(a.weights + pair) : 1.f;
+    if (mine < 0) weight = 0.f;
+  };
+  ask(t, mine, weight);
+  while (t < a.T) {
+    const int v = piece * 32 + lane;
     const bool on = v < vecs;
     const size_t at = static_cast<size_t>(t) * vecs + v;
     uint4 r = make_uint4(0, 0, 0, 0);
     if (a.R && on) r = static_cast<const uint4*>(a.R)[at];   // (may be `out`)
-    const size_t pair = static_cast<size_t>(t) * a.k + lane;
-    const int mine = row_of(a.rows, pair, lane < a.k, a.num_rows, a.status);
-    const float weight = mine < 0 ? 0.f : a.weights ? __ldg(a.weights + pair) : 1.f;
+    t += step_t;
+    piece += step_p;
+    if (piece >= pieces) {
+      piece -= pieces;
+      ++t;
+    }
+    int next_row;
+    float next_weight;
+    ask(t, next_row, next_weight);
     float sum[8];
     bf16x8_to_float(r, sum);
     for (int j0 = 0; j0 < a.k; j0 += SUM_ROWS) {
@@ -284,29 +340,34 @@ combine_kernel(const CombineCall a) {
       }
     }
     if (on) static_cast<uint4*>(a.out)[at] = float_to_bf16x8(sum);
+    mine = next_row;
+    weight = next_weight;
   }
 }
 
-// A block takes a token: a thread eight columns at a time of the gradient and of
-// all its rows; the dot products are summed over the block in a fixed order.
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS)
+// A team of threads (a warp, or the block) takes a token: a thread eight columns at a
+// time of the gradient and of all its rows; the dot products are summed over the team
+// in a fixed order.
+template <int TEAM>
+__global__ void __launch_bounds__(SUM_THREADS)
 combine_backward_kernel(const CombineBwd a) {
-  __shared__ float part[SUM_ROWS][THREADS / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int TEAMS = SUM_THREADS / TEAM;
+  __shared__ float part[SUM_ROWS][SUM_THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, member = threadIdx.x % TEAM;
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int vecs = a.K >> 3;
   const uint4* Y = static_cast<const uint4*>(a.Y);
   uint4* dY = static_cast<uint4*>(a.dY);
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  for (long long t = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TEAM; t < a.T;
+       t += static_cast<long long>(gridDim.x) * TEAMS) {
     const uint4* dO = static_cast<const uint4*>(a.dO) + static_cast<size_t>(t) * vecs;
     const size_t pair = static_cast<size_t>(t) * a.k + lane;
     const int mine = row_of(a.rows, pair, lane < a.k, a.num_rows, a.status);
     const float weight = mine < 0 ? 0.f : a.weights ? __ldg(a.weights + pair) : 1.f;
     for (int j0 = 0; j0 < a.k; j0 += SUM_ROWS) {
       float dot[SUM_ROWS] = {};
-      for (int v = threadIdx.x; v < (vecs + 31) / 32 * 32; v += THREADS) {
+      for (int v = member; v < (vecs + 31) / 32 * 32; v += TEAM) {
         const bool on = v < vecs;
         uint4 d = make_uint4(0, 0, 0, 0);
         if (on) d = __ldg(dO + v);
@@ -340,22 +401,27 @@ combine_backward_kernel(const CombineBwd a) {
         }
       }
       if (a.dw) {
+        // lane j of each warp: the warp's sum of row j
+        float mine_dot = 0.f;
 #pragma unroll
         for (int j = 0; j < SUM_ROWS; ++j) {
 #pragma unroll
           for (int o = 16; o >= 1; o >>= 1) dot[j] += __shfl_xor_sync(ALL, dot[j], o);
-          if (lane == 0) part[j][warp] = dot[j];
+          if (lane == j) mine_dot = dot[j];
         }
-        __syncthreads();
-        if (threadIdx.x < SUM_ROWS && j0 + static_cast<int>(threadIdx.x) < a.k) {
-          float s = 0.f;
+        const int j = j0 + lane;
+        const int row = __shfl_sync(ALL, mine, j & 31);
+        if (TEAM > 32) {
+          if (lane < SUM_ROWS) part[lane][warp] = mine_dot;
+          __syncthreads();
+          mine_dot = 0.f;
+          if (lane < SUM_ROWS)
 #pragma unroll
-          for (int w = 0; w < THREADS / 32; ++w) s += part[threadIdx.x][w];
-          const size_t at = static_cast<size_t>(t) * a.k + j0 + threadIdx.x;
-          const int row = __ldg(a.rows + at);
-          a.dw[at] = row >= 0 && row < a.num_rows ? s : 0.f;
+            for (int w = 0; w < TEAM / 32; ++w) mine_dot += part[lane][w];
+          __syncthreads();
         }
-        __syncthreads();
+        if (lane < SUM_ROWS && j < a.k && (TEAM == 32 || warp == 0))
+          a.dw[static_cast<size_t>(t) * a.k + j] = row >= 0 ? mine_dot : 0.f;
       }
     }
   }
@@ -369,27 +435,30 @@ int move_grid(long long units, int per_block, int per_sm, int num_sms, bool limi
 }  // namespace
 
 cudaError_t rows_set_up() {
-  const void* kernels[] = {reinterpret_cast<const void*>(expert_rows_kernel<kRowsRagged>),
-                           reinterpret_cast<const void*>(expert_rows_kernel<kRowsContiguous>),
-                           reinterpret_cast<const void*>(expert_rows_kernel<kRowsMasked>)};
+  const void* kernels[] = {reinterpret_cast<const void*>(expert_rows_kernel<kRowsRagged, 32>),
+                           reinterpret_cast<const void*>(expert_rows_kernel<kRowsContiguous, 32>),
+                           reinterpret_cast<const void*>(expert_rows_kernel<kRowsMasked, 32>)};
   for (const void* k : kernels) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               sort_smem(kRowsMaxExperts));
+                                               sort_smem(32, kRowsMaxExperts));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
 cudaError_t launch_rows(const RowsCall& a, RowsLayout layout, int num_sms, cudaStream_t stream) {
-  // a block sorts 4096 pairs in less time than a second one takes to join
+  // a block for every 2048 pairs (16384 pairs of 32 experts with their rows of 7168 in 8
+  // bits: 36.6 us so and with 1024, 38.7 with 4096, 42.2 with 8192)
   int cluster = 1;
-  while (cluster < SORT_CLUSTER && 2 * cluster <= num_sms && a.pairs > 4096 * cluster) cluster *= 2;
-  const int per = SORT_WARPS * cluster;
+  while (cluster < SORT_CLUSTER && 2 * cluster <= num_sms && a.pairs > 2048 * cluster) cluster *= 2;
+  const int warps = a.pairs <= 1024 ? 8 : 32, per = warps * cluster;
   const int chunk = ((a.pairs + per - 1) / per + 31) / 32 * 32;
+  int bits = 1;
+  while ((1 << bits) < a.G) ++bits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster, 1, 1);
-  cfg.blockDim = dim3(SORT_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = sort_smem(a.G);
+  cfg.blockDim = dim3(32 * warps, 1, 1);
+  cfg.dynamicSmemBytes = sort_smem(warps, a.G);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -400,11 +469,12 @@ cudaError_t launch_rows(const RowsCall& a, RowsLayout layout, int num_sms, cudaS
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
+  auto go = [&](auto few, auto many) { return cudaLaunchKernelEx(&cfg, warps == 8 ? few : many, a, cluster, chunk, bits); };
   switch (layout) {
-    case kRowsRagged: return cudaLaunchKernelEx(&cfg, expert_rows_kernel<kRowsRagged>, a, cluster, chunk);
+    case kRowsRagged: return go(expert_rows_kernel<kRowsRagged, 8>, expert_rows_kernel<kRowsRagged, 32>);
     case kRowsContiguous:
-      return cudaLaunchKernelEx(&cfg, expert_rows_kernel<kRowsContiguous>, a, cluster, chunk);
-    default: return cudaLaunchKernelEx(&cfg, expert_rows_kernel<kRowsMasked>, a, cluster, chunk);
+      return go(expert_rows_kernel<kRowsContiguous, 8>, expert_rows_kernel<kRowsContiguous, 32>);
+    default: return go(expert_rows_kernel<kRowsMasked, 8>, expert_rows_kernel<kRowsMasked, 32>);
   }
 }
 
@@ -418,14 +488,22 @@ cudaError_t launch_dispatch(const DispatchCall& a, int num_sms, bool limited, cu
 
 cudaError_t launch_combine(const CombineCall& a, int num_sms, bool limited, cudaStream_t stream) {
   const long long units = static_cast<long long>(a.T) * (((a.K >> 3) + 31) / 32);
-  return launch_dependent(combine_kernel, dim3(move_grid(units, SUM_THREADS / 32, 8, num_sms, limited)),
+  return launch_dependent(combine_kernel, dim3(move_grid(units, SUM_THREADS / 32, SUM_PER_SM, num_sms, limited)),
                           SUM_THREADS, stream, 0, a);
 }
 
 cudaError_t launch_combine_backward(const CombineBwd& a, int num_sms, bool limited,
                                     cudaStream_t stream) {
-  return launch_dependent(combine_backward_kernel<256>, dim3(move_grid(a.T, 1, 8, num_sms, limited)), 256,
-                          stream, 0, a);
+  // A warp a token where there are enough of them for the SMs (10571 of one row of 280:
+  // 13 us, with a block each 44; 297 of 4 rows of 976: 6.4 and 3.6) and their rows are
+  // short (4096 of 8 rows of 7168: 217 and 181).  (Whatever the limit on the SMs: the
+  // sums' order is that of the team.)
+  constexpr int kTeamK = 1024, kTeamT = 8 * 152;
+  if (a.K <= kTeamK && a.T >= kTeamT)
+    return launch_dependent(combine_backward_kernel<32>, dim3(move_grid(a.T, SUM_THREADS / 32, 8, num_sms, limited)),
+                            SUM_THREADS, stream, 0, a);
+  return launch_dependent(combine_backward_kernel<SUM_THREADS>, dim3(move_grid(a.T, 1, 8, num_sms, limited)),
+                          SUM_THREADS, stream, 0, a);
 }
 
 }  // namespace dgk

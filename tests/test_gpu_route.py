@@ -69,7 +69,8 @@ def check(x, bias, k, sigmoid, groups=1, top_groups=1, best=1, renorm=True, scal
 CASES = [  # T, G, k, groups, top_groups, best
     (1, 8, 1, 1, 1, 1), (7, 256, 8, 8, 4, 2), (33, 60, 6, 1, 1, 1), (5, 1, 1, 1, 1, 1), (64, 160, 6, 8, 3, 1),
     (9, 33, 32, 1, 1, 1), (3, 1024, 32, 32, 17, 2), (17, 384, 8, 6, 2, 2), (4, 500, 9, 4, 2, 1),
-    (130, 64, 4, 32, 16, 2), (12, 96, 3, 3, 3, 2)]
+    (130, 64, 4, 32, 16, 2), (12, 96, 3, 3, 3, 2), (37, 7, 3, 1, 1, 1), (99, 16, 8, 8, 6, 1),
+    (50, 32, 5, 4, 2, 2), (1, 24, 8, 3, 2, 2), (35, 64, 16, 16, 7, 2), (2, 48, 11, 12, 5, 2), (6, 30, 10, 3, 3, 1)]
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "x".join(map(str, c)))
@@ -141,6 +142,33 @@ def test_masked_experts(sigmoid, biased, groups):
     within(w, ww, 64 * U * np.abs(ww) + 1e-30)
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("groups,best", [(1, 1), (8, 2), (8, 1)])
+def test_biases_that_decide_by_themselves(sigmoid, groups, best):
+    x = logits(30, 64, False, 8)
+    bias = torch.from_numpy(np.random.default_rng(2).normal(size=64) * 0.1).float()
+    bias[5], bias[6], bias[17], bias[40] = float("inf"), -float("inf"), 1e6, -3e7
+    bias[41] = float("nan")       # (not available, as with -infinity)
+    e, w = run(x, bias, 7, sigmoid, groups, max(1, groups // 2), best)
+    b = bias.numpy().copy()
+    b[41] = -np.inf
+    we, ww = M.route(x.double().numpy(), b, 7, sigmoid, groups, max(1, groups // 2), best)
+    assert np.array_equal(e, we)
+    within(w, ww, 64 * U * np.abs(ww) + TINY)
+
+
+@pytest.mark.parametrize("G,k,groups,top_groups", [(384, 16, 8, 3), (1024, 32, 32, 9), (64, 5, 2, 1), (60, 8, 1, 1),
+                                                   (16, 4, 4, 2), (8, 3, 1, 1)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_many_values_within_a_rounding(G, k, groups, top_groups, sigmoid):
+    # c of every expert within 3e-8 of each other: all of them in doubt in 32 bits
+    x = logits(25, G, False, 4)
+    for t in range(25):
+        s, _ = M.scores(x[t].double().numpy(), sigmoid)
+        check(x[t:t + 1], torch.from_numpy(1.0 - s).float(), k, sigmoid, groups, top_groups, 2)
+    check(x, torch.from_numpy(1.0 - s).float(), k, sigmoid, groups, top_groups, 2)   # (one token in doubt)
+
+
 def back(x, e, dw, sigmoid, renorm, scale):
     T, G = x.shape
     d = torch.full_like(x, 9.0).cuda()
@@ -160,7 +188,7 @@ def check_gradient(x, e, dw, sigmoid, renorm, scale):
     within(got, want, lim)
 
 
-@pytest.mark.parametrize("shape", [(1, 8, 2), (33, 256, 8), (9, 60, 6), (130, 1024, 32), (5, 33, 1)],
+@pytest.mark.parametrize("shape", [(1, 8, 2), (33, 256, 8), (9, 60, 6), (130, 1024, 32), (5, 33, 1), (7, 64, 13), (3, 16, 16)],
                          ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
