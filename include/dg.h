@@ -495,8 +495,8 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
  *   of them may be null (not computed)
  *   lse        what the forward call wrote for these X and W
  *   workspace  dg_linear_cross_entropy_backward_workspace_bytes(T, V, K) bytes, as above
- *              (a piece of p: 96 MB, or 4096 words of each token, at most; and dX in
- *              fp32 where there is more than one piece)
+ *              (a piece of p: 384 MB, or 4096 words of each token, at most; and dX in
+ *              fp32 where there is more than one piece, or in parts of few tokens)
  * The sums run in a fixed order: the same inputs give the same bits on the same
  * number of SMs.  K a multiple of 8; too large (DG_ERR_UNSUPPORTED_SHAPE): T or K of 2^23
  * or more, V within 8192 of 2^31, X or W of 2^34 elements, T * V of 2^38.  X, W, dX

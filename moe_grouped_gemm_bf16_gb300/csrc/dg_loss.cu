@@ -20,7 +20,10 @@
 // the -1 at the targets, the largest entries of all, stay near -1 (with d_loss in p,
 // 1 / T rounded to bf16 in every token's largest entry: dX and dW off by up to 0.0037
 // of themselves, so 0.0017, which is their own rounding).  A piece is as wide as makes
-// p about 96 MB, which L2 holds until both products have read it.
+// p 384 MB at most: fewer sums of dX in fp32 and fewer last waves of tiles than with
+// pieces that stay in L2 (4095 tokens of 50003 x 4096, pieces of 24 / 96 / 384 MB: 3370 /
+// 3070 / 2950 us; 4096 of 131072 x 2048: 4640 / 4065 / 3850; 8192 of 32000 x 2048: 2140 /
+// 2110 / 1950; 2048 of 50003 x 7168: 2860 / 2578 / 2602).
 //
 // Bounded by the tensor cores; with few tokens by reading W (and writing dW).
 #include <algorithm>
@@ -32,7 +35,7 @@
 namespace dgk {
 namespace {
 
-constexpr long long kPieceBytes = 96ll << 20;   // of p
+constexpr long long kPieceBytes = 384ll << 20;  // of p
 constexpr int kPieceLeast = 4096;               // words: whole waves of tiles
 
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }

@@ -171,6 +171,10 @@ expert_rows_kernel(const RowsCall a, int cluster, int chunk, int bits) {
     if (tid == 0) first[a.G] = base;   // (the last round's)
     __syncthreads();
   }
+  // This block has used all that it read of its peers; none leaves before they all
+  // have (a relaxed arrival: there is nothing to publish, and a release would wait for
+  // the stores below).
+  if (cluster > 1) cluster_arrive_relaxed();
   for (int p = begin; p < end; p += 32 * SORT_BATCH) {
     const bool again = chunk > 32 * SORT_BATCH;
     if (again) ask(p);
@@ -200,9 +204,7 @@ expert_rows_kernel(const RowsCall a, int cluster, int chunk, int bits) {
          r += cluster * THREADS)
       a.m_indices[r] = -1;
   }
-  // (a peer may still read this block's counts)
-  __syncwarp();
-  if (cluster > 1) cluster_sync();
+  if (cluster > 1) cluster_wait();
 }
 
 // ------------------------------------------------------- rows of experts ----
@@ -276,7 +278,9 @@ dispatch_kernel(const DispatchCall a) {
 }
 
 // ---------------------------------------------------------- weighted sum ----
-constexpr int SUM_THREADS = 256, SUM_PER_SM = 4;
+// (blocks per SM: with 2, 3 and 4, the last with spills, 4096 tokens of 8 rows of 7168 take
+// 127, 102 and 107 us, their gradient 209, 174 and 192)
+constexpr int SUM_THREADS = 256, SUM_PER_SM = 3;
 constexpr int SUM_ROWS = 8;   // rows of a token in flight at a time
 
 // A warp takes 256 columns of a token, a lane eight of them, of all its rows:
@@ -349,7 +353,7 @@ combine_kernel(const CombineCall a) {
 // time of the gradient and of all its rows; the dot products are summed over the team
 // in a fixed order.
 template <int TEAM>
-__global__ void __launch_bounds__(SUM_THREADS)
+__global__ void __launch_bounds__(SUM_THREADS, SUM_PER_SM)
 combine_backward_kernel(const CombineBwd a) {
   constexpr int TEAMS = SUM_THREADS / TEAM;
   __shared__ float part[SUM_ROWS][SUM_THREADS / 32];
@@ -359,12 +363,22 @@ combine_backward_kernel(const CombineBwd a) {
   const int vecs = a.K >> 3;
   const uint4* Y = static_cast<const uint4*>(a.Y);
   uint4* dY = static_cast<uint4*>(a.dY);
-  for (long long t = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TEAM; t < a.T;
-       t += static_cast<long long>(gridDim.x) * TEAMS) {
-    const uint4* dO = static_cast<const uint4*>(a.dO) + static_cast<size_t>(t) * vecs;
+  const long long step = static_cast<long long>(gridDim.x) * TEAMS;
+  int next_row = -1;
+  float next_weight = 0.f;
+  auto ask = [&](long long t) {
     const size_t pair = static_cast<size_t>(t) * a.k + lane;
-    const int mine = row_of(a.rows, pair, lane < a.k, a.num_rows, a.status);
-    const float weight = mine < 0 ? 0.f : a.weights ? __ldg(a.weights + pair) : 1.f;
+    const bool on = t < a.T && lane < a.k;
+    next_row = row_of(a.rows, pair, on, a.num_rows, a.status);
+    next_weight = !on ? 0.f : a.weights ? __ldg(a.weights + pair) : 1.f;
+  };
+  long long t = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TEAM;
+  ask(t);
+  for (; t < a.T; t += step) {
+    const uint4* dO = static_cast<const uint4*>(a.dO) + static_cast<size_t>(t) * vecs;
+    const int mine = next_row;
+    const float weight = mine < 0 ? 0.f : next_weight;
+    ask(t + step);   // (on its way meanwhile)
     for (int j0 = 0; j0 < a.k; j0 += SUM_ROWS) {
       float dot[SUM_ROWS] = {};
       for (int v = member; v < (vecs + 31) / 32 * 32; v += TEAM) {
@@ -500,9 +514,9 @@ cudaError_t launch_combine_backward(const CombineBwd& a, int num_sms, bool limit
   // sums' order is that of the team.)
   constexpr int kTeamK = 1024, kTeamT = 8 * 152;
   if (a.K <= kTeamK && a.T >= kTeamT)
-    return launch_dependent(combine_backward_kernel<32>, dim3(move_grid(a.T, SUM_THREADS / 32, 8, num_sms, limited)),
+    return launch_dependent(combine_backward_kernel<32>, dim3(move_grid(a.T, SUM_THREADS / 32, SUM_PER_SM, num_sms, limited)),
                             SUM_THREADS, stream, 0, a);
-  return launch_dependent(combine_backward_kernel<SUM_THREADS>, dim3(move_grid(a.T, 1, 8, num_sms, limited)),
+  return launch_dependent(combine_backward_kernel<SUM_THREADS>, dim3(move_grid(a.T, 1, SUM_PER_SM, num_sms, limited)),
                           SUM_THREADS, stream, 0, a);
 }
 
