@@ -110,6 +110,9 @@ struct BfSmem {
   __host__ __device__ static constexpr int fixed(int G) { return 1024 + TAB + 2 * (G + 1) * 4 + BF_EPI * 4; }
 };
 
+// Slots that the logits' accumulation in tensor memory runs over: 512 of the reduction.
+__host__ __device__ constexpr int bf_stretch(bool pair) { return pair ? 8 : 4; }
+
 // Reduction depth of a slot.
 __host__ __device__ constexpr int bf_bk(bool pair) { return pair ? 64 : 128; }
 
@@ -572,12 +575,20 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
         const BfTile T = bf_tile<BK, FORM, EPI>(t, p, first, blk, krank, group);
         if (T.kbeg == T.kend) continue;
         const uint32_t idesc = idesc_bf16_f32(PAIR ? 256 : 128, mma_n(T.cols), P_MN, TN);
-        const uint32_t d = tmem + static_cast<uint32_t>(b * ACC);
+        uint32_t d = tmem + static_cast<uint32_t>(b * ACC);
         bool ok = wait_bar(bar(L::T_EMPTY + b), bph ^ 1, abort_flag, p);
         tc_fence_after();
         const bool rag = ragged(T);
         const int n = T.kend - T.kbeg;
         for (int j = 0; j < n; ++j) {
+          // (the logits' sums: an accumulator for every few slots)
+          const bool starts = EPI == kBfStats ? j % bf_stretch(PAIR) == 0 : j == 0;
+          const bool ends = j == n - 1 || (EPI == kBfStats && (j + 1) % bf_stretch(PAIR) == 0);
+          if (starts && j > 0) {
+            d = tmem + static_cast<uint32_t>(b * ACC);
+            ok = wait_bar(bar(L::T_EMPTY + b), bph ^ 1, abort_flag, p) && ok;
+            tc_fence_after();
+          }
           // a ragged last slot comes first, when warp 3 has had the time of the
           // previous tile for it (8192 rows in 16 groups, 2048 x 7168: 189 us with
           // it last, 179 so, 166 without any zeroing)
@@ -612,28 +623,30 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
             };
             const int left = T.kn - i * BK;
             if (left >= BK) {
-              step(0, j > 0);
+              step(0, !starts);
 #pragma unroll
               for (int kk = 1; kk < BK / 16; ++kk) step(kk, 1);
             } else {
-              for (int kk = 0; 16 * kk < left; ++kk) step(kk, j > 0 || kk > 0);
+              for (int kk = 0; 16 * kk < left; ++kk) step(kk, !starts || kk > 0);
             }
             if constexpr (PAIR) mma_commit_pair_multicast(bar(L::EMPTY + s), mask);
             else mma_commit(bar(L::EMPTY + s));
-            if (j == n - 1) {
+            if (ends) {
               if constexpr (PAIR) mma_commit_pair_multicast(bar(L::T_FULL + b), mask);
               else mma_commit(bar(L::T_FULL + b));
             }
           }
           __syncwarp();
+          if (ends) {
+            b ^= 1;
+            if (b == 0) bph ^= 1;
+          }
           if (++s == p.stages) {
             s = 0;
             ph ^= 1;
             if constexpr (kDebug) ++turn;
           }
         }
-        b ^= 1;
-        if (b == 0) bph ^= 1;
       }
       if (issuer) {
         if constexpr (PAIR) mma_commit_pair_multicast(bar(L::MMA_DONE), static_cast<uint16_t>(1u << leader));
@@ -860,54 +873,109 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
         const int l_end = min(p.N, T.l0 + p.lanes);
         // first lane of the warp's quarter, in half a
         auto quarter = [&](int a) { return T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + q * 32; };
-        if (x.words_on_lanes) {
-          // (a first chunk's tokens are asked for before the wait)
-          Token k = token(T.q0 + 32 * eh + lane, 32 * eh + lane < T.cols);
-          const bool ok =
-              __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
-          tc_fence_after();
-          for (int c = 32 * eh; c < T.cols; c += 64) {
-            if (c >= 64) k = token(T.q0 + c + lane, c + lane < T.cols);
-            if (!ok) k.l = -1;
-            for (int a = 0; a < halves; ++a) {
-              if (quarter(a) >= l_end) break;
-              uint32_t v[32];
-              tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
-              tmem_wait_ld(v);
-              transpose_32x32(v);
-              take(k, v, quarter(a), l_end - quarter(a));
+        auto give_back = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR && side != 0) mbar_arrive_remote_relaxed(bar(L::T_EMPTY + b), leader);
+            else mbar_arrive(bar(L::T_EMPTY + b));
+          }
+          b ^= 1;
+          if (b == 0) bph ^= 1;
+        };
+        constexpr int A = PAIR ? 1 : 2, C = BC / 64;   // halves of the lanes, chunks of a warp's columns
+        auto chunk = [&](int i) { return 32 * eh + 64 * i; };
+        // tokens on the lanes: one of each half (asked for before the wait)
+        Token k[A];
+        if (!x.words_on_lanes) {
+#pragma unroll
+          for (int a = 0; a < A; ++a)
+            k[a] = token(quarter(a) + lane, a < halves && quarter(a) + lane < l_end);
+        }
+        bool ok = true;
+        if constexpr (EPI == kBfStats) {
+          // The tensor cores' fp32 accumulation drops bits towards zero, at each of its
+          // steps of 16: after K / 16 of them a loss of 12 was off by 2e-5 (K = 5520).  So
+          // every few slots' sums are added up here, rounded to nearest.
+          uint32_t z[A][C][32] = {};
+          const int stretches = (T.nk + bf_stretch(PAIR) - 1) / bf_stretch(PAIR);
+          for (int i = 0; i < stretches; ++i) {
+            ok = __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p)) && ok;
+            tc_fence_after();
+#pragma unroll
+            for (int a = 0; a < A; ++a)
+#pragma unroll
+              for (int j = 0; j < C; ++j)
+                if (a < halves && chunk(j) < T.cols) {
+#pragma unroll
+                  for (int h = 0; h < 32; h += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(t_lane + static_cast<uint32_t>(b * ACC + a * BC + chunk(j) + h), v);
+                    tmem_wait_ld16(v);
+#pragma unroll
+                    for (int m = 0; m < 16; ++m)
+                      z[a][j][h + m] = __float_as_uint(__uint_as_float(z[a][j][h + m]) + __uint_as_float(v[m]));
+                  }
+                }
+            give_back();
+          }
+          if (x.words_on_lanes) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+              if (chunk(j) >= T.cols) break;
+              Token u = token(T.q0 + chunk(j) + lane, ok && chunk(j) + lane < T.cols);
+#pragma unroll
+              for (int a = 0; a < A; ++a) {
+                if (a >= halves || quarter(a) >= l_end) break;
+                transpose_32x32(z[a][j]);
+                take(u, z[a][j], quarter(a), l_end - quarter(a));
+              }
+              leave(u, (T.l0 / p.lanes * (PAIR ? 2 : 1) + static_cast<int>(side)) * 4 + q);
             }
-            leave(k, (T.l0 / p.lanes * (PAIR ? 2 : 1) + static_cast<int>(side)) * 4 + q);
+          } else {
+#pragma unroll
+            for (int a = 0; a < A; ++a) {
+              if (a >= halves) break;
+              if (!ok) k[a].l = -1;
+#pragma unroll
+              for (int j = 0; j < C; ++j)
+                if (chunk(j) < T.cols) take(k[a], z[a][j], T.q0 + chunk(j), T.cols - chunk(j));
+              leave(k[a], T.q0 / p.bc * 2 + eh);
+            }
           }
         } else {
-          Token k[2];
-#pragma unroll
-          for (int a = 0; a < (PAIR ? 1 : 2); ++a)
-            k[a] = token(quarter(a) + lane, a < halves && quarter(a) + lane < l_end);
-          const bool ok =
-              __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
+          Token u{};
+          if (x.words_on_lanes) u = token(T.q0 + 32 * eh + lane, 32 * eh + lane < T.cols);
+          ok = __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
           tc_fence_after();
-#pragma unroll
-          for (int a = 0; a < (PAIR ? 1 : 2); ++a) {
-            if (a >= halves) break;
-            if (!ok) k[a].l = -1;
+          if (x.words_on_lanes) {
             for (int c = 32 * eh; c < T.cols; c += 64) {
-              uint32_t v[32];
-              tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
-              tmem_wait_ld(v);
-              take(k[a], v, T.q0 + c, T.cols - c);
+              if (c >= 64) u = token(T.q0 + c + lane, c + lane < T.cols);
+              if (!ok) u.l = -1;
+              for (int a = 0; a < halves; ++a) {
+                if (quarter(a) >= l_end) break;
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
+                tmem_wait_ld(v);
+                transpose_32x32(v);
+                take(u, v, quarter(a), l_end - quarter(a));
+              }
             }
-            leave(k[a], T.q0 / p.bc * 2 + eh);
+          } else {
+#pragma unroll
+            for (int a = 0; a < A; ++a) {
+              if (a >= halves) break;
+              if (!ok) k[a].l = -1;
+              for (int c = 32 * eh; c < T.cols; c += 64) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
+                tmem_wait_ld(v);
+                take(k[a], v, T.q0 + c, T.cols - c);
+              }
+            }
           }
+          give_back();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR && side != 0) mbar_arrive_remote_relaxed(bar(L::T_EMPTY + b), leader);
-          else mbar_arrive(bar(L::T_EMPTY + b));
-        }
-        b ^= 1;
-        if (b == 0) bph ^= 1;
       }
     }
   } else if (p.split == 1) {

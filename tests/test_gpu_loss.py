@@ -251,3 +251,16 @@ def test_forced_tilings_that_the_products_lack_are_refused():
         finally:
             dg.debug_force_ragged_plan()
         assert e.value.status == 2
+
+
+@pytest.mark.parametrize("T", [5, 100])
+def test_deep_reductions_lose_no_precision(T):
+    # the tensor cores' sums drop bits at each of their 448 steps here (2.2e-6 of the loss in all);
+    # 32 of them at a time, added up in fp32: a step drops half of 2^-23 of its partial sum on
+    # average, the 14 partial sums, half as large on the way, come to sqrt(14) times their total:
+    # 32 / 2 2^-23 / 2 sqrt(14) / 4 < 1e-6
+    X, W, t, _ = inputs(T, 3000, 7168, seed=3, ignored=0.0)
+    loss, lse = forward(X, W, t)
+    want, want_lse = L.loss(X, W, t)
+    for got, ref in ((loss, want), (lse, want_lse)):
+        assert (got.double() - ref).norm() <= 1e-6 * ref.norm()
