@@ -160,6 +160,7 @@ struct LossEnd {
   float* loss;
   float* lse;
   int T, V, pairs;
+  unsigned int* status;
 };
 
 __device__ __forceinline__ void join(float& top, float& sum, float m, float s) {
@@ -203,7 +204,7 @@ loss_end_kernel(const LossEnd a) {
       join(top, sum, __shfl_xor_sync(0xffffffffu, top, o), __shfl_xor_sync(0xffffffffu, sum, o));
     if (lane < END_TOKENS) share[warp][lane] = make_float2(top, sum);
     __syncthreads();
-    if (threadIdx.x < END_TOKENS && t < a.T) {
+    if (threadIdx.x < END_TOKENS && t < a.T && in_bounds(a, t, 1, a.T)) {
 #pragma unroll
       for (int w = 1; w < END_THREADS / 32; ++w) join(top, sum, share[w][lane].x, share[w][lane].y);
       constexpr float kLn2 = 0.6931471805599453f;
@@ -223,6 +224,7 @@ struct LossJoin {
   void* dX;           // bf16 [elements]
   long long elements; // a multiple of 8
   int parts;
+  unsigned int* status;
 };
 
 constexpr int JOIN_THREADS = 256;
@@ -240,6 +242,7 @@ loss_join_kernel(const LossJoin a) {
       const float4 x = *reinterpret_cast<const float4*>(a.sum + j * a.elements + i);
       s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
     }
+    if (!in_bounds(a, i, 4, a.elements)) continue;
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dX) + i) =
         make_uint2(pack_bf16x2(u * s.x, u * s.y), pack_bf16x2(u * s.z, u * s.w));
   }
@@ -272,7 +275,8 @@ cudaError_t launch_loss(const LossCall& a, int num_sms, cudaStream_t stream) {
   const int blocks = (a.T + END_TOKENS - 1) / END_TOKENS;
   return launch_dependent(loss_end_kernel, dim3(std::min(blocks, a.limited ? num_sms : 4 * num_sms)),
                           END_THREADS, stream, 0,
-                          LossEnd{c.loss.pair, c.loss.hit, a.targets, a.loss, a.lse, a.T, a.V, c.loss.pairs});
+                          LossEnd{c.loss.pair, c.loss.hit, a.targets, a.loss, a.lse, a.T, a.V, c.loss.pairs,
+                                  a.status});
 }
 
 cudaError_t launch_loss_backward(const LossCall& a, int num_sms, cudaStream_t stream) {
@@ -314,7 +318,7 @@ cudaError_t launch_loss_backward(const LossCall& a, int num_sms, cudaStream_t st
         e = launch_dependent(
             loss_join_kernel,
             dim3(static_cast<unsigned>(std::min<long long>(blocks, a.limited ? num_sms : 8 * num_sms))),
-            JOIN_THREADS, stream, 0, LossJoin{sum, unit, a.dX, n, c.loss.parts});
+            JOIN_THREADS, stream, 0, LossJoin{sum, unit, a.dX, n, c.loss.parts, a.status});
       }
     }
     if (e != cudaSuccess) return e;

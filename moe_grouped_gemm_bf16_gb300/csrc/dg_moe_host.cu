@@ -57,6 +57,7 @@ dg_status route(dgk::RouteFwd a, bool bf16, void* stream) {
   dgk::HostState st;
   const dg_status s = dgk::host_state(&st);
   if (s != DG_OK) return s;
+  a.status = st.status;
   const cudaError_t e =
       dgk::launch_route(a, bf16, st.sms, st.sms < st.device_sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "routing launch") : host_ok();
@@ -209,7 +210,7 @@ dg_status dg_route_top_k_fp32(const float* logits, const float* bias, int32_t* e
                               int top_groups, int group_best, int renormalize, float scale,
                               void* stream) {
   return route(dgk::RouteFwd{logits, bias, experts, weights, T, num_experts, top_k, sigmoid != 0,
-                             num_groups, top_groups, group_best, renormalize != 0, scale},
+                             num_groups, top_groups, group_best, renormalize != 0, scale, nullptr},
                false, stream);
 }
 
@@ -218,7 +219,7 @@ dg_status dg_route_top_k_bf16(const void* logits, const float* bias, int32_t* ex
                               int top_groups, int group_best, int renormalize, float scale,
                               void* stream) {
   return route(dgk::RouteFwd{logits, bias, experts, weights, T, num_experts, top_k, sigmoid != 0,
-                             num_groups, top_groups, group_best, renormalize != 0, scale},
+                             num_groups, top_groups, group_best, renormalize != 0, scale, nullptr},
                true, stream);
 }
 

@@ -27,6 +27,7 @@
 #include "dg_launch.h"
 #include "dg_params.h"
 #include "dg_route.h"
+#include "dg_wait.cuh"
 #include "ptx.cuh"
 
 namespace dgk {
@@ -548,6 +549,7 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
     }
     if (member < a.k && t < a.T) {
       const size_t at = static_cast<size_t>(t) * a.k + member;
+      if (!in_bounds(a, at, 1, static_cast<size_t>(a.T) * a.k)) continue;
       a.experts[at] = chosen;
       a.weights[at] = s * a.scale;
     }
@@ -556,6 +558,13 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
 
 __device__ __forceinline__ void write_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void write_logit(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Element i of the gradient of token t.
+template <class X>
+__device__ __forceinline__ void write_logit(const RouteBwd& a, int t, int i, float v) {
+  const size_t at = static_cast<size_t>(t) * a.G + i;
+  if (in_bounds(a, at, 1, static_cast<size_t>(a.T) * a.G)) write_logit(static_cast<X*>(a.d_logits) + at, v);
+}
 
 // Gradient of the logits, the choice taken as it is.  With d_j the gradient of
 // w_j times the scale:
@@ -592,9 +601,10 @@ route_backward_few_kernel(const RouteBwd a, bool whole) {
     if (t < a.T) {
       if (whole) {
         for (int i = member * STEP; i < a.G; i += LANES * STEP)
-          *reinterpret_cast<uint4*>(out + i) = make_uint4(0, 0, 0, 0);
+          if (in_bounds(a, static_cast<size_t>(t) * a.G + i, STEP, static_cast<size_t>(a.T) * a.G))
+            *reinterpret_cast<uint4*>(out + i) = make_uint4(0, 0, 0, 0);
       } else {
-        for (int i = member; i < a.G; i += LANES) write_logit(out + i, 0.f);
+        for (int i = member; i < a.G; i += LANES) write_logit<X>(a, t, i, 0.f);
       }
     }
     if (!there) d = 0.f;
@@ -625,7 +635,7 @@ route_backward_few_kernel(const RouteBwd a, bool whole) {
       }
     }
     __syncwarp();   // (the zeros come before the values)
-    if (e >= 0 && first) write_logit(out + e, sum);
+    if (e >= 0 && first) write_logit<X>(a, t, e, sum);
   }
 }
 
@@ -641,7 +651,6 @@ route_backward_kernel(const RouteBwd a) {
   grid_dep_launch_dependents();
   for (int t = blockIdx.x * RT_WARPS + warp; t < a.T; t += gridDim.x * RT_WARPS) {
     const X* logits = static_cast<const X*>(a.logits) + static_cast<size_t>(t) * a.G;
-    X* out = static_cast<X*>(a.d_logits) + static_cast<size_t>(t) * a.G;
     const size_t pair = static_cast<size_t>(t) * a.k + lane;
     int e = -1;
     float d = 0.f;
@@ -678,7 +687,7 @@ route_backward_kernel(const RouteBwd a) {
     }
     __syncwarp();
     for (int i = lane; i < a.G; i += 32)
-      write_logit(out + i, expf(clean(read_logit(logits + i)) - top) * share * (row[i] - dot));
+      write_logit<X>(a, t, i, expf(clean(read_logit(logits + i)) - top) * share * (row[i] - dot));
     __syncwarp();
   }
 }

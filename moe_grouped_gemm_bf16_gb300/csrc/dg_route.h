@@ -19,6 +19,7 @@ struct RouteFwd {
   int groups, top_groups, best;
   bool renormalize;
   float scale;
+  unsigned int* status;
 };
 
 struct RouteBwd {

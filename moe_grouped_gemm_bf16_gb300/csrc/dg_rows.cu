@@ -165,7 +165,7 @@ expert_rows_kernel(const RowsCall a, int cluster, int chunk, int bits) {
           n = a.room;
         }
         if (LAYOUT == kRowsContiguous && first_row + all > a.room) raise_status(a, ST_KS_RANGE);
-        a.sizes[x] = n;
+        if (in_bounds(a, x, 1, a.G)) a.sizes[x] = n;
       }
     }
     if (tid == 0) first[a.G] = base;   // (the last round's)
@@ -190,19 +190,20 @@ expert_rows_kernel(const RowsCall a, int cluster, int chunk, int bits) {
       if (x >= 0 && less == 0) mine[x] += __popc(all_same);
       __syncwarp();
       if (LAYOUT != kRowsRagged && row >= a.room) row = -1;
-      if (LAYOUT == kRowsContiguous && row >= 0) a.m_indices[row] = x;
+      if (LAYOUT == kRowsContiguous && row >= 0 && in_bounds(a, row, 1, a.room)) a.m_indices[row] = x;
       if (LAYOUT == kRowsMasked && row >= 0) row += x * a.room;
-      if (at < end) a.rows[at] = row;
+      if (at < end && in_bounds(a, at, 1, a.pairs)) a.rows[at] = row;
     }
   }
   if (bad) raise_status(a, ST_EXPERT_RANGE);
   if (LAYOUT == kRowsContiguous) {
     // -1 behind each expert's rows (a warp an expert), and behind the last expert
     for (int x = rank * WARPS + warp; x < a.G; x += cluster * WARPS)
-      for (int r = first[x] + have[x] + lane; r < min(first[x + 1], a.room); r += 32) a.m_indices[r] = -1;
+      for (int r = first[x] + have[x] + lane; r < min(first[x + 1], a.room); r += 32)
+        if (in_bounds(a, r, 1, a.room)) a.m_indices[r] = -1;
     for (long long r = static_cast<long long>(first[a.G]) + rank * THREADS + tid; r < a.room;
          r += cluster * THREADS)
-      a.m_indices[r] = -1;
+      if (in_bounds(a, r, 1, a.room)) a.m_indices[r] = -1;
   }
   if (cluster > 1) cluster_wait();
 }
@@ -253,7 +254,9 @@ dispatch_kernel(const DispatchCall a) {
         uint4* dst = D + static_cast<size_t>(r) * a.vecs + v0;
 #pragma unroll
         for (int i = 0; i < MOVE_VECS; ++i)
-          if (v0 + 32 * i < a.vecs) dst[32 * i] = x[i];
+          if (v0 + 32 * i < a.vecs && in_bounds(a, static_cast<size_t>(r) * a.vecs + v0 + 32 * i, 1,
+                                                static_cast<size_t>(a.num_rows) * a.vecs))
+            dst[32 * i] = x[i];
       }
     } else {
       const long long w = u - moves;
@@ -271,7 +274,8 @@ dispatch_kernel(const DispatchCall a) {
         uint32_t* dst = a.sa_out + (static_cast<size_t>(z) * a.kb + g0) * a.ld_out + m;
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i)
-          if (g0 + i < a.kb) dst[static_cast<size_t>(i) * a.ld_out] = s[i];
+          if (g0 + i < a.kb && in_bounds(a, m, 1, a.ld_out) && in_bounds(a, z, 1, a.num_rows / a.per))
+            dst[static_cast<size_t>(i) * a.ld_out] = s[i];
       }
     }
   }
@@ -343,7 +347,8 @@ combine_kernel(const CombineCall a) {
           for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, x[i], sum[i]);
       }
     }
-    if (on) static_cast<uint4*>(a.out)[at] = float_to_bf16x8(sum);
+    if (on && in_bounds(a, at, 1, static_cast<size_t>(a.T) * vecs))
+      static_cast<uint4*>(a.out)[at] = float_to_bf16x8(sum);
     mine = next_row;
     weight = next_weight;
   }
@@ -406,7 +411,8 @@ combine_backward_kernel(const CombineBwd a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], x[i], dot[j]);
           }
-          if (j0 + j < a.k && row >= 0 && on) {
+          if (j0 + j < a.k && row >= 0 && on &&
+              in_bounds(a, static_cast<size_t>(row) * vecs + v, 1, static_cast<size_t>(a.num_rows) * vecs)) {
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = w * g[i];
@@ -434,7 +440,8 @@ combine_backward_kernel(const CombineBwd a) {
             for (int w = 0; w < TEAM / 32; ++w) mine_dot += part[lane][w];
           __syncthreads();
         }
-        if (lane < SUM_ROWS && j < a.k && (TEAM == 32 || warp == 0))
+        if (lane < SUM_ROWS && j < a.k && (TEAM == 32 || warp == 0) &&
+            in_bounds(a, static_cast<size_t>(t) * a.k + j, 1, static_cast<size_t>(a.T) * a.k))
           a.dw[static_cast<size_t>(t) * a.k + j] = row >= 0 ? mine_dot : 0.f;
       }
     }
