@@ -92,21 +92,31 @@ __device__ __forceinline__ uint64_t warp_most(uint64_t v) {
 
 // What the choice in fp32 leaves open, in 64 bits.  row: the token's values as
 // order_of(c) in fp32 (0: not available), whose differences are off by less than
-// `margin`; only the values that this leaves in doubt are computed, a lane one of its
-// own at a time (few lanes have more than one).  Returns the j-th choice in lane j.
-// (All values in 64 bits took 7 us for a token of 128 experts, 13 of 384.)
+// `margin`; or by_logit, and the logits themselves decide.  Only the values that this
+// leaves in doubt are computed, a lane one of its own at a time (few lanes have more
+// than one).  Returns the j-th choice in lane j.  (All values in 64 bits took 7 us for a
+// token of 128 experts, 13 of 384.)
 template <class X, int NPL>
 __device__ __noinline__ int choose_exact(const RouteFwd a, const X* logits, const uint32_t* row,
-                                         float margin) {
+                                         bool by_logit, float margin) {
   const int lane = threadIdx.x & 31, e0 = lane * NPL;
   uint32_t key[NPL];
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) key[i] = e0 + i < a.G ? row[e0 + i] : 0;
+  for (int i = 0; i < NPL; ++i) {
+    key[i] = 0;
+    if (e0 + i >= a.G) continue;
+    if (by_logit) {
+      const float x = clean(read_logit(logits + e0 + i));
+      key[i] = x > -INFINITY ? order_of(x) : 0;
+    } else {
+      key[i] = row[e0 + i];
+    }
+  }
   uint64_t c[NPL];   // order of the exact values; 0: not needed
 #pragma unroll
   for (int i = 0; i < NPL; ++i) c[i] = 0;
   double top = 0, sum = 1;
-  if (!a.sigmoid) {
+  if (!a.sigmoid && !by_logit) {
     float m = -INFINITY;
     for (int e = lane; e < a.G; e += 32) m = fmaxf(m, clean(read_logit(logits + e)));
     top = static_cast<double>(float_of(__reduce_max_sync(ALL, order_of(m))));
@@ -123,9 +133,11 @@ __device__ __noinline__ int choose_exact(const RouteFwd a, const X* logits, cons
       const int at = want ? __ffs(want) - 1 : 0;
       uint64_t v = 0;
       if (want) {
-        const double x = clean(read_logit(logits + e0 + at));
-        double s = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum;
-        if (a.bias) s += static_cast<double>(__ldg(a.bias + e0 + at));
+        double s = clean(read_logit(logits + e0 + at));
+        if (!by_logit) {
+          s = a.sigmoid ? 1.0 / (1.0 + exp(-s)) : exp(s - top) / sum;
+          if (a.bias) s += static_cast<double>(__ldg(a.bias + e0 + at));
+        }
         v = order_of(s);
       }
 #pragma unroll
@@ -141,14 +153,18 @@ __device__ __noinline__ int choose_exact(const RouteFwd a, const X* logits, cons
     const int per = a.G / a.groups;
     uint64_t mine = 0;   // lane g: group g's value
     uint32_t edge = 0;   // lane g: group g's best-th
-    if (lane < a.groups) {
+    for (int g = 0; g < a.groups; ++g) {
       uint32_t one = 0, two = 0;
-      for (int e = 0; e < per; ++e) {
-        const uint32_t v = row[lane * per + e];
-        two = max(two, min(one, v));
-        one = max(one, v);
-      }
-      edge = a.best == 2 && two ? two : one;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (e0 + i >= g * per && e0 + i < (g + 1) * per) {
+          two = max(two, min(one, key[i]));
+          one = max(one, key[i]);
+        }
+      const uint32_t first = __reduce_max_sync(ALL, one);
+      const int owner = __ffs(__ballot_sync(ALL, one == first)) - 1;
+      const uint32_t second = __reduce_max_sync(ALL, lane == owner ? two : one);
+      if (lane == g) edge = a.best == 2 && second ? second : first;
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
@@ -253,10 +269,12 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // (below which e is 0); the sum, common to both, by (4 + 2.5 ln(1024)) u for its terms
 // and 40 u for its additions and its reciprocal: with s d < 0.37 below 2^-17 in all, with
 // d < 104 below 2^-14 of s.
-// Each c: u of itself.
+// Each c: u of itself, and by NPL 2^-23 of itself, as a key whose last bits say which of
+// the lane's values it is.
+template <int NPL>
 __device__ __forceinline__ float doubt(bool sigmoid, float c, float bias) {
   const float s = sigmoid ? 0x1p-19f : fminf(0x1p-17f, 0x1p-14f * (fabsf(c) + bias));
-  return s + 0x1p-22f * fabsf(c);
+  return s + (NPL + 1) * 0x1p-22f * fabsf(c);
 }
 
 // A lane's NPL consecutive logits (or biases) from e0 on, -infinity behind the last.
@@ -356,6 +374,7 @@ struct RoutePlan {
   int per;             // experts of a group
   uint32_t per_inv;    // x / per = __umulhi(x, per_inv) for x < 2^16 (per = 1: 0)
   bool grouped;        // groups are left out
+  bool lane_group;     // a lane's experts are of one group
   bool whole, whole_bias;
 };
 
@@ -399,52 +418,69 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
   }
   const bool grouped = plan.grouped;
   const bool by_logit = even && (!grouped || a.best == 1);
+  const bool full = by_logit && sizeof(X) == 2;   // keys that say the expert
   for (int t0 = first_t; t0 < a.T; t0 += gridDim.x * RT_WARPS * TEAMS) {
     const int t = t0 + team;
     const X* logits = logits_of(t);
     if (t0 != first_t) read_row<NPL>(logits, e0, a.G, plan.whole, x);
-    uint32_t key[NPL];   // order of c, or of the logit; 0: not available
+    // Order of c, or of the logit; 0: not available.  The last bits of a key say which
+    // value it is: of bf16 logits, whose order leaves 16 bits free, the expert (the lower,
+    // the larger), else which of the lane's (so that values that differ no further are in
+    // doubt).
+    uint32_t key[NPL];
+    bool there_is[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      // (NaN compares false)
-      key[i] = x[i] > -INFINITY ? order_of(fminf(x[i], FLT_MAX) + 0.f) : 0;
-      x[i] = key[i] ? fminf(x[i], FLT_MAX) : -INFINITY;
+      there_is[i] = x[i] > -INFINITY;   // (false for NaN)
+      x[i] = fminf(x[i], FLT_MAX);
     }
-    // the scores are needed in full for c, or for a softmax's sum
+    auto low_bits = [&](uint32_t o, int i) { return (o & ~(NPL - 1u)) | (NPL - 1 - i); };
     float top = 0.f, sum = 1.f;
+    // the scores are needed in full for c, or for a softmax's sum
     if (!a.sigmoid && !(by_logit && a.renormalize)) {
-      const uint32_t most = team_max<LANES>(largest<NPL>(key));
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) most = max(most, there_is[i] ? order_of(x[i]) : 0);
+      most = team_max<LANES>(most);
       top = most ? float_of(most) : 0.f;
-      sum = 0.f;
-      if (!a.renormalize) {
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-          x[i] = expf(x[i] - top);   // (0 for -infinity)
-          sum += x[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-          x[i] = exp_fast(x[i] - top);
-          sum += x[i];
-        }
-      }
-      sum = team_sum<LANES>(sum);
-    } else if (!by_logit) {
+    }
+    if (by_logit) {
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
-        const float e = exp_fast(-fabsf(x[i]));
-        x[i] = (x[i] < 0.f ? e : 1.f) * rcp_fast(1.f + e);
+        const uint32_t o = order_of(x[i] + 0.f);   // (-0 as 0)
+        key[i] = !there_is[i] ? 0 : full ? (o & 0xFFFF0000u) | (0xFFFFu - (e0 + i)) : low_bits(o, i);
       }
-    }
-    if (!by_logit) {
+      if (!a.sigmoid && !a.renormalize) {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) sum += there_is[i] ? expf(x[i] - top) : 0.f;
+        sum = team_sum<LANES>(sum);
+      }
+    } else {
+      if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          const float e = exp_fast(-fabsf(x[i]));
+          x[i] = (x[i] < 0.f ? e : 1.f) * rcp_fast(1.f + e);
+        }
+      } else {
+        sum = 0.f;
+        // (also the weights' sum, where they are not renormalised)
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          const float d = x[i] - top;
+          x[i] = !there_is[i] ? 0.f : a.renormalize ? exp_fast(d) : expf(d);
+          sum += x[i];
+        }
+        sum = team_sum<LANES>(sum);
+      }
       const float share = a.sigmoid ? 1.f : rcp_fast(sum);
       float b[NPL] = {};
       if (a.bias) read_row<NPL>(a.bias, e0, a.G, plan.whole_bias, b);   // (in L1)
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
         const float c = fmaf(x[i], share, b[i]);
-        key[i] = key[i] && c > -INFINITY ? order_of(c) : 0;
+        key[i] = there_is[i] && c > -INFINITY ? low_bits(order_of(fminf(c, FLT_MAX)), i) : 0;
       }
     }
     bool sure = true;
@@ -486,49 +522,67 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       const uint32_t lanes = __ballot_sync(ALL, stays) >> (team * LANES);
       const uint32_t last = ~team_max<LANES>(stays ? ~value : 0);
       const uint32_t next = team_max<LANES>(stays ? 0 : value);
-      if (!by_logit && next) {
+      if (next) {
         const float l = float_of(last), n = float_of(next);
-        sure = l - n > 2.f * doubt(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most);
+        sure = full || (by_logit ? (last ^ next) >= static_cast<uint32_t>(NPL)
+                                 : l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most));
       }
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
+      auto stays_at = [&](int i) {
         const uint32_t of = plan.per_inv ? __umulhi(e0 + i, plan.per_inv) : e0 + i;
-        if (!((lanes >> (of << shift & 31)) & 1u)) key[i] = 0;
+        return ((lanes >> (of << shift & 31)) & 1u) != 0;
+      };
+      if (plan.lane_group) {
+        const bool all = stays_at(0);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) key[i] = all ? key[i] : 0;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) key[i] = stays_at(i) ? key[i] : 0;
       }
     }
     // k rounds, and one more for what the last choice was close to
     int chosen = -1;
-    const int rounds = by_logit ? a.k : a.k + 1;
-    float before = 0.f;
-    for (int j = 0; j < rounds; ++j) {
-      const uint32_t v = largest<NPL>(key);
-      const uint32_t best = team_max<LANES>(v);
-      if (!by_logit && best) {
-        const float n = float_of(best);
-        if (j > 0) sure = sure && before - n > doubt(a.sigmoid, fmaxf(fabsf(before), fabsf(n)), bias_most);
-        before = n;
+    if (full) {
+      for (int j = 0; j < a.k; ++j) {
+        const uint32_t best = team_max<LANES>(largest<NPL>(key));
+        if (member == j && best) chosen = 0xFFFF - (best & 0xFFFFu);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) key[i] = key[i] == best ? 0 : key[i];
       }
-      const int owner = team_first<LANES>(v == best, team);
-      int at = 0;
+    } else {
+      uint32_t mine = 0, best = 0;   // lane j: the j-th key; the last round's
+      for (int j = 0; j <= a.k; ++j) {
+        const uint32_t v = largest<NPL>(key);
+        best = team_max<LANES>(v);
+        const int owner = team_first<LANES>(v == best, team);
+        if (member == j && j < a.k && best) {
+          chosen = owner * NPL + NPL - 1 - static_cast<int>(best & (NPL - 1u));
+          mine = best;
+        }
+        const uint32_t gone = member == owner ? best : 0xFFFFFFFFu;
 #pragma unroll
-      for (int i = NPL - 1; i >= 1; --i) at = key[i] == best ? i : at;
-      if (NPL > 1) at = key[0] == best ? 0 : at;
-      const int e = __shfl_sync(ALL, e0 + at, team * LANES + owner);
-      if (member == j && j < a.k && best) chosen = e;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (member == owner && i == at) key[i] = 0;
+        for (int i = 0; i < NPL; ++i) key[i] = key[i] == gone ? 0 : key[i];
+      }
+      // each choice against the next one
+      uint32_t next = __shfl_down_sync(ALL, mine, 1);
+      if (member == a.k - 1) next = best;
+      if (member < a.k && mine && next) {
+        const float l = float_of(mine), n = float_of(next);
+        sure = sure && (by_logit ? (mine ^ next) >= static_cast<uint32_t>(NPL)
+                                 : l - n > doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most));
+      }
     }
-    if (!__all_sync(ALL, sure)) {
+    const uint32_t open = __ballot_sync(ALL, !sure);
+    if (open) {
       // (|c| at most that of the scores and the biases; an infinite bias decides by
       // itself).  All lanes take one token at a time.
-      const uint32_t open = __ballot_sync(ALL, !sure);
-      const float margin = 2.f * doubt(a.sigmoid, 1.f + (bias_most < INFINITY ? bias_most : 0.f), bias_most);
+      const float margin = 2.f * doubt<NPL>(a.sigmoid, 1.f + (bias_most < INFINITY ? bias_most : 0.f), bias_most);
       for (int i = 0; i < TEAMS; ++i) {
-        if (!((open >> (i * LANES)) & 1u)) continue;
-        const int e = choose_exact<X, (NPL * LANES + 31) / 32>(a, logits_of(t0 + i), rows + i * a.G, margin);
-        const int mine = __shfl_sync(ALL, e, member);
-        if (team == i) chosen = mine;
+        if (((open >> (i * LANES)) & (LANES == 32 ? ALL : (1u << (LANES & 31)) - 1)) == 0) continue;
+        const int e = choose_exact<X, (NPL * LANES + 31) / 32>(a, logits_of(t0 + i), rows + i * a.G, by_logit,
+                                                               by_logit ? 0.f : margin);
+        const int theirs = __shfl_sync(ALL, e, member);
+        if (team == i) chosen = theirs;
       }
     }
     // weights: lane j that of the j-th choice
@@ -705,6 +759,7 @@ cudaError_t launch_fwd(const RouteFwd& a, int num_sms, bool limited, cudaStream_
   p.per = a.G / a.groups;
   p.per_inv = p.per > 1 ? 0xffffffffu / p.per + 1 : 0;
   p.grouped = a.groups > a.top_groups;
+  p.lane_group = p.per % NPL == 0;
   p.whole = whole_rows<X, NPL>(a.logits, a.G);
   p.whole_bias = whole_rows<float, NPL>(a.bias, a.G);
   const int smem = p.grouped || a.bias ? RT_WARPS * TEAMS * a.G * 4 : 0;
