@@ -383,8 +383,9 @@ dg_status dg_k_grouped_gemm_bf16_tn_ragged(const void* A, const void* B, const v
  *   weights[t][j] = scale * s, of that expert; with renormalize != 0 divided by the
  *   sum of the chosen s (sigmoid: plus 1e-20)
  * The bias moves the choice only, for an even load.  The choice is that of the
- * formulas in 64 bits, whatever is rounded on the way (where all biases are equal and
- * no sum of two decides, it is made by the logits, which both scores rise with).  An expert whose logit is -infinity or NaN is not available; where
+ * formulas in 64 bits, whatever is rounded on the way (where all biases are equal,
+ * experts are chosen by the logits, which both scores rise with, and so are groups by
+ * their single largest).  An expert whose logit is -infinity or NaN is not available; where
  * fewer than top_k are, the entries left over are expert -1, weight 0 (a token
  * whose experts are all masked has no row and no weight).  A logit of +infinity
  * counts as the largest number.

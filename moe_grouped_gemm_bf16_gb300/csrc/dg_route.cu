@@ -12,7 +12,7 @@
 // integers, which the first lane that holds it takes out.
 //
 // The choice is that of the formulas in 64 bits, whatever the rounding here: where all
-// biases are equal it is made by the logits themselves (both scores rise with
+// biases are equal, experts are chosen by the logits themselves (both scores rise with
 // them), else by c in fp32, and a token with two values nearer to each other
 // than their errors, at a place where that decides, is chosen again in 64 bits
 // (choose_exact; about one token in a thousand of 256 experts).
@@ -90,27 +90,28 @@ __device__ __forceinline__ uint64_t warp_most(uint64_t v) {
   return static_cast<uint64_t>(high) << 32 | low;
 }
 
+template <class X>
+__device__ __forceinline__ uint32_t logit_order(const X* p) {
+  const float x = clean(read_logit(p));
+  return x > -INFINITY ? order_of(x) : 0;
+}
+
 // What the choice in fp32 leaves open, in 64 bits.  row: the token's values as
 // order_of(c) in fp32 (0: not available), whose differences are off by less than
-// `margin`; or by_logit, and the logits themselves decide.  Only the values that this
-// leaves in doubt are computed, a lane one of its own at a time (few lanes have more
-// than one).  Returns the j-th choice in lane j.  (All values in 64 bits took 7 us for a
-// token of 128 experts, 13 of 384.)
+// `margin`; or by_logit, and the logits themselves decide (even: between the experts of
+// the groups that stay).  Only the values that this leaves in doubt are computed, a lane
+// one of its own at a time (few lanes have more than one).  Returns the j-th choice in
+// lane j.  (All values in 64 bits took 7 us for a token of 128 experts, 13 of 384.)
 template <class X, int NPL>
 __device__ __noinline__ int choose_exact(const RouteFwd a, const X* logits, const uint32_t* row,
-                                         bool by_logit, float margin) {
+                                         bool even, bool by_logit, float margin) {
   const int lane = threadIdx.x & 31, e0 = lane * NPL;
   uint32_t key[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     key[i] = 0;
     if (e0 + i >= a.G) continue;
-    if (by_logit) {
-      const float x = clean(read_logit(logits + e0 + i));
-      key[i] = x > -INFINITY ? order_of(x) : 0;
-    } else {
-      key[i] = row[e0 + i];
-    }
+    key[i] = by_logit ? logit_order(logits + e0 + i) : row[e0 + i];
   }
   uint64_t c[NPL];   // order of the exact values; 0: not needed
 #pragma unroll
@@ -199,6 +200,14 @@ __device__ __noinline__ int choose_exact(const RouteFwd a, const X* logits, cons
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
       if (!((keep >> min((e0 + i) / per, 31)) & 1u)) key[i] = c[i] = 0;
+    if (even && !by_logit) {
+      by_logit = true;
+      margin = 0.f;
+      done = 0;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (key[i]) key[i] = logit_order(logits + e0 + i);
+    }
   }
   // the values that may be among the k largest: not below the k-th in fp32 by more
   // than the margin
@@ -416,9 +425,11 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
     even = __all_sync(ALL, even);
     bias_most = __uint_as_float(__reduce_max_sync(ALL, __float_as_uint(bias_most)));
   }
+  // (|c| at most that of the scores and the biases; an infinite bias decides by itself)
+  const float margin = 2.f * doubt<NPL>(a.sigmoid, 1.f + (bias_most < INFINITY ? bias_most : 0.f), bias_most);
   const bool grouped = plan.grouped;
   const bool by_logit = even && (!grouped || a.best == 1);
-  const bool full = by_logit && sizeof(X) == 2;   // keys that say the expert
+  const bool full = even && sizeof(X) == 2;   // (in the end) keys that say the expert
   for (int t0 = first_t; t0 < a.T; t0 += gridDim.x * RT_WARPS * TEAMS) {
     const int t = t0 + team;
     const X* logits = logits_of(t);
@@ -435,6 +446,10 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       x[i] = fminf(x[i], FLT_MAX);
     }
     auto low_bits = [&](uint32_t o, int i) { return (o & ~(NPL - 1u)) | (NPL - 1 - i); };
+    auto logit_key = [&](float x, int i) {
+      const uint32_t o = order_of(x + 0.f);   // (-0 as 0)
+      return full ? (o & 0xFFFF0000u) | (0xFFFFu - (e0 + i)) : low_bits(o, i);
+    };
     float top = 0.f, sum = 1.f;
     // the scores are needed in full for c, or for a softmax's sum
     if (!a.sigmoid && !(by_logit && a.renormalize)) {
@@ -446,10 +461,7 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
     }
     if (by_logit) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const uint32_t o = order_of(x[i] + 0.f);   // (-0 as 0)
-        key[i] = !there_is[i] ? 0 : full ? (o & 0xFFFF0000u) | (0xFFFFu - (e0 + i)) : low_bits(o, i);
-      }
+      for (int i = 0; i < NPL; ++i) key[i] = there_is[i] ? logit_key(x[i], i) : 0;
       if (!a.sigmoid && !a.renormalize) {
         sum = 0.f;
 #pragma unroll
@@ -524,7 +536,7 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       const uint32_t next = team_max<LANES>(stays ? 0 : value);
       if (next) {
         const float l = float_of(last), n = float_of(next);
-        sure = full || (by_logit ? (last ^ next) >= static_cast<uint32_t>(NPL)
+        sure = (full && by_logit) || (by_logit ? (last ^ next) >= static_cast<uint32_t>(NPL)
                                  : l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most));
       }
       auto stays_at = [&](int i) {
@@ -540,6 +552,12 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         for (int i = 0; i < NPL; ++i) key[i] = stays_at(i) ? key[i] : 0;
       }
     }
+    if (even && !by_logit) {
+      // the groups chosen by sums of c: their experts by the logits again
+      read_row<NPL>(logits, e0, a.G, plan.whole, x);   // (in L1)
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) key[i] = key[i] ? logit_key(fminf(x[i], FLT_MAX), i) : 0;
+    }
     // k rounds, and one more for what the last choice was close to
     int chosen = -1;
     if (full) {
@@ -550,37 +568,98 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         for (int i = 0; i < NPL; ++i) key[i] = key[i] == best ? 0 : key[i];
       }
     } else {
-      uint32_t mine = 0, best = 0;   // lane j: the j-th key; the last round's
-      for (int j = 0; j <= a.k; ++j) {
+      // lane j: the j-th key and whose it is (also of the last round, where there is a lane)
+      uint32_t mine = 0, best = 0;
+      int whose = -1;
+      auto pick = [&](int j) {
         const uint32_t v = largest<NPL>(key);
         best = team_max<LANES>(v);
         const int owner = team_first<LANES>(v == best, team);
-        if (member == j && j < a.k && best) {
-          chosen = owner * NPL + NPL - 1 - static_cast<int>(best & (NPL - 1u));
+        if (member == j && best) {
+          whose = owner * NPL + NPL - 1 - static_cast<int>(best & (NPL - 1u));
           mine = best;
         }
         const uint32_t gone = member == owner ? best : 0xFFFFFFFFu;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) key[i] = key[i] == gone ? 0 : key[i];
-      }
+      };
+      for (int j = 0; j <= a.k; ++j) pick(j);
+      chosen = member < a.k ? whose : -1;
       // each choice against the next one
       uint32_t next = __shfl_down_sync(ALL, mine, 1);
       if (member == a.k - 1) next = best;
+      bool apart = true;
       if (member < a.k && mine && next) {
         const float l = float_of(mine), n = float_of(next);
-        sure = sure && (by_logit ? (mine ^ next) >= static_cast<uint32_t>(NPL)
-                                 : l - n > doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most));
+        apart = even ? (mine ^ next) >= static_cast<uint32_t>(NPL)
+                     : l - n > doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most);
+      }
+      constexpr uint32_t TEAM = LANES == 32 ? ALL : (1u << (LANES & 31)) - 1;
+      const uint32_t close = __ballot_sync(ALL, !apart);
+      const bool open = ((close >> (team * LANES)) & TEAM) != 0;
+      if (even || a.k >= LANES) {
+        sure = sure && !open;
+      } else if (__any_sync(ALL, open && sure)) {
+        // The choices and all that come after them within the margin, one to a lane, in
+        // 64 bits, and their order by that.
+        const uint32_t last_in = __shfl_sync(ALL, mine, team * LANES + a.k - 1);
+        int n = a.k + 1;
+        bool more = open && sure && last_in != 0;
+        auto near_last = [&]() { return best && float_of(last_in) - float_of(best) <= margin; };
+        more = more && near_last();
+        while (__any_sync(ALL, more && n < LANES)) {
+          // (a team that is done, or full, takes none: its `more` stays as it is)
+          const bool go = more && n < LANES;
+          pick(go ? n : LANES);
+          if (go) {
+            ++n;
+            more = near_last();
+          }
+        }
+        double total = 1.0;
+        if (!a.sigmoid) {
+          read_row<NPL>(logits, e0, a.G, plan.whole, x);
+          total = 0.0;
+#pragma unroll
+          for (int i = 0; i < NPL; ++i)
+            if (there_is[i]) total += exp(static_cast<double>(fminf(x[i], FLT_MAX)) - static_cast<double>(top));
+#pragma unroll
+          for (int o = LANES / 2; o >= 1; o >>= 1) total += __shfl_xor_sync(ALL, total, o);
+        }
+        uint64_t exact = 0;
+        if (mine && member < n) {
+          double v = clean(read_logit(logits + whose));
+          v = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - static_cast<double>(top)) / total;
+          if (a.bias) v += static_cast<double>(__ldg(a.bias + whose));
+          exact = order_of(v);
+        }
+        int rank = 0;
+        const int most = static_cast<int>(__reduce_max_sync(ALL, static_cast<unsigned>(n)));
+        for (int i = 0; i < most; ++i) {
+          const uint64_t v = __shfl_sync(ALL, exact, team * LANES + i);
+          const int e = __shfl_sync(ALL, whose, team * LANES + i);
+          rank += v > exact || (v == exact && v && e < whose);
+        }
+        int sorted = -1;
+        for (int j = 0; j < a.k; ++j) {
+          const int from = team_first<LANES>(exact && rank == j, team);
+          const int e = __shfl_sync(ALL, whose, team * LANES + max(from, 0));
+          if (member == j && from >= 0) sorted = e;
+        }
+        // (more within the margin than lanes: by choose_exact)
+        if (open && sure) {
+          if (more) sure = false;
+          else if (member < a.k) chosen = sorted;
+        }
       }
     }
-    const uint32_t open = __ballot_sync(ALL, !sure);
-    if (open) {
-      // (|c| at most that of the scores and the biases; an infinite bias decides by
-      // itself).  All lanes take one token at a time.
-      const float margin = 2.f * doubt<NPL>(a.sigmoid, 1.f + (bias_most < INFINITY ? bias_most : 0.f), bias_most);
+    const uint32_t unsettled = __ballot_sync(ALL, !sure);
+    if (unsettled) {
+      // all lanes take one token at a time
       for (int i = 0; i < TEAMS; ++i) {
-        if (((open >> (i * LANES)) & (LANES == 32 ? ALL : (1u << (LANES & 31)) - 1)) == 0) continue;
-        const int e = choose_exact<X, (NPL * LANES + 31) / 32>(a, logits_of(t0 + i), rows + i * a.G, by_logit,
-                                                               by_logit ? 0.f : margin);
+        if (!((unsettled >> (i * LANES)) & 1u)) continue;
+        const int e = choose_exact<X, (NPL * LANES + 31) / 32>(a, logits_of(t0 + i), rows + i * a.G, even,
+                                                               by_logit, by_logit ? 0.f : margin);
         const int theirs = __shfl_sync(ALL, e, member);
         if (team == i) chosen = theirs;
       }

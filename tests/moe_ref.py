@@ -26,12 +26,13 @@ def route(logits, bias, k, sigmoid, groups=1, top_groups=1, best=1, renorm=True,
     experts, weights = np.full((T, k), -1, np.int32), np.zeros((T, k))
     for t in range(T):
         s, on = scores(logits[t].astype(np.float64), sigmoid)
-        # both scores rise with the logit, beyond where 64 bits tell them apart:
-        # where all biases are equal and no sum of two decides, the logits order them
-        if (bias is None or (bias == bias[0]).all()) and (top_groups == groups or best == 1):
-            c = np.minimum(logits[t].astype(np.float64), F32_MAX)
-        else:
-            c = s + (0.0 if bias is None else bias.astype(np.float64))
+        # both scores rise with the logit, beyond where 64 bits tell them apart: where all
+        # biases are equal the logits order them (but sums of two, which order the groups)
+        x = np.minimum(logits[t].astype(np.float64), F32_MAX)
+        even = bias is None or (bias == bias[0]).all()
+        c = s + (0.0 if bias is None else bias.astype(np.float64))
+        if even and (top_groups == groups or best == 1):
+            c = x.copy()
         c[~on] = -np.inf
         if top_groups < groups:
             g = c.reshape(groups, -1)
@@ -40,7 +41,9 @@ def route(logits, bias, k, sigmoid, groups=1, top_groups=1, best=1, renorm=True,
                 r = sorted((v for v in row if v > -np.inf), reverse=True)[:best]
                 value.append(sum(r) if r else -np.inf)
             stay = sorted(range(groups), key=lambda i: (-value[i], i))[:top_groups]
+            g = (x if even else c).reshape(groups, -1)
             c = np.concatenate([g[i] if i in stay else np.full(len(g[i]), -np.inf) for i in range(groups)])
+            c[~on] = -np.inf
         order = [e for e in sorted(range(G), key=lambda i: (-c[i], i)) if c[e] > -np.inf][:k]
         w = s[order]
         if renorm and len(order):

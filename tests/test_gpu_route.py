@@ -167,6 +167,14 @@ def test_many_values_within_a_rounding(G, k, groups, top_groups, sigmoid):
         s, _ = M.scores(x[t].double().numpy(), sigmoid)
         check(x[t:t + 1], torch.from_numpy(1.0 - s).float(), k, sigmoid, groups, top_groups, 2)
     check(x, torch.from_numpy(1.0 - s).float(), k, sigmoid, groups, top_groups, 2)   # (one token in doubt)
+    # neighbouring tokens (which share a warp where there are few experts), one with all of its
+    # values in doubt, one with a few, one with none
+    y = x.clone()
+    y[24] = x[24] + 1e-3 * torch.arange(G)
+    y[20] = y[21] = x[24]
+    y[21, 3:] = x[21, 3:]
+    check(y, torch.from_numpy(1.0 - s).float(), k, sigmoid, groups, top_groups, 2)
+    check(y, torch.from_numpy(1.0 - s).float(), k, sigmoid)
 
 
 def back(x, e, dw, sigmoid, renorm, scale):
