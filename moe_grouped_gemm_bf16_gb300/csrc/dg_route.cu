@@ -388,8 +388,10 @@ struct RoutePlan {
 };
 
 // NPL: experts per lane, LANES: lanes per token (the others of the warp take further
-// tokens: 9268 tokens of 16 experts took 9 us with a warp each).
-template <class X, int NPL, int LANES>
+// tokens: 9268 tokens of 16 experts took 9 us with a warp each).  LOGITS: there are no
+// biases and no sums of two, so that the logits decide (16384 tokens of 128 experts in
+// bf16: 8.9 us without instances of its own).
+template <class X, int NPL, int LANES, bool LOGITS>
 __global__ void __launch_bounds__(32 * RT_WARPS, NPL <= 4 ? 5 : NPL == 8 ? 4 : NPL == 16 ? 2 : 1)
 route_kernel(const RouteFwd a, const RoutePlan plan) {
   constexpr int TEAMS = 32 / LANES;
@@ -409,9 +411,9 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
   // (the first row and the biases asked for together)
   if (first_t < a.T) read_row<NPL>(logits_of(first_t + team), e0, a.G, plan.whole, x);
   // all biases equal: the choice is by the logits
-  bool even = true;
+  bool even = true;   // (a constant with LOGITS)
   float bias_most = 0.f;
-  if (a.bias) {
+  if (!LOGITS && a.bias) {
     float b[NPL];
     read_row<NPL>(a.bias, e0, a.G, plan.whole_bias, b);
     const float first = __shfl_sync(ALL, b[0], 0);
@@ -428,7 +430,7 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
   // (|c| at most that of the scores and the biases; an infinite bias decides by itself)
   const float margin = 2.f * doubt<NPL>(a.sigmoid, 1.f + (bias_most < INFINITY ? bias_most : 0.f), bias_most);
   const bool grouped = plan.grouped;
-  const bool by_logit = even && (!grouped || a.best == 1);
+  const bool by_logit = LOGITS || (even && (!grouped || a.best == 1));
   const bool full = even && sizeof(X) == 2;   // (in the end) keys that say the expert
   for (int t0 = first_t; t0 < a.T; t0 += gridDim.x * RT_WARPS * TEAMS) {
     const int t = t0 + team;
@@ -842,8 +844,9 @@ cudaError_t launch_fwd(const RouteFwd& a, int num_sms, bool limited, cudaStream_
   p.whole = whole_rows<X, NPL>(a.logits, a.G);
   p.whole_bias = whole_rows<float, NPL>(a.bias, a.G);
   const int smem = p.grouped || a.bias ? RT_WARPS * TEAMS * a.G * 4 : 0;
-  return launch_dependent(route_kernel<X, NPL, LANES>, dim3(route_grid(a.T, TEAMS, num_sms, limited)),
-                          32 * RT_WARPS, stream, smem, a, p);
+  const bool logits = !a.bias && (!p.grouped || a.best == 1);
+  return launch_dependent(logits ? route_kernel<X, NPL, LANES, true> : route_kernel<X, NPL, LANES, false>,
+                          dim3(route_grid(a.T, TEAMS, num_sms, limited)), 32 * RT_WARPS, stream, smem, a, p);
 }
 
 template <class X>
