@@ -1116,7 +1116,8 @@ double bf_cost(const BfCall& c, const BfPlan& f, int num_sms) {
   const int halves = f.pair ? 1 : (f.lanes + 127) / 128;
   const double cols = std::min<double>(f.bc, per);
   const double slots = std::max(1.0, std::ceil(depth / bf_bk(f.pair) / f.split));
-  const double main = slots * (f.pair ? 0.33 : 0.08 + 0.0026 * f.lanes + 0.002 * f.bc);
+  const double main =
+      slots * (f.pair ? 0.33 * (0.6 + 0.4 * f.bc / 256) : 0.08 + 0.0026 * f.lanes + 0.002 * f.bc);
   const double epilogue = 0.0037 * cols * halves;
   const double run = main + epilogue + (waves - 1) * std::max(main, epilogue);
   const double N = c.N, K = c.K, M = c.M, T = c.rows;
@@ -1156,6 +1157,11 @@ BfPlan bf_plan(const BfCall& c, int num_sms) {
     }
   };
   if (per > 32) consider(true, 256, 256);
+  // (the loss: lower tiles where they fill the last wave better; its forward pass of 2000
+  // tokens, 5000 x 3000: 64 us with 256 words to a tile, 58 with 192; of 1000, 8000 x 512: 15.2
+  // with 256, 14.6 with 224)
+  if (c.epilogue != kBfPlain && !tn && per > 192)
+    for (int bc = 192; bc < 256; bc += 32) consider(true, 256, bc);
   // rows of D per tile near the average group's (tn: whole 64-wide boxes)
   for (int bc = tn ? 64 : 16; bc <= 128; bc *= 2) {
     if (!tn && (per > 4 * bc || (bc > 16 && per < bc / 4))) continue;

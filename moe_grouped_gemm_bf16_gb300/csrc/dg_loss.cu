@@ -106,6 +106,7 @@ cudaError_t launch_product(BfCall& c, const LossCall& a, int num_sms, cudaStream
   c.epilogue = static_cast<BfEpilogue>(EPI);
   BfPlan f = a.forced.lanes > 0 ? a.forced : bf_plan(c, num_sms);
   if (FORM == kBfNT) f.split = 1;
+  if (FORM == kBfTN && f.pair) f.bc = 256;   // (whole 128-wide halves)
   if (EPI == kBfSum) c.loss.parts = std::max(1, c.loss.parts);
   if (EPI == kBfStats)   // (of the words, for the joining kernel)
     c.loss.pairs = c.loss.words_on_lanes ? 4 * (f.pair ? 2 : 1) * ((c.N + f.lanes - 1) / f.lanes)

@@ -137,7 +137,7 @@ dg_status bf16_ragged(dgk::BfForm form, const void* A, const void* B, const void
   c.forced = dgk::bf16_forced_plan();
   if (c.forced.lanes > 0) {
     // boxes of an MN-major operand are 64 wide (nn, tn: B's; tn: A's)
-    if ((!c.forced.pair && ((form != dgk::kBfNT && c.forced.lanes % 64) || (tn && c.forced.bc % 64))) ||
+    if ((c.forced.pair && tn && c.forced.bc != 256) || (!c.forced.pair && ((form != dgk::kBfNT && c.forced.lanes % 64) || (tn && c.forced.bc % 64))) ||
         c.forced.split * (c.forced.pair ? 2 : 1) > st.sms ||
         (c.limited && dgk::bf16_grid(c, c.forced, st.sms) > st.sms))
       return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "no kernel for the forced plan");
@@ -273,7 +273,7 @@ dg_status dg_debug_force_ragged_plan(int pair, int lanes, int rows, int split) {
     g_ragged_plan.store(0);
     return host_ok();
   }
-  const bool ok = pair ? lanes == 256 && rows == 256 && (split == 1 || split == 2 || split == 4)
+  const bool ok = pair ? lanes == 256 && (rows == 192 || rows == 224 || rows == 256) && (split == 1 || split == 2 || split == 4)
                        : lanes >= 64 && lanes <= 256 && lanes % 16 == 0 && rows >= 16 && rows <= 128 &&
                              rows % 16 == 0 && split >= 1 && split <= 8;
   if (!ok)

@@ -91,7 +91,7 @@ def check_backward(X, W, t, lse, d, dX, dW):
 
 
 SHAPES = [(1, 1, 8), (1, 1000, 256), (3, 17, 8), (61, 130, 64), (128, 128, 128), (130, 2051, 264), (257, 513, 72),
-          (40, 32003, 512), (700, 5000, 136), (300, 257, 1032), (2, 50003, 2048)]
+          (40, 32003, 512), (700, 5000, 136), (2000, 5000, 264), (300, 257, 1032), (2, 50003, 2048)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
@@ -210,7 +210,7 @@ def test_streams_graphs_and_limits():
         check_backward(X, W, t, outs[1], d, outs[2], outs[3])
 
 
-@pytest.mark.parametrize("plan", [(True, 256, 256, 1), (True, 256, 256, 2), (True, 256, 256, 4), (False, 64, 64, 1),
+@pytest.mark.parametrize("plan", [(True, 256, 256, 1), (True, 256, 192, 1), (True, 256, 224, 2), (True, 256, 256, 2), (True, 256, 256, 4), (False, 64, 64, 1),
                                   (False, 64, 64, 8), (False, 128, 64, 2), (False, 192, 64, 4),
                                   (False, 256, 128, 1), (False, 128, 128, 3), (False, 256, 128, 8)],
                          ids=lambda p: "x".join(str(int(v)) for v in p))
