@@ -285,17 +285,21 @@ dispatch_kernel(const DispatchCall a) {
 // (blocks per SM: with 2, 3 and 4, the last with spills, 4096 tokens of 8 rows of 7168 take
 // 127, 102 and 107 us, their gradient 209, 174 and 192)
 constexpr int SUM_THREADS = 256, SUM_PER_SM = 3;
-constexpr int SUM_ROWS = 8;   // rows of a token in flight at a time
+// 16-byte vectors that a thread has in flight: of ROWS rows, VECS of each.  Few choices
+// take more of each row (3393 tokens of one row of 5016: 35 us with one vector of it).
+constexpr int SUM_LOADS = 8;
 
-// A warp takes 256 columns of a token, a lane eight of them, of all its rows:
+// A warp takes 256 VECS columns of a token, a lane eight of each 256, of all its rows:
 // products and sum in fp32 in the order of the choices, the residual added first.
 // The next token's rows and weights are on their way meanwhile.
+template <int ROWS>
 __global__ void __launch_bounds__(SUM_THREADS, SUM_PER_SM)
 combine_kernel(const CombineCall a) {
+  constexpr int VECS = SUM_LOADS / ROWS;
   const int lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int vecs = a.K >> 3, pieces = (vecs + 31) / 32;
+  const int vecs = a.K >> 3, pieces = (vecs + 32 * VECS - 1) / (32 * VECS);
   const uint4* Y = static_cast<const uint4*>(a.Y);
   const unsigned warps = gridDim.x * (SUM_THREADS / 32), w0 = blockIdx.x * (SUM_THREADS / 32) + (threadIdx.x >> 5);
   // (the warp's first unit, and the step from one to the next, without a division each)
@@ -312,11 +316,14 @@ combine_kernel(const CombineCall a) {
   };
   ask(t, mine, weight);
   while (t < a.T) {
-    const int v = piece * 32 + lane;
-    const bool on = v < vecs;
+    const int v = piece * (32 * VECS) + lane;
     const size_t at = static_cast<size_t>(t) * vecs + v;
-    uint4 r = make_uint4(0, 0, 0, 0);
-    if (a.R && on) r = static_cast<const uint4*>(a.R)[at];   // (may be `out`)
+    uint4 r[VECS];
+#pragma unroll
+    for (int h = 0; h < VECS; ++h) {
+      r[h] = make_uint4(0, 0, 0, 0);
+      if (a.R && v + 32 * h < vecs) r[h] = static_cast<const uint4*>(a.R)[at + 32 * h];   // (may be `out`)
+    }
     t += step_t;
     piece += step_p;
     if (piece >= pieces) {
@@ -326,42 +333,52 @@ combine_kernel(const CombineCall a) {
     int next_row;
     float next_weight;
     ask(t, next_row, next_weight);
-    float sum[8];
-    bf16x8_to_float(r, sum);
-    for (int j0 = 0; j0 < a.k; j0 += SUM_ROWS) {
-      uint4 y[SUM_ROWS];
+    float sum[VECS][8];
 #pragma unroll
-      for (int j = 0; j < SUM_ROWS; ++j) {
+    for (int h = 0; h < VECS; ++h) bf16x8_to_float(r[h], sum[h]);
+    for (int j0 = 0; j0 < a.k; j0 += ROWS) {
+      uint4 y[ROWS][VECS];
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
         const int row = __shfl_sync(ALL, mine, (j0 + j) & 31);
-        y[j] = make_uint4(0, 0, 0, 0);
-        if (j0 + j < a.k && row >= 0 && on) y[j] = ld_stream_v4(Y + static_cast<size_t>(row) * vecs + v);
+#pragma unroll
+        for (int h = 0; h < VECS; ++h) {
+          y[j][h] = make_uint4(0, 0, 0, 0);
+          if (j0 + j < a.k && row >= 0 && v + 32 * h < vecs)
+            y[j][h] = ld_stream_v4(Y + static_cast<size_t>(row) * vecs + v + 32 * h);
+        }
       }
 #pragma unroll
-      for (int j = 0; j < SUM_ROWS; ++j) {
+      for (int j = 0; j < ROWS; ++j) {
         const float w = __shfl_sync(ALL, weight, (j0 + j) & 31);
-        float x[8];
-        bf16x8_to_float(y[j], x);
         // (a choice without a row adds nothing, also to an infinite sum)
         if (j0 + j < a.k)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, x[i], sum[i]);
+          for (int h = 0; h < VECS; ++h) {
+            float x[8];
+            bf16x8_to_float(y[j][h], x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[h][i] = fmaf(w, x[i], sum[h][i]);
+          }
       }
     }
-    if (on && in_bounds(a, at, 1, static_cast<size_t>(a.T) * vecs))
-      static_cast<uint4*>(a.out)[at] = float_to_bf16x8(sum);
+#pragma unroll
+    for (int h = 0; h < VECS; ++h)
+      if (v + 32 * h < vecs && in_bounds(a, at + 32 * h, 1, static_cast<size_t>(a.T) * vecs))
+        static_cast<uint4*>(a.out)[at + 32 * h] = float_to_bf16x8(sum[h]);
     mine = next_row;
     weight = next_weight;
   }
 }
 
-// A team of threads (a warp, or the block) takes a token: a thread eight columns at a
-// time of the gradient and of all its rows; the dot products are summed over the team
+// A team of threads (32 to 256) takes a token: a thread eight columns at a time (VECS
+// times) of the gradient and of all its rows; the dot products are summed over the team
 // in a fixed order.
-template <int TEAM>
+template <int TEAM, int ROWS>
 __global__ void __launch_bounds__(SUM_THREADS, SUM_PER_SM)
 combine_backward_kernel(const CombineBwd a) {
-  constexpr int TEAMS = SUM_THREADS / TEAM;
-  __shared__ float part[SUM_ROWS][SUM_THREADS / 32];
+  constexpr int TEAMS = SUM_THREADS / TEAM, VECS = SUM_LOADS / ROWS;
+  __shared__ float part[ROWS][SUM_THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, member = threadIdx.x % TEAM;
   grid_dep_wait();
   grid_dep_launch_dependents();
@@ -384,39 +401,50 @@ combine_backward_kernel(const CombineBwd a) {
     const int mine = next_row;
     const float weight = mine < 0 ? 0.f : next_weight;
     ask(t + step);   // (on its way meanwhile)
-    for (int j0 = 0; j0 < a.k; j0 += SUM_ROWS) {
-      float dot[SUM_ROWS] = {};
-      for (int v = member; v < (vecs + 31) / 32 * 32; v += TEAM) {
-        const bool on = v < vecs;
-        uint4 d = make_uint4(0, 0, 0, 0);
-        if (on) d = __ldg(dO + v);
-        uint4 y[SUM_ROWS];
+    for (int j0 = 0; j0 < a.k; j0 += ROWS) {
+      float dot[ROWS] = {};
+      // (the bound a whole number of warps: the shuffles below)
+      for (int v = member; v < (vecs + 31) / 32 * 32; v += TEAM * VECS) {
+        uint4 d[VECS], y[ROWS][VECS];
+#pragma unroll
+        for (int h = 0; h < VECS; ++h) {
+          d[h] = make_uint4(0, 0, 0, 0);
+          if (v + h * TEAM < vecs) d[h] = __ldg(dO + v + h * TEAM);
+        }
         if (a.dw) {
 #pragma unroll
-          for (int j = 0; j < SUM_ROWS; ++j) {
+          for (int j = 0; j < ROWS; ++j) {
             const int row = __shfl_sync(ALL, mine, (j0 + j) & 31);
-            y[j] = make_uint4(0, 0, 0, 0);
-            if (j0 + j < a.k && row >= 0 && on) y[j] = ld_stream_v4(Y + static_cast<size_t>(row) * vecs + v);
+#pragma unroll
+            for (int h = 0; h < VECS; ++h) {
+              y[j][h] = make_uint4(0, 0, 0, 0);
+              if (j0 + j < a.k && row >= 0 && v + h * TEAM < vecs)
+                y[j][h] = ld_stream_v4(Y + static_cast<size_t>(row) * vecs + v + h * TEAM);
+            }
           }
         }
-        float g[8];
-        bf16x8_to_float(d, g);
 #pragma unroll
-        for (int j = 0; j < SUM_ROWS; ++j) {
-          const int row = __shfl_sync(ALL, mine, (j0 + j) & 31);
-          const float w = __shfl_sync(ALL, weight, (j0 + j) & 31);
-          if (a.dw) {
-            float x[8];
-            bf16x8_to_float(y[j], x);
+        for (int h = 0; h < VECS; ++h) {
+          float g[8];
+          bf16x8_to_float(d[h], g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], x[i], dot[j]);
-          }
-          if (j0 + j < a.k && row >= 0 && on &&
-              in_bounds(a, static_cast<size_t>(row) * vecs + v, 1, static_cast<size_t>(a.num_rows) * vecs)) {
-            float x[8];
+          for (int j = 0; j < ROWS; ++j) {
+            const int row = __shfl_sync(ALL, mine, (j0 + j) & 31);
+            const float w = __shfl_sync(ALL, weight, (j0 + j) & 31);
+            if (a.dw) {
+              float x[8];
+              bf16x8_to_float(y[j][h], x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = w * g[i];
-            dY[static_cast<size_t>(row) * vecs + v] = float_to_bf16x8(x);
+              for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], x[i], dot[j]);
+            }
+            const size_t at = static_cast<size_t>(max(row, 0)) * vecs + v + h * TEAM;
+            if (j0 + j < a.k && row >= 0 && v + h * TEAM < vecs &&
+                in_bounds(a, at, 1, static_cast<size_t>(a.num_rows) * vecs)) {
+              float x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] = w * g[i];
+              dY[at] = float_to_bf16x8(x);
+            }
           }
         }
       }
@@ -424,7 +452,7 @@ combine_backward_kernel(const CombineBwd a) {
         // lane j of each warp: the warp's sum of row j
         float mine_dot = 0.f;
 #pragma unroll
-        for (int j = 0; j < SUM_ROWS; ++j) {
+        for (int j = 0; j < ROWS; ++j) {
 #pragma unroll
           for (int o = 16; o >= 1; o >>= 1) dot[j] += __shfl_xor_sync(ALL, dot[j], o);
           if (lane == j) mine_dot = dot[j];
@@ -432,15 +460,16 @@ combine_backward_kernel(const CombineBwd a) {
         const int j = j0 + lane;
         const int row = __shfl_sync(ALL, mine, j & 31);
         if (TEAM > 32) {
-          if (lane < SUM_ROWS) part[lane][warp] = mine_dot;
-          __syncthreads();
+          const int team = threadIdx.x / TEAM;
+          if (lane < ROWS) part[lane][warp] = mine_dot;
+          named_bar_sync(1 + team, TEAM);
           mine_dot = 0.f;
-          if (lane < SUM_ROWS)
+          if (lane < ROWS)
 #pragma unroll
-            for (int w = 0; w < TEAM / 32; ++w) mine_dot += part[lane][w];
-          __syncthreads();
+            for (int w = 0; w < TEAM / 32; ++w) mine_dot += part[lane][team * (TEAM / 32) + w];
+          named_bar_sync(1 + team, TEAM);
         }
-        if (lane < SUM_ROWS && j < a.k && (TEAM == 32 || warp == 0) &&
+        if (lane < ROWS && j < a.k && member < 32 &&
             in_bounds(a, static_cast<size_t>(t) * a.k + j, 1, static_cast<size_t>(a.T) * a.k))
           a.dw[static_cast<size_t>(t) * a.k + j] = row >= 0 ? mine_dot : 0.f;
       }
@@ -508,23 +537,46 @@ cudaError_t launch_dispatch(const DispatchCall& a, int num_sms, bool limited, cu
 }
 
 cudaError_t launch_combine(const CombineCall& a, int num_sms, bool limited, cudaStream_t stream) {
-  const long long units = static_cast<long long>(a.T) * (((a.K >> 3) + 31) / 32);
-  return launch_dependent(combine_kernel, dim3(move_grid(units, SUM_THREADS / 32, SUM_PER_SM, num_sms, limited)),
+  const int rows = a.k <= 2 ? 2 : a.k <= 4 ? 4 : 8, wide = 32 * SUM_LOADS / rows;
+  const long long units = static_cast<long long>(a.T) * (((a.K >> 3) + wide - 1) / wide);
+  const dim3 grid(move_grid(units, SUM_THREADS / 32, SUM_PER_SM, num_sms, limited));
+  return launch_dependent(rows == 2 ? combine_kernel<2> : rows == 4 ? combine_kernel<4> : combine_kernel<8>, grid,
                           SUM_THREADS, stream, 0, a);
+}
+
+// Threads to a token in the gradient of combine: those with the least rounds of tokens
+// times what one takes (a round of loads for each of its iterations, and one more for
+// the sums): 9451 tokens of one row of 360 take 9.3, 14, 24 and 39 us with 32, 64, 128 and
+// 256, 480 of 8 rows of 7688 82, 48, 34 and 35, 4096 of 8 rows of 7168 216, 185, 170 and
+// 174.  (By the whole device's SMs, whatever the limit: the sums' order is the team's.)
+static int team_of(int T, int vecs, int k, int rows) {
+  constexpr long long kThreads = 152ll * SUM_PER_SM * SUM_THREADS;
+  int best = SUM_THREADS;
+  long long least = -1;
+  for (int team = SUM_THREADS; team >= 32; team /= 2) {
+    const long long each = team * (SUM_LOADS / rows);
+    const long long turns = (vecs + each - 1) / each * ((k + rows - 1) / rows);
+    const long long cost = ((T + kThreads / team - 1) / (kThreads / team)) * (1 + turns);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = team;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_combine_backward(const CombineBwd& a, int num_sms, bool limited,
                                     cudaStream_t stream) {
-  // A warp a token where there are enough of them for the SMs (10571 of one row of 280:
-  // 13 us, with a block each 44; 297 of 4 rows of 976: 6.4 and 3.6) and their rows are
-  // short (4096 of 8 rows of 7168: 217 and 181).  (Whatever the limit on the SMs: the
-  // sums' order is that of the team.)
-  constexpr int kTeamK = 1024, kTeamT = 8 * 152;
-  if (a.K <= kTeamK && a.T >= kTeamT)
-    return launch_dependent(combine_backward_kernel<32>, dim3(move_grid(a.T, SUM_THREADS / 32, SUM_PER_SM, num_sms, limited)),
-                            SUM_THREADS, stream, 0, a);
-  return launch_dependent(combine_backward_kernel<SUM_THREADS>, dim3(move_grid(a.T, 1, SUM_PER_SM, num_sms, limited)),
-                          SUM_THREADS, stream, 0, a);
+  const int rows = a.k <= 2 ? 2 : a.k <= 4 ? 4 : 8;
+  const int team = team_of(a.T, a.K >> 3, a.k, rows);
+  const dim3 grid(move_grid(a.T, SUM_THREADS / team, SUM_PER_SM, num_sms, limited));
+  auto go = [&](auto two, auto four, auto eight) {
+    return launch_dependent(rows == 2 ? two : rows == 4 ? four : eight, grid, SUM_THREADS, stream, 0, a);
+  };
+  return team == 32    ? go(combine_backward_kernel<32, 2>, combine_backward_kernel<32, 4>, combine_backward_kernel<32, 8>)
+         : team == 64  ? go(combine_backward_kernel<64, 2>, combine_backward_kernel<64, 4>, combine_backward_kernel<64, 8>)
+         : team == 128 ? go(combine_backward_kernel<128, 2>, combine_backward_kernel<128, 4>, combine_backward_kernel<128, 8>)
+                       : go(combine_backward_kernel<256, 2>, combine_backward_kernel<256, 4>, combine_backward_kernel<256, 8>);
 }
 
 }  // namespace dgk
