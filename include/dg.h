@@ -489,7 +489,7 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
  *              16-byte aligned; its contents need not be kept.  It belongs to one
  *              call at a time: calls on different streams, and graphs that may run
  *              at the same time, each need their own
- * and its gradient, with d_loss fp32 [T] that of loss:
+ * and its gradient, with d_loss fp32 [T], finite, that of loss:
  *   p = (exp(z[t][v] - lse[t]) - [v = y]) * d_loss[t] (0 for a token without a target,
  *       whose d_loss is not read), rounded to bf16 relative to the largest |d_loss|
  *   dX = p W, bf16 [T][K];  dW = p^T X, bf16 [V][K]: sums in fp32, one rounding; one

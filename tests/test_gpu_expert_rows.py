@@ -326,3 +326,63 @@ def test_streams_graphs_and_limits():
     finally:
         dg.set_num_sms(0)
     assert torch.equal(at, free)
+
+
+def test_operands_past_32_bits():
+    # 4.9e9 elements: rows at both ends, with their scales
+    R, K, T = 600000, 8192, 4
+    assert R * K > 2 ** 32
+    at = torch.tensor([[0, R - 1], [R // 2, 5], [R - 2, 300001], [7, -1]], dtype=torch.int32).cuda()
+    X = normal(T, K, seed=1)
+    D = torch.zeros(R, K, dtype=BF16, device="cuda")
+    dg.dispatch_rows_bf16(X, at, D, T, K, 2, R)
+    for t in range(T):
+        for r in at[t].tolist():
+            if r >= 0:
+                assert torch.equal(D[r], X[t])
+    assert int((D[:, 0] != 0).sum()) == 7
+    out, w = torch.empty(T, K, dtype=BF16, device="cuda"), torch.full((T, 2), 0.5, device="cuda")
+    dg.combine_rows(D, at, w, None, out, T, K, 2, R)
+    assert torch.equal(out[:3], X[:3]) and torch.equal(out[3], 0.5 * X[3])
+    dY, dw = torch.zeros_like(D), torch.empty(T, 2, device="cuda")
+    dg.combine_rows_backward(X, D, at, w, dY, dw, T, K, 2, R)
+    assert torch.equal(dY[R - 1], 0.5 * X[0]) and torch.equal(dY[300001], 0.5 * X[2])
+    assert int((dY[:, 0] != 0).sum()) == 7
+    del D, dY
+    G, max_m = 64, 10000
+    Q = torch.randint(0, 256, (T, K), device="cuda", dtype=torch.uint8)
+    sa = torch.rand(K // 128, 4, device="cuda") + 0.5
+    A = torch.zeros(G, max_m, K, dtype=torch.uint8, device="cuda")
+    out_sa = torch.zeros(G, K // 128, max_m, device="cuda")
+    at = torch.tensor([[0, G * max_m - 1], [320000, 5], [G * max_m - 2, 300001], [7, -1]], dtype=torch.int32).cuda()
+    dg.dispatch_rows_fp8_1x128(Q, sa, 4, at, A, out_sa, max_m, T, K, 2, G, max_m)
+    for t in range(T):
+        for r in at[t].tolist():
+            if r >= 0:
+                z, m = divmod(r, max_m)
+                assert torch.equal(A[z, m], Q[t]) and torch.equal(out_sa[z, :, m], sa[:, t])
+    assert int((out_sa[:, 0] != 0).sum()) == 7
+
+
+@pytest.mark.parametrize("team", [(9451, 360, 1), (2000, 2048, 3), (700, 2000, 4), (40, 8, 2), (300, 4096, 9), (5, 16384, 2)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_teams_of_the_gradient(team):
+    # few and many tokens, short and long rows: each takes teams of another size
+    T, K, k = team
+    _, rows, _ = M.rows(choices(T, 16, k, seed=T), 16, "ragged")
+    Y, dO, w = normal(T * k, K, seed=1), normal(T, K, seed=2), torch.rand(T, k, device="cuda")
+    r = torch.from_numpy(rows).cuda()
+    dY, dw = torch.full_like(Y, KEEP), torch.full((T, k), KEEP, device="cuda")
+    dg.combine_rows_backward(dO, Y, r, w, dY, dw, T, K, k, T * k)
+    on = r >= 0
+    at = r.clamp_min(0).long()
+    prod = dO.double()[:, None] * Y[at].double()
+    lim = (K / 8 + 16) * U * prod.abs().sum(2)
+    assert ((dw.double() - torch.where(on, prod.sum(2), 0.0)).abs() <= torch.where(on, lim, 0.0)).all()
+    want = torch.full(Y.shape, KEEP, dtype=torch.float64, device="cuda")
+    want[at[on]] = (dO.double()[:, None] * w.double()[..., None])[on]
+    R.check_close(dY, want, 2 * U * want.abs(), "gradient of the rows")
+    out = torch.full_like(dO, KEEP)
+    dg.combine_rows(Y, r, w, dO, out, T, K, k, T * k)
+    sums = torch.where(on[..., None], w.double()[..., None] * Y[at].double(), 0.0)
+    R.check_close(out, dO.double() + sums.sum(1), (k + 1) * U * (dO.double().abs() + sums.abs().sum(1)), "combine")

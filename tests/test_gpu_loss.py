@@ -264,3 +264,79 @@ def test_deep_reductions_lose_no_precision(T):
     want, want_lse = L.loss(X, W, t)
     for got, ref in ((loss, want), (lse, want_lse)):
         assert (got.double() - ref).norm() <= 1e-6 * ref.norm()
+
+
+def test_operands_past_32_bits():
+    # 2.4e9 elements of W and of dW; the words of interest at both ends
+    T, V, K = 3, 300000, 8008
+    assert V * K > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randn(T, K, generator=g, device="cuda").to(BF16)
+    W = torch.empty(V, K, dtype=BF16, device="cuda").normal_(0.0, 2 * K ** -0.5, generator=g)
+    t = torch.tensor([V - 1, 0, 270000], dtype=torch.int32, device="cuda")
+    d = torch.tensor([1.0, -0.5, 0.25], device="cuda")
+    loss, lse = forward(X, W, t)
+    z = torch.cat([L.logits(X, w) for w in W.split(20000)], 1)
+    want = torch.logsumexp(z, 1)
+    assert ((lse.double() - want).abs() <= 2e-5 * want).all()
+    hit = z.gather(1, t.long()[:, None])[:, 0]
+    assert ((loss.double() - (want - hit)).abs() <= 2e-5 * want).all()
+    dX, dW = backward(X, W, t, lse, d)
+    p = torch.exp(z - lse.double()[:, None])
+    p[torch.arange(3), t.long()] -= 1.0
+    p *= d.double()[:, None]
+    wx = sum(p[:, i:i + 20000] @ W[i:i + 20000].double() for i in range(0, V, 20000))
+    assert (dX.double() - wx).norm() <= 2 * L.BF16_ROUND * wx.norm()
+    for rows in (slice(0, 300), slice(269900, 270100), slice(V - 300, V)):
+        ww = p[:, rows].t() @ X.double()
+        assert (dW[rows].double() - ww).norm() <= 2 * L.BF16_ROUND * ww.norm()
+
+
+def test_waits_that_run_out():
+    # the loads switched off: the waits give up, which is reported, and nothing is stored
+    X, W, t, d = inputs(300, 2000, 256, seed=2)
+    n = dg.linear_cross_entropy_backward_workspace_bytes(300, 2000, 256)
+    work, lse = workspace(n), forward(X, W, t)[1]
+    dX, dW = torch.full_like(X, KEEP), torch.full_like(W, KEEP)
+    dg.set_wait_timeout_ns(2_000_000)
+    dg.debug_set_skip_producer(True)
+    try:
+        dg.linear_cross_entropy_backward(X, W, t, lse, d, dX, dW, work, n, 300, 2000, 256)
+        torch.cuda.synchronize()
+        assert dg.get_device_status() == 7
+        dg.linear_cross_entropy(X, W, t, torch.empty(300, device="cuda"), lse, work, n, 300, 2000, 256)
+        torch.cuda.synchronize()
+        assert dg.get_device_status() == 7
+    finally:
+        dg.debug_set_skip_producer(False)
+        dg.set_wait_timeout_ns(0)
+    assert (dW == KEEP).all()
+    # and the next call is whole again
+    loss, lse = forward(X, W, t)
+    check_forward(X, W, t, loss, lse)
+    check_backward(X, W, t, lse, d, *backward(X, W, t, lse, d))
+
+
+def test_two_calls_at_once():
+    # on two streams, each with a workspace of its own
+    a, b = inputs(500, 9000, 512, seed=1), inputs(33, 30000, 256, seed=2)
+    want = []
+    for X, W, t, d in (a, b):
+        loss, lse = forward(X, W, t)
+        want.append((loss, lse, *backward(X, W, t, lse, d)))
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for X, W, t, d in (a, b):
+        T, V, K = X.shape[0], W.shape[0], X.shape[1]
+        n = max(dg.linear_cross_entropy_workspace_bytes(T, V, K),
+                dg.linear_cross_entropy_backward_workspace_bytes(T, V, K))
+        outs.append((torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(X),
+                     torch.empty_like(W), workspace(n), n))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (X, W, t, d), (loss, lse, dX, dW, work, n) in zip(streams, (a, b), outs):
+            T, V, K = X.shape[0], W.shape[0], X.shape[1]
+            dg.linear_cross_entropy(X, W, t, loss, lse, work, n, T, V, K, stream=s)
+            dg.linear_cross_entropy_backward(X, W, t, lse, d, dX, dW, work, n, T, V, K, stream=s)
+    torch.cuda.synchronize()
+    for got, ref in zip(outs, want):
+        assert all(torch.equal(x, y) for x, y in zip(got, ref))
