@@ -13,9 +13,10 @@
 //
 // The choice is that of the formulas in 64 bits, whatever the rounding here: where all
 // biases are equal, experts are chosen by the logits themselves (both scores rise with
-// them), else by c in fp32, and a token with two values nearer to each other
-// than their errors, at a place where that decides, is chosen again in 64 bits
-// (choose_exact; about one token in a thousand of 256 experts).
+// them), else by c in fp32.  A token with two values nearer to each other than their
+// errors, at a place where that decides (about one in a thousand of 256 experts), has its
+// choices and what comes after them within the error sorted again in 64 bits, or, where
+// groups are in doubt, is chosen again altogether (choose_exact).
 //
 // Bounded by latency and by instructions, not by memory.
 #include <float.h>
@@ -502,7 +503,8 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
-        if (e0 + i < a.G) row[e0 + i] = key[i];
+        if (e0 + i < a.G)   // (the logits' order itself: a group's largest is not in doubt)
+          row[e0 + i] = !by_logit ? key[i] : there_is[i] ? order_of(x[i] + 0.f) : 0;
       __syncwarp();
     }
     if (grouped) {
@@ -536,10 +538,9 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       const uint32_t lanes = __ballot_sync(ALL, stays) >> (team * LANES);
       const uint32_t last = ~team_max<LANES>(stays ? ~value : 0);
       const uint32_t next = team_max<LANES>(stays ? 0 : value);
-      if (next) {
+      if (!by_logit && next) {
         const float l = float_of(last), n = float_of(next);
-        sure = (full && by_logit) || (by_logit ? (last ^ next) >= static_cast<uint32_t>(NPL)
-                                 : l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most));
+        sure = l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most);
       }
       auto stays_at = [&](int i) {
         const uint32_t of = plan.per_inv ? __umulhi(e0 + i, plan.per_inv) : e0 + i;
@@ -599,15 +600,18 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       constexpr uint32_t TEAM = LANES == 32 ? ALL : (1u << (LANES & 31)) - 1;
       const uint32_t close = __ballot_sync(ALL, !apart);
       const bool open = ((close >> (team * LANES)) & TEAM) != 0;
-      if (even || a.k >= LANES) {
+      if (a.k >= LANES) {
         sure = sure && !open;
       } else if (__any_sync(ALL, open && sure)) {
-        // The choices and all that come after them within the margin, one to a lane, in
-        // 64 bits, and their order by that.
+        // The choices and all that come after them within the margin (of logits: of the same
+        // key but for the last bits), one to a lane, in 64 bits, and their order by that.
         const uint32_t last_in = __shfl_sync(ALL, mine, team * LANES + a.k - 1);
         int n = a.k + 1;
         bool more = open && sure && last_in != 0;
-        auto near_last = [&]() { return best && float_of(last_in) - float_of(best) <= margin; };
+        auto near_last = [&]() {
+          return best && (even ? (last_in ^ best) < static_cast<uint32_t>(NPL)
+                               : float_of(last_in) - float_of(best) <= margin);
+        };
         more = more && near_last();
         while (__any_sync(ALL, more && n < LANES)) {
           // (a team that is done, or full, takes none: its `more` stays as it is)
@@ -619,7 +623,7 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
           }
         }
         double total = 1.0;
-        if (!a.sigmoid) {
+        if (!a.sigmoid && !even) {
           read_row<NPL>(logits, e0, a.G, plan.whole, x);
           total = 0.0;
 #pragma unroll
@@ -630,10 +634,15 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         }
         uint64_t exact = 0;
         if (mine && member < n) {
-          double v = clean(read_logit(logits + whose));
-          v = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - static_cast<double>(top)) / total;
-          if (a.bias) v += static_cast<double>(__ldg(a.bias + whose));
-          exact = order_of(v);
+          const float y = clean(read_logit(logits + whose));
+          if (even) {
+            exact = static_cast<uint64_t>(order_of(y)) << 32;
+          } else {
+            double v = y;
+            v = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - static_cast<double>(top)) / total;
+            if (a.bias) v += static_cast<double>(__ldg(a.bias + whose));
+            exact = order_of(v);
+          }
         }
         int rank = 0;
         const int most = static_cast<int>(__reduce_max_sync(ALL, static_cast<unsigned>(n)));
@@ -853,7 +862,8 @@ template <class X>
 cudaError_t launch_fwd(const RouteFwd& a, int num_sms, bool limited, cudaStream_t stream) {
   // a lane for each choice and each group at least; as few lanes, and registers for the
   // row of logits, as its length needs
-  const int least = std::max(a.k, a.groups);
+  // (and one for what the last choice is compared with)
+  const int least = std::max(a.k + 1, a.groups);
   if (a.G <= 8 && least <= 8) return launch_fwd<X, 1, 8>(a, num_sms, limited, stream);
   if (a.G <= 16 && least <= 8) return launch_fwd<X, 2, 8>(a, num_sms, limited, stream);
   if (a.G <= 32 && least <= 8) return launch_fwd<X, 4, 8>(a, num_sms, limited, stream);

@@ -500,7 +500,11 @@ cudaError_t launch_rows(const RowsCall& a, RowsLayout layout, int num_sms, cudaS
   // a block for every 2048 pairs (16384 pairs of 32 experts with their rows of 7168 in 8
   // bits: 36.6 us so and with 1024, 38.7 with 4096, 42.2 with 8192)
   int cluster = 1;
-  while (cluster < SORT_CLUSTER && 2 * cluster <= num_sms && a.pairs > 2048 * cluster) cluster *= 2;
+  // and for every 4096 rows to mark (28 choices of 184 experts, 23552 rows: 10.2 us with one
+  // block, dispatch included, 8.5 with eight)
+  const int room = layout == kRowsContiguous ? a.room : 0;
+  while (cluster < SORT_CLUSTER && 2 * cluster <= num_sms && (a.pairs > 2048 * cluster || room > 4096 * cluster))
+    cluster *= 2;
   const int warps = a.pairs <= 1024 ? 8 : 32, per = warps * cluster;
   const int chunk = ((a.pairs + per - 1) / per + 31) / 32 * 32;
   int bits = 1;

@@ -109,6 +109,22 @@ def test_values_nearer_than_a_rounding():
     check(x, torch.from_numpy(0.1 - p).float(), 8, False, 4, 2, 2)
 
 
+@pytest.mark.parametrize("G,k,groups,best", [(8, 8, 1, 1), (16, 7, 4, 1), (32, 8, 4, 2), (64, 16, 1, 1), (128, 6, 8, 1),
+                                              (256, 8, 8, 2), (500, 32, 1, 1), (1024, 9, 16, 1)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_many_equal_logits_in_fp32(G, k, groups, best, sigmoid):
+    # logits of a bf16 product as fp32: equal ones in most tokens, also at the last choice, and
+    # neighbours by one unit in the last place
+    x = logits(300, G, True, G).float()
+    top = max(1, groups // 2) if k <= G // groups * max(1, groups // 2) else groups
+    check(x, None, k, sigmoid, groups, top, best)
+    check(x, torch.full((G,), -0.5), k, sigmoid, groups, top, best)
+    near = x[:, :1].expand(300, G).contiguous()
+    step = torch.from_numpy(np.random.default_rng(G).integers(0, 4, size=(300, G)).astype(np.int32))
+    near = (near.view(torch.int32) + step).view(torch.float32)
+    check(near, None, k, sigmoid, groups, top, best)
+
+
 def test_far_logits():
     x = torch.tensor([[100.0, -100.0, 90.0, 0.0, -90.0, 30.0, -3e38, 3e38]])
     for sigmoid in (False, True):
