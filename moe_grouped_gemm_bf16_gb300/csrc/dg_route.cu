@@ -15,8 +15,9 @@
 // biases are equal, experts are chosen by the logits themselves (both scores rise with
 // them), else by c in fp32.  A token with two values nearer to each other than their
 // errors, at a place where that decides (about one in a thousand of 256 experts), has its
-// choices and what comes after them within the error sorted again in 64 bits, or, where
-// groups are in doubt, is chosen again altogether (choose_exact).
+// choices and what comes after them within the error sorted again in 64 bits, and so its
+// groups; where that many values are in doubt that lanes do not suffice, or a group's
+// largest are not clear, it is chosen again altogether (choose_exact).
 //
 // Bounded by latency and by instructions, not by memory.
 #include <float.h>
@@ -396,6 +397,7 @@ template <class X, int NPL, int LANES, bool LOGITS>
 __global__ void __launch_bounds__(32 * RT_WARPS, NPL <= 4 ? 5 : NPL == 8 ? 4 : NPL == 16 ? 2 : 1)
 route_kernel(const RouteFwd a, const RoutePlan plan) {
   constexpr int TEAMS = 32 / LANES;
+  constexpr uint32_t TEAM = LANES == 32 ? ALL : (1u << (LANES & 31)) - 1;   // a team's lanes in a ballot
   extern __shared__ uint32_t route_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team = lane / LANES, member = lane % LANES, e0 = member * NPL;
@@ -498,6 +500,26 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         key[i] = there_is[i] && c > -INFINITY ? low_bits(order_of(fminf(c, FLT_MAX)), i) : 0;
       }
     }
+    // a softmax's sum in 64 bits (of the whole team), and c of an expert
+    auto exact_total = [&]() {
+      double total = 1.0;
+      if (!a.sigmoid) {
+        float y[NPL];
+        read_row<NPL>(logits, e0, a.G, plan.whole, y);
+        total = 0.0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+          if (there_is[i]) total += exp(static_cast<double>(fminf(y[i], FLT_MAX)) - static_cast<double>(top));
+#pragma unroll
+        for (int o = LANES / 2; o >= 1; o >>= 1) total += __shfl_xor_sync(ALL, total, o);
+      }
+      return total;
+    };
+    auto exact_score = [&](int e, double total) {
+      double v = clean(read_logit(logits + e));
+      v = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - static_cast<double>(top)) / total;
+      return a.bias ? v + static_cast<double>(__ldg(a.bias + e)) : v;
+    };
     bool sure = true;
     if (grouped || !by_logit) {
       __syncwarp();
@@ -534,13 +556,63 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         const uint32_t v = __shfl_sync(ALL, value, team * LANES + (h << shift));
         rank += v > value || (v == value && h < g);
       }
-      const bool stays = mine && value && rank < a.top_groups;
-      const uint32_t lanes = __ballot_sync(ALL, stays) >> (team * LANES);
+      bool stays = mine && value && rank < a.top_groups;
+      uint32_t lanes = __ballot_sync(ALL, stays) >> (team * LANES);
       const uint32_t last = ~team_max<LANES>(stays ? ~value : 0);
       const uint32_t next = team_max<LANES>(stays ? 0 : value);
       if (!by_logit && next) {
         const float l = float_of(last), n = float_of(next);
         sure = l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most);
+      }
+      if (__any_sync(ALL, !sure)) {
+        // The groups' values in 64 bits, by the first lane of each: of its largest values in
+        // fp32, unless the next one is within the margin of them (then by choose_exact).
+        const double total = exact_total();
+        uint64_t exact = 0;
+        bool clear = true;
+        const bool first = mine && (member & (width - 1)) == 0;
+        if (first) {
+          uint32_t v1 = 0, v2 = 0, v3 = 0;
+          int e1 = 0, e2 = 0;
+#pragma unroll 4
+          for (int e = g * plan.per; e < (g + 1) * plan.per; ++e) {
+            const uint32_t v = row[e];
+            if (v > v1) {
+              v3 = v2;
+              v2 = v1;
+              e2 = e1;
+              v1 = v;
+              e1 = e;
+            } else if (v > v2) {
+              v3 = v2;
+              v2 = v;
+              e2 = e;
+            } else {
+              v3 = max(v3, v);
+            }
+          }
+          const uint32_t in = a.best == 2 ? v2 : v1, out = a.best == 2 ? v3 : v2;
+          clear = !(in && out && float_of(in) - float_of(out) <= margin);
+          if (v1) {
+            double v = exact_score(e1, total);
+            if (a.best == 2 && v2) v += exact_score(e2, total);
+            exact = order_of(v);
+          }
+        }
+        int place = 0;
+        for (int h = 0; h < a.groups; ++h) {
+          const uint64_t v = __shfl_sync(ALL, exact, team * LANES + (h << shift));
+          place += v > exact || (v == exact && h < g);
+        }
+        // (a group's other lanes follow the first)
+        const int from = team * LANES + (min(g, a.groups - 1) << shift);
+        const bool stay = mine && __shfl_sync(ALL, exact && place < a.top_groups ? 1 : 0, from) != 0;
+        const uint32_t unclear = __ballot_sync(ALL, !clear) >> (team * LANES);
+        const uint32_t settled = __ballot_sync(ALL, stay) >> (team * LANES);
+        if (!sure && (unclear & TEAM) == 0) {
+          sure = true;
+          lanes = settled;
+        }
       }
       auto stays_at = [&](int i) {
         const uint32_t of = plan.per_inv ? __umulhi(e0 + i, plan.per_inv) : e0 + i;
@@ -597,7 +669,6 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         apart = even ? (mine ^ next) >= static_cast<uint32_t>(NPL)
                      : l - n > doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most);
       }
-      constexpr uint32_t TEAM = LANES == 32 ? ALL : (1u << (LANES & 31)) - 1;
       const uint32_t close = __ballot_sync(ALL, !apart);
       const bool open = ((close >> (team * LANES)) & TEAM) != 0;
       if (a.k >= LANES) {
@@ -622,27 +693,11 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
             more = near_last();
           }
         }
-        double total = 1.0;
-        if (!a.sigmoid && !even) {
-          read_row<NPL>(logits, e0, a.G, plan.whole, x);
-          total = 0.0;
-#pragma unroll
-          for (int i = 0; i < NPL; ++i)
-            if (there_is[i]) total += exp(static_cast<double>(fminf(x[i], FLT_MAX)) - static_cast<double>(top));
-#pragma unroll
-          for (int o = LANES / 2; o >= 1; o >>= 1) total += __shfl_xor_sync(ALL, total, o);
-        }
+        const double total = even ? 1.0 : exact_total();
         uint64_t exact = 0;
         if (mine && member < n) {
-          const float y = clean(read_logit(logits + whose));
-          if (even) {
-            exact = static_cast<uint64_t>(order_of(y)) << 32;
-          } else {
-            double v = y;
-            v = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - static_cast<double>(top)) / total;
-            if (a.bias) v += static_cast<double>(__ldg(a.bias + whose));
-            exact = order_of(v);
-          }
+          exact = even ? static_cast<uint64_t>(logit_order(logits + whose)) << 32
+                       : order_of(exact_score(whose, total));
         }
         int rank = 0;
         const int most = static_cast<int>(__reduce_max_sync(ALL, static_cast<unsigned>(n)));
