@@ -606,7 +606,9 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         }
         // (a group's other lanes follow the first)
         const int from = team * LANES + (min(g, a.groups - 1) << shift);
-        const bool stay = mine && __shfl_sync(ALL, exact && place < a.top_groups ? 1 : 0, from) != 0;
+        // (asked for by all lanes, also those without a group)
+        const int theirs = __shfl_sync(ALL, exact && place < a.top_groups ? 1 : 0, from);
+        const bool stay = mine && theirs != 0;
         const uint32_t unclear = __ballot_sync(ALL, !clear) >> (team * LANES);
         const uint32_t settled = __ballot_sync(ALL, stay) >> (team * LANES);
         if (!sure && (unclear & TEAM) == 0) {

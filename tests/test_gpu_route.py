@@ -125,6 +125,20 @@ def test_many_equal_logits_in_fp32(G, k, groups, best, sigmoid):
     check(near, None, k, sigmoid, groups, top, best)
 
 
+@pytest.mark.parametrize("G,k,groups,top", [(54, 2, 18, 15), (24, 5, 3, 2), (60, 8, 5, 2), (42, 6, 7, 3),
+                                            (96, 6, 12, 4), (100, 9, 25, 7), (520, 8, 13, 4)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_groups_in_doubt_of_which_lanes_are_left_over(G, k, groups, top, sigmoid):
+    # numbers of groups that do not divide the lanes; many tokens whose groups' sums are
+    # equal, or apart by less than they are off by in fp32
+    x = torch.round(logits(200, G, False, G) * 2) / 2
+    bias = torch.from_numpy(np.random.default_rng(G).integers(0, 3, size=G)).float() / 4
+    for b in (None, bias, torch.full((G,), 0.25)):
+        check(x, b, k, sigmoid, groups, top, 2)
+        check(x.repeat(3, 1) + 1e-6 * logits(600, G, False, 9), b, k, sigmoid, groups, top, 2)
+    check(x, bias, k, sigmoid, groups, top, 1)
+
+
 def test_far_logits():
     x = torch.tensor([[100.0, -100.0, 90.0, 0.0, -90.0, 30.0, -3e38, 3e38]])
     for sigmoid in (False, True):
