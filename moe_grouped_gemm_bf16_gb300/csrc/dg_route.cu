@@ -565,34 +565,44 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         sure = l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most);
       }
       if (__any_sync(ALL, !sure)) {
-        // The groups' values in 64 bits, by the first lane of each: of its largest values in
-        // fp32, unless the next one is within the margin of them (then by choose_exact).
+        // The groups' values in 64 bits, by the first lane of each, of its largest values in
+        // fp32.  Where the next one is within the margin of them: of its largest logits, if
+        // the biases are equal, else by choose_exact.
         const double total = exact_total();
         uint64_t exact = 0;
         bool clear = true;
         const bool first = mine && (member & (width - 1)) == 0;
         if (first) {
-          uint32_t v1 = 0, v2 = 0, v3 = 0;
-          int e1 = 0, e2 = 0;
+          uint32_t v1, v2, v3;
+          int e1, e2;
+          auto largest_of = [&](bool logit) {
+            v1 = v2 = v3 = 0;
+            e1 = e2 = 0;
 #pragma unroll 4
-          for (int e = g * plan.per; e < (g + 1) * plan.per; ++e) {
-            const uint32_t v = row[e];
-            if (v > v1) {
-              v3 = v2;
-              v2 = v1;
-              e2 = e1;
-              v1 = v;
-              e1 = e;
-            } else if (v > v2) {
-              v3 = v2;
-              v2 = v;
-              e2 = e;
-            } else {
-              v3 = max(v3, v);
+            for (int e = g * plan.per; e < (g + 1) * plan.per; ++e) {
+              const uint32_t v = logit ? logit_order(logits + e) : row[e];
+              if (v > v1) {
+                v3 = v2;
+                v2 = v1;
+                e2 = e1;
+                v1 = v;
+                e1 = e;
+              } else if (v > v2) {
+                v3 = v2;
+                v2 = v;
+                e2 = e;
+              } else {
+                v3 = max(v3, v);
+              }
             }
-          }
+          };
+          largest_of(false);
           const uint32_t in = a.best == 2 ? v2 : v1, out = a.best == 2 ? v3 : v2;
           clear = !(in && out && float_of(in) - float_of(out) <= margin);
+          if (!clear && even) {
+            largest_of(true);
+            clear = true;
+          }
           if (v1) {
             double v = exact_score(e1, total);
             if (a.best == 2 && v2) v += exact_score(e2, total);
