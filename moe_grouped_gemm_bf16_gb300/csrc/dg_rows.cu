@@ -485,14 +485,17 @@ int move_grid(long long units, int per_block, int per_sm, int num_sms, bool limi
 }  // namespace
 
 cudaError_t rows_set_up() {
-  const void* kernels[] = {reinterpret_cast<const void*>(expert_rows_kernel<kRowsRagged, 32>),
-                           reinterpret_cast<const void*>(expert_rows_kernel<kRowsContiguous, 32>),
-                           reinterpret_cast<const void*>(expert_rows_kernel<kRowsMasked, 32>)};
-  for (const void* k : kernels) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               sort_smem(32, kRowsMaxExperts));
+  auto opt_in = [](auto kernel, int warps) {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                sort_smem(warps, kRowsMaxExperts));
+  };
+  const cudaError_t set[] = {
+      opt_in(expert_rows_kernel<kRowsRagged, 8>, 8),      opt_in(expert_rows_kernel<kRowsRagged, 32>, 32),
+      opt_in(expert_rows_kernel<kRowsContiguous, 8>, 8),  opt_in(expert_rows_kernel<kRowsContiguous, 32>, 32),
+      opt_in(expert_rows_kernel<kRowsMasked, 8>, 8),      opt_in(expert_rows_kernel<kRowsMasked, 32>, 32)};
+  for (const cudaError_t e : set)
     if (e != cudaSuccess) return e;
-  }
   return cudaSuccess;
 }
 

@@ -72,6 +72,18 @@ def test_rows(shape, layout, skew):
         assert np.array_equal(got[2], want[2])
 
 
+@pytest.mark.parametrize("G", [1021, 1022, 1023, 1024])
+@pytest.mark.parametrize("layout", ["ragged", "contiguous", "masked"])
+def test_most_experts_and_few_choices(G, layout):
+    e = choices(9, G, 4, seed=G)
+    e[0, 0], e[1, 1] = G - 1, 0
+    room = {"ragged": 0, "contiguous": 37 * 128, "masked": 36}[layout]
+    got, want = find(e, G, layout, room), M.rows(e, G, layout, room)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    if layout == "contiguous":
+        assert np.array_equal(got[2], want[2])
+
+
 @pytest.mark.parametrize("T,G,k", [(33000, 64, 8), (70001, 1024, 2), (300000, 256, 1)])
 def test_many_rows(T, G, k):
     e = choices(T, G, k, seed=3, skew=True)
