@@ -500,8 +500,8 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
  *              fp32 where there is more than one piece, or in parts of few tokens)
  * The sums run in a fixed order: the same inputs give the same bits on the same
  * number of SMs.  K a multiple of 8; too large (DG_ERR_UNSUPPORTED_SHAPE): T or K of 2^23
- * or more, V within 8192 of 2^31, X or W of 2^34 elements, T * V of 2^38.  X, W, dX
- * and dW 16-byte, the others 4-byte aligned.  T == 0: dW = 0, nothing else. */
+ * or more, V of 2^29, X or W of 2^34 elements, T * V of 2^38.  X, W, dX and dW
+ * 16-byte, the others 4-byte aligned.  T == 0: dW = 0, nothing else. */
 dg_status dg_linear_cross_entropy(const void* X, const void* W, const int32_t* targets, float* loss,
                                   float* lse, void* workspace, long long workspace_bytes, int T, int V,
                                   int K, void* stream);

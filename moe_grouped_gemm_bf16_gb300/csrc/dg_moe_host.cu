@@ -160,7 +160,8 @@ dg_status check_vocabulary(const char* name, int T, int V, int K) {
   if (T < 0 || V < 1 || K < 1) return host_fail(DG_ERR_INVALID_ARG, "%s: T=%d V=%d K=%d", name, T, V, K);
   if (K % 8 != 0) return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: K=%d (a multiple of 8)", name, K);
   const long long t = T, v = V, k = K;
-  if (V > INT_MAX - 8192 || T >= (1 << 23) || K >= (1 << 23) || v * k >= (1ll << 34) || t * k >= (1ll << 34) ||
+  // (V: the tiles' decoding divides numbers of lane blocks in fp32)
+  if (v >= (1 << 29) || T >= (1 << 23) || K >= (1 << 23) || v * k >= (1ll << 34) || t * k >= (1ll << 34) ||
       t * v >= (1ll << 38) || (v / 16 + 1) * (t / 64 + 1) >= (1ll << 31))
     return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "%s: T=%d V=%d K=%d: too large", name, T, V, K);
   return DG_OK;

@@ -134,6 +134,12 @@ LOSS_COMMON = [(dict(X=None), INVALID), (dict(W=None), INVALID), (dict(targets=N
                (dict(targets=P + 2), MISALIGNED), (dict(lse=P + 2), MISALIGNED)]
 
 
+@pytest.mark.parametrize("V,code", [(1 << 29, SHAPE), ((1 << 29) - 1, INVALID)])
+def test_the_largest_vocabulary(V, code):
+    # (within the limit it is the workspace that is refused, before anything else)
+    assert status(dg.linear_cross_entropy, {**LOSS, "V": V, "K": 8, "workspace_bytes": 64}) == code
+
+
 @pytest.mark.parametrize("kw,code", LOSS_COMMON + [
     (dict(loss=None, lse=None), INVALID), (dict(loss=P + 1), MISALIGNED),
     (dict(T=0, X=None, W=None, targets=None, loss=None, lse=None, workspace=None), OK)])
