@@ -276,15 +276,17 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // A sigmoid: e by (4 + 1.5 |x|) u of itself (ex2.approx, its argument), s = 1 / (1 + e)
 // by a quarter of that at most and |x| s (1 - s) < 0.23, sum, reciprocal and product by
 // 4 u: below 2^-21 each.
-// A softmax's s: e by (4 + 2.5 d) u of itself, d = |x - max| at most ln(1 / s) and 104
-// (below which e is 0); the sum, common to both, by (4 + 2.5 ln(1024)) u for its terms
-// and 40 u for its additions and its reciprocal: with s d < 0.37 below 2^-17 in all, with
-// d < 104 below 2^-14 of s.
+// A softmax's s, `share` (1 / the sum) the largest of them: e by (4 + 2.5 d) u of itself,
+// d = |x - max| = ln(share / s), at most 104 (below which e is 0); the sum, common to
+// both, by (4 + 2.5 ln(1024)) u for its terms and 40 u for its additions and its
+// reciprocal: with s d < 0.37 share below 2^-17 share in all, with d < 104 below 2^-14 of
+// s.  (2769 tokens of 160 experts in 8 groups by sums of two: 9.9 us, with 2^-17 for all
+// 18.6.)
 // Each c: u of itself, and by NPL 2^-23 of itself, as a key whose last bits say which of
 // the lane's values it is.
 template <int NPL>
-__device__ __forceinline__ float doubt(bool sigmoid, float c, float bias) {
-  const float s = sigmoid ? 0x1p-19f : fminf(0x1p-17f, 0x1p-14f * (fabsf(c) + bias));
+__device__ __forceinline__ float doubt(bool sigmoid, float c, float bias, float share) {
+  const float s = sigmoid ? 0x1p-19f : fminf(0x1p-17f * share, 0x1p-14f * (fabsf(c) + bias));
   return s + (NPL + 1) * 0x1p-22f * fabsf(c);
 }
 
@@ -430,8 +432,6 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
     even = __all_sync(ALL, even);
     bias_most = __uint_as_float(__reduce_max_sync(ALL, __float_as_uint(bias_most)));
   }
-  // (|c| at most that of the scores and the biases; an infinite bias decides by itself)
-  const float margin = 2.f * doubt<NPL>(a.sigmoid, 1.f + (bias_most < INFINITY ? bias_most : 0.f), bias_most);
   const bool grouped = plan.grouped;
   const bool by_logit = LOGITS || (even && (!grouped || a.best == 1));
   const bool full = even && sizeof(X) == 2;   // (in the end) keys that say the expert
@@ -456,6 +456,7 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       return full ? (o & 0xFFFF0000u) | (0xFFFFu - (e0 + i)) : low_bits(o, i);
     };
     float top = 0.f, sum = 1.f;
+    float share = 1.f;   // 1 / the sum of a softmax, where c is computed
     // the scores are needed in full for c, or for a softmax's sum
     if (!a.sigmoid && !(by_logit && a.renormalize)) {
       uint32_t most = 0;
@@ -491,7 +492,7 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         }
         sum = team_sum<LANES>(sum);
       }
-      const float share = a.sigmoid ? 1.f : rcp_fast(sum);
+      if (!a.sigmoid) share = rcp_fast(sum);
       float b[NPL] = {};
       if (a.bias) read_row<NPL>(a.bias, e0, a.G, plan.whole_bias, b);   // (in L1)
 #pragma unroll
@@ -500,6 +501,9 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         key[i] = there_is[i] && c > -INFINITY ? low_bits(order_of(fminf(c, FLT_MAX)), i) : 0;
       }
     }
+    // (|c| at most that of the scores and the biases; an infinite bias decides by itself)
+    const float margin =
+        2.f * doubt<NPL>(a.sigmoid, share + (bias_most < INFINITY ? bias_most : 0.f), bias_most, share);
     // a softmax's sum in 64 bits (of the whole team), and c of an expert
     auto exact_total = [&]() {
       double total = 1.0;
@@ -562,7 +566,7 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       const uint32_t next = team_max<LANES>(stays ? 0 : value);
       if (!by_logit && next) {
         const float l = float_of(last), n = float_of(next);
-        sure = l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most);
+        sure = l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most, share);
       }
       if (__any_sync(ALL, !sure)) {
         // The groups' values in 64 bits, by the first lane of each, of its largest values in
@@ -679,7 +683,7 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       if (member < a.k && mine && next) {
         const float l = float_of(mine), n = float_of(next);
         apart = even ? (mine ^ next) >= static_cast<uint32_t>(NPL)
-                     : l - n > doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most);
+                     : l - n > doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most, share);
       }
       const uint32_t close = __ballot_sync(ALL, !apart);
       const bool open = ((close >> (team * LANES)) & TEAM) != 0;
@@ -736,8 +740,9 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       // all lanes take one token at a time
       for (int i = 0; i < TEAMS; ++i) {
         if (!((unsettled >> (i * LANES)) & 1u)) continue;
+        const float within = by_logit ? 0.f : __shfl_sync(ALL, margin, i * LANES);
         const int e = choose_exact<X, (NPL * LANES + 31) / 32>(a, logits_of(t0 + i), rows + i * a.G, even,
-                                                               by_logit, by_logit ? 0.f : margin);
+                                                               by_logit, within);
         const int theirs = __shfl_sync(ALL, e, member);
         if (team == i) chosen = theirs;
       }
