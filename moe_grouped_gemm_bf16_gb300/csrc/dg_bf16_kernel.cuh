@@ -1165,7 +1165,11 @@ BfPlan bf_plan(const BfCall& c, int num_sms) {
   // rows of D per tile near the average group's (tn: whole 64-wide boxes)
   for (int bc = tn ? 64 : 16; bc <= 128; bc *= 2) {
     if (!tn && (per > 4 * bc || (bc > 16 && per < bc / 4))) continue;
-    for (int lanes = 128; lanes <= 256 && lanes - 64 < c.N; lanes += 64) consider(false, lanes, bc);
+    // (words on the lanes: whole quarters of 32 of them, which fill the last wave better: 16
+    // tokens of 131072 x 2048 85.6 us, with multiples of 64 92.4; 1 of 128256 x 4096 154 and
+    // 160.  Of a short reduction the epilogues outweigh that: 40 of 40000 x 512 18.4 and 17.2)
+    const int step = c.loss.words_on_lanes && c.K >= 1024 ? 32 : 64;
+    for (int lanes = 128; lanes <= 256 && lanes - step < c.N; lanes += step) consider(false, lanes, bc);
   }
   return best;
 }
