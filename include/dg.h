@@ -385,8 +385,8 @@ dg_status dg_k_grouped_gemm_bf16_tn_ragged(const void* A, const void* B, const v
  * The bias moves the choice only, for an even load.  The choice is that of the
  * formulas in 64 bits, whatever is rounded on the way (where all biases are equal,
  * experts are chosen by the logits, which both scores rise with, and so are groups by
- * their single largest).  An expert whose logit is -infinity or NaN is not available; where
- * fewer than top_k are, the entries left over are expert -1, weight 0 (a token
+ * their single largest).  An expert whose logit or bias is -infinity or NaN is not
+ * available; where fewer than top_k are, the entries left over are expert -1, weight 0 (a token
  * whose experts are all masked has no row and no weight).  A logit of +infinity
  * counts as the largest number.
  *   logits fp32 or bf16 [T][num_experts], bias fp32 [num_experts] or null,
