@@ -277,16 +277,18 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // by a quarter of that at most and |x| s (1 - s) < 0.23, sum, reciprocal and product by
 // 4 u: below 2^-21 each.
 // A softmax's s, `share` (1 / the sum) the largest of them: e by (4 + 2.5 d) u of itself,
-// d = |x - max| = ln(share / s), at most 104 (below which e is 0); the sum, common to
+// d = |x - max| = ln(share / s), below 88 where e is held; the sum, common to
 // both, by (4 + 2.5 ln(1024)) u for its terms and 40 u for its additions and its
-// reciprocal: with s d < 0.37 share below 2^-17 share in all, with d < 104 below 2^-14 of
+// reciprocal: with s d < 0.37 share below 2^-17 share in all, with d < 88 below 2^-14 of
 // s.  (2769 tokens of 160 experts in 8 groups by sums of two: 9.9 us, with 2^-17 for all
-// 18.6.)
+// 18.6.)  From there on, below 2^-126, e is 0, which is off by all that it was: 2^-125 for
+// both, whatever s is.
 // Each c: u of itself, and by NPL 2^-23 of itself, as a key whose last bits say which of
 // the lane's values it is.
 template <int NPL>
 __device__ __forceinline__ float doubt(bool sigmoid, float c, float bias, float share) {
-  const float s = sigmoid ? 0x1p-19f : fminf(0x1p-17f * share, 0x1p-14f * (fabsf(c) + bias));
+  const float s =
+      sigmoid ? 0x1p-19f : fminf(0x1p-17f * share, 0x1p-14f * (fabsf(c) + bias)) + 0x1p-125f;
   return s + (NPL + 1) * 0x1p-22f * fabsf(c);
 }
 

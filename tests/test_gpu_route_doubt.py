@@ -1,0 +1,52 @@
+"""The choice of experts where fp32 does not decide it: scores below what fp32 holds.
+The choice is exact, the weights' bounds are those of test_gpu_route.py."""
+import numpy as np
+import pytest
+import torch
+
+import moe_grouped_gemm_bf16_gb300 as dg
+from moe_grouped_gemm_bf16_gb300 import _build
+from tests import moe_ref as M
+from tests.test_gpu_route import TINY, U, check, logits, run, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    _build.build()
+    torch.cuda.init()
+    dg.get_device_status()
+    yield
+    assert dg.get_device_status() == 0
+
+
+def test_groups_of_scores_below_normal_numbers():
+    # softmax scores of e^-86.25 are held, those of e^-87.5 are below 2^-126: the second
+    # group's sum is the larger one by less than the third's single score
+    x = torch.tensor([[0.0, -200.0, -86.4, -87.5, -86.25, -200.0]])
+    check(x, None, 2, False, 3, 2, 2)
+    check(x.repeat(70, 1) - torch.arange(70)[:, None], None, 2, False, 3, 2, 2)
+    # in a row of 256, among others
+    y = torch.full((3, 256), -300.0)
+    y[:, 0], y[:, 32:34], y[:, 64:66] = 0.0, x[0, 2:4], x[0, 4:6]
+    check(y, None, 9, False, 8, 2, 2)
+    check(y.to(torch.bfloat16), None, 9, False, 8, 2, 2)
+
+
+@pytest.mark.parametrize("unit", [0.0, 1e-40, 3e-37, 1e-30])
+def test_biases_next_to_scores_below_normal_numbers(unit):
+    # one score has it all, the others are 1e-34 to 1e-56; biases as small, not all equal, or
+    # zero but for one that is not available
+    for G, k in ((16, 5), (64, 8), (256, 8)):
+        x = logits(40, G, False, G, scale=4.0) - 100.0
+        x[:, 3] = 0.0
+        bias = torch.from_numpy(np.random.default_rng(G).normal(size=G) * unit).float()
+        bias[5] = float("nan")
+        b = bias.numpy().copy()
+        b[5] = -np.inf
+        for groups, top in ((1, 1), (4, 3)):
+            e, w = run(x, bias, k, False, groups, top, 2)
+            we, ww = M.route(x.double().numpy(), b, k, False, groups, top, 2)
+            assert np.array_equal(e, we), np.argwhere(e != we)[:5].tolist()
+            within(w, ww, (48 + 130) * U * np.abs(ww) + TINY)
