@@ -566,9 +566,17 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       uint32_t lanes = __ballot_sync(ALL, stays) >> (team * LANES);
       const uint32_t last = ~team_max<LANES>(stays ? ~value : 0);
       const uint32_t next = team_max<LANES>(stays ? 0 : value);
+      // What is rounded are a sum's two values: of opposite signs (only biases are negative),
+      // they are larger than it.  (By all lanes: `next` differs between the warp's tokens.)
+      float more = 0.f;
+      if (!LOGITS && a.bias) {
+        const float c1 = two ? float_of(one) : 0.f, c2 = two ? float_of(two) : 0.f;
+        more = a.best == 2 && c1 > 0.f && c2 < 0.f ? fminf(c1, -c2) : 0.f;
+        more = __uint_as_float(team_max<LANES>(__float_as_uint(more)));
+      }
       if (!by_logit && next) {
         const float l = float_of(last), n = float_of(next);
-        sure = l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)), bias_most, share);
+        sure = l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)) + more, bias_most, share);
       }
       if (__any_sync(ALL, !sure)) {
         // The groups' values in 64 bits, by the first lane of each, of its largest values in

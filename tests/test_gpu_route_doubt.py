@@ -1,5 +1,6 @@
-"""The choice of experts where fp32 does not decide it: scores below what fp32 holds.
-The choice is exact, the weights' bounds are those of test_gpu_route.py."""
+"""The choice of experts where fp32 does not decide it: scores below what fp32 holds,
+biases that cancel in a group's sum.  The choice is exact, the weights' bounds are
+those of test_gpu_route.py."""
 import numpy as np
 import pytest
 import torch
@@ -50,3 +51,17 @@ def test_biases_next_to_scores_below_normal_numbers(unit):
             we, ww = M.route(x.double().numpy(), b, k, False, groups, top, 2)
             assert np.array_equal(e, we), np.argwhere(e != we)[:5].tolist()
             within(w, ww, (48 + 130) * U * np.abs(ww) + TINY)
+
+
+@pytest.mark.parametrize("G,groups,top,k", [(64, 8, 3, 8), (256, 8, 4, 8), (16, 8, 3, 4), (60, 5, 2, 6), (512, 16, 5, 9)])
+@pytest.mark.parametrize("size", [2.0, 100.0, 3000.0])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_biases_that_cancel_in_a_groups_sum(G, groups, top, k, size, sigmoid):
+    # a group's two largest c are near +size and -size: each is rounded by what `size` is, their
+    # sum is of the size of the scores
+    per = G // groups
+    bias = torch.full((groups, per), -2.0)
+    bias[:, 0], bias[:, per - 1] = 1.0, -1.0
+    x = logits(400, G, False, G)
+    check(x, size * bias.flatten(), k, sigmoid, groups, top, 2)
+    check(x.to(torch.bfloat16), size * bias.flatten(), k, sigmoid, groups, top, 2)
