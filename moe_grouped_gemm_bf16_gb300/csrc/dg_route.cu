@@ -98,6 +98,13 @@ __device__ __forceinline__ uint32_t logit_order(const X* p) {
   return x > -INFINITY ? order_of(x) : 0;
 }
 
+// The margin at a value c.  A c of +infinity, by its bias, is held as the largest number
+// but for the key's last bits: what is that large is settled in 64 bits, where all of them
+// are equal.
+__device__ __forceinline__ float margin_at(float c, float margin) {
+  return c > 0x1p127f ? fmaxf(margin, 0x1p126f) : margin;
+}
+
 // What the choice in fp32 leaves open, in 64 bits.  row: the token's values as
 // order_of(c) in fp32 (0: not available), whose differences are off by less than
 // `margin`; or by_logit, and the logits themselves decide (even: between the experts of
@@ -172,7 +179,7 @@ __device__ __noinline__ int choose_exact(const RouteFwd a, const X* logits, cons
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const uint32_t limit = __shfl_sync(ALL, edge, min((e0 + i) / per, 31));
-      if (key[i] && float_of(key[i]) >= float_of(limit) - margin) done |= 1u << i;
+      if (key[i] && float_of(key[i]) >= float_of(limit) - margin_at(float_of(limit), margin)) done |= 1u << i;
     }
     compute(done);
     for (int g = 0; g < a.groups; ++g) {
@@ -232,7 +239,7 @@ __device__ __noinline__ int choose_exact(const RouteFwd a, const X* logits, cons
   uint32_t want = 0;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    if (key[i] && float_of(key[i]) >= float_of(edge) - margin) {
+    if (key[i] && float_of(key[i]) >= float_of(edge) - margin_at(float_of(edge), margin)) {
       if (!((done >> i) & 1u)) want |= 1u << i;
     } else {
       c[i] = 0;
@@ -429,7 +436,7 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
     for (int i = 0; i < NPL; ++i)
       if (e0 + i < a.G) {
         even = even && b[i] == first;
-        bias_most = fmaxf(bias_most, fabsf(b[i]));
+        if (fabsf(b[i]) < INFINITY) bias_most = fmaxf(bias_most, fabsf(b[i]));
       }
     even = __all_sync(ALL, even);
     bias_most = __uint_as_float(__reduce_max_sync(ALL, __float_as_uint(bias_most)));
@@ -503,9 +510,8 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         key[i] = there_is[i] && c > -INFINITY ? low_bits(order_of(fminf(c, FLT_MAX)), i) : 0;
       }
     }
-    // (|c| at most that of the scores and the biases; an infinite bias decides by itself)
-    const float margin =
-        2.f * doubt<NPL>(a.sigmoid, share + (bias_most < INFINITY ? bias_most : 0.f), bias_most, share);
+    // (|c| at most that of the scores and the biases)
+    const float margin = 2.f * doubt<NPL>(a.sigmoid, share + bias_most, bias_most, share);
     // a softmax's sum in 64 bits (of the whole team), and c of an expert
     auto exact_total = [&]() {
       double total = 1.0;
@@ -704,10 +710,11 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
         // key but for the last bits), one to a lane, in 64 bits, and their order by that.
         const uint32_t last_in = __shfl_sync(ALL, mine, team * LANES + a.k - 1);
         int n = a.k + 1;
+        const float reach = margin_at(float_of(last_in), margin);
         bool more = open && sure && last_in != 0;
         auto near_last = [&]() {
           return best && (even ? (last_in ^ best) < static_cast<uint32_t>(NPL)
-                               : float_of(last_in) - float_of(best) <= margin);
+                               : float_of(last_in) - float_of(best) <= reach);
         };
         more = more && near_last();
         while (__any_sync(ALL, more && n < LANES)) {

@@ -1,6 +1,6 @@
 """The choice of experts where fp32 does not decide it: scores below what fp32 holds,
-biases that cancel in a group's sum.  The choice is exact, the weights' bounds are
-those of test_gpu_route.py."""
+biases that cancel in a group's sum, and infinite ones beside others.  The choice is
+exact, the weights' bounds are those of test_gpu_route.py."""
 import numpy as np
 import pytest
 import torch
@@ -65,3 +65,32 @@ def test_biases_that_cancel_in_a_groups_sum(G, groups, top, k, size, sigmoid):
     x = logits(400, G, False, G)
     check(x, size * bias.flatten(), k, sigmoid, groups, top, 2)
     check(x.to(torch.bfloat16), size * bias.flatten(), k, sigmoid, groups, top, 2)
+
+
+@pytest.mark.parametrize("G,k,groups,top", [(64, 6, 1, 1), (256, 8, 1, 1), (256, 8, 8, 4), (16, 4, 1, 1), (512, 32, 8, 3)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_an_infinite_bias_beside_large_ones(G, k, groups, top, sigmoid, sign):
+    # c of the others near 1000, many of them within a rounding of that; and of a few units
+    x = logits(200, G, False, G)
+    small = torch.from_numpy(np.random.default_rng(G).normal(size=G)).float()
+    for bias in (1000.0 + 1e-3 * small, small):
+        bias[G // 2] = sign * float("inf")
+        check(x, bias, k, sigmoid, groups, top, 2)
+        check(x, bias, k, sigmoid, groups, top, 1)
+
+
+@pytest.mark.parametrize("G,k", [(64, 3), (256, 8), (16, 4), (1024, 32)])
+@pytest.mark.parametrize("groups,best", [(1, 1), (4, 1), (4, 2)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_more_infinite_biases_than_choices(G, k, groups, best, sigmoid):
+    # all of them equal: the lowest indices, whichever lanes hold them
+    x = logits(50, G, False, G)
+    at = np.random.default_rng(k).permutation(G)[:min(G, 2 * k + 3)]
+    bias = torch.from_numpy(np.random.default_rng(G).normal(size=G)).float()
+    bias[torch.from_numpy(at)] = float("inf")
+    check(x, bias, k, sigmoid, groups, max(1, groups // 2), best)
+    few = torch.zeros(G)
+    few[torch.from_numpy(at[:max(1, k - 1)])] = float("inf")   # (and one more by its score)
+    few[at[-1]] = -1.0
+    check(x, few, k, sigmoid, groups, max(1, groups // 2), best)
