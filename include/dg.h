@@ -491,7 +491,8 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
  *              at the same time, each need their own
  * and its gradient, with d_loss fp32 [T], finite, that of loss:
  *   p = (exp(z[t][v] - lse[t]) - [v = y]) * d_loss[t] (0 for a token without a target,
- *       whose d_loss is not read), rounded to bf16 relative to the largest |d_loss|
+ *       whose d_loss does not count), rounded to bf16 relative to the largest |d_loss|;
+ *       z is summed up as in the forward call
  *   dX = p W, bf16 [T][K];  dW = p^T X, bf16 [V][K]: sums in fp32, one rounding; one
  *   of them may be null (not computed)
  *   lse        what the forward call wrote for these X and W

@@ -341,6 +341,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
   using L = BfSmem;
   constexpr int BK = bf_bk(PAIR);
   constexpr bool TN = FORM == kBfTN, P_MN = FORM != kBfNT;
+  constexpr bool LOGITS = EPI == kBfStats || EPI == kBfGrad;   // (whose sums are added up here)
   // columns of one accumulator: two M = 128 halves side by side, or the pair's
   constexpr int ACC = PAIR ? BC : 2 * BC;
   static_assert(2 * ACC <= 512, "two accumulators");
@@ -582,8 +583,8 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
         const int n = T.kend - T.kbeg;
         for (int j = 0; j < n; ++j) {
           // (the logits' sums: an accumulator for every few slots)
-          const bool starts = EPI == kBfStats ? j % bf_stretch(PAIR) == 0 : j == 0;
-          const bool ends = j == n - 1 || (EPI == kBfStats && (j + 1) % bf_stretch(PAIR) == 0);
+          const bool starts = LOGITS ? j % bf_stretch(PAIR) == 0 : j == 0;
+          const bool ends = j == n - 1 || (LOGITS && (j + 1) % bf_stretch(PAIR) == 0);
           if (starts && j > 0) {
             d = tmem + static_cast<uint32_t>(b * ACC);
             ok = wait_bar(bar(L::T_EMPTY + b), bph ^ 1, abort_flag, p) && ok;
@@ -783,7 +784,7 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
     return T.l0 + (PAIR ? static_cast<int>(side) : a) * 128 + q * 32 + (lane & ~1);
   };
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16);
-  if constexpr (EPI == kBfStats || EPI == kBfGrad) {
+  if constexpr (LOGITS) {
     if (warp >= 4) {
       const BfLoss& x = p.loss;
       int b = 0;
@@ -817,17 +818,25 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
         float lse, scale; // -log2(e) lse; d_loss / unit
         float top, sum;
       };
-      auto token = [&](int l, bool on) {
-        Token k{on ? l : -1, -1, -INFINITY, 0.f, -INFINITY, 0.f};
-        if (!on) return k;
-        const int y = __ldg(x.targets + l);
-        const bool there = y >= 0 && y < x.words;
-        if (there) k.target = y - x.word0;
-        if (EPI == kBfGrad && there) {
-          if (unit_d != 0.f) k.scale = __fdiv_rn(__ldg(x.d_loss + l), unit_d);
-          k.lse = -kLog2e * __ldg(x.lse + l);
+      // (its values asked for together, and used once the tile's sums are there)
+      auto ask = [&](int l, bool on) {
+        Token k{on ? l : -1, -1, 0.f, 0.f, -INFINITY, 0.f};
+        if (on) {
+          k.target = __ldg(x.targets + l);
+          if (EPI == kBfGrad) {
+            k.lse = __ldg(x.lse + l);
+            k.scale = __ldg(x.d_loss + l);
+          }
         }
         return k;
+      };
+      auto ready = [&](Token& k) {
+        const bool there = k.target >= 0 && k.target < x.words;
+        k.target = there ? k.target - x.word0 : -1;
+        if (EPI == kBfGrad) {
+          k.lse = there ? -kLog2e * k.lse : -INFINITY;
+          k.scale = there && unit_d != 0.f ? __fdiv_rn(k.scale, unit_d) : 0.f;
+        }
       };
       auto take = [&](Token& k, uint32_t (&v)[32], int w, int n) {
         // (the target's word is number `hit` of these; one behind them is of a later
@@ -849,17 +858,36 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
             const float s = exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, k.lse));
             v[j] = __float_as_uint(k.scale * (j == hit ? s - 1.f : s));
           }
-          const size_t at = static_cast<size_t>(k.l) * x.pitch + w;
+          // Four lanes, whose tokens follow each other, store their four rows one after the
+          // other, 64 bytes of a row at a time: vector i of lane m to vector m of lane i.  (A
+          // lane its own row, 16 bytes of 32 rows at a time: 4096 of 131072 x 2048 4035 us in all,
+          // so 3827.)
+          uint32_t o[4][4];
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            // (the pitch is a multiple of 8: whole vectors up to it)
-            if (k.l >= 0 && j < n && in_bounds(p, at + j, 8, static_cast<size_t>(x.tokens) * x.pitch)) {
-              uint32_t o[4];
+          for (int j = 0; j < 32; j += 2)
+            o[j >> 3][(j >> 1) & 3] = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                o[i] = pack_bf16x2(__uint_as_float(v[j + 2 * i]), __uint_as_float(v[j + 2 * i + 1]));
-              *reinterpret_cast<uint4*>(p.D + at + j) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int s = 2; s >= 1; s >>= 1) {
+            const bool high = (lane & s) != 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i & s) continue;
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? o[i][h] : o[i | s][h], s);
+                if (high) o[i][h] = got;
+                else o[i | s][h] = got;
+              }
             }
+          }
+          const int j = 8 * (lane & 3);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int l = __shfl_sync(0xffffffffu, k.l, (lane & ~3) | i);
+            const size_t at = static_cast<size_t>(l) * x.pitch + w + j;
+            // (the pitch is a multiple of 8: whole vectors up to it)
+            if (l >= 0 && j < n && in_bounds(p, at, 8, static_cast<size_t>(x.tokens) * x.pitch))
+              *reinterpret_cast<uint4*>(p.D + at) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
           }
         }
       };
@@ -883,98 +911,101 @@ bf16_grouped_kernel(const __grid_constant__ BfMaps maps, const BfParams p) {
           b ^= 1;
           if (b == 0) bph ^= 1;
         };
-        constexpr int A = PAIR ? 1 : 2, C = BC / 64;   // halves of the lanes, chunks of a warp's columns
-        auto chunk = [&](int i) { return 32 * eh + 64 * i; };
-        // tokens on the lanes: one of each half (asked for before the wait)
-        Token k[A];
-        if (!x.words_on_lanes) {
+        // A warp's logits: two steps of R blocks of 32, of the halves of the lanes, or (pair) of
+        // two chunks of its columns each.
+        constexpr int R = PAIR ? BC / 128 : BC / 64;
+        auto half = [&](int s) { return PAIR ? 0 : s; };
+        auto chunk = [&](int s, int r) { return 32 * eh + 64 * (PAIR ? R * s + r : r); };
+        auto there = [&](int s, int r) { return half(s) < halves && chunk(s, r) < T.cols; };
+        // the tile's tokens, asked for before the wait: on the lanes one of each half; on the
+        // columns those of the first chunk
+        Token k[2];
+        if (x.words_on_lanes) {
+          k[0] = ask(T.q0 + chunk(0, 0) + lane, chunk(0, 0) + lane < T.cols);
+        } else {
 #pragma unroll
-          for (int a = 0; a < A; ++a)
-            k[a] = token(quarter(a) + lane, a < halves && quarter(a) + lane < l_end);
+          for (int s = 0; s < (PAIR ? 1 : 2); ++s)
+            k[s] = ask(quarter(s) + lane, s < halves && quarter(s) + lane < l_end);
         }
         bool ok = true;
-        if constexpr (EPI == kBfStats) {
-          // The tensor cores' fp32 accumulation drops bits towards zero, at each of its
-          // steps of 16: after K / 16 of them a loss of 12 was off by 2e-5 (K = 5520).  So
-          // every few slots' sums are added up here, rounded to nearest.
-          uint32_t z[A][C][32] = {};
-          const int stretches = (T.nk + bf_stretch(PAIR) - 1) / bf_stretch(PAIR);
-          for (int i = 0; i < stretches; ++i) {
-            ok = __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p)) && ok;
-            tc_fence_after();
+        // The tensor cores' fp32 accumulation drops bits towards zero, at each of its
+        // steps of 16: after K / 16 of them a loss of 12 was off by 2e-5 (K = 5520), and the
+        // gradient of a token that is certain but for 1e-4 by more than itself.  So every few
+        // slots' sums are added up here, rounded to nearest.
+        uint32_t z[2][R][32];
+        const int stretches = (T.nk + bf_stretch(PAIR) - 1) / bf_stretch(PAIR);
+        for (int i = 0; i < stretches; ++i) {
+          ok = __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p)) && ok;
+          tc_fence_after();
+          auto from = [&](int s, int r) {
+            return t_lane + static_cast<uint32_t>(b * ACC + half(s) * BC + chunk(s, r));
+          };
+          if (i == 0) {
 #pragma unroll
-            for (int a = 0; a < A; ++a)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-              for (int j = 0; j < C; ++j)
-                if (a < halves && chunk(j) < T.cols) {
+              for (int r = 0; r < R; ++r)
+                if (there(s, r)) tmem_ld_32x32b_x32(from(s, r), z[s][r]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int r = 0; r < R; ++r)
+                if (there(s, r)) tmem_wait_ld(z[s][r]);
+          } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int r = 0; r < R; ++r)
+                if (there(s, r)) {
 #pragma unroll
                   for (int h = 0; h < 32; h += 16) {
                     uint32_t v[16];
-                    tmem_ld_32x32b_x16(t_lane + static_cast<uint32_t>(b * ACC + a * BC + chunk(j) + h), v);
+                    tmem_ld_32x32b_x16(from(s, r) + h, v);
                     tmem_wait_ld16(v);
 #pragma unroll
                     for (int m = 0; m < 16; ++m)
-                      z[a][j][h + m] = __float_as_uint(__uint_as_float(z[a][j][h + m]) + __uint_as_float(v[m]));
+                      z[s][r][h + m] = __float_as_uint(__uint_as_float(z[s][r][h + m]) + __uint_as_float(v[m]));
                   }
                 }
-            give_back();
-          }
-          if (x.words_on_lanes) {
-#pragma unroll
-            for (int j = 0; j < C; ++j) {
-              if (chunk(j) >= T.cols) break;
-              Token u = token(T.q0 + chunk(j) + lane, ok && chunk(j) + lane < T.cols);
-#pragma unroll
-              for (int a = 0; a < A; ++a) {
-                if (a >= halves || quarter(a) >= l_end) break;
-                transpose_32x32(z[a][j]);
-                take(u, z[a][j], quarter(a), l_end - quarter(a));
-              }
-              leave(u, (T.l0 / p.lanes * (PAIR ? 2 : 1) + static_cast<int>(side)) * 4 + q);
-            }
-          } else {
-#pragma unroll
-            for (int a = 0; a < A; ++a) {
-              if (a >= halves) break;
-              if (!ok) k[a].l = -1;
-#pragma unroll
-              for (int j = 0; j < C; ++j)
-                if (chunk(j) < T.cols) take(k[a], z[a][j], T.q0 + chunk(j), T.cols - chunk(j));
-              leave(k[a], T.q0 / p.bc * 2 + eh);
-            }
-          }
-        } else {
-          Token u{};
-          if (x.words_on_lanes) u = token(T.q0 + 32 * eh + lane, 32 * eh + lane < T.cols);
-          ok = __all_sync(0xffffffffu, wait_bar(bar(L::T_FULL + b), bph, abort_flag, p));
-          tc_fence_after();
-          if (x.words_on_lanes) {
-            for (int c = 32 * eh; c < T.cols; c += 64) {
-              if (c >= 64) u = token(T.q0 + c + lane, c + lane < T.cols);
-              if (!ok) u.l = -1;
-              for (int a = 0; a < halves; ++a) {
-                if (quarter(a) >= l_end) break;
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
-                tmem_wait_ld(v);
-                transpose_32x32(v);
-                take(u, v, quarter(a), l_end - quarter(a));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int a = 0; a < A; ++a) {
-              if (a >= halves) break;
-              if (!ok) k[a].l = -1;
-              for (int c = 32 * eh; c < T.cols; c += 64) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(b * ACC + a * BC + c), v);
-                tmem_wait_ld(v);
-                take(k[a], v, T.q0 + c, T.cols - c);
-              }
-            }
           }
           give_back();
+        }
+        // (The steps one after the other through the same code: unrolled, the gradient of 300
+        // tokens' logits, 20000 x 1024, took 25.9 us, so 22.4: two tiles to a CTA, whose time is
+        // that of fetching instructions too.)
+        Token u[R];
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          if (x.words_on_lanes) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              if (chunk(s, r) >= T.cols) break;
+              if (PAIR || s == 0) {
+                u[r] = s == 0 && r == 0 ? k[0] : ask(T.q0 + chunk(s, r) + lane, chunk(s, r) + lane < T.cols);
+                ready(u[r]);
+                if (!ok) u[r].l = -1;
+              }
+              if (half(s) < halves && quarter(half(s)) < l_end) {
+                transpose_32x32(z[0][r]);
+                take(u[r], z[0][r], quarter(half(s)), l_end - quarter(half(s)));
+              }
+              if (PAIR || s == 1) leave(u[r], (T.l0 / p.lanes * (PAIR ? 2 : 1) + static_cast<int>(side)) * 4 + q);
+            }
+          } else if (half(s) < halves) {
+            if (!PAIR || s == 0) {
+              ready(k[0]);
+              if (!ok) k[0].l = -1;
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              if (there(s, r)) take(k[0], z[0][r], T.q0 + chunk(s, r), T.cols - chunk(s, r));
+            if (!PAIR || s == 1) leave(k[0], T.q0 / p.bc * 2 + eh);
+            if (!PAIR) k[0] = k[1];
+          }
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z[0][r][j] = z[1][r][j];
         }
       }
     }
