@@ -481,7 +481,8 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
 /* Softmax cross entropy of a product over a vocabulary, without its logits in
  * memory: the loss behind a model's last norm.  With z = X W^T in fp32 and y the
  * target of token t:
- *   lse[t] = log sum_v exp(z[t][v]);  loss[t] = lse[t] - z[t][y]
+ *   lse[t] = log sum_v exp(z[t][v]);  loss[t] = lse[t] - z[t][y], rounded once: never
+ *   negative, and exact to 2^-21 also where lse is large
  * A token whose target is outside [0, V) (-1, say: padding) has loss 0.
  *   X bf16 [T][K] and W bf16 [V][K], finite values; targets int32 [T]; loss, lse fp32
  *   [T], one of them may be null (lse: for the gradient)

@@ -209,10 +209,20 @@ loss_end_kernel(const LossEnd a) {
 #pragma unroll
       for (int w = 1; w < END_THREADS / 32; ++w) join(top, sum, share[w][lane].x, share[w][lane].y);
       constexpr float kLn2 = 0.6931471805599453f;
-      const float lse = (top + log2f(sum)) * kLn2;
+      const float rest = log2f(sum);
       const int y = __ldg(a.targets + t);
-      if (a.lse) a.lse[t] = lse;
-      if (a.loss) a.loss[t] = y >= 0 && y < a.V ? lse - __ldg(a.hit + t) : 0.f;
+      if (a.lse) a.lse[t] = (top + rest) * kLn2;
+      if (a.loss) {
+        // Not as lse less the target's logit, which may be hundreds and their difference 1e-3 or,
+        // rounded, negative: `top` is a logit times log2(e), rounded, and `rest` counts for what
+        // that is off by.
+        float loss = 0.f;
+        if (y >= 0 && y < a.V) {
+          loss = (fmaf(-__ldg(a.hit + t), kLog2e, top) + rest) * kLn2;
+          loss = loss < 0.f ? 0.f : loss;
+        }
+        a.loss[t] = loss;
+      }
     }
     __syncthreads();
   }

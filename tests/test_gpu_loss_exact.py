@@ -1,5 +1,5 @@
 """The cross entropy where its values are known more closely than loss_ref.py's bounds
-say: tokens that are nearly certain, whole-number logits, far logits."""
+say: whole-number logits, tokens that are nearly certain, far logits."""
 import pytest
 import torch
 
@@ -26,6 +26,26 @@ def whole(T, V, K, seed, words=3):
     X = torch.randint(-2, 3, (T, K), generator=g, device="cuda").to(BF16)
     W = torch.randint(-words, words + 1, (V, K), generator=g, device="cuda").to(BF16)
     return X, W
+
+
+@pytest.mark.parametrize("shape", [(40, 3000, 256), (300, 3000, 256), (7, 20000, 1024), (500, 1500, 1024), (9, 1, 64),
+                                   (130, 1, 64), (70, 2, 8)], ids=lambda s: "x".join(map(str, s)))
+def test_losses_of_exact_logits(shape):
+    # The loss by itself is off by what its exponentials (2^-21 of each, as everywhere), the
+    # sums (V / 64 and 32 terms) and its logarithm are, relative to the loss or to the one that
+    # the target's exponential is; not by a rounding of lse, which may be hundreds.
+    T, V, K = shape
+    X, W = whole(T, V, K, seed=K)
+    z = L.logits(X, W)
+    assert z.abs().max() < 2 ** 24
+    for t in (z.argmax(1), z.argsort(1)[:, V // 2], z.argmin(1)):
+        t = t.to(torch.int32)
+        loss, _ = forward(X, W, t)
+        want = L.loss(X, W, t)[0]
+        # (a log2 of the sum: off by 2 ulp, below 2^-22 of its value, which is at most 2 want + 2)
+        lim = 2.0 ** -21 * (1 + V / 2 ** 14) + 2.0 ** -21 * want
+        assert (loss >= 0).all(), loss.min()
+        assert ((loss.double() - want).abs() <= lim).all(), (loss.double() - want).abs().max()
 
 
 def certain(T, V, K, z, seed):
