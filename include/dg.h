@@ -627,8 +627,9 @@ dg_status dg_debug_force_block_scaled(int mode);
  * else the calls return DG_ERR_UNSUPPORTED_SHAPE; split: CTAs sharing a tile's
  * reduction, 1..8; calls of a few rows are tiled then, too; a plan of more CTAs
  * than a limit on the SMs allows is refused likewise).  It goes for the products of
- * the cross entropy as well (lanes and rows multiples of 64; its logits' products take
- * no split).  lanes = 0 leaves the choice to the library. */
+ * the cross entropy as well (rows multiples of 64; lanes too, of up to 64 tokens of 32,
+ * which the products of its gradients round up; its logits' products take no split).
+ * lanes = 0 leaves the choice to the library. */
 dg_status dg_debug_force_ragged_plan(int pair, int lanes, int rows, int split);
 
 #ifdef __cplusplus

@@ -54,13 +54,13 @@ long long piece_words(long long T, long long V) {
 // 32000 x 2048: 31 and 32); with more tokens the exchange between the lanes costs more
 // (128 of 32000 x 2048: 34 and 32, 300 of 20000 x 1024: 28 and 24, 4096 of 131072 x 2048:
 // 1176 and 1059).
-bool words_on_lanes(long long T) { return T <= 64; }
+constexpr int kWordsOnLanes = 64;   // tokens at most
 
 // Pairs of a token that the forward kernel may leave: with words on the lanes four per
 // 64 of them or more, else two per tile of at least 64 words (16 in a vocabulary of up
 // to 128).
 long long most_pairs(long long T, long long V) {
-  return (words_on_lanes(T) ? 4 : 2) * ((V + 63) / 64 + 8);
+  return (T <= kWordsOnLanes ? 4 : 2) * ((V + 63) / 64 + 8);
 }
 
 constexpr long long kHead = 256;   // bytes of the backward workspace before p: the unit
@@ -106,6 +106,7 @@ cudaError_t launch_product(BfCall& c, const LossCall& a, int num_sms, cudaStream
   c.epilogue = static_cast<BfEpilogue>(EPI);
   BfPlan f = a.forced.lanes > 0 ? a.forced : bf_plan(c, num_sms);
   if (FORM == kBfNT) f.split = 1;
+  else f.lanes = static_cast<int>(round_up(f.lanes, 64));   // (W's and X's boxes; of a forced plan)
   if (FORM == kBfTN && f.pair) f.bc = 256;   // (whole 128-wide halves)
   if (EPI == kBfSum) c.loss.parts = std::max(1, c.loss.parts);
   if (EPI == kBfStats)   // (of the words, for the joining kernel)
@@ -138,7 +139,7 @@ BfCall product(const LossCall& a, BfForm form, const void* A, const void* B, voi
 // The product whose sums are the logits of n words from w0 on.
 BfCall logits(const LossCall& a, int w0, int n) {
   const void* W = static_cast<const uint8_t*>(a.W) + 2ll * w0 * a.K;
-  const bool lanes = words_on_lanes(a.T);
+  const bool lanes = a.T <= kWordsOnLanes;
   BfCall c = lanes ? product(a, kBfNT, a.X, W, nullptr, a.T, 0, n, a.K)
                    : product(a, kBfNT, W, a.X, nullptr, n, 0, a.T, a.K);
   c.loss.words_on_lanes = lanes;
@@ -260,6 +261,8 @@ loss_join_kernel(const LossJoin a) {
 }
 
 }  // namespace
+
+bool loss_words_on_lanes(long long T) { return T <= kWordsOnLanes; }
 
 long long loss_workspace(long long T, long long V) { return T * (8 * most_pairs(T, V) + 4); }
 

@@ -25,8 +25,13 @@ struct LossCall {
   unsigned int debug_flags;
   bool limited;             // fewer SMs than the device has: no grid of more CTAs
   PFN_cuTensorMapEncodeTiled_v12000 encode;
-  BfPlan forced;            // lanes > 0: this plan (tests; the logits' product without a split)
+  BfPlan forced;            // lanes > 0: this plan (tests; the logits' product without a split,
+                            // the gradients' in whole 64-wide boxes)
 };
+
+// Whether T tokens have the words on the accumulator's lanes, in tiles of multiples of 32
+// (else of 64).
+bool loss_words_on_lanes(long long T);
 
 // Workspace of a call, in bytes.
 long long loss_workspace(long long T, long long V);

@@ -185,8 +185,9 @@ dg_status loss_state(dgk::LossCall* a, int* sms) {
   a->limited = st.sms < st.device_sms;
   a->encode = st.encode;
   a->forced = dgk::bf16_forced_plan();
-  // (the products read 64-wide boxes along the lanes and, for dW, the columns)
-  if (a->forced.lanes > 0 && !a->forced.pair && (a->forced.lanes % 64 != 0 || a->forced.bc % 64 != 0))
+  // (dW reads 64-wide boxes along the columns; words on the lanes are taken 32 at a time)
+  if (a->forced.lanes > 0 && !a->forced.pair &&
+      (a->forced.lanes % (dgk::loss_words_on_lanes(a->T) ? 32 : 64) != 0 || a->forced.bc % 64 != 0))
     return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "cross entropy: no kernel for the forced plan");
   if (a->forced.split * (a->forced.pair ? 2 : 1) > st.sms || (a->limited && a->forced.split > 1))
     return host_fail(DG_ERR_UNSUPPORTED_SHAPE, "cross entropy: forced plan past the limit on the SMs");
