@@ -106,8 +106,11 @@ struct BfSmem {
   // (checked build: fill counters of the lane and the column operand's slots)
   static constexpr int FILLS = MISC + 8;
   static constexpr int TAB = (FILLS + (kDebug ? 2 * BF_MAX_STAGES * 4 : 0) + 15) / 16 * 16;
-  // (the last: a word per epilogue warp)
-  __host__ __device__ static constexpr int fixed(int G) { return 1024 + TAB + 2 * (G + 1) * 4 + BF_EPI * 4; }
+  __host__ __device__ static constexpr int fixed(int G) { return 1024 + TAB + 2 * (G + 1) * 4; }
+  // (and of the gradient of the logits a word per epilogue warp)
+  __host__ __device__ static constexpr int fixed(int G, int epilogue) {
+    return fixed(G) + (epilogue == kBfGrad ? BF_EPI * 4 : 0);
+  }
 };
 
 // Slots that the logits' accumulation in tensor memory runs over: 512 of the reduction.
@@ -1228,7 +1231,7 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
   const int p_rows = PAIR ? 128 : lanes, q_rows = PAIR ? bc / 2 : bc;
   p.p_bytes = p_rows * BK * 2;
   p.q_bytes = q_rows * BK * 2;
-  p.stages = std::min(BF_MAX_STAGES, (kBfMaxSmem - BfSmem::fixed(c.G)) / (p.p_bytes + p.q_bytes));
+  p.stages = std::min(BF_MAX_STAGES, (kBfMaxSmem - BfSmem::fixed(c.G, EPI)) / (p.p_bytes + p.q_bytes));
   p.sizes = c.sizes;
   p.D = static_cast<uint16_t*>(c.D);
   p.C = static_cast<const uint16_t*>(c.C);
@@ -1279,7 +1282,7 @@ cudaError_t launch_tiles(const BfCall& c, PFN_cuTensorMapEncodeTiled_v12000 enco
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(bf16_grid(c, plan, num_sms)), 1, 1);
   cfg.blockDim = dim3(BF_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = p.stages * (p.p_bytes + p.q_bytes) + BfSmem::fixed(c.G);
+  cfg.dynamicSmemBytes = p.stages * (p.p_bytes + p.q_bytes) + BfSmem::fixed(c.G, EPI);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
