@@ -324,7 +324,7 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
   if (s != DG_OK) return s;
   const cudaError_t e = dgk::launch_combine_backward(
       dgk::CombineBwd{dO, Y, rows, weights, dY, d_weights, T, K, top_k, num_rows, st.status}, st.sms,
-      st.sms < st.device_sms, static_cast<cudaStream_t>(stream));
+      st.device_sms, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_fail(e, "combine gradient launch") : host_ok();
 }
 

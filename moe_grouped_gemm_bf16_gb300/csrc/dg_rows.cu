@@ -284,10 +284,10 @@ dispatch_kernel(const DispatchCall a) {
 // ---------------------------------------------------------- weighted sum ----
 // (blocks per SM: with 2, 3 and 4, the last with spills, 4096 tokens of 8 rows of 7168 take
 // 127, 102 and 107 us, their gradient 209, 174 and 192)
-constexpr int SUM_THREADS = 256, SUM_PER_SM = 3;
+constexpr int SUM_THREADS = kSumThreads, SUM_PER_SM = kSumPerSm;
 // 16-byte vectors that a thread has in flight: of ROWS rows, VECS of each.  Few choices
 // take more of each row (3393 tokens of one row of 5016: 35 us with one vector of it).
-constexpr int SUM_LOADS = 8;
+constexpr int SUM_LOADS = kSumLoads;
 
 // A warp takes 256 VECS columns of a token, a lane eight of each 256, of all its rows:
 // products and sum in fp32 in the order of the choices, the residual added first.
@@ -551,32 +551,11 @@ cudaError_t launch_combine(const CombineCall& a, int num_sms, bool limited, cuda
                           SUM_THREADS, stream, 0, a);
 }
 
-// Threads to a token in the gradient of combine: those with the least rounds of tokens
-// times what one takes (a round of loads for each of its iterations, and one more for
-// the sums): 9451 tokens of one row of 360 take 9.3, 14, 24 and 39 us with 32, 64, 128 and
-// 256, 480 of 8 rows of 7688 82, 48, 34 and 35, 4096 of 8 rows of 7168 216, 185, 170 and
-// 174.  (By the whole device's SMs, whatever the limit: the sums' order is the team's.)
-static int team_of(int T, int vecs, int k, int rows) {
-  constexpr long long kThreads = 152ll * SUM_PER_SM * SUM_THREADS;
-  int best = SUM_THREADS;
-  long long least = -1;
-  for (int team = SUM_THREADS; team >= 32; team /= 2) {
-    const long long each = team * (SUM_LOADS / rows);
-    const long long turns = (vecs + each - 1) / each * ((k + rows - 1) / rows);
-    const long long cost = ((T + kThreads / team - 1) / (kThreads / team)) * (1 + turns);
-    if (least < 0 || cost < least) {
-      least = cost;
-      best = team;
-    }
-  }
-  return best;
-}
-
-cudaError_t launch_combine_backward(const CombineBwd& a, int num_sms, bool limited,
+cudaError_t launch_combine_backward(const CombineBwd& a, int num_sms, int device_sms,
                                     cudaStream_t stream) {
   const int rows = a.k <= 2 ? 2 : a.k <= 4 ? 4 : 8;
-  const int team = team_of(a.T, a.K >> 3, a.k, rows);
-  const dim3 grid(move_grid(a.T, SUM_THREADS / team, SUM_PER_SM, num_sms, limited));
+  const int team = combine_team(a.T, a.K >> 3, a.k, rows, device_sms);
+  const dim3 grid(move_grid(a.T, SUM_THREADS / team, SUM_PER_SM, num_sms, num_sms < device_sms));
   auto go = [&](auto two, auto four, auto eight) {
     return launch_dependent(rows == 2 ? two : rows == 4 ? four : eight, grid, SUM_THREADS, stream, 0, a);
   };

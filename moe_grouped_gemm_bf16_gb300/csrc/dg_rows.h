@@ -63,7 +63,33 @@ cudaError_t rows_set_up();   // opts the kernels into their shared memory (once 
 cudaError_t launch_rows(const RowsCall& a, RowsLayout layout, int num_sms, cudaStream_t stream);
 cudaError_t launch_dispatch(const DispatchCall& a, int num_sms, bool limited, cudaStream_t stream);
 cudaError_t launch_combine(const CombineCall& a, int num_sms, bool limited, cudaStream_t stream);
-cudaError_t launch_combine_backward(const CombineBwd& a, int num_sms, bool limited,
+cudaError_t launch_combine_backward(const CombineBwd& a, int num_sms, int device_sms,
                                     cudaStream_t stream);
+
+// Threads of a block, blocks per SM and 16-byte vectors that a thread has in flight in combine
+// and its gradient (dg_rows.cu says why).
+constexpr int kSumThreads = 256, kSumPerSm = 3, kSumLoads = 8;
+
+// Threads to a token in the gradient of combine, `rows` of its k rows of `vecs` vectors at a
+// time: those with the least rounds of tokens times what one takes (a round of loads for each of its
+// iterations, and one more for the sums): 9451 tokens of one row of 360 take 9.3, 14, 24 and 39 us
+// with 32, 64, 128 and 256, 480 of 8 rows of 7688 82, 48, 34 and 35, 4096 of 8 rows of 7168 216,
+// 185, 170 and 174.  (By the whole device's SMs, whatever the limit: the sums' order is the
+// team's.)
+inline int combine_team(int T, int vecs, int k, int rows, int device_sms) {
+  const long long threads = 1ll * device_sms * kSumPerSm * kSumThreads;
+  int best = kSumThreads;
+  long long least = -1;
+  for (int team = kSumThreads; team >= 32; team /= 2) {
+    const long long each = team * (kSumLoads / rows);
+    const long long turns = (vecs + each - 1) / each * ((k + rows - 1) / rows);
+    const long long cost = ((T + threads / team - 1) / (threads / team)) * (1 + turns);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = team;
+    }
+  }
+  return best;
+}
 
 }  // namespace dgk
