@@ -18,7 +18,9 @@
  *
  * Conventions shared by all entry points
  *  - All tensor arguments are DEVICE pointers owned by the caller; the library
- *    keeps no reference after the call returns and allocates nothing.
+ *    keeps no reference after the call returns and allocates nothing.  What a call
+ *    writes (workspaces too) overlaps none of its other arguments, but where it says
+ *    that one may be another.
  *  - A, B, D and sa must be 16-byte aligned; sb 4-byte aligned.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *    default stream).  A call never synchronises, never reads device memory
@@ -450,7 +452,8 @@ dg_status dg_expert_rows_masked(const int32_t* experts, int32_t* masked_m, int32
  *              (num_groups = 1, max_m = M_total: the contiguous layout); K a
  *              multiple of 128, ld_sa >= T and ld_out >= max_m multiples of 4
  * A row outside [-1, num_rows) is left out and reported as DG_ERR_EXPERT_RANGE.
- * Tensors 16-byte, rows 4-byte aligned; D overlaps nothing else.  T == 0 is a no-op. */
+ * Two choices share no row (whose X it then held would be left to chance).  Tensors
+ * 16-byte, rows 4-byte aligned.  T == 0 is a no-op. */
 dg_status dg_dispatch_rows_bf16(const void* X, const int32_t* rows, void* D, int T, int K, int top_k,
                                 int num_rows, void* stream);
 dg_status dg_dispatch_rows_fp8_1x128(const void* Q, const float* sa, int ld_sa, const int32_t* rows,
@@ -481,8 +484,8 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
 /* Softmax cross entropy of a product over a vocabulary, without its logits in
  * memory: the loss behind a model's last norm.  With z = X W^T in fp32 and y the
  * target of token t:
- *   lse[t] = log sum_v exp(z[t][v]);  loss[t] = lse[t] - z[t][y], rounded once: never
- *   negative, and exact to 2^-21 also where lse is large
+ *   lse[t] = log sum_v exp(z[t][v]);  loss[t] = lse[t] - z[t][y] (not of the
+ *   rounded lse: never negative, and no less exact where lse is in the hundreds)
  * A token whose target is outside [0, V) (-1, say: padding) has loss 0.
  *   X bf16 [T][K] and W bf16 [V][K], finite values; targets int32 [T]; loss, lse fp32
  *   [T], one of them may be null (lse: for the gradient)

@@ -9,10 +9,12 @@
 // the accumulator's columns and tokens on its lanes (of few tokens the other way
 // round).  A lane then has 256 logits of one token, and leaves the largest of them and
 // the sum of the exponentials relative to it; a second kernel joins the tiles' pairs.
-// The logits never leave tensor memory.
+// The logits never leave the SM.
 //
 // Backward: per piece of the vocabulary the logits again, whose epilogue writes p in
-// bf16 (as every operand of these products; one rounding, by 2^-9 of itself at most),
+// bf16 (as every operand of these products; one rounding, by 2^-8 of itself at most; a
+// component that W's rows share is multiplied by what a token's roundings come to, as p itself
+// sums to 0),
 // then the piece's rows of dW (form tn) and its share of dX (form nn), which is added
 // up in fp32 over the pieces and rounded once with the last.  p is written relative
 // to the largest |d_loss|, the unit, and the products' sums are multiplied by it: with
@@ -48,13 +50,14 @@ long long piece_words(long long T, long long V) {
   return round_up((V + pieces - 1) / pieces, 256);
 }
 
-// Whether the words are on the accumulator's lanes.  A tile then is 256 words by as
-// many tokens as there are, and the time that of reading W once (forward, 7 tokens of
-// 50003 x 4096: 70 us so, 92 with tokens on the lanes, 1 of 8000 x 1000: 12 and 16, 61 of
-// 32000 x 2048: 31 and 32); with more tokens the exchange between the lanes costs more
-// (128 of 32000 x 2048: 34 and 32, 300 of 20000 x 1024: 28 and 24, 4096 of 131072 x 2048:
-// 1176 and 1059).
-constexpr int kWordsOnLanes = 64;   // tokens at most
+// Up to how many tokens the words are on the accumulator's lanes.  A tile then is up to
+// 256 words by as many tokens as there are, and the time that of reading W once (forward, 7
+// tokens of 50003 x 4096: 70 us so, 97 with tokens on the lanes, 1 of 8000 x 1000: 11 and 16, 61 of
+// 32000 x 2048: 29.4 and 31.9); with more tokens the exchange between the lanes costs more
+// (65 of 32000 x 2048: 33.6 and 31.9, 128: 34.6 and 32.1, 300 of 20000 x 1024: 27.7 and 23.9,
+// 4096 of 131072 x 2048, a dozen calls by themselves, before the power cap lowers the clock:
+// 1409 and 1100).
+constexpr int kWordsOnLanes = 64;
 
 // Pairs of a token that the forward kernel may leave: with words on the lanes four per
 // 64 of them or more, else two per tile of at least 64 words (16 in a vocabulary of up

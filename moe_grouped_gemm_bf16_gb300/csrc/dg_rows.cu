@@ -282,8 +282,9 @@ dispatch_kernel(const DispatchCall a) {
 }
 
 // ---------------------------------------------------------- weighted sum ----
-// (blocks per SM: with 2, 3 and 4, the last with spills, 4096 tokens of 8 rows of 7168 take
-// 127, 102 and 107 us, their gradient 209, 174 and 192)
+// (blocks per SM: with 2, 3 and 4, 4096 tokens of 8 rows of 7168 take 127, 102 and 107 us,
+// their gradient 209, 174 and 192.  Of 80 registers a thread some spill, 28 to 84 bytes, in
+// every instance but those of 8 rows at a time in combine and in its gradient by warps.)
 constexpr int SUM_THREADS = kSumThreads, SUM_PER_SM = kSumPerSm;
 // 16-byte vectors that a thread has in flight: of ROWS rows, VECS of each.  Few choices
 // take more of each row (3393 tokens of one row of 5016: 35 us with one vector of it).
