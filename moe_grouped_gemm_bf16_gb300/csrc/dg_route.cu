@@ -287,7 +287,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // d = |x - max| = ln(share / s), below 88 where e is held; the sum, common to
 // both, by (4 + 2.5 ln(1024)) u for its terms and 40 u for its additions and its
 // reciprocal: with s d < 0.37 share below 2^-17 share in all, with d < 88 below 2^-14 of
-// s.  (2769 tokens of 160 experts in 8 groups by sums of two: 9.9 us, with 2^-17 for all
+// s.  (2769 tokens of 160 experts in 8 groups by sums of two: 10.9 us, with 2^-17 for all
 // 18.6.)  From there on, below 2^-126, e is 0, which is off by all that it was: 2^-125 for
 // both, whatever s is.
 // Each c: u of itself, and by NPL 2^-23 of itself, as a key whose last bits say which of
@@ -404,9 +404,9 @@ struct RoutePlan {
 // tokens: 9268 tokens of 16 experts took 9 us with a warp each).  LOGITS: there are no
 // biases and no sums of two, so that the logits decide (16384 tokens of 128 experts in
 // bf16: 8.9 us without instances of its own).  The blocks per SM leave 48 or 64
-// registers a thread of up to 8 experts, and spills (of 8 experts with biases 172 bytes, in
-// bf16 244): with a block less 8192 tokens of 256 in 8 groups by sums of two with biases take
-// 19.1 us, so 17.4, by softmax 23.6 and 22.6, but 2769 of 160 without biases 9.7 and 10.9.
+// registers a thread of up to 8 experts, and spills (of 8 experts with biases 178 bytes, in
+// bf16 246): with a block less 8192 tokens of 256 in 8 groups by sums of two with biases take
+// 18.6 us, so 17.0, by softmax 23.2 and 22.3, but 2769 of 160 without biases 9.6 and 10.9.
 template <class X, int NPL, int LANES, bool LOGITS>
 __global__ void __launch_bounds__(32 * RT_WARPS, NPL <= 4 ? 5 : NPL == 8 ? 4 : NPL == 16 ? 2 : 1)
 route_kernel(const RouteFwd a, const RoutePlan plan) {
@@ -439,10 +439,17 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
     for (int i = 0; i < NPL; ++i)
       if (e0 + i < a.G) {
         even = even && b[i] == first;
-        if (fabsf(b[i]) < INFINITY) bias_most = fmaxf(bias_most, fabsf(b[i]));
+        bias_most = fmaxf(bias_most, fabsf(b[i]));
       }
     even = __all_sync(ALL, even);
     bias_most = __uint_as_float(__reduce_max_sync(ALL, __float_as_uint(bias_most)));
+    if (bias_most == INFINITY) {   // (in all lanes) the largest finite one
+      bias_most = 0.f;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (e0 + i < a.G && fabsf(b[i]) < INFINITY) bias_most = fmaxf(bias_most, fabsf(b[i]));
+      bias_most = __uint_as_float(__reduce_max_sync(ALL, __float_as_uint(bias_most)));
+    }
   }
   const bool grouped = plan.grouped;
   const bool by_logit = LOGITS || (even && (!grouped || a.best == 1));
@@ -575,14 +582,9 @@ route_kernel(const RouteFwd a, const RoutePlan plan) {
       uint32_t lanes = __ballot_sync(ALL, stays) >> (team * LANES);
       const uint32_t last = ~team_max<LANES>(stays ? ~value : 0);
       const uint32_t next = team_max<LANES>(stays ? 0 : value);
-      // What is rounded are a sum's two values: of opposite signs (only biases are negative),
-      // they are larger than it.  (By all lanes: `next` differs between the warp's tokens.)
-      float more = 0.f;
-      if (!LOGITS && a.bias) {
-        const float c1 = two ? float_of(one) : 0.f, c2 = two ? float_of(two) : 0.f;
-        more = a.best == 2 && c1 > 0.f && c2 < 0.f ? fminf(c1, -c2) : 0.f;
-        more = __uint_as_float(team_max<LANES>(__float_as_uint(more)));
-      }
+      // What is rounded are a sum's two values: of opposite signs they are larger than it, by
+      // no more than the bias of the negative one.
+      const float more = !LOGITS && a.best == 2 ? bias_most : 0.f;
       if (!by_logit && next) {
         const float l = float_of(last), n = float_of(next);
         sure = l - n > 2.f * doubt<NPL>(a.sigmoid, fmaxf(fabsf(l), fabsf(n)) + more, bias_most, share);
