@@ -498,11 +498,12 @@ dg_status dg_combine_rows_backward(const void* dO, const void* Y, const int32_t*
  *       whose d_loss does not count), rounded to bf16 relative to the largest |d_loss|;
  *       z is summed up as in the forward call
  *   dX = p W, bf16 [T][K];  dW = p^T X, bf16 [V][K]: sums in fp32, one rounding; one
- *   of them may be null (not computed)
+ *   of them may be null (not computed).  dW's sums run over all tokens in the tensor cores,
+ *   which drop half of 2^-23 of them every 16: of 2^20 tokens and more, bits that bf16 holds
  *   lse        what the forward call wrote for these X and W
  *   workspace  dg_linear_cross_entropy_backward_workspace_bytes(T, V, K) bytes, as above
- *              (a piece of p: 384 MB, or 4096 words of each token, at most; and dX in
- *              fp32 where there is more than one piece, or in parts of few tokens)
+ *              (a piece of p: 384 MB, or 4096 words of each token, at most, and 2^20 words;
+ *              and dX in fp32 where there is more than one piece, or in parts of few tokens)
  * The sums run in a fixed order: the same inputs give the same bits on the same
  * number of SMs.  K a multiple of 8; too large (DG_ERR_UNSUPPORTED_SHAPE): T or K of 2^23
  * or more, V of 2^29, X or W of 2^34 elements, T * V of 2^38.  X, W, dX and dW

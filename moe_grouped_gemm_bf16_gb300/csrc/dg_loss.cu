@@ -39,12 +39,15 @@ namespace {
 
 constexpr long long kPieceBytes = 384ll << 20;  // of p
 constexpr int kPieceLeast = 4096;               // words: whole waves of tiles
+// and at most: dX's sum over a piece drops up to half of 2^-23 of itself at each 16 words (of
+// 4e8 words in two pieces it was off by 0.06 of itself)
+constexpr int kPieceMost = 1 << 20;
 
 long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
 
 // Words of a piece, a multiple of 8 (of 256 where there are more pieces).
 long long piece_words(long long T, long long V) {
-  const long long most = std::max<long long>(kPieceLeast, kPieceBytes / (2 * std::max(1ll, T)));
+  const long long most = std::clamp<long long>(kPieceBytes / (2 * std::max(1ll, T)), kPieceLeast, kPieceMost);
   if (V <= most) return round_up(V, 8);
   const long long pieces = (V + most - 1) / most;
   return round_up((V + pieces - 1) / pieces, 256);

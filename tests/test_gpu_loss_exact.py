@@ -129,3 +129,27 @@ def test_rows_of_the_output_matrix_that_share_a_component():
     loss, lse = forward(X, W, t)
     check_forward(X, W, t, loss, lse)
     check_backward(X, W, t, lse, d, *backward(X, W, t, lse, d))
+
+
+def test_a_vocabulary_of_many_pieces():
+    # sums over 2^20 words at most, in 8 shares at least: 8192 steps of the tensor cores, each of
+    # which drops 2^-23 of its partial sum at most, 1e-3 in all; p's rounding and the output's
+    T, V, K = 3, 200_000_000, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randn(T, K, generator=g, device="cuda").to(BF16)
+    W = torch.empty(V, K, dtype=BF16, device="cuda").normal_(0.0, 0.7, generator=g)
+    t = torch.tensor([V - 1, 5, 2 ** 27 + 3], dtype=torch.int32, device="cuda")
+    d = torch.tensor([1.0, -0.5, 0.25], device="cuda")
+    loss, lse = forward(X, W, t)
+    z = torch.cat([L.logits(X, w) for w in W.split(25_000_000)], 1)
+    want = torch.logsumexp(z, 1)
+    assert ((lse.double() - want).abs() <= 1e-6 * want).all()
+    dX, dW = backward(X, W, t, lse, d)
+    p = torch.exp(z.sub_(lse.double()[:, None]))
+    p[torch.arange(T), t.long()] -= 1.0
+    p *= d.double()[:, None]
+    want = sum(p[:, i:i + 25_000_000] @ W[i:i + 25_000_000].double() for i in range(0, V, 25_000_000))
+    assert ((dX.double() - want).norm(dim=1) <= (2 * L.BF16_ROUND + 1e-3) * want.norm(dim=1)).all()
+    for rows in (slice(0, 300), slice(2 ** 27 - 100, 2 ** 27 + 200), slice(V - 300, V)):
+        want = p[:, rows].t() @ X.double()
+        assert (dW[rows].double() - want).norm() <= 2 * L.BF16_ROUND * want.norm()
